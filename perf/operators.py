@@ -18,7 +18,7 @@ import torch
 own = False
 
 PAGE = 64        # tokens of a cache page
-GROUP = 64       # channels that share one (half step, middle) pair
+GROUP = 64       # channels that share one (step, middle) pair
 CLAMP = 57344.0  # what a cached value saturates at
 DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
 
@@ -188,43 +188,43 @@ def _where(table, kv_len, start, n):
 
 
 def _parts(cache):
-    """The four parts of every page record: key codes [token][quad][step][byte], value codes
-    [four tokens][lane][token][group, two bytes], and their (half step, middle) pairs."""
+    """The four parts of every page record: key codes [token][quad][32 channels][byte], value
+    codes [four tokens][lane][group][token, two bytes], and their (step, middle) pairs."""
     d = cache.shape[2] // 72
     return (cache[:, :, :32 * d].unflatten(2, (PAGE, 4, d // 32, 4)),
-            cache[:, :, 32 * d:64 * d].unflatten(2, (16, 16, 4, d // 64, 2)),
+            cache[:, :, 32 * d:64 * d].unflatten(2, (16, 16, d // 64, 4, 2)),
             cache[:, :, 64 * d:68 * d].view(torch.float16).unflatten(2, (PAGE, d // 64, 2)),
             cache[:, :, 68 * d:].view(torch.float16).unflatten(2, (16, d // 64, 2, 4)))
 
 
 def _quantise(x):
-    """x[n][heads][dim] -> codes 0..15, half step and middle of each group, both 16-bit."""
+    """x[n][heads][dim] -> codes 0..15, step and middle of each group, both 16-bit."""
     x = x.float().clamp(-CLAMP, CLAMP).unflatten(2, (-1, GROUP))
     lo, hi = x.amin(3, True), x.amax(3, True)
-    mid = ((lo + hi) * 0.5).half()
-    half = (torch.maximum(hi - mid.float(), mid.float() - lo) * np.float32(1 / 15).item()).half()
-    h = half.float()
-    inv = torch.where(h > 0, 0.5 / h, torch.zeros_like(h))
-    code = ((x - mid.float()) * inv + 7.5).round().clamp(0, 15).to(torch.uint8)
-    return code.flatten(2), half.squeeze(3), mid.squeeze(3)
+    mid = (lo + (hi - lo) * np.float32(8 / 15).item()).half()
+    m = mid.float()
+    step = torch.maximum((hi - m) * np.float32(1 / 7).item(), (m - lo) * 0.125).half()
+    inv = torch.where(step > 0, 1 / step.float(), torch.zeros_like(m))
+    code = ((x - m) * inv + 8).round().clamp(0, 15).to(torch.uint8)
+    return code.flatten(2), step.squeeze(3), mid.squeeze(3)
 
 
 def _write(cache, page, place, k, v):
     kc, vc, km, vm = _parts(cache)
     n, heads, d = k.shape
-    code, half, mid = _quantise(k)
+    code, step, mid = _quantise(k)
     code = code.view(n, heads, d // 32, 4, 4, 2).transpose(2, 3)
     kc[page, :, place] = code[..., 0] | code[..., 1] << 4
-    km[page, :, place] = torch.stack([half, mid], 3)
-    code, half, mid = _quantise(v)
+    km[page, :, place] = torch.stack([step, mid], 3)
+    code, step, mid = _quantise(v)
     code = code.view(n, heads, d // 64, 16, 2, 2).transpose(2, 3)
-    vc[page, :, place // 4, :, place % 4] = code[..., 0] | code[..., 1] << 4
-    vm[page, :, place // 4, :, :, place % 4] = torch.stack([half, mid], 3)
+    vc[page, :, place // 4, :, :, place % 4] = code[..., 0] | code[..., 1] << 4
+    vm[page, :, place // 4, :, :, place % 4] = torch.stack([step, mid], 3)
 
 
-def _value(code, half, mid):
+def _value(code, step, mid):
     """codes [..., groups, 64] -> fp32 values."""
-    return mid.float()[..., None] + half.float()[..., None] * (code.float() * 2 - 15)
+    return mid.float()[..., None] + step.float()[..., None] * (code.float() - 8)
 
 
 def _nibbles(x):
@@ -232,22 +232,22 @@ def _nibbles(x):
 
 
 def _key_rows(codes, meta):
-    """[..., quad, step, byte] and [..., group, 2] -> [..., dim]."""
+    """[..., quad, 32 channels, byte] and [..., group, 2] -> [..., dim]."""
     c = _nibbles(codes).transpose(-3, -2).flatten(-3).unflatten(-1, (-1, GROUP))
     return _value(c, meta[..., 0], meta[..., 1]).flatten(-2)
 
 
-def _value_rows(codes, half, mid):
+def _value_rows(codes, step, mid):
     """[..., lane, group, 2] and [..., group] -> [..., dim]."""
     c = _nibbles(codes).transpose(-3, -2).flatten(-2)
-    return _value(c, half, mid).flatten(-2)
+    return _value(c, step, mid).flatten(-2)
 
 
 def _read(cache, page, place):
     kc, vc, km, vm = _parts(cache)
     m = vm[page, :, place // 4, :, :, place % 4]
     return (_key_rows(kc[page, :, place], km[page, :, place]),
-            _value_rows(vc[page, :, place // 4, :, place % 4], m[..., 0], m[..., 1]))
+            _value_rows(vc[page, :, place // 4, :, :, place % 4], m[..., 0], m[..., 1]))
 
 
 def _plain_cache(s):
@@ -263,7 +263,7 @@ def _plain_attn(s):
     kc, vc, km, vm = _parts(s["cache"][s["table"].clamp(min=0).long()].flatten(0, 1))
     k = _key_rows(kc, km).unflatten(0, (seqs, -1)).transpose(1, 2).flatten(2, 3)
     vm = vm.permute(0, 1, 2, 5, 3, 4)   # [page][head][four tokens][token][group][2]
-    v = _value_rows(vc.transpose(3, 4), vm[..., 0], vm[..., 1]).flatten(2, 3)
+    v = _value_rows(vc.permute(0, 1, 2, 5, 3, 4, 6), vm[..., 0], vm[..., 1]).flatten(2, 3)
     v = v.unflatten(0, (seqs, -1)).transpose(1, 2).flatten(2, 3)
     t = k.shape[2]
     j = torch.arange(t, device=dev)
@@ -390,10 +390,10 @@ def _exact_rows(rec, d):
         for step in range(d // 32):
             for i, c in enumerate(_bits(kw[:, quad, step], 8)):
                 k[:, 32 * step + 8 * quad + i] = c
-    vw = rec[32 * d:64 * d].view("<u2").reshape(16, 16, 4, g)
+    vw = rec[32 * d:64 * d].view("<u2").reshape(16, 16, g, 4)
     for lane in range(16):
         for p in range(g):
-            for i, c in enumerate(_bits(vw[:, lane, :, p], 4)):
+            for i, c in enumerate(_bits(vw[:, lane, p], 4)):
                 v[:, 64 * p + 4 * lane + i] = c.reshape(-1)
     km = rec[64 * d:68 * d].view("<f2").astype(np.float64).reshape(PAGE, g, 2)
     vm = rec[68 * d:].view("<f2").astype(np.float64).reshape(16, g, 2, 4).transpose(0, 3, 1, 2)
@@ -401,8 +401,8 @@ def _exact_rows(rec, d):
     with np.errstate(invalid="ignore"):
         for p in range(g):
             at = slice(64 * p, 64 * p + 64)
-            k[:, at] = km[:, p, 1:] + km[:, p, :1] * (2 * k[:, at] - 15)
-            v[:, at] = vm[:, p, 1:] + vm[:, p, :1] * (2 * v[:, at] - 15)
+            k[:, at] = km[:, p, 1:] + km[:, p, :1] * (k[:, at] - 8)
+            v[:, at] = vm[:, p, 1:] + vm[:, p, :1] * (v[:, at] - 8)
     return k, v
 
 
@@ -413,12 +413,12 @@ def _exact_cached(x):
     x = np.clip(x.astype(f4), -f4(CLAMP), f4(CLAMP))
     x = x.reshape(x.shape[0], x.shape[1], -1, GROUP)
     lo, hi = x.min(3, keepdims=True), x.max(3, keepdims=True)
-    mid = ((lo + hi) * f4(0.5)).astype(np.float16).astype(f4)
-    half = (np.maximum(hi - mid, mid - lo) * f4(1 / 15)).astype(np.float16).astype(f4)
+    mid = (lo + (hi - lo) * f4(8 / 15)).astype(np.float16).astype(f4)
+    step = np.maximum((hi - mid) * f4(1 / 7), (mid - lo) * f4(1 / 8)).astype(np.float16).astype(f4)
     with np.errstate(divide="ignore"):
-        inv = np.where(half > 0, f4(0.5) / half, f4(0))
-    code = np.clip(np.rint((x - mid) * inv + f4(7.5)), 0, 15).astype(np.float64)
-    return (mid + half.astype(np.float64) * (2 * code - 15)).reshape(x.shape[0], x.shape[1], -1)
+        inv = np.where(step > 0, f4(1) / step, f4(0))
+    code = np.clip(np.rint((x - mid) * inv + f4(8)), 0, 15).astype(np.float64)
+    return (mid + step.astype(np.float64) * (code - 8)).reshape(x.shape[0], x.shape[1], -1)
 
 
 def exact(case, seed):
