@@ -48,6 +48,11 @@ extern "C" {
 #define BITNET_MAX_GROUP 8          /* matrices per bitnet_linear_i2s call     */
 #define BITNET_LINEAR_FUSED_MAX_N 2 /* bitnet_linear_i2s: one fused launch up to this N */
 #define BITNET_LUT_MAX_K 8192       /* largest K of the table-lookup decode call */
+#define BITNET_KV4_PAGE 64          /* tokens of a page of the 4-bit cache     */
+#define BITNET_KV4_GROUP 64         /* channels that share a step and a middle */
+#define BITNET_KV4_MAX_HEADS 1024   /* query heads, and kv heads, of a call    */
+#define BITNET_KV4_MAX_SEQS (1 << 20)  /* sequences of a call                  */
+#define BITNET_KV4_MAX_PAGES (1 << 24) /* pages of a sequence (2^30 tokens)    */
 
 typedef enum {
     BITNET_OK = 0,
@@ -281,6 +286,147 @@ int bitnet_absmean_i2s(const void *w, int dtype, int64_t M, int64_t K,
  */
 int bitnet_pack_i2s_f32(const float *w, int64_t M, int64_t K, uint8_t *packed,
                         float *w_max, void *stream);
+
+/*
+ * bitnet_block_norm_quant_i8 -- the boundary between two blocks of a layer: the
+ * norm after the block, its gate and residual scale, the residual stream, the
+ * norm before the next block, and the tokens for that block's matmuls.
+ * [P4 "Forward Pass"; P1 §4-5]
+ *
+ *   b        [N][F] the block's output (e.g. a projection's y), fp32 or bf16
+ *            (b_dtype).
+ *   post     non-zero: norm b first, with the gain post_gamma [F] or 1 (NULL).
+ *   gate     fp32 or NULL (1): token n's row at gate + n * gate_stride;
+ *            gate_stride is 0 (one row for every token) or at least F.
+ *   scale    the residual scale, finite (1 for none).
+ *   res, h   [N][F] the residual stream before and after, fp32 or bf16 (dtype).
+ *            res NULL: no residual, h must be NULL.  h NULL: not stored.  h may
+ *            be res itself; no other two arrays may overlap.
+ *   gamma    [F] fp32 gain of the norm before the next block, or NULL for 1.
+ *   eps      both norms' epsilon (positive, finite).
+ *   v        [N][F] the normed tokens, in dtype, or NULL.
+ *   xq, x_scale, x_sum   the tokens as bitnet_quant_act_i8 writes them, ready
+ *            for the matmul calls; all three or none (NULL).
+ *   At least one of h, v and xq is required.  F as K of the matmuls; rows and
+ *   gains 16-byte aligned.  0 <= N < 2^31; N == 0 is a no-op.
+ *
+ * Per token, every operation one fp32 rounding and in this order:
+ *   t = b;  post: t = (t * c) * post_gamma;  t = t * gate;  t = t * scale;
+ *   with res: h = res + t, rounded to dtype, and the norm reads h as stored;
+ *   v = (h * c) * gamma;  xq, x_scale, x_sum = bitnet_quant_act_i8 of v in fp32
+ * where c = fp32(1 / sqrt(ss / F + eps)), ss the sum of the F squares in
+ * binary64 (each square exact; one fixed order, which depends on F alone).
+ * Non-finite inputs give unspecified results.
+ */
+int bitnet_block_norm_quant_i8(const void *b, int b_dtype, int post, const float *post_gamma,
+                               const float *gate, int64_t gate_stride, float scale,
+                               const void *res, void *h, int dtype, const float *gamma,
+                               float eps, int64_t N, int64_t F, void *v, int8_t *xq,
+                               float *x_scale, int32_t *x_sum, void *stream);
+
+/*
+ * The 4-bit key/value cache, and the sequences of a call.
+ *
+ * The cache is n_pages pages of BITNET_KV4_PAGE tokens; a page is n_kv_heads
+ * records of 72 * head_dim bytes (4.5 bits a value).  head_dim is 64, 128 or
+ * 256.  The memory is the caller's; it needs no initialisation, and what no
+ * token was written to is never used.  Position p of sequence b is at token
+ * p % 64 of page table[b][p / 64].  A table entry outside [0, n_pages) marks an
+ * absent page: its tokens are not written, read as zeros and are not attended.
+ *
+ * A call's rows are tokens in order of their sequences: sequence b has the rows
+ * [q_start[b], q_start[b + 1]), and they are its LAST positions: row q_start[b]
+ * + i is at position kv_len[b] - (q_start[b + 1] - q_start[b]) + i.  So a step
+ * adds its new tokens to kv_len and then passes the same q_start to the append
+ * and the attention call.  q_start must not decrease, and all its rows lie in
+ * [0, N).  Rows in front of q_start[0] and behind q_start[n_seqs] are neither
+ * read nor written.  A row whose position is negative is not written, reads as
+ * zeros and attends to nothing.  kv_len is held to [0, 64 * max_pages].
+ *
+ * A value is quantised with the 63 others of its token's group of 64 channels
+ * (every operation one fp32 rounding):
+ *   x is held to [-57344, 57344] (a NaN counts as -57344); lo, hi the group's ends
+ *   mid  = fp16(lo + (hi - lo) * fp32(8/15))
+ *   step = fp16(max((hi - mid) * fp32(1/7), (mid - lo) / 8))
+ *   code = clamp(round_half_even((x - mid) * fp32(1/step) + 8), 0, 15); 8 if step is 0
+ *   the value it stands for: mid + step * (code - 8)
+ * The record: key codes [64 tokens][4][head_dim/32] dwords, dword (i, j) with
+ * channels 32 j + 8 i + 0..7, the first in its low bits; value codes [16][16]
+ * [head_dim/64][4] halfwords, halfword (a, i, g, t) with channels 64 g + 4 i +
+ * 0..3 of token 4 a + t; key pairs [64][head_dim/64] (step, mid); value pairs
+ * [16][head_dim/64] (4 steps, 4 mids) of four tokens.
+ *
+ *   table    [n_seqs][max_pages]   kv_len [n_seqs]   q_start [n_seqs + 1]
+ * are DEVICE int32 arrays, read when the call's kernels run, so a captured call
+ * follows their contents.  The descriptor itself is read during the call only.
+ */
+typedef struct {
+    void *cache;            /* 16-byte aligned */
+    int64_t n_pages;        /* 1 .. 2^31-1 */
+    int64_t n_kv_heads;     /* 1 .. BITNET_KV4_MAX_HEADS */
+    int64_t head_dim;       /* 64, 128 or 256 */
+    const int32_t *table;
+    int64_t max_pages;      /* 1 .. BITNET_KV4_MAX_PAGES */
+    const int32_t *kv_len;
+    const int32_t *q_start;
+    int64_t n_seqs;         /* 0 .. BITNET_KV4_MAX_SEQS */
+} bitnet_kv4_batch;
+
+/*
+ * bitnet_kv4_append -- quantise the keys and values of a call's rows into the
+ * cache.
+ *
+ *   k, v     rows of n_kv_heads * head_dim fp32 or bf16 values, row n at k + n *
+ *            k_stride elements (16-byte aligned, as the strides in bytes; a
+ *            stride of at least a row, so slices of one merged projection do).
+ *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or n_seqs == 0 is a no-op.
+ * If two rows have the same place (one page in two sequences' tables), what
+ * that token holds afterwards is unspecified; other tokens are not touched.
+ */
+int bitnet_kv4_append(const bitnet_kv4_batch *batch, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, int dtype, int64_t N, void *stream);
+
+/*
+ * bitnet_kv4_read -- what the cache holds at a call's rows, as fp32 or bf16
+ * (the fp32 value rounded to nearest even).
+ *
+ *   k, v     [N][n_kv_heads][head_dim] outputs, 16-byte aligned; one may be NULL.
+ */
+int bitnet_kv4_read(const bitnet_kv4_batch *batch, void *k, void *v, int dtype, int64_t N,
+                    void *stream);
+
+/*
+ * bitnet_attn_kv4 -- causal attention of a call's rows over the cache, for
+ * single tokens and prompts alike; the rows' own tokens are appended first.
+ *
+ *   q        rows of n_heads * head_dim fp32 or bf16 values, as k of the append;
+ *            n_heads a multiple of n_kv_heads, head h reads kv head
+ *            h / (n_heads / n_kv_heads).
+ *   scale    of q . k, positive and finite (usually 1 / sqrt(head_dim)).
+ *   window   0: a row at position p sees the positions 0 .. p; else those above
+ *            p - window and the first `sinks` positions.
+ *   max_kv   the longest kv_len that is expected (at most 64 * max_pages): it
+ *            decides how many workgroups share a sequence and so the workspace
+ *            and the speed, not what is computed.
+ *   out      [N][n_heads][head_dim] in dtype, 16-byte aligned.  A row that sees
+ *            nothing gets zeros.
+ *   workspace   device scratch of at least bitnet_attn_kv4_workspace bytes of the
+ *            same sizes, 16-byte aligned (may be NULL where that is 0); used until the
+ *            call's kernels have ended, so calls that may run at once need one
+ *            each.
+ *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or n_seqs == 0 is a no-op.
+ *
+ * fp32 calls compute to about fp32 accuracy (fp32 sums; factors of 22 bits),
+ * bf16 calls round q and the softmax weights to 11 bits and the output to bf16.
+ * Repeated calls with the same sizes give identical bits.
+ */
+int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t n_heads,
+                                  int64_t n_kv_heads, int64_t head_dim, int64_t max_kv);
+
+int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int64_t q_stride, int dtype,
+                    int64_t N, int64_t n_heads, float scale, int64_t window, int64_t sinks,
+                    int64_t max_kv, void *out, void *workspace, int64_t workspace_bytes,
+                    void *stream);
 
 /* Thread-local description of the last non-OK status on this thread
  * (empty string if none).  The pointer stays valid until the next call on

@@ -34,6 +34,18 @@ class I2SMatrix(ctypes.Structure):
                 ("y", ctypes.c_void_p)]
 
 
+KV4_PAGE = 64              # tokens of a page of the 4-bit cache
+
+
+class KV4Batch(ctypes.Structure):
+    """Mirror of bitnet_kv4_batch."""
+    _fields_ = [("cache", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("max_pages", ctypes.c_int64),
+                ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int64)]
+
+
 class BitnetError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"bitnet status {status}: {msg}")
@@ -116,6 +128,18 @@ def _open(path: str) -> ctypes.CDLL:
     L.bitnet_absmean_i2s.restype = ctypes.c_int
     L.bitnet_pack_i2s_f32.argtypes = [p, i64, i64, p, ctypes.POINTER(ctypes.c_float), p]
     L.bitnet_pack_i2s_f32.restype = ctypes.c_int
+    i32, kv4 = ctypes.c_int, ctypes.POINTER(KV4Batch)
+    L.bitnet_block_norm_quant_i8.argtypes = [p, i32, i32, p, p, i64, f32, p, p, i32, p, f32, i64,
+                                             i64, p, p, p, p, p]
+    L.bitnet_block_norm_quant_i8.restype = ctypes.c_int
+    L.bitnet_kv4_append.argtypes = [kv4, p, i64, p, i64, i32, i64, p]
+    L.bitnet_kv4_append.restype = ctypes.c_int
+    L.bitnet_kv4_read.argtypes = [kv4, p, p, i32, i64, p]
+    L.bitnet_kv4_read.restype = ctypes.c_int
+    L.bitnet_attn_kv4_workspace.argtypes = [i64] * 6
+    L.bitnet_attn_kv4_workspace.restype = i64
+    L.bitnet_attn_kv4.argtypes = [kv4, p, i64, i32, i64, i64, f32, i64, i64, i64, p, p, i64, p]
+    L.bitnet_attn_kv4.restype = ctypes.c_int
     for fn in ("bitnet_pack_i2s", "bitnet_quant_act_i8", "bitnet_gemv_i2s_i8",
                "bitnet_gemm_i2s_i8", "bitnet_gemv_i2s_lut", "bitnet_abi_version"):
         getattr(L, fn).restype = ctypes.c_int
@@ -415,3 +439,202 @@ def linear(x, mats, want_dot=True, want_y=True, out=None, qout=None):
     _check(load().bitnet_linear_i2s(_ptr(x), dt, N, K, _mat_array(mats, out), len(mats),
                                     _ptr(xq), _ptr(xs), _ptr(xsum), _stream(x)))
     return out, qout
+
+
+def _on(device):
+    """The tensors' device, made current for a launch on its current stream."""
+    import contextlib
+    import torch
+    if device.type != "cuda":
+        raise ValueError("tensor must live on the GPU")
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _dtype(t, name):
+    import torch
+    dt = {torch.float32: F32, torch.bfloat16: BF16}.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return dt
+
+
+def block_norm_quant(b, res=None, post_norm=False, post_gamma=None, gate=None, scale=1.0,
+                     gamma=None, eps=1e-5, want_v=False, want_q=True, out=None):
+    """The boundary between two blocks: norm of the block's output b[N][F]
+    (``post_norm``, gain ``post_gamma``), times ``gate`` ([F] or [N][F]) and
+    ``scale``, added to the residual stream ``res``; then the norm (gain
+    ``gamma``) whose tokens the next block takes, as int8 for the matmuls
+    (``want_q``) and / or as they are (``want_v``).
+
+    b and res are fp32 or bf16; h and v have res's type (b's without a res).
+    ``out``: (h, v, (xq, s, xsum)) to write into, None where not wanted; h may
+    be ``res`` itself.  Returns (h | None, v | None, (xq, s, xsum) | None)."""
+    import torch
+    if b.dim() != 2:
+        raise TypeError("b must be 2-D [N][F]")
+    N, F = b.shape
+    bd, dev = _dtype(b, "b"), b.device
+    stream = b if res is None else res
+    sd = _dtype(stream, "res")
+    if res is not None:
+        _expect(res, "res", res.dtype, (N, F), dev)
+    for name, t in (("post_gamma", post_gamma), ("gamma", gamma)):
+        if t is not None:
+            _expect(t, name, torch.float32, (F,), dev)
+    if post_gamma is not None and not post_norm:
+        raise ValueError("post_gamma without post_norm")
+    gate_stride = 0
+    if gate is not None:
+        _expect(gate, "gate", torch.float32, (F,) if gate.dim() == 1 else (N, F), dev)
+        gate_stride = 0 if gate.dim() == 1 else F
+    if out is None:
+        h = torch.empty_like(res) if res is not None else None
+        v = torch.empty((N, F), dtype=stream.dtype, device=dev) if want_v else None
+        q = (torch.empty((N, F), dtype=torch.int8, device=dev),
+             torch.empty((N,), dtype=torch.float32, device=dev),
+             torch.empty((N,), dtype=torch.int32, device=dev)) if want_q else None
+    else:
+        h, v, q = out
+        if h is not None:
+            if res is None:
+                raise ValueError("h without res")
+            _expect(h, "h", res.dtype, (N, F), dev)
+        if v is not None:
+            _expect(v, "v", stream.dtype, (N, F), dev)
+        if q is not None:
+            _expect(q[0], "xq", torch.int8, (N, F), dev)
+            _expect(q[1], "x_scale", torch.float32, (N,), dev)
+            _expect(q[2], "x_sum", torch.int32, (N,), dev)
+    xq, xs, xsum = q if q is not None else (None, None, None)
+    with _on(dev):
+        _check(load().bitnet_block_norm_quant_i8(
+            _ptr(b), bd, int(bool(post_norm)), _ptr(post_gamma), _ptr(gate), gate_stride,
+            float(scale), _ptr(res), _ptr(h), sd, _ptr(gamma), float(eps), N, F, _ptr(v),
+            _ptr(xq), _ptr(xs), _ptr(xsum), _stream(b)))
+    return h, v, q
+
+
+def kv4_cache(n_pages, n_kv_heads, head_dim, device="cuda"):
+    """A 4-bit key/value cache of ``n_pages`` pages of 64 tokens (uninitialised:
+    what no token was written to is never used), uint8 [n_pages][n_kv_heads]
+    [72 * head_dim]."""
+    import torch
+    if head_dim not in (64, 128, 256):
+        raise ValueError(f"head_dim={head_dim} must be 64, 128 or 256")
+    return torch.empty((n_pages, n_kv_heads, 72 * head_dim), dtype=torch.uint8, device=device)
+
+
+def _kv4_batch(cache, table, kv_len, q_start):
+    """Cache and sequences -> (bitnet_kv4_batch, kv heads, head_dim)."""
+    import torch
+    if cache.dim() != 3 or cache.dtype != torch.uint8 or cache.shape[2] % 72:
+        raise TypeError("cache must be uint8 [n_pages][n_kv_heads][72 * head_dim]")
+    dev = cache.device
+    if table.dim() != 2:
+        raise ValueError("table must be 2-D [n_seqs][max_pages]")
+    B, P = table.shape
+    _expect(table, "table", torch.int32, (B, P), dev)
+    _expect(kv_len, "kv_len", torch.int32, (B,), dev)
+    _expect(q_start, "q_start", torch.int32, (B + 1,), dev)
+    n_pages, heads, rec = cache.shape
+    return (KV4Batch(_ptr(cache), n_pages, heads, rec // 72, _ptr(table), P, _ptr(kv_len),
+                     _ptr(q_start), B), heads, rec // 72)
+
+
+def _rows(t, name, heads, dim, device):
+    """[N][heads][dim] with any stride between tokens -> that stride."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError(f"{name} must have shape [N][{heads}][{dim}], got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the values of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def kv4_append(cache, table, kv_len, q_start, k, v):
+    """Quantise keys and values k, v [N][n_kv_heads][head_dim] (fp32 or bf16, any
+    stride between tokens) into the cache, as the last positions of their
+    sequences: rows q_start[b] .. q_start[b+1] - 1 end at position kv_len[b] - 1
+    (kv_len counts them already).  table [B][max_pages], kv_len [B], q_start
+    [B+1]: int32 on the device, read when the kernel runs."""
+    batch, heads, dim = _kv4_batch(cache, table, kv_len, q_start)
+    dt = _dtype(k, "k")
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise TypeError("k and v must have the same shape and type")
+    ks, vs = _rows(k, "k", heads, dim, cache.device), _rows(v, "v", heads, dim, cache.device)
+    with _on(cache.device):
+        _check(load().bitnet_kv4_append(ctypes.byref(batch), k.data_ptr(), ks, v.data_ptr(), vs,
+                                        dt, k.shape[0], _stream(cache)))
+
+
+def kv4_read(cache, table, kv_len, q_start, n, dtype=None, out=None):
+    """What the cache holds at the last positions of each sequence (q_start as
+    in kv4_append, n rows in all) -> (k, v) [n][n_kv_heads][head_dim], fp32 or
+    bf16 (``dtype``).  ``out``: (k, v) to write into, one of them may be None."""
+    import torch
+    batch, heads, dim = _kv4_batch(cache, table, kv_len, q_start)
+    if out is None:
+        shape = (n, heads, dim)
+        out = tuple(torch.empty(shape, dtype=dtype or torch.float32, device=cache.device)
+                    for _ in range(2))
+    dts = {_dtype(t, "out") for t in out if t is not None}
+    if len(dts) != 1:
+        raise TypeError("k and v must have one type, float32 or bfloat16")
+    for name, t in zip("kv", out):
+        if t is not None:
+            _expect(t, name, dtype or t.dtype, (n, heads, dim), cache.device)
+    with _on(cache.device):
+        _check(load().bitnet_kv4_read(ctypes.byref(batch), _ptr(out[0]), _ptr(out[1]), dts.pop(),
+                                      n, _stream(cache)))
+    return out
+
+
+def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, max_kv=None,
+             out=None, workspace=None):
+    """Causal attention of q [N][n_heads][head_dim] (fp32 or bf16, any stride
+    between tokens) over the 4-bit cache, for single tokens and prompts: row
+    q_start[b] + i stands at position kv_len[b] - (q_start[b+1] - q_start[b]) + i
+    and sees the positions up to its own; with a ``window`` the last ``window``
+    of them and the first ``sinks``.  A row that sees nothing gets zeros.
+
+    scale: 1 / sqrt(head_dim) if None.  max_kv: the longest kv_len expected (the
+    table's capacity if None); it tunes the launch and changes no result beyond
+    rounding.  workspace: a uint8 tensor for calls that must not allocate
+    (attn_kv4_workspace bytes); one for each call that may run at once.
+    Returns out [N][n_heads][head_dim] in q's type."""
+    import torch
+    batch, kv_heads, dim = _kv4_batch(cache, table, kv_len, q_start)
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [N][n_heads][head_dim]")
+    N, heads, dev = q.shape[0], q.shape[1], cache.device
+    dt = _dtype(q, "q")
+    stride = _rows(q, "q", heads, dim, dev)
+    most = KV4_PAGE * table.shape[1]
+    max_kv = most if max_kv is None else min(int(max_kv), most)
+    need = attn_kv4_workspace(table.shape[0], N, heads, kv_heads, dim, max_kv)
+    if out is None:
+        out = torch.empty((N, heads, dim), dtype=q.dtype, device=dev)
+    else:
+        _expect(out, "out", q.dtype, (N, heads, dim), dev)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
+        raise ValueError(f"workspace must be {need} bytes of uint8 on {dev}")
+    with _on(dev):
+        _check(load().bitnet_attn_kv4(
+            ctypes.byref(batch), q.data_ptr(), stride, dt, N, heads,
+            dim ** -0.5 if scale is None else float(scale), int(window), int(sinks), max_kv,
+            _ptr(out), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            _stream(cache)))
+    return out
+
+
+def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv):
+    """Bytes of workspace that attn_kv4 takes for these sizes."""
+    need = load().bitnet_attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv)
+    if need < 0:
+        raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
+    return need

@@ -3,6 +3,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -450,6 +451,186 @@ BITNET_API int bitnet_linear_i2s(const void *x, int dtype, int64_t N, int64_t K,
                                  float *x_scale, int32_t *x_sum, void *stream) {
     return linear_impl("bitnet_linear_i2s", x, dtype, N, K, mats, n_mats, xq, x_scale, x_sum,
                        stream);
+}
+
+BITNET_API int bitnet_block_norm_quant_i8(const void *b, int b_dtype, int post,
+                                          const float *post_gamma, const float *gate,
+                                          int64_t gate_stride, float scale, const void *res,
+                                          void *h, int dtype, const float *gamma, float eps,
+                                          int64_t N, int64_t F, void *v, int8_t *xq,
+                                          float *x_scale, int32_t *x_sum, void *stream) {
+    const char *fn = "bitnet_block_norm_quant_i8";
+    for (int d : {b_dtype, dtype})
+        if (d != BITNET_F32 && d != BITNET_BF16)
+            return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, d);
+    if (N < 0 || N > 0x7fffffffLL)
+        return fail(BITNET_E_SHAPE, "%s: N=%lld out of range", fn, (long long)N);
+    if (int s = check_k(fn, F)) return s;
+    if (!(eps > 0.0f) || !(eps < 3.4e38f))
+        return fail(BITNET_E_VALUE, "%s: eps must be positive and finite", fn);
+    if (!(scale > -3.4e38f) || !(scale < 3.4e38f))
+        return fail(BITNET_E_VALUE, "%s: scale must be finite", fn);
+    if (gate && gate_stride != 0 && (gate_stride < F || gate_stride % 4 != 0))
+        return fail(BITNET_E_SHAPE, "%s: gate_stride=%lld must be 0 or a multiple of 4, at least F",
+                    fn, (long long)gate_stride);
+    if (N == 0) return ok();
+    if (!b) return fail(BITNET_E_NULL, "%s: b is required", fn);
+    if (h && !res) return fail(BITNET_E_NULL, "%s: h without res", fn);
+    if (post_gamma && !post) return fail(BITNET_E_VALUE, "%s: post_gamma without post", fn);
+    if ((xq || x_scale || x_sum) && !(xq && x_scale && x_sum))
+        return fail(BITNET_E_NULL, "%s: xq, x_scale and x_sum come together", fn);
+    if (!h && !v && !xq) return fail(BITNET_E_NULL, "%s: h, v and xq are all NULL", fn);
+    for (const void *p : {b, (const void *)post_gamma, (const void *)gate, res, (const void *)h,
+                          (const void *)gamma, (const void *)v, (const void *)xq})
+        if (!aligned(p, 16))
+            return fail(BITNET_E_ALIGN, "%s: rows and gains must be 16-byte aligned", fn);
+    if (!aligned(x_scale, 4) || !aligned(x_sum, 4))
+        return fail(BITNET_E_ALIGN, "%s: x_scale and x_sum must be 4-byte aligned", fn);
+    const bitnet::BlockNormArgs a{b, post_gamma, gate, gamma, res, h, v, xq, x_scale, x_sum,
+                                  gate_stride, scale, eps, (int)F, post != 0};
+    hipError_t e = bitnet::launch_block_norm(a, N, b_dtype == BITNET_BF16, dtype == BITNET_BF16,
+                                             static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+// Validate a cache descriptor and a call's row count (shared by the cache calls).
+static int check_kv4(const char *fn, const bitnet_kv4_batch *c, int dtype, int64_t N) {
+    if (!c) return fail(BITNET_E_NULL, "%s: batch is NULL", fn);
+    if (dtype != BITNET_F32 && dtype != BITNET_BF16)
+        return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, dtype);
+    if (N < 0 || N > BITNET_GEMM_MAX_N)
+        return fail(BITNET_E_SHAPE, "%s: N=%lld outside [0, %d]", fn, (long long)N,
+                    BITNET_GEMM_MAX_N);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return fail(BITNET_E_SHAPE, "%s: head_dim=%lld must be 64, 128 or 256", fn,
+                    (long long)c->head_dim);
+    if (c->n_kv_heads < 1 || c->n_kv_heads > BITNET_KV4_MAX_HEADS)
+        return fail(BITNET_E_SHAPE, "%s: n_kv_heads=%lld outside [1, %d]", fn,
+                    (long long)c->n_kv_heads, BITNET_KV4_MAX_HEADS);
+    if (c->n_pages < 1 || c->n_pages > 0x7fffffffLL)
+        return fail(BITNET_E_SHAPE, "%s: n_pages=%lld out of range", fn, (long long)c->n_pages);
+    if (c->max_pages < 1 || c->max_pages > BITNET_KV4_MAX_PAGES)
+        return fail(BITNET_E_SHAPE, "%s: max_pages=%lld outside [1, %d]", fn,
+                    (long long)c->max_pages, BITNET_KV4_MAX_PAGES);
+    if (c->n_seqs < 0 || c->n_seqs > BITNET_KV4_MAX_SEQS)
+        return fail(BITNET_E_SHAPE, "%s: n_seqs=%lld outside [0, %d]", fn, (long long)c->n_seqs,
+                    BITNET_KV4_MAX_SEQS);
+    if (N == 0 || c->n_seqs == 0) return BITNET_OK;
+    if (!c->cache || !c->table || !c->kv_len || !c->q_start)
+        return fail(BITNET_E_NULL, "%s: cache, table, kv_len and q_start are required", fn);
+    if (!aligned(c->cache, 16))
+        return fail(BITNET_E_ALIGN, "%s: cache must be 16-byte aligned", fn);
+    if (!aligned(c->table, 4) || !aligned(c->kv_len, 4) || !aligned(c->q_start, 4))
+        return fail(BITNET_E_ALIGN, "%s: table, kv_len and q_start must be 4-byte aligned", fn);
+    return BITNET_OK;
+}
+
+// A [N] row array of heads * dim values with a stride, in elements.
+static int check_rows(const char *fn, const char *name, const void *p, int64_t stride, int64_t row,
+                      int dtype) {
+    const int64_t per16 = dtype == BITNET_BF16 ? 8 : 4;
+    if (!p) return fail(BITNET_E_NULL, "%s: %s is required", fn, name);
+    if (stride < row || stride % per16 != 0 || stride > (1LL << 40))
+        return fail(BITNET_E_SHAPE, "%s: %s_stride=%lld must be a multiple of %lld and at least %lld",
+                    fn, name, (long long)stride, (long long)per16, (long long)row);
+    if (!aligned(p, 16)) return fail(BITNET_E_ALIGN, "%s: %s must be 16-byte aligned", fn, name);
+    return BITNET_OK;
+}
+
+static bitnet::Kv4Args kv4_args(const bitnet_kv4_batch *c) {
+    return bitnet::Kv4Args{static_cast<uint8_t *>(c->cache), c->table, c->kv_len, c->q_start,
+                           c->n_pages, c->max_pages, c->n_seqs, (int)c->n_kv_heads};
+}
+
+BITNET_API int bitnet_kv4_append(const bitnet_kv4_batch *batch, const void *k, int64_t k_stride,
+                                 const void *v, int64_t v_stride, int dtype, int64_t N,
+                                 void *stream) {
+    const char *fn = "bitnet_kv4_append";
+    if (int s = check_kv4(fn, batch, dtype, N)) return s;
+    if (N == 0 || batch->n_seqs == 0) return ok();
+    const int64_t row = batch->n_kv_heads * batch->head_dim;
+    if (int s = check_rows(fn, "k", k, k_stride, row, dtype)) return s;
+    if (int s = check_rows(fn, "v", v, v_stride, row, dtype)) return s;
+    hipError_t e = bitnet::launch_kv4_append(kv4_args(batch), k, v, dtype == BITNET_BF16, k_stride,
+                                             v_stride, N, (int)batch->head_dim,
+                                             static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+BITNET_API int bitnet_kv4_read(const bitnet_kv4_batch *batch, void *k, void *v, int dtype,
+                               int64_t N, void *stream) {
+    const char *fn = "bitnet_kv4_read";
+    if (int s = check_kv4(fn, batch, dtype, N)) return s;
+    if (N == 0 || batch->n_seqs == 0) return ok();
+    if (!k && !v) return fail(BITNET_E_NULL, "%s: k and v are both NULL", fn);
+    if (!aligned(k, 16) || !aligned(v, 16))
+        return fail(BITNET_E_ALIGN, "%s: k and v must be 16-byte aligned", fn);
+    hipError_t e = bitnet::launch_kv4_read(kv4_args(batch), k, v, dtype == BITNET_BF16, N,
+                                           (int)batch->head_dim, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+static int check_heads(const char *fn, int64_t heads, int64_t kv_heads) {
+    if (heads < 1 || heads > BITNET_KV4_MAX_HEADS || kv_heads < 1 || heads % kv_heads != 0)
+        return fail(BITNET_E_SHAPE, "%s: n_heads=%lld must be a multiple of n_kv_heads=%lld, at most %d",
+                    fn, (long long)heads, (long long)kv_heads, BITNET_KV4_MAX_HEADS);
+    return BITNET_OK;
+}
+
+BITNET_API int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t n_heads,
+                                             int64_t n_kv_heads, int64_t head_dim,
+                                             int64_t max_kv) {
+    const char *fn = "bitnet_attn_kv4_workspace";
+    if (check_heads(fn, n_heads, n_kv_heads)) return -1;
+    if (n_seqs < 0 || n_seqs > BITNET_KV4_MAX_SEQS || N < 0 || N > BITNET_GEMM_MAX_N ||
+        max_kv < 0 || max_kv > (int64_t)BITNET_KV4_MAX_PAGES * BITNET_KV4_PAGE ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256)) {
+        fail(BITNET_E_SHAPE, "%s: sizes out of range", fn);
+        return -1;
+    }
+    g_last_error.clear();
+    if (n_seqs == 0 || N == 0) return 0;
+    const int64_t splits = bitnet::attn4_splits(n_seqs, N, n_heads, n_kv_heads, max_kv);
+    return splits > 1 ? splits * N * n_heads * (head_dim + 4) * 4 : 0;
+}
+
+BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int64_t q_stride,
+                               int dtype, int64_t N, int64_t n_heads, float scale, int64_t window,
+                               int64_t sinks, int64_t max_kv, void *out, void *workspace,
+                               int64_t workspace_bytes, void *stream) {
+    const char *fn = "bitnet_attn_kv4";
+    if (int s = check_kv4(fn, batch, dtype, N)) return s;
+    if (int s = check_heads(fn, n_heads, batch->n_kv_heads)) return s;
+    if (!(scale > 0.0f) || !(scale < 3.4e38f))
+        return fail(BITNET_E_VALUE, "%s: scale must be positive and finite", fn);
+    if (window < 0 || sinks < 0 || window > 0x7fffffffLL || sinks > 0x7fffffffLL)
+        return fail(BITNET_E_SHAPE, "%s: window=%lld, sinks=%lld out of range", fn,
+                    (long long)window, (long long)sinks);
+    if (max_kv < 0 || max_kv > batch->max_pages * BITNET_KV4_PAGE)
+        return fail(BITNET_E_SHAPE, "%s: max_kv=%lld outside [0, 64 * max_pages]", fn,
+                    (long long)max_kv);
+    if (N == 0 || batch->n_seqs == 0) return ok();
+    if (int s = check_rows(fn, "q", q, q_stride, n_heads * batch->head_dim, dtype)) return s;
+    if (!out) return fail(BITNET_E_NULL, "%s: out is required", fn);
+    if (!aligned(out, 16) || !aligned(workspace, 16))
+        return fail(BITNET_E_ALIGN, "%s: out and workspace must be 16-byte aligned", fn);
+    const int64_t need = bitnet_attn_kv4_workspace(batch->n_seqs, N, n_heads, batch->n_kv_heads,
+                                                   batch->head_dim, max_kv);
+    if (need > 0 && !workspace)
+        return fail(BITNET_E_NULL, "%s: a workspace of %lld bytes is required", fn, (long long)need);
+    if (workspace_bytes < need)
+        return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
+                    (long long)workspace_bytes, (long long)need);
+    const int splits = bitnet::attn4_splits(batch->n_seqs, N, n_heads, batch->n_kv_heads, max_kv);
+    const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
+                              window, sinks, scale * 1.4426950408889634f, (int)n_heads, splits};
+    hipError_t e = bitnet::launch_attn4(a, dtype == BITNET_BF16, (int)batch->head_dim,
+                                        static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
 }
 
 #ifdef BITNET_STAMPS
