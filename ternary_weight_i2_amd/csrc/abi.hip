@@ -626,7 +626,8 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
                     (long long)workspace_bytes, (long long)need);
     const int splits = bitnet::attn4_splits(batch->n_seqs, N, n_heads, batch->n_kv_heads, max_kv);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
-                              window, sinks, scale * 1.4426950408889634f, (int)n_heads, splits};
+                              scale * 1.4426950408889634f, (int)n_heads, splits, (int)window,
+                              (int)sinks};
     hipError_t e = bitnet::launch_attn4(a, dtype == BITNET_BF16, (int)batch->head_dim,
                                         static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);

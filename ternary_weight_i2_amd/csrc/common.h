@@ -329,9 +329,9 @@ struct Attn4Args {
     const void *q;
     void *out;
     float *part;           // per split, row: dim accumulators, then maximum and sum
-    int64_t q_stride, N, window, sinks;
+    int64_t q_stride, N;
     float scale_log2;      // softmax scale times log2(e)
-    int heads, splits;
+    int heads, splits, window, sinks;
 };
 // How many workgroups share the pages of one row tile, for histories of up to
 // max_kv tokens; and the scratch floats that the joining of their parts needs.
