@@ -7,22 +7,28 @@
 // that share a kv head are rows of one problem: row r of a sequence is token
 // r / G, head r % G of the group.
 //
-// Both products run on the fp16 16x16x32 matrix instruction with the codes as
-// they are: code - 8 is a small integer, exact in fp16, and one packed
-// operation away from the stored nibble.  For a group of 64 channels
-//   q . k_t = sum_g step_tg (q_g . code_tg) + mid_tg sum(q_g)
-//   sum_t p_t v_t = sum_t (p_t step_tg) code_tg + sum_t p_t mid_tg
-// so the pairs enter in fp32 after the first product and through p * step in
-// front of the second.  q is scaled by a power of two per row, p * step by one
-// per wave (from the largest step met so far, tracked like the maximum), so
-// neither leaves fp16's normal range; bf16 calls round both once to fp16 (8 and
-// 11 bits: finer than the output), fp32 calls carry them as two fp16 terms (22
-// bits).  Sums, maxima and accumulators are fp32.
+// Both products run on the fp16 16x16x32 matrix instruction with the codes in
+// place of the values.  For a group of 64 channels, value = mid + step * (code - 8):
+//   q . k_t       = sum_g step_tg (q_g . (code_tg - 8)) + mid_tg sum(q_g)
+//   sum_t p_t v_t = sum_t (p_t step_tg) (code_tg - 8)   + sum_t p_t mid_tg
+// The second terms are matrix products too, of the pairs as they are stored with
+// the sums of q and with p; a row of ones among them gives sum p.
+//   bf16 calls take the nibbles as they are: in the low bits of an fp16 a nibble is
+// the subnormal number code * 2^-24 (or 16 times that, one nibble up), which the
+// instruction takes, at five operations for eight codes; the 8 moves into the
+// second terms.  Its sums are then good to about 2^-17 (it aligns a subnormal's
+// product by the smallest normal exponent), far below what a bf16 result holds.
+//   fp32 calls make code - 8 a normal number, exactly, at nine operations.
+// q is scaled by a power of two per row, p * step by one per page (from the
+// largest step met so far, tracked like the maximum), so neither leaves fp16's
+// normal range; bf16 calls round q (8 bits), p and p * step once to fp16's 11 bits,
+// finer than the output, fp32 calls carry them as two fp16 terms (22 bits).  Sums,
+// maxima and accumulators are fp32.
 //
 // The first product is taken transposed (tokens x rows), which leaves a lane
 // with 16 tokens of one row: that is exactly the fragment that the second
 // product (channels x rows) takes, so p never crosses lanes, and the running
-// maximum, the sum and the accumulators of a row all live in the same lanes.
+// maximum and the accumulators of a row all live in the same lanes.
 #include "kv4.h"
 
 namespace bitnet {
@@ -37,6 +43,7 @@ constexpr int kRows = 16;          // rows of a tile
 constexpr int kWaves = 4;          // waves of a workgroup; each takes every fourth page
 constexpr int kWanted = 1024;      // workgroups that a launch is split into
 constexpr int kMaxSplits = 256;
+constexpr int kJoinThreads = 1024;
 constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
 
 __device__ __forceinline__ h2 as_h2(uint32_t w) { return __builtin_bit_cast(h2, w); }
@@ -51,23 +58,32 @@ __device__ __forceinline__ uint32_t ones_1024() {
     asm("v_mov_b32 %0, 0x64006400" : "=v"(w));
     return w;
 }
-// Eight nibbles of a word as code - 8, in the order 0 4, 1 5, 2 6, 3 7.  A
-// nibble in the low mantissa bits of 1024 makes 1024 + code (or 1024 + 16 code
-// one place up); both results are exact.  9 operations for 8 codes.
+// The eight codes of a word in the order 0 4, 1 5, 2 6, 3 7.  RAW: as fp16
+// subnormals code * 2^-24, the second and fourth pair 16 times as large.  Else
+// code - 8: a nibble in the low mantissa bits of 1024 makes 1024 + code (or 1024
+// + 16 code one place up), and one packed operation the rest, exactly.
+template <bool RAW>
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t one, h2 (&c)[4]) {
-    const h2 s = {(_Float16)0.0625f, (_Float16)0.0625f};
     const uint32_t w8 = w >> 8;
-    c[0] = as_h2((w & 0x000f000fu) | one) - (_Float16)1032.0f;
-    c[1] = as_h2((w & 0x00f000f0u) | one) * s - (_Float16)72.0f;
-    c[2] = as_h2((w8 & 0x000f000fu) | one) - (_Float16)1032.0f;
-    c[3] = as_h2((w8 & 0x00f000f0u) | one) * s - (_Float16)72.0f;
+    if constexpr (RAW) {
+        c[0] = as_h2(w & 0x000f000fu);
+        c[1] = as_h2(w & 0x00f000f0u);
+        c[2] = as_h2(w8 & 0x000f000fu);
+        c[3] = as_h2(w8 & 0x00f000f0u);
+    } else {
+        const h2 s = {(_Float16)0.0625f, (_Float16)0.0625f};
+        c[0] = as_h2((w & 0x000f000fu) | one) - (_Float16)1032.0f;
+        c[1] = as_h2((w & 0x00f000f0u) | one) * s - (_Float16)72.0f;
+        c[2] = as_h2((w8 & 0x000f000fu) | one) - (_Float16)1032.0f;
+        c[3] = as_h2((w8 & 0x00f000f0u) | one) * s - (_Float16)72.0f;
+    }
 }
-// A zero that the compiler does not know: p * step + zero is then one
-// v_fma_mix_f32, which takes the fp16 step without a conversion.
-__device__ __forceinline__ float opaque_zero() {
-    float z;
-    asm("v_mov_b32 %0, 0" : "=v"(z));
-    return z;
+__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+// 2^e as fp16, -24 <= e <= 15.
+__device__ __forceinline__ _Float16 pow2_f16(int e) {
+    return __builtin_bit_cast(_Float16, (uint16_t)(e >= -14 ? (e + 15) << 10 : 1 << (e + 24)));
 }
 
 // Over the four lanes that hold a row (l, l ^ 16, l ^ 32, l ^ 48): the swaps
@@ -212,19 +228,13 @@ __device__ __forceinline__ void store_out(void *out, int64_t at, float4 acc, flo
     }
 }
 
-// What a wave carries along its pages.
-template <int D, int NT>
-struct Running {
-    float m, l, omid[D / 64];   // maximum, sum of p and of p * middle, of this lane's tokens
-    int E;                      // every step so far is below 2^E
-    f4 o[D / 64][4];            // channel 64 g + 16 quad + 4 e + i of o[g][i][e]
-};
-
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(const Attn4Args a) {
     using L = Kv4Page<D>;
     constexpr int NG = L::kGroups, NS = L::kSteps, NT = BF16 ? 1 : 2;
+    constexpr int kCodeExp = BF16 ? 24 : 0;   // raw codes carry 2^-24, and every second pair 16
     __shared__ __align__(16) uint32_t pairs[kWaves][2 * D];   // 8 D bytes a page
+    __shared__ __align__(16) uint32_t ones[2];                // four fp16 ones
     __shared__ __align__(16) float o_all[kWaves][kRows][D];
     __shared__ float m_all[kWaves][kRows], l_all[kWaves][kRows];
 
@@ -232,19 +242,34 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, quad = lane >> 4;
     const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
-    const int kv_head = blockIdx.y, split = blockIdx.z;
-    const Tile t = find_tile(a, blockIdx.x, G);
+    // heads first: with eight of them a head's tiles share an XCD and its L2
+    const uint32_t x = blockIdx.x / (uint32_t)a.c.kv_heads;
+    const int kv_head = (int)(blockIdx.x - x * a.c.kv_heads);
+    const uint32_t tile = x / (uint32_t)a.splits;
+    const int split = (int)(x - tile * a.splits);
+    const Tile t = find_tile(a, tile, G);
     if (t.rows == 0) return;   // the whole workgroup
-    const uint32_t one = ones_1024();
-    const float zero = opaque_zero();
+    const int i_begin = min(split * a.chunk, t.pages);
+    const int i_end = split == a.splits - 1 ? t.pages : min(i_begin + a.chunk, t.pages);
+    if (a.splits > 1 && i_begin == i_end) {   // nothing here: parts without a sum
+        if (threadIdx.x < kRows && t.row0 + threadIdx.x < t.rows) {
+            const uint32_t r = t.row0 + threadIdx.x, tok = r / G;
+            const int64_t line = (int64_t)(t.token0 + (int)tok) * a.heads + kv_head * G + (r - tok * G);
+            float *part = a.part + ((int64_t)split * a.N * a.heads + line) * (D + 4);
+            part[D] = kNoMax;
+            part[D + 1] = 0.0f;
+        }
+        return;
+    }
 
+    const uint32_t one = BF16 ? 0 : ones_1024();
     // ---- this lane's row and its query, 8 channels of every 32
     const uint32_t row = min(t.row0 + n, t.rows - 1), row_tok = row / G;
     const int head = kv_head * (int)G + (int)(row - row_tok * G);
     const int pos = t.pos0 + (int)row_tok;
     const int low = a.window > 0 ? pos - a.window + 1 : 0;   // may be negative
-    h8 qf[NT][NS];
-    float qsum[NG], qs;
+    h8 qf[NT][NS], cf;
+    float qs;
     {
         float v[NS][8], top = 0.0f;
         const int64_t at = (int64_t)(t.token0 + (int)row_tok) * a.q_stride + head * D + 8 * quad;
@@ -255,35 +280,38 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[j][e]));
         top = quad_max(top);
-        // times 2^k, so that the largest is in [2^9, 2^10)
-        const int k = top > 0.0f ? min(10 - __builtin_amdgcn_frexp_expf(top), 126) : 0;
-        qs = fmaxf(ldexpf(a.scale_log2, -k), 1.2e-38f);
+        // q times 2^k: the largest is in [2^14, 2^15); the sums of q times 2^(k -
+        // 11): the largest they can be is 2^10
+        const int k = top > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(top), 140) : 0;
+        qs = fmaxf(ldexpf(a.scale_log2, kCodeExp - k), 1.2e-38f);
+        cf = h8{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             float sum = 0.0f;
 #pragma unroll
-            for (int j = 2 * g; j < 2 * g + 2; ++j) {
-                float y[8];
+            for (int j = 2 * g; j < 2 * g + 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    y[e] = ldexpf(v[j][e], k);
-                    sum += y[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float z = y[(e >> 1) + 4 * (e & 1)];
+                    const int ch = (e >> 1) + 4 * (e & 1);
+                    sum += ldexpf(v[j][ch], k - 11);
+                    const float z = ldexpf(v[j][ch], k - (BF16 && (e & 2) ? 4 : 0));
                     const _Float16 hi = (_Float16)z;
                     qf[0][j][e] = hi;
                     if constexpr (NT == 2) qf[NT - 1][j][e] = (_Float16)(z - (float)hi);
                 }
-            }
-            qsum[g] = quad_sum(sum);
+            sum = quad_sum(sum);
+            // against a token's (step, mid): -8 (raw codes) and 1 times the sum, its
+            // upper term in the first 8 of 32 places and its lower in the next
+            const _Float16 hi = (_Float16)sum;
+            const _Float16 part = quad == 0   ? hi
+                                  : quad == 1 ? (_Float16)(sum - (float)hi)
+                                              : (_Float16)0.0f;
+            cf[2 * g] = BF16 ? (_Float16)-8.0f * part : (_Float16)0.0f;
+            cf[2 * g + 1] = part;
         }
     }
 
     // ---- the pages of this split, every kWaves-th to this wave
-    const int i0 = (int)((uint32_t)t.pages * split / a.splits) + wave;
-    const int i_end = (int)((uint32_t)t.pages * (split + 1) / a.splits);
     const int pos_first = t.pos0 + (int)(t.row0 / G);
     const int low_last = a.window > 0
                              ? t.pos0 + (int)((min(t.row0 + kRows, t.rows) - 1) / G) - a.window + 1
@@ -293,16 +321,24 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
     const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
     const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
 
-    Running<D, NT> R;
-    R.m = kNoMax;
-    R.l = 0.0f;
-    R.E = -14;
+    // What is carried along the pages.  The weights p are 2^(x - m + 15), the
+    // steps in front of the second product are divided by 2^E.  `sums` is the product of p with what row n of 16 stands for:
+    // row 2 g the steps of group g, 2 g + 1 its middles, 2 NG + 1 ones.
+    float m = kNoMax;
+    int E = -14;                 // every step so far is below 2^E
+    f4 o[NG][4], sums = {0.0f, 0.0f, 0.0f, 0.0f};   // o[g][i][e]: channel 64 g + 16 quad + 4 e + i
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        R.omid[g] = 0.0f;
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) R.o[g][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+        for (int i = 0; i < 4; ++i) o[g][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (threadIdx.x < 2) ones[threadIdx.x] = 0x3c003c00u;
+    __syncthreads();
+    const uint32_t *sums_from[4];   // this lane's row of `sums`, for tokens 16 i + 4 quad ..
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sums_from[i] = n == 2 * NG + 1
+                           ? ones
+                           : &pairs[wave][D + (4 * i + quad) * NG * 4 + 2 * (n & (2 * NG - 1))];
 
     auto process = [&](int i, RawPage<D> &r) {
         const int t0 = page_at(i) * kPage;
@@ -321,18 +357,21 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
             }
         }
         // the largest step: lanes 32 on hold four steps, then four middles, and so on
+        const bool steps_here = lane >= 32 && (D > 64 || !(lane & 1));
         uint32_t smax = 0;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
             if (D == 64 || !(w & 2)) smax = max(smax, max(r.m[w] & 0xffffu, r.m[w] >> 16));
-        if (lane < 32 || (D == 64 && (lane & 1))) smax = 0;
-        const int E_new = max(R.E, (wave_max_u16((int)smax) >> 10) - 14);
+        const int E_new = max(E, (wave_max_u16(steps_here ? (int)smax : 0) >> 10) - 14);
         {
+            const _Float16 f = steps_here ? pow2_f16(-E_new) : (_Float16)1.0f;
             uint32_t *dst = &pairs[wave][lane * (D / 32)];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) dst[w] = r.m[w];
+            for (int w = 0; w < D / 32; ++w)
+                dst[w] = D == 64 || !(w & 2) ? __builtin_bit_cast(uint32_t, as_h2(r.m[w]) * f)
+                                             : r.m[w];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
@@ -340,6 +379,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
         float s[4][4], top = -INFINITY;
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {
+            h8 pf = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const h2 p = as_h2(pairs[wave][(16 * i4 + n) * NG + g]);
+                pf[2 * g] = p[0];
+                pf[2 * g + 1] = p[1];
+            }
+            const f4 rest = mfma(pf, cf, f4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i4][e] = rest[e] * (BF16 ? 0x1p-13f : 0x1p11f);
             const uint32_t *kp = &pairs[wave][(16 * i4 + 4 * quad) * NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -347,19 +396,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
 #pragma unroll
                 for (int j = 2 * g; j < 2 * g + 2; ++j) {
                     h2 c[4];
-                    codes8(r.k[i4][j], one, c);
-                    const h8 kf = join(c[0], c[1], c[2], c[3]);
+                    codes8<BF16>(r.k[i4][j], one, c);
 #pragma unroll
                     for (int n2 = 0; n2 < NT; ++n2)
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n2][j], acc, 0, 0, 0);
+                        acc = mfma(join(c[0], c[1], c[2], c[3]), qf[n2][j], acc);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const h2 p = as_h2(kp[e * NG + g]);
-                    const float b = g == 0 ? (float)p[1] * qsum[0]
-                                           : fmaf((float)p[1], qsum[g], s[i4][e]);
-                    s[i4][e] = fmaf((float)p[0], acc[e], b);
-                }
+                for (int e = 0; e < 4; ++e)
+                    s[i4][e] = fmaf((float)as_h2(kp[e * NG + g])[0], acc[e], s[i4][e]);
             }
         }
         const bool all_seen =
@@ -378,70 +422,64 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
         for (int i4 = 0; i4 < 4; ++i4)
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i4][e]);
-        const float m_new = fmaxf(R.m, quad_max(top) * qs);
-        if (E_new > R.E || __any(m_new > R.m)) {
-            const float f = __builtin_amdgcn_exp2f(R.m - m_new + (float)(R.E - E_new));
-            R.l *= f;
+        const float m_new = fmaxf(m, quad_max(top) * qs);
+        if (E_new > E || __any(m_new > m)) {
+            const float f = __builtin_amdgcn_exp2f(m - m_new), fs = ldexpf(f, E - E_new);
+            sums[0] *= fs;
+            sums[1] *= f;
+            sums[2] *= fs;
+            sums[3] *= f;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                R.omid[g] *= f;
+            for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) R.o[g][i] *= f;
-            }
-            R.m = m_new;
-            R.E = E_new;
+                for (int i = 0; i < 4; ++i) o[g][i] *= fs;
+            m = m_new;
+            E = E_new;
         }
-        // ---- p * 2^(15 - E), and the second product
-        const float ref = R.m - (float)(15 - R.E);
+        // ---- p, and the second product
+        const float ref = m - 15.0f;
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 s[i4][e] = __builtin_amdgcn_exp2f(fmaf(s[i4][e], qs, -ref));
-                R.l += s[i4][e];
-            }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
+            h2 p[NT][4];   // pairs of tokens: two of subtile 2 hf, two of 2 hf + 1
+            h2 from[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float p0 = s[2 * hf + (w >> 1)][2 * (w & 1)];
+                const float p1 = s[2 * hf + (w >> 1)][2 * (w & 1) + 1];
+                p[0][w] = h2{(_Float16)p0, (_Float16)p1};
+                if constexpr (NT == 2)
+                    p[NT - 1][w] = h2{(_Float16)(p0 - (float)p[0][w][0]),
+                                      (_Float16)(p1 - (float)p[0][w][1])};
+                from[w] = as_h2(sums_from[2 * hf + (w >> 1)][w & 1]);
+            }
+#pragma unroll
+            for (int n2 = 0; n2 < NT; ++n2)
+                sums = mfma(join(from[0], from[1], from[2], from[3]),
+                            join(p[n2][0], p[n2][1], p[n2][2], p[n2][3]), sums);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                h8 pf[NT];
+                h2 ps[NT][4], c[4][4];   // p * step, and the codes [two tokens][channel]
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t *vp =
-                        &pairs[wave][D + ((4 * (2 * hf + b) + quad) * NG + g) * 4];
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const float p0 = s[2 * hf + b][2 * w], p1 = s[2 * hf + b][2 * w + 1];
-                        const h2 md = as_h2(vp[2 + w]);
-                        R.omid[g] = fmaf(p0, (float)md[0], R.omid[g]);
-                        R.omid[g] = fmaf(p1, (float)md[1], R.omid[g]);
-                        const h2 st = as_h2(vp[w]);
-                        const h2 hi = {(_Float16)fmaf(p0, (float)st[0], zero),
-                                       (_Float16)fmaf(p1, (float)st[1], zero)};
-                        pf[0][4 * b + 2 * w] = hi[0];
-                        pf[0][4 * b + 2 * w + 1] = hi[1];
-                        if constexpr (NT == 2) {
-                            pf[NT - 1][4 * b + 2 * w] =
-                                (_Float16)fmaf(p0, (float)st[0], -(float)hi[0]);
-                            pf[NT - 1][4 * b + 2 * w + 1] =
-                                (_Float16)fmaf(p1, (float)st[1], -(float)hi[1]);
-                        }
-                    }
+                for (int w = 0; w < 4; ++w) {
+                    const h2 st = as_h2(
+                        pairs[wave][D + ((4 * (2 * hf + (w >> 1)) + quad) * NG + g) * 4 + (w & 1)]);
+                    ps[0][w] = p[0][w] * st;
+                    if constexpr (NT == 2)
+                        ps[NT - 1][w] = __builtin_elementwise_fma(
+                            p[NT - 1][w], st, __builtin_elementwise_fma(p[0][w], st, -ps[0][w]));
+                    codes8<BF16>(r.v[2 * hf + (w >> 1)][2 * g + (w & 1)], one, c[w]);
                 }
-                h2 c[4][4];   // [two tokens][channel]
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-                        codes8(r.v[2 * hf + b][2 * g + w], one, c[2 * b + w]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const h8 vf = join(c[0][i], c[1][i], c[2][i], c[3][i]);
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int n2 = 0; n2 < NT; ++n2)
-                        R.o[g][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n2], R.o[g][i],
-                                                                           0, 0, 0);
-                }
+                        o[g][i] = mfma(join(c[0][i], c[1][i], c[2][i], c[3][i]),
+                                       join(ps[n2][0], ps[n2][1], ps[n2][2], ps[n2][3]), o[g][i]);
             }
         }
     };
@@ -453,7 +491,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
     // (from the L2): the count of loads in flight is then the same on every path.
     // At 256 channels two pages and the accumulators are more than a wave's
     // registers.
-    for (int from = i0; from < i_end; from += 64 * kWaves) {
+    for (int from = i_begin + wave; from < i_end; from += 64 * kWaves) {
         const int mine = from + kWaves * lane;
         const int ids = mine < i_end ? table[page_at(mine)] : -1;
         uint64_t there = __ballot(ids >= 0 && ids < a.c.n_pages);
@@ -488,22 +526,25 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
         }
     }
 
-    // ---- join the waves: everything of a row is scaled by 2^-(m + E)
-    R.l = quad_sum(R.l);
+    // ---- join the waves: everything of a row is scaled by 2^(15 - m)
+    auto sum_row = [&](int r) { return __shfl(sums[r & 3], n + 16 * (r >> 2)); };
+    const float l = sum_row(2 * NG + 1), up = ldexpf(1.0f, kCodeExp + E);
+    const float up1 = BF16 ? up * 0.0625f : up;
     if (quad == 0) {
-        m_all[wave][n] = R.m + (float)R.E;
-        l_all[wave][n] = R.l;
+        m_all[wave][n] = m;
+        l_all[wave][n] = l;
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const float omid = quad_sum(R.omid[g]);
+        float rest = sum_row(2 * g + 1);
+        if (BF16) rest -= sum_row(2 * g) * ldexpf(8.0f, E);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float4 w;
-            w.x = R.o[g][0][e] + omid;
-            w.y = R.o[g][1][e] + omid;
-            w.z = R.o[g][2][e] + omid;
-            w.w = R.o[g][3][e] + omid;
+            w.x = fmaf(o[g][0][e], up, rest);
+            w.y = fmaf(o[g][1][e], up1, rest);
+            w.z = fmaf(o[g][2][e], up, rest);
+            w.w = fmaf(o[g][3][e], up1, rest);
             *reinterpret_cast<float4 *>(&o_all[wave][n][64 * g + 16 * quad + 4 * e]) = w;
         }
     }
@@ -537,15 +578,17 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
 }
 
 // Joins the splits of a row: D / 4 lanes to its channels, `par` (a power of
-// two) groups of them to its splits, always added in the same order.
+// two) groups of them to its splits, always added in the same order.  A part
+// without a sum has no accumulators.
 template <int D, bool BF16>
-__global__ __launch_bounds__(256) void attn4_join_kernel(const Attn4Args a, int par) {
-    constexpr int kLanes = D / 4, kSlots = 256 / kLanes;
-    __shared__ float4 o_all[256];
-    __shared__ float m_all[kSlots], l_all[kSlots];
+__global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Args a, int par) {
+    constexpr int kLanes = D / 4, kMaxSlots = kJoinThreads / kLanes;
+    __shared__ float4 o_all[kJoinThreads];
+    __shared__ float m_all[kMaxSlots], l_all[kMaxSlots];
+    const int slots = blockDim.x / kLanes;
     const int slot = threadIdx.x / kLanes, ch = 4 * (threadIdx.x % kLanes);
     const int g = slot & (par - 1);
-    const int64_t line = (int64_t)blockIdx.x * (kSlots / par) + slot / par, lines = a.N * a.heads;
+    const int64_t line = (int64_t)blockIdx.x * (slots / par) + slot / par, lines = a.N * a.heads;
     const bool mine = line < lines && row_in_call(a.c, line / a.heads);
     const float *part = a.part + line * (D + 4);
     const int64_t stride = lines * (D + 4);
@@ -556,8 +599,10 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(const Attn4Args a, int 
 #pragma unroll 4
         for (int s = g; s < a.splits; s += par) {
             const float *p = part + s * stride;
-            add_part(acc, sum, __builtin_amdgcn_exp2f(p[D] - top),
-                     *reinterpret_cast<const float4 *>(p + ch), p[D + 1]);
+            const float l = p[D + 1];
+            if (l > 0.0f)
+                add_part(acc, sum, __builtin_amdgcn_exp2f(p[D] - top),
+                         *reinterpret_cast<const float4 *>(p + ch), l);
         }
     }
     if (par > 1) {
@@ -583,28 +628,35 @@ void launch_d(const Attn4Args &a, hipStream_t st) {
     const int64_t G = a.heads / a.c.kv_heads;
     const int64_t tiles = a.N * G / kRows + a.c.n_seqs;
     hipLaunchKernelGGL((attn4_kernel<D, BF16>),
-                       dim3((unsigned)tiles, (unsigned)a.c.kv_heads, (unsigned)a.splits),
-                       dim3(64 * kWaves), 0, st, a);
+                       dim3((unsigned)(tiles * a.c.kv_heads * a.splits)), dim3(64 * kWaves), 0, st,
+                       a);
     if (a.splits > 1) {
-        constexpr int kSlots = 256 / (D / 4);
+        // few rows with many splits: whole workgroups of 1024 to a row
+        const int64_t lines = a.N * a.heads;
+        const int threads = a.splits > 16 ? kJoinThreads : 256, slots = threads / (D / 4);
         int par = 1;
-        while (par < kSlots && 2 * par < a.splits) par *= 2;
-        const int64_t lines = a.N * a.heads, per = kSlots / par;
+        while (par < slots && 2 * par < a.splits) par *= 2;
+        const int64_t per = slots / par;
         hipLaunchKernelGGL((attn4_join_kernel<D, BF16>),
-                           dim3((unsigned)((lines + per - 1) / per)), dim3(256), 0, st, a, par);
+                           dim3((unsigned)((lines + per - 1) / per)), dim3(threads), 0, st, a, par);
     }
 }
 
 }  // namespace
 
-int attn4_splits(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t max_kv) {
-    // workgroups without a split, and enough splits for four to a compute unit,
-    // with at least one page for each wave
+Attn4Split attn4_split(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
+                       int64_t max_kv) {
+    // Chunks of pages, so that a batch's workgroups are alike however its lengths
+    // differ: enough of them for kWanted workgroups, each at least one page for
+    // every wave.
     const int64_t tiles = (N * (heads / kv_heads) / kRows + n_seqs) * kv_heads;
     const int64_t pages = (max_kv + kPage - 1) / kPage;
     int64_t s = (kWanted + tiles - 1) / tiles;
-    if (s > (pages + kWaves - 1) / kWaves) s = (pages + kWaves - 1) / kWaves;
-    return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
+    if (s > kMaxSplits) s = kMaxSplits;
+    int64_t chunk = (pages + s - 1) / s;
+    chunk = chunk < kWaves ? kWaves : (chunk + kWaves - 1) / kWaves * kWaves;
+    s = (pages + chunk - 1) / chunk;
+    return Attn4Split{s < 1 ? 1 : (int)s, (int)chunk};
 }
 
 hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st) {

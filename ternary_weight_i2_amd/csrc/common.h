@@ -331,11 +331,15 @@ struct Attn4Args {
     float *part;           // per split, row: dim accumulators, then maximum and sum
     int64_t q_stride, N;
     float scale_log2;      // softmax scale times log2(e)
-    int heads, splits, window, sinks;
+    int heads, splits, chunk, window, sinks;
 };
-// How many workgroups share the pages of one row tile, for histories of up to
-// max_kv tokens; and the scratch floats that the joining of their parts needs.
-int attn4_splits(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t max_kv);
+// How many workgroups share the pages of one row tile, and how many pages each
+// takes (the last one the rest), for histories of up to max_kv tokens.
+struct Attn4Split {
+    int splits, chunk;
+};
+Attn4Split attn4_split(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
+                       int64_t max_kv);
 hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st);
 
 // One-time weight conversion (AbsMean ternariser, sign/threshold packer).
