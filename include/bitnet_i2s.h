@@ -421,7 +421,8 @@ int bitnet_kv4_read(const bitnet_kv4_batch *batch, void *k, void *v, int dtype, 
  * Repeated calls with the same sizes give identical bits.
  */
 int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t n_heads,
-                                  int64_t n_kv_heads, int64_t head_dim, int64_t max_kv);
+                                  int64_t n_kv_heads, int64_t head_dim, int64_t max_kv,
+                                  int64_t window, int64_t sinks);
 
 int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int64_t q_stride, int dtype,
                     int64_t N, int64_t n_heads, float scale, int64_t window, int64_t sinks,

@@ -136,7 +136,7 @@ def _open(path: str) -> ctypes.CDLL:
     L.bitnet_kv4_append.restype = ctypes.c_int
     L.bitnet_kv4_read.argtypes = [kv4, p, p, i32, i64, p]
     L.bitnet_kv4_read.restype = ctypes.c_int
-    L.bitnet_attn_kv4_workspace.argtypes = [i64] * 6
+    L.bitnet_attn_kv4_workspace.argtypes = [i64] * 8
     L.bitnet_attn_kv4_workspace.restype = i64
     L.bitnet_attn_kv4.argtypes = [kv4, p, i64, i32, i64, i64, f32, i64, i64, i64, p, p, i64, p]
     L.bitnet_attn_kv4.restype = ctypes.c_int
@@ -614,7 +614,8 @@ def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, ma
     stride = _rows(q, "q", heads, dim, dev)
     most = KV4_PAGE * table.shape[1]
     max_kv = most if max_kv is None else min(int(max_kv), most)
-    need = attn_kv4_workspace(table.shape[0], N, heads, kv_heads, dim, max_kv)
+    need = attn_kv4_workspace(table.shape[0], N, heads, kv_heads, dim, max_kv, int(window),
+                              int(sinks))
     if out is None:
         out = torch.empty((N, heads, dim), dtype=q.dtype, device=dev)
     else:
@@ -632,9 +633,10 @@ def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, ma
     return out
 
 
-def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv):
+def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window=0, sinks=0):
     """Bytes of workspace that attn_kv4 takes for these sizes."""
-    need = load().bitnet_attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv)
+    need = load().bitnet_attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv,
+                                            window, sinks)
     if need < 0:
         raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
     return need

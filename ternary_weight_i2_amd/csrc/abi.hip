@@ -582,11 +582,12 @@ static int check_heads(const char *fn, int64_t heads, int64_t kv_heads) {
 
 BITNET_API int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t n_heads,
                                              int64_t n_kv_heads, int64_t head_dim,
-                                             int64_t max_kv) {
+                                             int64_t max_kv, int64_t window, int64_t sinks) {
     const char *fn = "bitnet_attn_kv4_workspace";
     if (check_heads(fn, n_heads, n_kv_heads)) return -1;
     if (n_seqs < 0 || n_seqs > BITNET_KV4_MAX_SEQS || N < 0 || N > BITNET_GEMM_MAX_N ||
-        max_kv < 0 || max_kv > (int64_t)BITNET_KV4_MAX_PAGES * BITNET_KV4_PAGE ||
+        max_kv < 0 || max_kv > (int64_t)BITNET_KV4_MAX_PAGES * BITNET_KV4_PAGE || window < 0 ||
+        window > 0x7fffffffLL || sinks < 0 || sinks > 0x7fffffffLL ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256)) {
         fail(BITNET_E_SHAPE, "%s: sizes out of range", fn);
         return -1;
@@ -594,7 +595,7 @@ BITNET_API int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t 
     g_last_error.clear();
     if (n_seqs == 0 || N == 0) return 0;
     const int64_t splits =
-        bitnet::attn4_split(n_seqs, N, n_heads, n_kv_heads, max_kv).splits;
+        bitnet::attn4_split(n_seqs, N, n_heads, n_kv_heads, max_kv, window, sinks).splits;
     return splits > 1 ? splits * N * n_heads * (head_dim + 4) * 4 : 0;
 }
 
@@ -619,14 +620,15 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
     if (!aligned(out, 16) || !aligned(workspace, 16))
         return fail(BITNET_E_ALIGN, "%s: out and workspace must be 16-byte aligned", fn);
     const int64_t need = bitnet_attn_kv4_workspace(batch->n_seqs, N, n_heads, batch->n_kv_heads,
-                                                   batch->head_dim, max_kv);
+                                                   batch->head_dim, max_kv, window, sinks);
     if (need > 0 && !workspace)
         return fail(BITNET_E_NULL, "%s: a workspace of %lld bytes is required", fn, (long long)need);
     if (workspace_bytes < need)
         return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
                     (long long)workspace_bytes, (long long)need);
     const bitnet::Attn4Split sp =
-        bitnet::attn4_split(batch->n_seqs, N, n_heads, batch->n_kv_heads, max_kv);
+        bitnet::attn4_split(batch->n_seqs, N, n_heads, batch->n_kv_heads, max_kv, window,
+                            sinks);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
                               scale * 1.4426950408889634f, (int)n_heads, sp.splits,
                               sp.chunk, (int)window, (int)sinks};

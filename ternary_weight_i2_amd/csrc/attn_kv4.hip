@@ -29,6 +29,8 @@
 // with 16 tokens of one row: that is exactly the fragment that the second
 // product (channels x rows) takes, so p never crosses lanes, and the running
 // maximum and the accumulators of a row all live in the same lanes.
+#include <algorithm>
+
 #include "kv4.h"
 
 namespace bitnet {
@@ -41,7 +43,7 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 16;          // rows of a tile
 constexpr int kWaves = 4;          // waves of a workgroup; each takes every fourth page
-constexpr int kWanted = 1024;      // workgroups that a launch is split into
+constexpr int kWanted = 512;      // workgroups that a launch is split into
 constexpr int kMaxSplits = 256;
 constexpr int kJoinThreads = 1024;
 constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
@@ -256,11 +258,42 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
             const uint32_t r = t.row0 + threadIdx.x, tok = r / G;
             const int64_t line = (int64_t)(t.token0 + (int)tok) * a.heads + kv_head * G + (r - tok * G);
             float *part = a.part + ((int64_t)split * a.N * a.heads + line) * (D + 4);
-            part[D] = kNoMax;
             part[D + 1] = 0.0f;
         }
         return;
     }
+
+    // ---- the pages of this split, every kWaves-th to this wave.  64 table entries
+    // at a time, one a lane, with a bit for each page that is there; they are
+    // waited for before the pages, so that no wait of the inner loop takes in the
+    // page that is on its way while another is worked on.  For the same reason a
+    // page is always loaded, at the end the last one again (from the L2): the
+    // count of loads in flight is then the same on every path.
+    const int32_t *table = a.c.table + (int64_t)t.seq * a.c.max_pages;
+    auto page_at = [&](int i) { return i < t.sink_pages ? i : t.first + i - t.sink_pages; };
+    const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
+    const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
+    int from = i_begin + wave, ids = -1, id = 0, at_bit = 0;
+    uint64_t there = 0;
+    bool more = false;   // whether the page fetched last is one to work on
+    auto load_ids = [&]() {
+        const int mine = from + kWaves * lane;
+        ids = mine < i_end ? table[page_at(mine)] : -1;
+        there = __ballot(ids >= 0 && ids < a.c.n_pages);
+    };
+    auto fetch = [&](RawPage<D> &r) {
+        more = there != 0;
+        if (more) {
+            at_bit = __builtin_ctzll(there);
+            there &= there - 1;
+            id = __builtin_amdgcn_readlane(ids, at_bit);
+        }
+        load_page<D>(cache + id * page_bytes, lane, r);
+        return from + kWaves * at_bit;
+    };
+    RawPage<D> ra;
+    load_ids();
+    int i = fetch(ra);
 
     const uint32_t one = BF16 ? 0 : ones_1024();
     // ---- this lane's row and its query, 8 channels of every 32
@@ -311,15 +344,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
         }
     }
 
-    // ---- the pages of this split, every kWaves-th to this wave
     const int pos_first = t.pos0 + (int)(t.row0 / G);
     const int low_last = a.window > 0
                              ? t.pos0 + (int)((min(t.row0 + kRows, t.rows) - 1) / G) - a.window + 1
                              : 0;
-    const int32_t *table = a.c.table + (int64_t)t.seq * a.c.max_pages;
-    auto page_at = [&](int i) { return i < t.sink_pages ? i : t.first + i - t.sink_pages; };
-    const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
-    const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
 
     // What is carried along the pages.  The weights p are 2^(x - m + 15), the
     // steps in front of the second product are divided by 2^E.  `sums` is the product of p with what row n of 16 stands for:
@@ -340,8 +368,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
                            ? ones
                            : &pairs[wave][D + (4 * i + quad) * NG * 4 + 2 * (n & (2 * NG - 1))];
 
-    auto process = [&](int i, RawPage<D> &r) {
-        const int t0 = page_at(i) * kPage;
+    auto process = [&](int at, RawPage<D> &r) {
+        const int t0 = page_at(at) * kPage;
         // tokens behind the last have pairs of any value
         if (t0 + kPage > t.held) {
             const int left = t.held - t0;
@@ -484,46 +512,26 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
         }
     };
 
-    // 64 table entries at a time, one a lane, with a bit for each page that is
-    // there; they are waited for before the pages, so that no wait of the inner
-    // loop takes in the page that is on its way while another is worked on.  For
-    // the same reason a page is always loaded, at the end the last one again
-    // (from the L2): the count of loads in flight is then the same on every path.
-    // At 256 channels two pages and the accumulators are more than a wave's
-    // registers.
-    for (int from = i_begin + wave; from < i_end; from += 64 * kWaves) {
-        const int mine = from + kWaves * lane;
-        const int ids = mine < i_end ? table[page_at(mine)] : -1;
-        uint64_t there = __ballot(ids >= 0 && ids < a.c.n_pages);
-        int j = 0;
-        bool more = there != 0;
-        if (!more) continue;
-        auto fetch = [&](RawPage<D> &r) {   // the next page; its index
-            more = there != 0;
-            if (more) j = __builtin_ctzll(there);
-            there &= there - 1;
-            load_page<D>(cache + __builtin_amdgcn_readlane(ids, j) * page_bytes, lane, r);
-            return from + kWaves * j;
-        };
-        RawPage<D> ra;
-        int i = fetch(ra);
-        if constexpr (D < 256) {
+    while (true) {
+        if constexpr (D * NT < 256) {
             RawPage<D> rb;
-            while (true) {
+            while (more) {
                 const int i2 = fetch(rb);
                 process(i, ra);
                 if (!more) break;
                 i = fetch(ra);
                 process(i2, rb);
-                if (!more) break;
             }
-        } else {
-            while (true) {
+        } else {   // two pages and the rest are more than a wave's registers
+            while (more) {
                 process(i, ra);
-                if (there == 0) break;
                 i = fetch(ra);
             }
         }
+        from += 64 * kWaves;
+        if (from >= i_end) break;
+        load_ids();
+        i = fetch(ra);
     }
 
     // ---- join the waves: everything of a row is scaled by 2^(15 - m)
@@ -595,14 +603,32 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
     float top = kNoMax, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (mine) {
-        for (int s = g; s < a.splits; s += par) top = fmaxf(top, part[s * stride + D]);
-#pragma unroll 4
-        for (int s = g; s < a.splits; s += par) {
-            const float *p = part + s * stride;
-            const float l = p[D + 1];
-            if (l > 0.0f)
-                add_part(acc, sum, __builtin_amdgcn_exp2f(p[D] - top),
-                         *reinterpret_cast<const float4 *>(p + ch), l);
+        // four parts at a time, all of their loads before the first use
+        constexpr int kBatch = 4;
+        for (int s = g; s < a.splits; s += kBatch * par) {
+            float ms[kBatch], ls[kBatch], best = top;
+            float4 os[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float *p = part + min(s + i * par, a.splits - 1) * stride;
+                os[i] = *reinterpret_cast<const float4 *>(p + ch);
+                ms[i] = p[D];
+                ls[i] = p[D + 1];
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (s + i * par >= a.splits) ls[i] = 0.0f;
+                if (ls[i] > 0.0f) best = fmaxf(best, ms[i]);
+                else os[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            const float f = __builtin_amdgcn_exp2f(top - best);
+            sum *= f;
+            acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+            top = best;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                add_part(acc, sum, ls[i] > 0.0f ? __builtin_amdgcn_exp2f(ms[i] - top) : 0.0f,
+                         os[i], ls[i]);
         }
     }
     if (par > 1) {
@@ -645,12 +671,14 @@ void launch_d(const Attn4Args &a, hipStream_t st) {
 }  // namespace
 
 Attn4Split attn4_split(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
-                       int64_t max_kv) {
+                       int64_t max_kv, int64_t window, int64_t sinks) {
     // Chunks of pages, so that a batch's workgroups are alike however its lengths
     // differ: enough of them for kWanted workgroups, each at least one page for
     // every wave.
     const int64_t tiles = (N * (heads / kv_heads) / kRows + n_seqs) * kv_heads;
-    const int64_t pages = (max_kv + kPage - 1) / kPage;
+    int64_t pages = (max_kv + kPage - 1) / kPage;
+    if (window > 0)   // what a tile's rows can see of it: the windows of 16 tokens, the sinks
+        pages = std::min(pages, (window + kRows) / kPage + 2 + (sinks + kPage - 1) / kPage);
     int64_t s = (kWanted + tiles - 1) / tiles;
     if (s > kMaxSplits) s = kMaxSplits;
     int64_t chunk = (pages + s - 1) / s;

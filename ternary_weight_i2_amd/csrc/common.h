@@ -339,7 +339,7 @@ struct Attn4Split {
     int splits, chunk;
 };
 Attn4Split attn4_split(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
-                       int64_t max_kv);
+                       int64_t max_kv, int64_t window, int64_t sinks);
 hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st);
 
 // One-time weight conversion (AbsMean ternariser, sign/threshold packer).

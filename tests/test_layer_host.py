@@ -119,7 +119,7 @@ def test_attention_validation(L):
     for bad in (255, 258, 0):
         assert f(L, _batch(), qs=bad) == E_SHAPE
     # a long history is shared by several workgroups, which takes a workspace
-    need = L.bitnet_attn_kv4_workspace(2, 3, 4, 2, 64, 64 * 100)
+    need = L.bitnet_attn_kv4_workspace(2, 3, 4, 2, 64, 64 * 100, 0, 0)
     assert need > 0
     long = _batch(max_pages=100)
     assert f(L, long, max_kv=6400) == E_NULL
@@ -128,10 +128,14 @@ def test_attention_validation(L):
 
 def test_workspace_sizes(L):
     w = L.bitnet_attn_kv4_workspace
-    assert w(0, 3, 4, 2, 64, 6400) == 0 and w(2, 0, 4, 2, 64, 6400) == 0
-    for bad in ((-1, 3, 4, 2, 64, 64), (2, -1, 4, 2, 64, 64), (2, 3, 5, 2, 64, 64),
-                (2, 3, 4, 0, 64, 64), (2, 3, 4, 2, 96, 64), (2, 3, 4, 2, 64, -1),
-                (2, 3, 4, 2, 64, (1 << 30) + 1)):
+    assert w(0, 3, 4, 2, 64, 6400, 0, 0) == 0 and w(2, 0, 4, 2, 64, 6400, 0, 0) == 0
+    assert 0 < w(2, 3, 4, 2, 64, 640000, 0, 0)
+    assert w(2, 3, 4, 2, 64, 640000, 64, 4) < w(2, 3, 4, 2, 64, 640000, 0, 0)
+    for bad in ((-1, 3, 4, 2, 64, 64, 0, 0), (2, -1, 4, 2, 64, 64, 0, 0),
+                (2, 3, 5, 2, 64, 64, 0, 0), (2, 3, 4, 0, 64, 64, 0, 0),
+                (2, 3, 4, 2, 96, 64, 0, 0), (2, 3, 4, 2, 64, -1, 0, 0),
+                (2, 3, 4, 2, 64, (1 << 30) + 1, 0, 0), (2, 3, 4, 2, 64, 64, -1, 0),
+                (2, 3, 4, 2, 64, 64, 0, -1), (2, 3, 4, 2, 64, 64, 1 << 31, 0)):
         assert w(*bad) == -1
         assert L.bitnet_last_error()
 
