@@ -631,7 +631,7 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
                             sinks);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
                               scale * 1.4426950408889634f, (int)n_heads, sp.prompt,
-                              sp.splits, sp.chunk, (int)window, (int)sinks};
+                              sp.splits, sp.chunk, (int)window, (int)sinks, 0};
     hipError_t e = bitnet::launch_attn4(a, dtype == BITNET_BF16, (int)batch->head_dim,
                                         static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);

@@ -41,13 +41,13 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-constexpr int kRows = 16;          // rows of a tile
-constexpr int kWaves = 4;          // waves of a workgroup; each takes every fourth page
+constexpr int kWaves = 4;          // waves of a workgroup
 constexpr int kWanted = 512;      // workgroups that a launch is split into
 constexpr int kMaxSplits = 256;
 constexpr int kPromptFrom = 64;   // rows of a sequence, on average
 constexpr int kPromptChunk = 16;
 constexpr int kJoinThreads = 1024;
+constexpr float kBehind = 8.0f, kUp = 7.0f;   // see attn4_kernel
 constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
 
 __device__ __forceinline__ h2 as_h2(uint32_t w) { return __builtin_bit_cast(h2, w); }
@@ -176,17 +176,12 @@ __device__ __forceinline__ Tile find_tile(const Attn4Args &a, uint32_t x, uint32
     return t;
 }
 
-template <int D>
-struct RawPage {   // a page's codes as one lane loads them, and its share of the pairs
-    uint32_t k[4][D / 32];
-    uint32_t v[4][D / 32];
-    uint32_t m[D / 32];
-};
-
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
-    static_assert(N == 2 || N == 4 || N == 8, "8, 16 or 32 bytes");
-    if constexpr (N == 2) {
+    static_assert(N == 1 || N == 2 || N == 4 || N == 8, "4, 8, 16 or 32 bytes");
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
         const uint2 a = *reinterpret_cast<const uint2 *>(p);
         w[0] = a.x; w[1] = a.y;
     } else {
@@ -198,30 +193,15 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
-template <int D>
-__device__ __forceinline__ void load_page(const uint8_t *rec, int lane, RawPage<D> &r) {
-    using L = Kv4Page<D>;
-    const int n = lane & 15, q = lane >> 4;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        load_words(rec + (16 * s + n) * L::kRow + q * (D / 8), r.k[s]);
-        load_words(rec + L::kValues + ((4 * s + q) * 16 + n) * (D / 8), r.v[s]);
-    }
-    load_words(rec + L::kKeyPairs + lane * (D / 8), r.m);
-}
-
-__device__ __forceinline__ void add_part(float4 &acc, float &sum, float f, const float4 &o,
-                                         float l) {
-    sum = fmaf(f, l, sum);
+__device__ __forceinline__ void add_part(float4 &acc, float f, const float4 &o) {
     acc.x = fmaf(f, o.x, acc.x);
     acc.y = fmaf(f, o.y, acc.y);
     acc.z = fmaf(f, o.z, acc.z);
     acc.w = fmaf(f, o.w, acc.w);
 }
-// Four channels of a finished row; a row that saw nothing has no sum.
+// Four channels of a finished row; inv: one over its sum, or 0 if it saw nothing.
 template <bool BF16>
-__device__ __forceinline__ void store_out(void *out, int64_t at, float4 acc, float sum) {
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+__device__ __forceinline__ void store_out(void *out, int64_t at, float4 acc, float inv) {
     acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
     if constexpr (BF16) {
         uint2 w;
@@ -231,6 +211,40 @@ __device__ __forceinline__ void store_out(void *out, int64_t at, float4 acc, flo
     } else {
         *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = acc;
     }
+}
+
+// The pages [begin, end) of a tile's list that a split takes (the last one the
+// rest).  A tile whose pages are one split's has its result written by it; its part
+// then says so in place of a sum, and the join leaves the row alone.
+constexpr float kFinal = -1.0f;
+struct Share {
+    int begin, end;
+    bool shared;
+};
+__device__ __forceinline__ Share share_of(const Attn4Args &a, const Tile &t, int split) {
+    Share s;
+    s.begin = min(split * a.chunk, t.pages);
+    s.end = split == a.splits - 1 ? t.pages : min(s.begin + a.chunk, t.pages);
+    s.shared = t.pages > a.chunk && a.splits > 1;
+    return s;
+}
+// The output line of a sequence's row r, and its part of a split.
+__device__ __forceinline__ int64_t line_of(const Attn4Args &a, const Tile &t, uint32_t r, int kv_head,
+                                           uint32_t G) {
+    const uint32_t tok = r / G;
+    return (int64_t)(t.token0 + (int)tok) * a.heads + kv_head * (int)G + (int)(r - tok * G);
+}
+template <int D>
+__device__ __forceinline__ float *part_of(const Attn4Args &a, int split, int64_t line) {
+    return a.part + ((int64_t)split * a.N * a.heads + line) * (D + 4);
+}
+// A split without pages leaves parts without a sum, where they are looked at.
+template <int D>
+__device__ __forceinline__ void write_nothing(const Attn4Args &a, const Tile &t, const Share &s,
+                                              int kv_head, uint32_t G, int split, uint32_t rows) {
+    const uint32_t r = t.row0 + threadIdx.x;
+    if (s.shared && threadIdx.x < rows && r < t.rows)
+        part_of<D>(a, split, line_of(a, t, r, kv_head, G))[D + 1] = 0.0f;
 }
 
 // A row's query as the first product takes it, 8 channels of every 32 in this
@@ -280,109 +294,143 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
     }
 }
 
-template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(const Attn4Args a) {
+// A workgroup has 16 * RT rows, 16 to each of RT fragments, and its four waves
+// take turns at their pages.  RT is 1 for tokens; fp32 prompts have 2 where the
+// registers allow it, which shares what a page's codes cost to unpack.
+constexpr int prompt_rt(int dim) { return dim == 64 ? 2 : 1; }
+constexpr int least_waves(int dim, int rt, bool bf16) {   // to a SIMD, without spills
+    return dim == 256 ? 1 : dim * rt * (bf16 ? 1 : 2) <= 128 ? 3 : 2;
+}
+
+template <int D, bool BF16, int RT>
+__global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_kernel(
+    const Attn4Args a) {
     using L = Kv4Page<D>;
-    constexpr int NG = L::kGroups, NS = L::kSteps, NT = BF16 ? 1 : 2;
+    constexpr int NG = L::kGroups, NS = L::kSteps, NT = BF16 ? 1 : 2, ROWS = 16 * RT;
+    constexpr int SUBS = 2;   // 16-token quarters of a page that are worked on together
     constexpr int kCodeExp = BF16 ? 24 : 0;   // raw codes carry 2^-24, and every second pair 16
-    __shared__ __align__(16) uint32_t pairs[kWaves][2 * D];   // 8 D bytes a page
-    __shared__ __align__(16) uint32_t ones[2];                // four fp16 ones
-    __shared__ __align__(16) float o_all[kWaves][kRows][D];
-    __shared__ float m_all[kWaves][kRows], l_all[kWaves][kRows];
+    __shared__ __align__(16) uint32_t pairs_all[kWaves][2 * D];   // 8 D bytes a page
+    __shared__ __align__(16) uint32_t ones_all[kWaves][2];        // four fp16 ones
+    __shared__ __align__(16) float4 o_all[kWaves][RT * NG * 4][64];
+    __shared__ float m_all[kWaves][ROWS], l_all[kWaves][ROWS];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, quad = lane >> 4;
+    uint32_t *const pairs = pairs_all[wave], *const ones = ones_all[wave];
     const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
-    // heads first: with eight of them a head's tiles share an XCD and its L2
+    // heads first: with eight of them a head's tiles share an XCD and its L2;
+    // a prompt's last tiles, which see the most, before its first
     const uint32_t x = blockIdx.x / (uint32_t)a.c.kv_heads;
     const int kv_head = (int)(blockIdx.x - x * a.c.kv_heads);
     const uint32_t tile = x / (uint32_t)a.splits;
     const int split = (int)(x - tile * a.splits);
-    const Tile t = find_tile<kRows>(a, tile, G);
+    const Tile t = find_tile<ROWS>(a, a.tiles - 1 - tile, G);
     if (t.rows == 0) return;   // the whole workgroup
-    const int i_begin = min(split * a.chunk, t.pages);
-    const int i_end = split == a.splits - 1 ? t.pages : min(i_begin + a.chunk, t.pages);
-    if (a.splits > 1 && i_begin == i_end) {   // nothing here: parts without a sum
-        if (threadIdx.x < kRows && t.row0 + threadIdx.x < t.rows) {
-            const uint32_t r = t.row0 + threadIdx.x, tok = r / G;
-            const int64_t line = (int64_t)(t.token0 + (int)tok) * a.heads + kv_head * G + (r - tok * G);
-            float *part = a.part + ((int64_t)split * a.N * a.heads + line) * (D + 4);
-            part[D + 1] = 0.0f;
-        }
+    const Share sh = share_of(a, t, split);
+    if (sh.begin == sh.end && split > 0) {
+        write_nothing<D>(a, t, sh, kv_head, G, split, ROWS);
         return;
     }
 
-    // ---- the pages of this split, every kWaves-th to this wave.  64 table entries
+    // ---- the pages of this split, every fourth to this wave.  64 table entries
     // at a time, one a lane, with a bit for each page that is there; they are
-    // waited for before the pages, so that no wait of the inner loop takes in the
-    // page that is on its way while another is worked on.  For the same reason a
-    // page is always loaded, at the end the last one again (from the L2): the
-    // count of loads in flight is then the same on every path.
+    // waited for before the pages, so that no wait of the loop takes in a page that
+    // is on its way.  For the same reason a page is always loaded, at the end the
+    // last one again (from the L2): the count of loads in flight is then the same
+    // on every path.
     const int32_t *table = a.c.table + (int64_t)t.seq * a.c.max_pages;
     auto page_at = [&](int i) { return i < t.sink_pages ? i : t.first + i - t.sink_pages; };
     const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
     const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
-    int from = i_begin + wave, ids = -1, id = 0, at_bit = 0;
+    int from = sh.begin + wave, ids = -1, id = 0, at_bit = 0;
     uint64_t there = 0;
-    bool more = false;   // whether the page fetched last is one to work on
     auto load_ids = [&]() {
         const int mine = from + kWaves * lane;
-        ids = mine < i_end ? table[page_at(mine)] : -1;
+        ids = mine < sh.end ? table[page_at(mine)] : -1;
         there = __ballot(ids >= 0 && ids < a.c.n_pages);
     };
-    auto fetch = [&](RawPage<D> &r) {
-        more = there != 0;
-        if (more) {
-            at_bit = __builtin_ctzll(there);
-            there &= there - 1;
-            id = __builtin_amdgcn_readlane(ids, at_bit);
+    // the next page: its first token, or -1; its record is at `rec`
+    const uint8_t *rec = cache;
+    auto next = [&]() {
+        while (there == 0) {
+            if (from >= sh.end - 64 * kWaves) return -1;
+            from += 64 * kWaves;
+            load_ids();
         }
-        load_page<D>(cache + id * page_bytes, lane, r);
-        return from + kWaves * at_bit;
+        at_bit = __builtin_ctzll(there);
+        there &= there - 1;
+        id = __builtin_amdgcn_readlane(ids, at_bit);
+        rec = cache + id * page_bytes;
+        return page_at(from + kWaves * at_bit) * kPage;
     };
-    RawPage<D> ra;
+    // codes of the quarters that come next, and this lane's share of a page's pairs
+    uint32_t raw_k[SUBS][D / 32], raw_v[SUBS][D / 32], raw_m[D / 32];
+    auto load_keys = [&](const uint8_t *r, int sub) {
+#pragma unroll
+        for (int i = 0; i < SUBS; ++i)
+            load_words(r + (16 * (sub + i) + n) * L::kRow + quad * (D / 8), raw_k[i]);
+    };
+    auto load_pairs = [&](const uint8_t *r) {
+        load_words(r + L::kKeyPairs + lane * (D / 8), raw_m);
+    };
+    auto load_values = [&](const uint8_t *r, int sub) {
+#pragma unroll
+        for (int i = 0; i < SUBS; ++i)
+            load_words(r + L::kValues + ((4 * (sub + i) + quad) * 16 + n) * (D / 8), raw_v[i]);
+    };
     load_ids();
-    int i = fetch(ra);
+    int t0 = next();
+    load_pairs(rec);
+    load_keys(rec, 0);
+    load_values(rec, 0);
 
+    // ---- this lane's rows and their queries, 8 channels of every 32
     const uint32_t one = BF16 ? 0 : ones_1024();
-    // ---- this lane's row and its query, 8 channels of every 32
-    const uint32_t row = min(t.row0 + n, t.rows - 1), row_tok = row / G;
-    const int head = kv_head * (int)G + (int)(row - row_tok * G);
-    const int pos = t.pos0 + (int)row_tok;
-    const int low = a.window > 0 ? pos - a.window + 1 : 0;   // may be negative
-    h8 qf[NT][NS], cf;
-    float qs;
-    load_query<D, BF16, BF16>(a, t.token0 + (int)row_tok, head, quad, qf, cf, qs);
-
+    int pos[RT], low[RT];
+    h8 qf[RT][NT][NS], cf[RT];
+    float qs[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const uint32_t row = min(t.row0 + 16 * rt + n, t.rows - 1), tok = row / G;
+        pos[rt] = t.pos0 + (int)tok;
+        low[rt] = a.window > 0 ? pos[rt] - a.window + 1 : 0;   // may be negative
+        load_query<D, BF16, BF16>(a, t.token0 + (int)tok, kv_head * (int)G + (int)(row - tok * G),
+                                  quad, qf[rt], cf[rt], qs[rt]);
+    }
     const int pos_first = t.pos0 + (int)(t.row0 / G);
     const int low_last = a.window > 0
-                             ? t.pos0 + (int)((min(t.row0 + kRows, t.rows) - 1) / G) - a.window + 1
+                             ? t.pos0 + (int)((min(t.row0 + ROWS, t.rows) - 1) / G) - a.window + 1
                              : 0;
 
-    // What is carried along the pages.  The weights p are 2^(x - m + 15), the
-    // steps in front of the second product are divided by 2^E.  `sums` is the product of p with what row n of 16 stands for:
-    // row 2 g the steps of group g, 2 g + 1 its middles, 2 NG + 1 ones.
-    float m = kNoMax;
+    // What is carried along the pages.  The weights p are 2^(x - m + 7), where m
+    // may stay up to 8 behind the largest x so that the accumulators are rescaled
+    // seldom; the steps in front of the second product are divided by 2^E.  `sums`
+    // is the product of p with what row n of 16 stands for: row 2 g the steps of
+    // group g, 2 g + 1 its middles, 2 NG + 1 ones.
+    float m[RT];
     int E = -14;                 // every step so far is below 2^E
-    f4 o[NG][4], sums = {0.0f, 0.0f, 0.0f, 0.0f};   // o[g][i][e]: channel 64 g + 16 quad + 4 e + i
+    f4 o[RT][NG][4], sums[RT];   // o[..][g][i][e]: channel 64 g + 16 quad + 4 e + i
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = kNoMax;
+        sums[rt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[g][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (threadIdx.x < 2) ones[threadIdx.x] = 0x3c003c00u;
-    __syncthreads();
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[rt][g][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    if (lane < 2) ones[lane] = 0x3c003c00u;
     const uint32_t *sums_from[4];   // this lane's row of `sums`, for tokens 16 i + 4 quad ..
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         sums_from[i] = n == 2 * NG + 1
                            ? ones
-                           : &pairs[wave][D + (4 * i + quad) * NG * 4 + 2 * (n & (2 * NG - 1))];
+                           : &pairs[D + (4 * i + quad) * NG * 4 + 2 * (n & (2 * NG - 1))];
 
-    auto process = [&](int at, RawPage<D> &r) {
-        const int t0 = page_at(at) * kPage;
-        // tokens behind the last have pairs of any value
-        if (t0 + kPage > t.held) {
+    while (t0 >= 0) {
+        // ---- the page's pairs go through LDS, its steps divided by 2^E
+        if (t0 + kPage > t.held) {   // tokens behind the last have pairs of any value
             const int left = t.held - t0;
             if (lane >= 32) {
 #pragma unroll
@@ -390,8 +438,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
                     // halfword i of the value pairs: token 4 (i / 8 / NG) + i % 4
                     const int h0 = (lane - 32) * (D / 16) + 2 * w;
                     const int tok = 4 * (h0 / (8 * NG)) + (h0 & 3);
-                    if (tok >= left) r.m[w] = 0;
-                    else if (tok + 1 >= left) r.m[w] &= 0xffffu;
+                    if (tok >= left) raw_m[w] = 0;
+                    else if (tok + 1 >= left) raw_m[w] &= 0xffffu;
                 }
             }
         }
@@ -400,212 +448,256 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn4_kernel(co
         uint32_t smax = 0;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
-            if (D == 64 || !(w & 2)) smax = max(smax, max(r.m[w] & 0xffffu, r.m[w] >> 16));
+            if (D == 64 || !(w & 2)) smax = max(smax, max(raw_m[w] & 0xffffu, raw_m[w] >> 16));
         const int E_new = max(E, (wave_max_u16(steps_here ? (int)smax : 0) >> 10) - 14);
         {
             const _Float16 f = steps_here ? pow2_f16(-E_new) : (_Float16)1.0f;
-            uint32_t *dst = &pairs[wave][lane * (D / 32)];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int w = 0; w < D / 32; ++w)
-                dst[w] = D == 64 || !(w & 2) ? __builtin_bit_cast(uint32_t, as_h2(r.m[w]) * f)
-                                             : r.m[w];
+                pairs[lane * (D / 32) + w] =
+                    D == 64 || !(w & 2) ? __builtin_bit_cast(uint32_t, as_h2(raw_m[w]) * f)
+                                        : raw_m[w];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
-        // ---- scores of 64 tokens: s[i][e] is token 16 i + 4 quad + e
-        float s[4][4], top = -INFINITY;
+        const uint8_t *const rec0 = rec;
+        int t1 = -1;
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
+        for (int sub = 0; sub < 4; sub += SUBS) {
+        // ---- scores: s[..][i][e] is token 16 (sub + i) + 4 quad + e
+        float s[RT][SUBS][4];
+#pragma unroll
+        for (int i4 = 0; i4 < SUBS; ++i4) {
+            __builtin_amdgcn_sched_barrier(0);   // unpack one quarter at a time: registers
             h8 pf = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const h2 p = as_h2(pairs[wave][(16 * i4 + n) * NG + g]);
+                const h2 p = as_h2(pairs[(16 * (sub + i4) + n) * NG + g]);
                 pf[2 * g] = p[0];
                 pf[2 * g + 1] = p[1];
             }
-            const f4 rest = mfma(pf, cf, f4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[i4][e] = rest[e] * (BF16 ? 0x1p-13f : 0x1p11f);
-            const uint32_t *kp = &pairs[wave][(16 * i4 + 4 * quad) * NG];
+            f4 acc[RT][NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) acc[rt][g] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = 2 * g; j < 2 * g + 2; ++j) {
                     h2 c[4];
-                    codes8<BF16>(r.k[i4][j], one, c);
+                    codes8<BF16>(raw_k[i4][j], one, c);
 #pragma unroll
-                    for (int n2 = 0; n2 < NT; ++n2)
-                        acc = mfma(join(c[0], c[1], c[2], c[3]), qf[n2][j], acc);
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int n2 = 0; n2 < NT; ++n2)
+                            acc[rt][g] =
+                                mfma(join(c[0], c[1], c[2], c[3]), qf[rt][n2][j], acc[rt][g]);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[i4][e] = fmaf((float)as_h2(kp[e * NG + g])[0], acc[e], s[i4][e]);
             }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const f4 rest = mfma(pf, cf[rt], f4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[rt][i4][e] = rest[e] * (BF16 ? 0x1p-13f : 0x1p11f);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        s[rt][i4][e] =
+                            fmaf((float)as_h2(pairs[(16 * (sub + i4) + 4 * quad + e) * NG + g])[0],
+                                 acc[rt][g][e], s[rt][i4][e]);
+                }
+            }
+        }
+        // the next keys come while these values are worked on, the next values
+        // while the next keys are
+        if (sub + SUBS < 4) {
+            load_keys(rec0, sub + SUBS);
+        } else {
+            t1 = next();
+            load_pairs(rec);
+            load_keys(rec, 0);
         }
         const bool all_seen =
             t0 + kPage - 1 <= pos_first && (t0 >= low_last || t0 + kPage <= a.sinks);
         if (!all_seen) {
 #pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4)
+            for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = t0 + 16 * i4 + 4 * quad + e;
-                    const bool hidden = (j > pos) | ((j < low) & (j >= a.sinks));
-                    s[i4][e] = hidden ? -INFINITY : s[i4][e];
-                }
+                for (int i4 = 0; i4 < SUBS; ++i4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = t0 + 16 * (sub + i4) + 4 * quad + e;
+                        const bool hidden = (j > pos[rt]) | ((j < low[rt]) & (j >= a.sinks));
+                        s[rt][i4][e] = hidden ? -INFINITY : s[rt][i4][e];
+                    }
         }
+        // ---- p
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4)
+        for (int rt = 0; rt < RT; ++rt) {
+            float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i4][e]);
-        const float m_new = fmaxf(m, quad_max(top) * qs);
-        if (E_new > E || __any(m_new > m)) {
-            const float f = __builtin_amdgcn_exp2f(m - m_new), fs = ldexpf(f, E - E_new);
-            sums[0] *= fs;
-            sums[1] *= f;
-            sums[2] *= fs;
-            sums[3] *= f;
+            for (int i4 = 0; i4 < SUBS; ++i4)
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[rt][i4][e]);
+            top = quad_max(top) * qs[rt];
+            if (E_new > E || __any(top > m[rt] + kBehind)) {
+                const float m_new = fmaxf(m[rt], top);
+                const float f = __builtin_amdgcn_exp2f(m[rt] - m_new), fs = ldexpf(f, E - E_new);
+                sums[rt][0] *= fs;
+                sums[rt][1] *= f;
+                sums[rt][2] *= fs;
+                sums[rt][3] *= f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[g][i] *= fs;
-            m = m_new;
-            E = E_new;
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[rt][g][i] *= fs;
+                m[rt] = m_new;
+            }
+            const float ref = m[rt] - kUp;
+#pragma unroll
+            for (int i4 = 0; i4 < SUBS; ++i4)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[rt][i4][e] = __builtin_amdgcn_exp2f(fmaf(s[rt][i4][e], qs[rt], -ref));
         }
-        // ---- p, and the second product
-        const float ref = m - 15.0f;
+        E = E_new;
+        // ---- the second product
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[i4][e] = __builtin_amdgcn_exp2f(fmaf(s[i4][e], qs, -ref));
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            h2 p[NT][4];   // pairs of tokens: two of subtile 2 hf, two of 2 hf + 1
-            h2 from[4];
+        for (int hf = 0; hf < SUBS / 2; ++hf) {
+            h2 p[RT][NT][4];   // pairs of tokens: two of 16 * 2 hf on, two of 16 (2 hf + 1) on
+            h2 row[4];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const float p0 = s[2 * hf + (w >> 1)][2 * (w & 1)];
-                const float p1 = s[2 * hf + (w >> 1)][2 * (w & 1) + 1];
-                p[0][w] = h2{(_Float16)p0, (_Float16)p1};
-                if constexpr (NT == 2)
-                    p[NT - 1][w] = h2{(_Float16)(p0 - (float)p[0][w][0]),
-                                      (_Float16)(p1 - (float)p[0][w][1])};
-                from[w] = as_h2(sums_from[2 * hf + (w >> 1)][w & 1]);
+                row[w] = as_h2(sums_from[sub + 2 * hf + (w >> 1)][w & 1]);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float p0 = s[rt][2 * hf + (w >> 1)][2 * (w & 1)];
+                    const float p1 = s[rt][2 * hf + (w >> 1)][2 * (w & 1) + 1];
+                    p[rt][0][w] = h2{(_Float16)p0, (_Float16)p1};
+                    if constexpr (NT == 2)
+                        p[rt][NT - 1][w] = h2{(_Float16)(p0 - (float)p[rt][0][w][0]),
+                                              (_Float16)(p1 - (float)p[rt][0][w][1])};
+                }
             }
 #pragma unroll
-            for (int n2 = 0; n2 < NT; ++n2)
-                sums = mfma(join(from[0], from[1], from[2], from[3]),
-                            join(p[n2][0], p[n2][1], p[n2][2], p[n2][3]), sums);
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int n2 = 0; n2 < NT; ++n2)
+                    sums[rt] = mfma(join(row[0], row[1], row[2], row[3]),
+                                    join(p[rt][n2][0], p[rt][n2][1], p[rt][n2][2], p[rt][n2][3]),
+                                    sums[rt]);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                h2 ps[NT][4], c[4][4];   // p * step, and the codes [two tokens][channel]
+                __builtin_amdgcn_sched_barrier(0);
+                h2 ps[RT][NT][4], c[4][4];   // p * step, and the codes [two tokens][channel]
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const h2 st = as_h2(
-                        pairs[wave][D + ((4 * (2 * hf + (w >> 1)) + quad) * NG + g) * 4 + (w & 1)]);
-                    ps[0][w] = p[0][w] * st;
-                    if constexpr (NT == 2)
-                        ps[NT - 1][w] = __builtin_elementwise_fma(
-                            p[NT - 1][w], st, __builtin_elementwise_fma(p[0][w], st, -ps[0][w]));
-                    codes8<BF16>(r.v[2 * hf + (w >> 1)][2 * g + (w & 1)], one, c[w]);
+                        pairs[D + ((4 * (sub + 2 * hf + (w >> 1)) + quad) * NG + g) * 4 + (w & 1)]);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        ps[rt][0][w] = p[rt][0][w] * st;
+                        if constexpr (NT == 2)
+                            ps[rt][NT - 1][w] = __builtin_elementwise_fma(
+                                p[rt][NT - 1][w], st,
+                                __builtin_elementwise_fma(p[rt][0][w], st, -ps[rt][0][w]));
+                    }
+                    codes8<BF16>(raw_v[2 * hf + (w >> 1)][2 * g + (w & 1)], one, c[w]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int n2 = 0; n2 < NT; ++n2)
-                        o[g][i] = mfma(join(c[0][i], c[1][i], c[2][i], c[3][i]),
-                                       join(ps[n2][0], ps[n2][1], ps[n2][2], ps[n2][3]), o[g][i]);
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int n2 = 0; n2 < NT; ++n2)
+                            o[rt][g][i] = mfma(join(c[0][i], c[1][i], c[2][i], c[3][i]),
+                                               join(ps[rt][n2][0], ps[rt][n2][1], ps[rt][n2][2],
+                                                    ps[rt][n2][3]),
+                                               o[rt][g][i]);
             }
         }
-    };
-
-    while (true) {
-        if constexpr (D * NT < 256) {
-            RawPage<D> rb;
-            while (more) {
-                const int i2 = fetch(rb);
-                process(i, ra);
-                if (!more) break;
-                i = fetch(ra);
-                process(i2, rb);
-            }
-        } else {   // two pages and the rest are more than a wave's registers
-            while (more) {
-                process(i, ra);
-                i = fetch(ra);
-            }
+        if (sub + SUBS < 4) load_values(rec0, sub + SUBS);
+        else load_values(rec, 0);
         }
-        from += 64 * kWaves;
-        if (from >= i_end) break;
-        load_ids();
-        i = fetch(ra);
+        t0 = t1;
     }
 
-    // ---- join the waves: everything of a row is scaled by 2^(15 - m)
-    auto sum_row = [&](int r) { return __shfl(sums[r & 3], n + 16 * (r >> 2)); };
-    const float l = sum_row(2 * NG + 1), up = ldexpf(1.0f, kCodeExp + E);
-    const float up1 = BF16 ? up * 0.0625f : up;
-    if (quad == 0) {
-        m_all[wave][n] = m;
-        l_all[wave][n] = l;
-    }
+    // ---- everything of a row at one scale, 2^(kUp - m)
+    const float up = ldexpf(1.0f, kCodeExp + E), up1 = BF16 ? up * 0.0625f : up;
+    float l[RT];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        float rest = sum_row(2 * g + 1);
-        if (BF16) rest -= sum_row(2 * g) * ldexpf(8.0f, E);
+    for (int rt = 0; rt < RT; ++rt) {
+        auto sum_row = [&](int r) { return __shfl(sums[rt][r & 3], n + 16 * (r >> 2)); };
+        l[rt] = sum_row(2 * NG + 1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float4 w;
-            w.x = fmaf(o[g][0][e], up, rest);
-            w.y = fmaf(o[g][1][e], up1, rest);
-            w.z = fmaf(o[g][2][e], up, rest);
-            w.w = fmaf(o[g][3][e], up1, rest);
-            *reinterpret_cast<float4 *>(&o_all[wave][n][64 * g + 16 * quad + 4 * e]) = w;
+        for (int g = 0; g < NG; ++g) {
+            float rest = sum_row(2 * g + 1);
+            if (BF16) rest -= sum_row(2 * g) * ldexpf(8.0f, E);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[rt][g][i][e] = fmaf(o[rt][g][i][e], i & 1 ? up1 : up, rest);
         }
+    }
+    // ---- join the waves: wave e takes the channels 4 e .. 4 e + 3 of every lane's 16
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        if (quad == 0) {
+            m_all[wave][16 * rt + n] = m[rt];
+            l_all[wave][16 * rt + n] = l[rt];
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o_all[wave][(rt * NG + g) * 4 + e][lane] =
+                    make_float4(o[rt][g][0][e], o[rt][g][1][e], o[rt][g][2][e], o[rt][g][3][e]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * (D / 4); i += 64 * kWaves) {
-        const int rr = i / (D / 4), ch = 4 * (i % (D / 4));
-        const uint32_t rrow = t.row0 + rr, tok = rrow / G;
-        if (rrow >= t.rows) continue;
-        float top = m_all[0][rr];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int rr = 16 * rt + n;
+        if (t.row0 + rr >= t.rows) continue;
+        float top = m_all[0][rr], f[kWaves];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_all[w][rr]);
         float sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            add_part(acc, sum, __builtin_amdgcn_exp2f(m_all[w][rr] - top),
-                     *reinterpret_cast<const float4 *>(&o_all[w][rr][ch]), l_all[w][rr]);
-        const int64_t line =
-            (int64_t)(t.token0 + (int)tok) * a.heads + kv_head * G + (rrow - tok * G);
-        if (a.splits > 1) {
-            float *part = a.part + ((int64_t)split * a.N * a.heads + line) * (D + 4);
-            *reinterpret_cast<float4 *>(part + ch) = acc;
-            if (ch == 0) {
-                part[D] = top;
-                part[D + 1] = sum;
-            }
-        } else {
-            store_out<BF16>(a.out, line * D + ch, acc, sum);
+        for (int w = 0; w < kWaves; ++w) {
+            f[w] = __builtin_amdgcn_exp2f(m_all[w][rr] - top);
+            sum = fmaf(f[w], l_all[w][rr], sum);
+        }
+        const int64_t line = line_of(a, t, t.row0 + rr, kv_head, G);
+        float *part = part_of<D>(a, split, line);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                add_part(acc, f[w], o_all[w][(rt * NG + g) * 4 + wave][lane]);
+            const int ch = 64 * g + 16 * quad + 4 * wave;
+            if (sh.shared) *reinterpret_cast<float4 *>(part + ch) = acc;
+            else store_out<BF16>(a.out, line * D + ch, acc, inv);
+        }
+        if (a.splits > 1 && wave == 0 && quad == 0) {
+            part[D] = top;
+            part[D + 1] = sh.shared ? sum : kFinal;
         }
     }
 }
 
-// Prompts: a workgroup takes kPromptRows rows, and its waves share each page
-// through LDS.  A page's codes become matrix fragments once, a quarter by each
-// wave, while the page before it is worked on: bf16 calls make them the values
-// themselves (one fp16 rounding, 11 bits), so a score needs nothing but the mask
-// and the exponential after its product; fp32 calls make them code - 8 and apply
-// the pairs as attn4_kernel does.
-template <int D, bool BF16>
+// bf16 prompts: a workgroup has 32 rows in each of its four waves (16 at 256
+// channels), which share each page through LDS.  A page's codes become matrix
+// fragments once, a quarter by each wave, while the page before it is worked on,
+// and become the values themselves (one fp16 rounding, 11 bits), so that a score
+// needs nothing but the mask and the exponential after its product.
+template <int D>
 struct Prompt {
-    static constexpr int kRt = D == 64 ? (BF16 ? 4 : 2) : D == 128 && BF16 ? 2 : 1;
-    static constexpr int kRows = 64 * kRt;   // 16 * kRt rows to each of four waves
+    static constexpr int kRt = D == 256 ? 1 : 2;
+    static constexpr int kRows = 64 * kRt;
 };
 
 // One page's codes and pairs as a wave loads its quarter: 16 tokens of the keys,
@@ -622,10 +714,7 @@ __device__ __forceinline__ void load_quarter(const uint8_t *rec, int lane, int w
     using L = Kv4Page<D>;
     const int n = lane & 15, q = lane >> 4;
     load_words(rec + (16 * wave + n) * L::kRow + q * (D / 8), r.k);
-    const uint32_t *kp =
-        reinterpret_cast<const uint32_t *>(rec + L::kKeyPairs) + (16 * wave + n) * L::kGroups;
-#pragma unroll
-    for (int g = 0; g < L::kGroups; ++g) r.kp[g] = kp[g];
+    load_words(rec + L::kKeyPairs + (16 * wave + n) * 4 * L::kGroups, r.kp);
 #pragma unroll
     for (int i = 0; i < RawQuarter<D>::kUnits; ++i) {
         const int u = (wave + 4 * i) % (2 * L::kGroups), hf = u / L::kGroups, g = u % L::kGroups;
@@ -638,74 +727,43 @@ __device__ __forceinline__ void load_quarter(const uint8_t *rec, int lane, int w
     }
 }
 
-__device__ __forceinline__ h8 join_scaled(const h2 (&c)[4], h2 step, h2 mid) {
-    return join(__builtin_elementwise_fma(c[0], step, mid), __builtin_elementwise_fma(c[1], step, mid),
-                __builtin_elementwise_fma(c[2], step, mid), __builtin_elementwise_fma(c[3], step, mid));
-}
-
-template <int D, bool BF16>
+template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn4_prompt_kernel(const Attn4Args a) {
     using L = Kv4Page<D>;
-    constexpr int NG = L::kGroups, NS = L::kSteps, NT = BF16 ? 1 : 2;
-    constexpr int RT = Prompt<D, BF16>::kRt, ROWS = Prompt<D, BF16>::kRows;
+    constexpr int NG = L::kGroups, NS = L::kSteps, RT = Prompt<D>::kRt, ROWS = Prompt<D>::kRows;
     __shared__ h8 kfrag[2][4 * NS * 64], vfrag[2][8 * NG * 64];
-    __shared__ __align__(16) uint32_t pairs[2][BF16 ? 4 : 2 * D];   // fp32 calls: 8 D bytes a page
-    __shared__ uint32_t smax_all[2][4], ones[2];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, quad = lane >> 4;
     const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
-    // heads first: with eight of them a head's tiles share an XCD and its L2;
-    // the last tiles, which see the most of a prompt, before the first
+    // heads first, the last tiles before the first, as in attn4_kernel
     const uint32_t x = blockIdx.x / (uint32_t)a.c.kv_heads;
     const int kv_head = (int)(blockIdx.x - x * a.c.kv_heads);
     const uint32_t tile = x / (uint32_t)a.splits;
     const int split = (int)(x - tile * a.splits);
-    const uint32_t tiles = gridDim.x / ((uint32_t)a.c.kv_heads * (uint32_t)a.splits);
-    const Tile t = find_tile<ROWS>(a, tiles - 1 - tile, G);
+    const Tile t = find_tile<ROWS>(a, a.tiles - 1 - tile, G);
     if (t.rows == 0) return;   // the whole workgroup
-    const int i_begin = min(split * a.chunk, t.pages);
-    const int i_end = split == a.splits - 1 ? t.pages : min(i_begin + a.chunk, t.pages);
-
-    // ---- this lane's rows and their queries
-    uint32_t row[RT];
-    int pos[RT], low[RT];
-    h8 qf[RT][NT][NS], cf[RT];
-    float qs[RT];
-    const uint32_t wave_row = t.row0 + wave * 16 * RT;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        row[rt] = min(wave_row + 16 * rt + n, t.rows - 1);
-        const uint32_t tok = row[rt] / G;
-        pos[rt] = t.pos0 + (int)tok;
-        low[rt] = a.window > 0 ? pos[rt] - a.window + 1 : 0;
-        load_query<D, BF16, false>(a, t.token0 + (int)tok, kv_head * (int)G + (int)(row[rt] - tok * G),
-                                   quad, qf[rt], cf[rt], qs[rt]);
+    const Share sh = share_of(a, t, split);
+    if (sh.begin == sh.end && split > 0) {
+        write_nothing<D>(a, t, sh, kv_head, G, split, ROWS);
+        return;
     }
-    // the wave's first and last row
-    const int pos_first = t.pos0 + (int)(min(wave_row, t.rows - 1) / G);
-    const int pos_last = t.pos0 + (int)(min(wave_row + 16 * RT, t.rows) - 1) / (int)G;
-    const int low_last = a.window > 0 ? pos_last - a.window + 1 : 0;
-    const bool idle = wave_row >= t.rows;
 
+    // the next page that is there, in every wave the same: 64 table entries at a
+    // time, one a lane
     const int32_t *table = a.c.table + (int64_t)t.seq * a.c.max_pages;
     auto page_at = [&](int i) { return i < t.sink_pages ? i : t.first + i - t.sink_pages; };
     const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
     const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
-    // the next page that is there, in every wave the same: 64 table entries at a
-    // time, one a lane
-    int from = i_begin - 64, ids = -1, id = 0;
+    int from = sh.begin - 64, ids = -1, id = 0;
     uint64_t there = 0;
-    auto next = [&]() {
+    auto next = [&]() {   // its first token, or -1
         while (there == 0) {
+            if (from >= sh.end - 64) return -1;
             from += 64;
-            if (from >= i_end) {
-                from = i_end;
-                return -1;
-            }
             const int mine = from + lane;
-            ids = mine < i_end ? table[page_at(mine)] : -1;
+            ids = mine < sh.end ? table[page_at(mine)] : -1;
             there = __ballot(ids >= 0 && ids < a.c.n_pages);
         }
         const int j = __builtin_ctzll(there);
@@ -714,29 +772,54 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn4_prompt_kernel(con
         return page_at(from + j) * kPage;
     };
     RawQuarter<D> raw;
-    uint32_t raw_pairs[D / 128 ? D / 128 : 1];   // fp32 calls: this thread's words of the pairs
-    auto load = [&]() {
-        const uint8_t *rec = cache + id * page_bytes;
-        load_quarter<D>(rec, lane, wave, raw);
-        if constexpr (!BF16) {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(rec + L::kKeyPairs);
+    auto load = [&]() { load_quarter<D>(cache + id * page_bytes, lane, wave, raw); };
+    int t0 = next(), t1 = -1;
+    load();
+
+    // ---- this lane's rows and their queries
+    int pos[RT], low[RT];
+    h8 qf[RT][1][NS];
+    float qs[RT];
+    const uint32_t wave_row = t.row0 + wave * 16 * RT;
 #pragma unroll
-            for (int i = 0; i < (D + 127) / 128; ++i)
-                raw_pairs[i] = w[(threadIdx.x + 256 * i) % (2 * D)];
-        }
-    };
+    for (int rt = 0; rt < RT; ++rt) {
+        const uint32_t row = min(wave_row + 16 * rt + n, t.rows - 1), tok = row / G;
+        pos[rt] = t.pos0 + (int)tok;
+        low[rt] = a.window > 0 ? pos[rt] - a.window + 1 : 0;
+        h8 unused;
+        load_query<D, true, false>(a, t.token0 + (int)tok, kv_head * (int)G + (int)(row - tok * G),
+                                   quad, qf[rt], unused, qs[rt]);
+    }
+    // the wave's first and last row
+    const int pos_first = t.pos0 + (int)(min(wave_row, t.rows - 1) / G);
+    const int pos_last = t.pos0 + (int)((min(wave_row + 16 * RT, t.rows) - 1) / G);
+    const int low_last = a.window > 0 ? pos_last - a.window + 1 : 0;
+
     const uint32_t one = ones_1024();
     // fragments of the loaded page, whose first token is t0, into buffer `to`
     auto stage = [&](int t0, int to) {
-        const int left = t.held - t0;   // tokens behind these have pairs of any value
+        if (t0 + kPage > t.held) {   // tokens behind the last have pairs of any value
+            const int left = t.held - t0;
+#pragma unroll
+            for (int i = 0; i < RawQuarter<D>::kUnits; ++i) {
+                const int hf = (wave + 4 * i) / NG;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int tok = 16 * (2 * hf + (w >> 1)) + 4 * quad + 2 * (w & 1);
+                    const uint32_t keep = tok + 1 < left ? 0xffffffffu : tok < left ? 0xffffu : 0u;
+                    raw.vp[i][w >> 1][w & 1] &= keep;
+                    raw.vp[i][w >> 1][2 + (w & 1)] &= keep;
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
             h2 c[4];
             codes8<false>(raw.k[j], one, c);
-            const h2 p = as_h2(raw.kp[j >> 1]);
-            kfrag[to][(wave * NS + j) * 64 + lane] =
-                BF16 ? join_scaled(c, h2{p[0], p[0]}, h2{p[1], p[1]})
-                     : join(c[0], c[1], c[2], c[3]);
+            const h2 p = as_h2(raw.kp[j >> 1]), st = {p[0], p[0]}, md = {p[1], p[1]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = __builtin_elementwise_fma(c[e], st, md);
+            kfrag[to][(wave * NS + j) * 64 + lane] = join(c[0], c[1], c[2], c[3]);
         }
 #pragma unroll
         for (int i = 0; i < RawQuarter<D>::kUnits; ++i) {
@@ -747,47 +830,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn4_prompt_kernel(con
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 codes8<false>(raw.v[i][w >> 1][w & 1], one, c[w]);
-                if constexpr (BF16) {
-                    uint32_t st = raw.vp[i][w >> 1][w & 1], md = raw.vp[i][w >> 1][2 + (w & 1)];
-                    const int tok = 16 * (2 * hf + (w >> 1)) + 4 * quad + 2 * (w & 1);
-                    const uint32_t keep = tok + 1 < left ? 0xffffffffu : tok < left ? 0xffffu : 0u;
-                    st &= keep;
-                    md &= keep;
+                const h2 st = as_h2(raw.vp[i][w >> 1][w & 1]);
+                const h2 md = as_h2(raw.vp[i][w >> 1][2 + (w & 1)]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        c[w][e] = __builtin_elementwise_fma(c[w][e], as_h2(st), as_h2(md));
-                }
+                for (int e = 0; e < 4; ++e) c[w][e] = __builtin_elementwise_fma(c[w][e], st, md);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 vfrag[to][((hf * NG + g) * 4 + e) * 64 + lane] =
                     join(c[0][e], c[1][e], c[2][e], c[3][e]);
         }
-        if constexpr (!BF16) {
-            uint32_t smax = 0;
-#pragma unroll
-            for (int i = 0; i < (D + 127) / 128; ++i) {
-                const int w = threadIdx.x + 256 * i;
-                if (w >= 2 * D) continue;
-                uint32_t v = raw_pairs[i];
-                if (w >= D) {   // value pairs: halfword h is of token 4 (h / 8 / NG) + h % 4
-                    const int h = 2 * (w - D), tok = 4 * (h / (8 * NG)) + (h & 3);
-                    v &= tok + 1 < left ? 0xffffffffu : tok < left ? 0xffffu : 0u;
-                    if (!(w & 2)) smax = max(smax, max(v & 0xffffu, v >> 16));
-                }
-                pairs[to][w] = v;
-            }
-            const int top = wave_max_u16((int)smax);
-            if (lane == 0) smax_all[to][wave] = (uint32_t)top;
-        }
     };
 
-    // What is carried along the pages, as in attn4_kernel, for each of the lane's
-    // rows; the weights are 2^(x - m + 7), where m may stay up to 8 behind the
-    // largest x, so that the accumulators are rescaled seldom.
-    constexpr float kBehind = 8.0f, kUp = 7.0f;
+    // What is carried along the pages, as in attn4_kernel; `sums` has the sum of p
+    // in all its rows.
     float m[RT];
-    int E = -14;
     f4 o[RT][NG][4], sums[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -798,55 +855,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn4_prompt_kernel(con
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[rt][g][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (threadIdx.x < 2) ones[threadIdx.x] = 0x3c003c00u;
-
-    auto scores = [&](int t0, int buf, float (&s)[RT][4][4]) {
+    auto scores = [&](int buf, f4 (&s)[RT][4]) {
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4) {
-            f4 acc[RT][BF16 ? 1 : NG];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int g = 0; g < (BF16 ? 1 : NG); ++g) acc[rt][g] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int rt = 0; rt < RT; ++rt) s[rt][i4] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
                 const h8 kf = kfrag[buf][(i4 * NS + j) * 64 + lane];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int n2 = 0; n2 < NT; ++n2) {
-                        f4 &c = acc[rt][BF16 ? 0 : j >> 1];
-                        c = mfma(kf, qf[rt][n2][j], c);
-                    }
-            }
-            if constexpr (BF16) {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[rt][i4][e] = acc[rt][0][e];
-            } else {
-                h8 pf = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const h2 p = as_h2(pairs[buf][(16 * i4 + n) * NG + g]);
-                    pf[2 * g] = p[0];
-                    pf[2 * g + 1] = p[1];
-                }
-                const uint32_t *kp = &pairs[buf][(16 * i4 + 4 * quad) * NG];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const f4 rest = mfma(pf, cf[rt], f4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[rt][i4][e] = rest[e] * 0x1p11f;
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-                            s[rt][i4][e] = fmaf((float)as_h2(kp[e * NG + g])[0], acc[rt][g][e],
-                                                s[rt][i4][e]);
-                    }
-                }
+                for (int rt = 0; rt < RT; ++rt) s[rt][i4] = mfma(kf, qf[rt][0][j], s[rt][i4]);
             }
         }
+    };
+    auto weigh = [&](int t0, int buf, f4 (&s)[RT][4]) {
         const bool all_seen =
             t0 + kPage - 1 <= pos_first && (t0 >= low_last || t0 + kPage <= a.sinks);
         if (!all_seen) {
@@ -861,14 +883,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn4_prompt_kernel(con
                         s[rt][i4][e] = hidden ? -INFINITY : s[rt][i4][e];
                     }
         }
-    };
-    auto weigh = [&](int buf, float (&s)[RT][4][4]) {
-        int E_new = E;
-        if constexpr (!BF16) {
-            const uint32_t top = max(max(smax_all[buf][0], smax_all[buf][1]),
-                                     max(smax_all[buf][2], smax_all[buf][3]));
-            E_new = max(E, (__builtin_amdgcn_readfirstlane((int)top) >> 10) - 14);
-        }
+        h2 p[RT][8];   // pairs of tokens: two of each 16's four
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float top = -INFINITY;
@@ -877,147 +892,83 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn4_prompt_kernel(con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, s[rt][i4][e]);
             top = quad_max(top) * qs[rt];
-            if (E_new > E || __any(top > m[rt] + kBehind)) {
-                const float m_new = fmaxf(m[rt], top);
-                const float f = __builtin_amdgcn_exp2f(m[rt] - m_new), fs = ldexpf(f, E - E_new);
+            if (__any(top > m[rt] + kBehind)) {
+                const float m_new = fmaxf(m[rt], top), f = __builtin_amdgcn_exp2f(m[rt] - m_new);
                 sums[rt] *= f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[rt][g][i] *= fs;
+                    for (int i = 0; i < 4; ++i) o[rt][g][i] *= f;
                 m[rt] = m_new;
             }
             const float ref = m[rt] - kUp;
 #pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[rt][i4][e] = __builtin_amdgcn_exp2f(fmaf(s[rt][i4][e], qs[rt], -ref));
+            for (int w = 0; w < 8; ++w) {
+                const float p0 = s[rt][w >> 1][2 * (w & 1)], p1 = s[rt][w >> 1][2 * (w & 1) + 1];
+                p[rt][w] = h2{(_Float16)__builtin_amdgcn_exp2f(fmaf(p0, qs[rt], -ref)),
+                              (_Float16)__builtin_amdgcn_exp2f(fmaf(p1, qs[rt], -ref))};
+            }
         }
-        E = E_new;
-        const _Float16 down = BF16 ? (_Float16)1.0f : pow2_f16(-E);
+        const _Float16 o1 = (_Float16)1.0f;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            h2 p[RT][NT][4];
+            h8 pf[RT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const float p0 = s[rt][2 * hf + (w >> 1)][2 * (w & 1)];
-                    const float p1 = s[rt][2 * hf + (w >> 1)][2 * (w & 1) + 1];
-                    p[rt][0][w] = h2{(_Float16)p0, (_Float16)p1};
-                    if constexpr (NT == 2)
-                        p[rt][NT - 1][w] = h2{(_Float16)(p0 - (float)p[rt][0][w][0]),
-                                              (_Float16)(p1 - (float)p[rt][0][w][1])};
-                }
-            h2 from4[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t *src =
-                    BF16 || n == 2 * NG + 1
-                        ? ones
-                        : &pairs[buf][D + (4 * (2 * hf + (w >> 1)) + quad) * NG * 4 +
-                                      2 * (n & (2 * NG - 1))];
-                from4[w] = as_h2(src[w & 1]);
+            for (int rt = 0; rt < RT; ++rt) {
+                pf[rt] = join(p[rt][4 * hf], p[rt][4 * hf + 1], p[rt][4 * hf + 2], p[rt][4 * hf + 3]);
+                sums[rt] = mfma(h8{o1, o1, o1, o1, o1, o1, o1, o1}, pf[rt], sums[rt]);
             }
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int n2 = 0; n2 < NT; ++n2)
-                    sums[rt] = mfma(join(from4[0], from4[1], from4[2], from4[3]),
-                                    join(p[rt][n2][0], p[rt][n2][1], p[rt][n2][2], p[rt][n2][3]),
-                                    sums[rt]);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                h2 ps[RT][NT][4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    if constexpr (BF16) {
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) ps[rt][0][w] = p[rt][0][w];
-                    } else {
-                        const h2 st = as_h2(pairs[buf][D + ((4 * (2 * hf + (w >> 1)) + quad) * NG + g) * 4 +
-                                                       (w & 1)]) * down;
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            ps[rt][0][w] = p[rt][0][w] * st;
-                            ps[rt][NT - 1][w] = __builtin_elementwise_fma(
-                                p[rt][NT - 1][w], st,
-                                __builtin_elementwise_fma(p[rt][0][w], st, -ps[rt][0][w]));
-                        }
-                    }
-                }
+            for (int g = 0; g < NG; ++g)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const h8 vf = vfrag[buf][((hf * NG + g) * 4 + i) * 64 + lane];
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int n2 = 0; n2 < NT; ++n2)
-                            o[rt][g][i] = mfma(vf,
-                                               join(ps[rt][n2][0], ps[rt][n2][1], ps[rt][n2][2],
-                                                    ps[rt][n2][3]),
-                                               o[rt][g][i]);
+                    for (int rt = 0; rt < RT; ++rt) o[rt][g][i] = mfma(vf, pf[rt], o[rt][g][i]);
                 }
-            }
         }
     };
 
-    // one page in LDS being worked on, the next one in registers or on its way
-    int t0 = next(), t1 = -1;
+    // one page in LDS being worked on, the next one in registers or on its way;
+    // what is staged behind the last is never used
     if (t0 >= 0) {
-        load();
         stage(t0, 0);
         t1 = next();
-        if (t1 >= 0) load();
+        load();
     }
     for (int buf = 0; t0 >= 0; buf ^= 1) {
         __syncthreads();   // the page is whole, and everyone is done with the other buffer
-        const bool seen = !idle && t0 <= pos_last;
-        float s[RT][4][4];
-        if (seen) scores(t0, buf, s);
-        int t2 = -1;
-        if (t1 >= 0) {
-            stage(t1, buf ^ 1);
-            t2 = next();
-            if (t2 >= 0) load();
-        }
-        if (seen) weigh(buf, s);
+        const int t2 = next();
+        f4 s[RT][4];
+        scores(buf, s);
+        stage(t1, buf ^ 1);
+        load();
+        if (t0 <= pos_last) weigh(t0, buf, s);
         t0 = t1;
         t1 = t2;
     }
 
     // ---- everything of a row is scaled by 2^(kUp - m)
-    const float up = ldexpf(1.0f, E);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        constexpr int kOnes = BF16 ? 0 : 2 * NG + 1;
-        const float l = __shfl(sums[rt][kOnes & 3], n + 16 * (kOnes >> 2));
-        const bool mine = wave_row + 16 * rt + n < t.rows;
-        const uint32_t tok = row[rt] / G;
-        const int64_t line =
-            (int64_t)(t.token0 + (int)tok) * a.heads + kv_head * G + (row[rt] - tok * G);
-        float *part = a.part + ((int64_t)split * a.N * a.heads + line) * (D + 4);
+        const uint32_t r = wave_row + 16 * rt + n;
+        if (r >= t.rows) continue;
+        const int64_t line = line_of(a, t, r, kv_head, G);
+        float *part = part_of<D>(a, split, line);
+        const float l = sums[rt][0], inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float rest =
-                BF16 ? 0.0f : __shfl(sums[rt][(2 * g + 1) & 3], n + 16 * ((2 * g + 1) >> 2));
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int ch = 64 * g + 16 * quad + 4 * e;
-                float4 w;
-                w.x = BF16 ? o[rt][g][0][e] : fmaf(o[rt][g][0][e], up, rest);
-                w.y = BF16 ? o[rt][g][1][e] : fmaf(o[rt][g][1][e], up, rest);
-                w.z = BF16 ? o[rt][g][2][e] : fmaf(o[rt][g][2][e], up, rest);
-                w.w = BF16 ? o[rt][g][3][e] : fmaf(o[rt][g][3][e], up, rest);
-                if (!mine) continue;
-                if (a.splits > 1) *reinterpret_cast<float4 *>(part + ch) = w;
-                else store_out<BF16>(a.out, line * D + ch, w, l);
+                const float4 w = make_float4(o[rt][g][0][e], o[rt][g][1][e], o[rt][g][2][e],
+                                             o[rt][g][3][e]);
+                if (sh.shared) *reinterpret_cast<float4 *>(part + ch) = w;
+                else store_out<true>(a.out, line * D + ch, w, inv);
             }
-        }
-        if (mine && a.splits > 1 && quad == 0) {
+        if (a.splits > 1 && quad == 0) {
             part[D] = m[rt];
-            part[D + 1] = l;
+            part[D + 1] = sh.shared ? l : kFinal;
         }
     }
 }
@@ -1034,8 +985,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
     const int slot = threadIdx.x / kLanes, ch = 4 * (threadIdx.x % kLanes);
     const int g = slot & (par - 1);
     const int64_t line = (int64_t)blockIdx.x * (slots / par) + slot / par, lines = a.N * a.heads;
-    const bool mine = line < lines && row_in_call(a.c, line / a.heads);
     const float *part = a.part + line * (D + 4);
+    const bool mine = line < lines && row_in_call(a.c, line / a.heads) && part[D + 1] != kFinal;
     const int64_t stride = lines * (D + 4);
     float top = kNoMax, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1063,9 +1014,11 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
             acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
             top = best;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                add_part(acc, sum, ls[i] > 0.0f ? __builtin_amdgcn_exp2f(ms[i] - top) : 0.0f,
-                         os[i], ls[i]);
+            for (int i = 0; i < kBatch; ++i) {
+                const float fi = ls[i] > 0.0f ? __builtin_amdgcn_exp2f(ms[i] - top) : 0.0f;
+                sum = fmaf(fi, ls[i], sum);
+                add_part(acc, fi, os[i]);
+            }
         }
     }
     if (par > 1) {
@@ -1079,23 +1032,26 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
         for (int i = 1; i < par; ++i) top = fmaxf(top, m_all[slot + i]);
         sum = 0.0f;
         acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int i = 0; i < par; ++i)
-            add_part(acc, sum, __builtin_amdgcn_exp2f(m_all[slot + i] - top),
-                     o_all[threadIdx.x + i * kLanes], l_all[slot + i]);
+        for (int i = 0; i < par; ++i) {
+            const float fi = __builtin_amdgcn_exp2f(m_all[slot + i] - top);
+            sum = fmaf(fi, l_all[slot + i], sum);
+            add_part(acc, fi, o_all[threadIdx.x + i * kLanes]);
+        }
     }
-    if (mine) store_out<BF16>(a.out, line * D + ch, acc, sum);
+    if (mine) store_out<BF16>(a.out, line * D + ch, acc, sum > 0.0f ? 1.0f / sum : 0.0f);
 }
 
 template <int D, bool BF16>
-void launch_d(const Attn4Args &a, hipStream_t st) {
+void launch_d(Attn4Args a, hipStream_t st) {
     const int64_t G = a.heads / a.c.kv_heads;
-    const int rows = a.prompt ? Prompt<D, BF16>::kRows : kRows;
+    constexpr int kRt = BF16 ? 1 : prompt_rt(D);
+    const int rows = !a.prompt ? 16 : BF16 ? Prompt<D>::kRows : 16 * kRt;
     const int64_t tiles = a.N * G / rows + a.c.n_seqs;
-    const dim3 grid((unsigned)(tiles * a.c.kv_heads * a.splits));
-    if (a.prompt)
-        hipLaunchKernelGGL((attn4_prompt_kernel<D, BF16>), grid, dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((attn4_kernel<D, BF16>), grid, dim3(64 * kWaves), 0, st, a);
+    a.tiles = (uint32_t)tiles;
+    const dim3 grid((unsigned)(tiles * a.c.kv_heads * a.splits)), block(64 * kWaves);
+    if (!a.prompt) hipLaunchKernelGGL((attn4_kernel<D, BF16, 1>), grid, block, 0, st, a);
+    else if (BF16) hipLaunchKernelGGL(attn4_prompt_kernel<D>, grid, block, 0, st, a);
+    else hipLaunchKernelGGL((attn4_kernel<D, false, kRt>), grid, block, 0, st, a);
     if (a.splits > 1) {
         // few rows with many splits: whole workgroups of 1024 to a row
         const int64_t lines = a.N * a.heads;
@@ -1118,7 +1074,7 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     // (prompts: kPromptChunk pages, since a workgroup has its rows to prepare).
     const int64_t rows = N * (heads / kv_heads);
     const bool prompt = rows >= kPromptFrom * n_seqs;
-    const int64_t tile = prompt ? 128 : kRows, least = prompt ? kPromptChunk : kWaves;
+    const int64_t tile = prompt ? 32 : 16, least = prompt ? kPromptChunk : kWaves;
     const int64_t groups = (rows / tile + n_seqs) * kv_heads;
     int64_t pages = (max_kv + kPage - 1) / kPage;
     if (window > 0)   // what a tile's rows can see of it: the window before each, the sinks

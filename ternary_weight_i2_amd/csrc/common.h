@@ -332,6 +332,7 @@ struct Attn4Args {
     int64_t q_stride, N;
     float scale_log2;      // softmax scale times log2(e)
     int heads, prompt, splits, chunk, window, sinks;
+    uint32_t tiles;        // set by the launch
 };
 // Which kernel a call's sizes take, how many workgroups share the pages of one
 // row tile, and how many pages each takes (the last one the rest).
