@@ -441,23 +441,41 @@ def linear(x, mats, want_dot=True, want_y=True, out=None, qout=None):
     return out, qout
 
 
-def _on(device):
-    """The tensors' device, made current for a launch on its current stream."""
-    import contextlib
+def _launch(fn, device, *args):
+    """fn(*args, the device's current stream), with the device current."""
     import torch
     if device.type != "cuda":
         raise ValueError("tensor must live on the GPU")
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status)
 
 
-def _dtype(t, name):
+def _float_code(dtype, name):
+    """BITNET_F32 or BITNET_BF16."""
     import torch
-    dt = {torch.float32: F32, torch.bfloat16: BF16}.get(t.dtype)
-    if dt is None:
-        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    return dt
+    if dtype == torch.float32:
+        return F32
+    if dtype == torch.bfloat16:
+        return BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+
+
+def _at(t, name, dtype, shape, device):
+    """The pointer of an operand that may be None, refused before any launch if it
+    is not contiguous or not what is expected."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _expect(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def block_norm_quant(b, res=None, post_norm=False, post_gamma=None, gate=None, scale=1.0,
@@ -474,45 +492,34 @@ def block_norm_quant(b, res=None, post_norm=False, post_gamma=None, gate=None, s
     import torch
     if b.dim() != 2:
         raise TypeError("b must be 2-D [N][F]")
-    N, F = b.shape
-    bd, dev = _dtype(b, "b"), b.device
-    stream = b if res is None else res
-    sd = _dtype(stream, "res")
-    if res is not None:
-        _expect(res, "res", res.dtype, (N, F), dev)
-    for name, t in (("post_gamma", post_gamma), ("gamma", gamma)):
-        if t is not None:
-            _expect(t, name, torch.float32, (F,), dev)
+    shape, dev = b.shape, b.device
+    N, F = shape
+    f32 = torch.float32
+    stream = b.dtype if res is None else res.dtype
+    bd, sd = _float_code(b.dtype, "b"), _float_code(stream, "res")
     if post_gamma is not None and not post_norm:
         raise ValueError("post_gamma without post_norm")
-    gate_stride = 0
-    if gate is not None:
-        _expect(gate, "gate", torch.float32, (F,) if gate.dim() == 1 else (N, F), dev)
-        gate_stride = 0 if gate.dim() == 1 else F
+    gate_rows = gate is not None and gate.dim() != 1
     if out is None:
         h = torch.empty_like(res) if res is not None else None
-        v = torch.empty((N, F), dtype=stream.dtype, device=dev) if want_v else None
-        q = (torch.empty((N, F), dtype=torch.int8, device=dev),
-             torch.empty((N,), dtype=torch.float32, device=dev),
-             torch.empty((N,), dtype=torch.int32, device=dev)) if want_q else None
+        v = torch.empty(shape, dtype=stream, device=dev) if want_v else None
+        q = (torch.empty(shape, dtype=torch.int8, device=dev),
+             torch.empty(N, dtype=f32, device=dev),
+             torch.empty(N, dtype=torch.int32, device=dev)) if want_q else None
     else:
         h, v, q = out
-        if h is not None:
-            if res is None:
-                raise ValueError("h without res")
-            _expect(h, "h", res.dtype, (N, F), dev)
-        if v is not None:
-            _expect(v, "v", stream.dtype, (N, F), dev)
-        if q is not None:
-            _expect(q[0], "xq", torch.int8, (N, F), dev)
-            _expect(q[1], "x_scale", torch.float32, (N,), dev)
-            _expect(q[2], "x_sum", torch.int32, (N,), dev)
+        if h is not None and res is None:
+            raise ValueError("h without res")
     xq, xs, xsum = q if q is not None else (None, None, None)
-    with _on(dev):
-        _check(load().bitnet_block_norm_quant_i8(
-            _ptr(b), bd, int(bool(post_norm)), _ptr(post_gamma), _ptr(gate), gate_stride,
-            float(scale), _ptr(res), _ptr(h), sd, _ptr(gamma), float(eps), N, F, _ptr(v),
-            _ptr(xq), _ptr(xs), _ptr(xsum), _stream(b)))
+    if q is not None and (xq is None or xs is None or xsum is None):
+        raise ValueError("xq, x_scale and x_sum come together")
+    _launch(load().bitnet_block_norm_quant_i8, dev, _at(b, "b", b.dtype, shape, dev), bd,
+            1 if post_norm else 0, _at(post_gamma, "post_gamma", f32, (F,), dev),
+            _at(gate, "gate", f32, shape if gate_rows else (F,), dev), F if gate_rows else 0, scale,
+            _at(res, "res", stream, shape, dev), _at(h, "h", stream, shape, dev), sd,
+            _at(gamma, "gamma", f32, (F,), dev), eps, N, F, _at(v, "v", stream, shape, dev),
+            _at(xq, "xq", torch.int8, shape, dev), _at(xs, "x_scale", f32, (N,), dev),
+            _at(xsum, "x_sum", torch.int32, (N,), dev))
     return h, v, q
 
 
@@ -529,29 +536,31 @@ def kv4_cache(n_pages, n_kv_heads, head_dim, device="cuda"):
 def _kv4_batch(cache, table, kv_len, q_start):
     """Cache and sequences -> (bitnet_kv4_batch, kv heads, head_dim)."""
     import torch
+    i32 = torch.int32
     if cache.dim() != 3 or cache.dtype != torch.uint8 or cache.shape[2] % 72:
         raise TypeError("cache must be uint8 [n_pages][n_kv_heads][72 * head_dim]")
     dev = cache.device
     if table.dim() != 2:
         raise ValueError("table must be 2-D [n_seqs][max_pages]")
     B, P = table.shape
-    _expect(table, "table", torch.int32, (B, P), dev)
-    _expect(kv_len, "kv_len", torch.int32, (B,), dev)
-    _expect(q_start, "q_start", torch.int32, (B + 1,), dev)
     n_pages, heads, rec = cache.shape
-    return (KV4Batch(_ptr(cache), n_pages, heads, rec // 72, _ptr(table), P, _ptr(kv_len),
-                     _ptr(q_start), B), heads, rec // 72)
+    if kv_len is None or q_start is None:
+        raise ValueError("kv_len and q_start are required")
+    at = _at(table, "table", i32, (B, P), dev)
+    lens, start = _at(kv_len, "kv_len", i32, (B,), dev), _at(q_start, "q_start", i32, (B + 1,), dev)
+    return KV4Batch(_ptr(cache), n_pages, heads, rec // 72, at, P, lens, start, B), heads, rec // 72
 
 
 def _rows(t, name, heads, dim, device):
     """[N][heads][dim] with any stride between tokens -> that stride."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise ValueError(f"{name} must have shape [N][{heads}][{dim}], got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    n, (token, head, one) = t.shape[0], t.stride()
+    if n and (one != 1 or (heads > 1 and head != dim)):
         raise ValueError(f"{name}: the values of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return token if n > 1 else heads * dim
 
 
 def kv4_append(cache, table, kv_len, q_start, k, v):
@@ -561,13 +570,11 @@ def kv4_append(cache, table, kv_len, q_start, k, v):
     (kv_len counts them already).  table [B][max_pages], kv_len [B], q_start
     [B+1]: int32 on the device, read when the kernel runs."""
     batch, heads, dim = _kv4_batch(cache, table, kv_len, q_start)
-    dt = _dtype(k, "k")
     if v.dtype != k.dtype or v.shape != k.shape:
         raise TypeError("k and v must have the same shape and type")
-    ks, vs = _rows(k, "k", heads, dim, cache.device), _rows(v, "v", heads, dim, cache.device)
-    with _on(cache.device):
-        _check(load().bitnet_kv4_append(ctypes.byref(batch), k.data_ptr(), ks, v.data_ptr(), vs,
-                                        dt, k.shape[0], _stream(cache)))
+    dev = cache.device
+    _launch(load().bitnet_kv4_append, dev, batch, k.data_ptr(), _rows(k, "k", heads, dim, dev),
+            v.data_ptr(), _rows(v, "v", heads, dim, dev), _float_code(k.dtype, "k"), k.shape[0])
 
 
 def kv4_read(cache, table, kv_len, q_start, n, dtype=None, out=None):
@@ -576,19 +583,17 @@ def kv4_read(cache, table, kv_len, q_start, n, dtype=None, out=None):
     bf16 (``dtype``).  ``out``: (k, v) to write into, one of them may be None."""
     import torch
     batch, heads, dim = _kv4_batch(cache, table, kv_len, q_start)
+    dev, shape = cache.device, (n, heads, dim)
     if out is None:
-        shape = (n, heads, dim)
-        out = tuple(torch.empty(shape, dtype=dtype or torch.float32, device=cache.device)
-                    for _ in range(2))
-    dts = {_dtype(t, "out") for t in out if t is not None}
-    if len(dts) != 1:
-        raise TypeError("k and v must have one type, float32 or bfloat16")
-    for name, t in zip("kv", out):
-        if t is not None:
-            _expect(t, name, dtype or t.dtype, (n, heads, dim), cache.device)
-    with _on(cache.device):
-        _check(load().bitnet_kv4_read(ctypes.byref(batch), _ptr(out[0]), _ptr(out[1]), dts.pop(),
-                                      n, _stream(cache)))
+        dtype = dtype or torch.float32
+        out = (torch.empty(shape, dtype=dtype, device=dev),
+               torch.empty(shape, dtype=dtype, device=dev))
+    k, v = out
+    if k is None and v is None:
+        raise ValueError("k and v are both None")
+    dtype = dtype or (k if k is not None else v).dtype
+    _launch(load().bitnet_kv4_read, dev, batch, _at(k, "k", dtype, shape, dev),
+            _at(v, "v", dtype, shape, dev), _float_code(dtype, "out"), n)
     return out
 
 
@@ -609,27 +614,25 @@ def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, ma
     batch, kv_heads, dim = _kv4_batch(cache, table, kv_len, q_start)
     if q.dim() != 3:
         raise ValueError("q must be 3-D [N][n_heads][head_dim]")
-    N, heads, dev = q.shape[0], q.shape[1], cache.device
-    dt = _dtype(q, "q")
-    stride = _rows(q, "q", heads, dim, dev)
-    most = KV4_PAGE * table.shape[1]
-    max_kv = most if max_kv is None else min(int(max_kv), most)
-    need = attn_kv4_workspace(table.shape[0], N, heads, kv_heads, dim, max_kv, int(window),
-                              int(sinks))
+    L, dev, dtype, shape = load(), cache.device, q.dtype, q.shape
+    N, heads = shape[0], shape[1]
+    code, stride = _float_code(dtype, "q"), _rows(q, "q", heads, dim, dev)
+    most = KV4_PAGE * batch.max_pages
+    max_kv = most if max_kv is None else min(max_kv, most)
+    need = L.bitnet_attn_kv4_workspace(batch.n_seqs, N, heads, kv_heads, dim, max_kv, window, sinks)
+    if need < 0:
+        raise BitnetError(E_SHAPE, L.bitnet_last_error().decode(errors="replace"))
     if out is None:
-        out = torch.empty((N, heads, dim), dtype=q.dtype, device=dev)
-    else:
-        _expect(out, "out", q.dtype, (N, heads, dim), dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
         raise ValueError(f"workspace must be {need} bytes of uint8 on {dev}")
-    with _on(dev):
-        _check(load().bitnet_attn_kv4(
-            ctypes.byref(batch), q.data_ptr(), stride, dt, N, heads,
-            dim ** -0.5 if scale is None else float(scale), int(window), int(sinks), max_kv,
-            _ptr(out), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-            _stream(cache)))
+    _launch(L.bitnet_attn_kv4, dev, batch, q.data_ptr(), stride, code, N, heads,
+            dim ** -0.5 if scale is None else scale, window, sinks, max_kv,
+            _at(out, "out", dtype, shape, dev), None if workspace is None else _ptr(workspace),
+            0 if workspace is None else workspace.numel())
     return out
 
 
