@@ -139,19 +139,8 @@ struct Tile {
 template <int ROWS>
 __device__ __forceinline__ Tile find_tile(const Attn4Args &a, uint32_t x, uint32_t G) {
     Tile t;
-    // the largest b with q_start[b] * G / ROWS + b <= x: a sequence has at least
-    // as many tiles to itself as its rows need.  64 probes at a time.
-    const int lane = threadIdx.x & 63;
-    int lo = 0, n = (int)a.c.n_seqs;   // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 63) >> 6, b = lo + lane * step;
-        const bool ok = lane * step < n && (uint32_t)a.c.q_start[b] * G / ROWS + b <= x;
-        const int hits = __popcll(__ballot(ok));   // all probes up to the answer's
-        const int k = hits > 0 ? hits - 1 : 0;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    lo = __builtin_amdgcn_readfirstlane(lo);
+    // a sequence has at least as many tiles to itself as its rows need
+    const int lo = sequence_of<ROWS, 1>(a.c.q_start, (int)a.c.n_seqs, G, x);
     t.seq = lo;
     const int begin = a.c.q_start[lo], end = a.c.q_start[lo + 1];
     t.token0 = begin;

@@ -70,54 +70,65 @@ __device__ __forceinline__ float block_factor(double ss, double (&part)[kNormMax
 }
 
 template <int R, bool BB, bool SB>
-__global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(const BlockNormArgs a) {
+__global__ __launch_bounds__(R == 4 ? kNormMaxThreads : 512) void block_norm_kernel(
+    const BlockNormArgs a) {
 #pragma clang fp contract(off)
     __shared__ NormShared sh;
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int pieces = a.F >> 3;
     const int64_t row = (int64_t)blockIdx.x * a.F;
-    float t[R][8];
-    // ---- the block's output, its norm, gate and scale
+    // Everything the token needs is requested before the first sum is waited for
+    // (rows of over 8192 channels: what the registers of a wider workgroup hold).
+    constexpr bool kAhead = R < 4;
+    float t[R][8], res[R][8], pg[kAhead ? R : 1][8], gt[kAhead ? R : 1][8], gm[kAhead ? R : 1][8];
+    auto load_gain = [&](const float *p, int64_t i, float (&x)[8]) {
+        if (p) {
+            load8<false>(p, i, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 1.0f;
+        }
+    };
+    const float *gate = a.gate ? a.gate + blockIdx.x * a.gate_stride : nullptr;
     double ss = 0.0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int p = tid + r * blockDim.x;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[r][e] = 0.0f;
-        if (p < pieces) load8<BB>(a.b, row + 8 * p, t[r]);
-        if (a.post) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fma((double)t[r][e], (double)t[r][e], ss);
+        const int p = tid + r * blockDim.x, q = min(p, pieces - 1);
+        load8<BB>(a.b, row + 8 * q, t[r]);
+        if (a.res) load8<SB>(a.res, row + 8 * q, res[r]);
+        if constexpr (kAhead) {
+            load_gain(a.post_gamma, 8 * q, pg[r]);
+            load_gain(gate, 8 * q, gt[r]);
+            load_gain(a.gamma, 8 * q, gm[r]);
         }
     }
-    const float c1 = a.post ? block_factor(ss, sh.sum[0], a.F, a.eps) : 1.0f;
+    // ---- the block's output, its norm, gate and scale
+    float c1 = 1.0f;
+    if (a.post) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (tid + r * blockDim.x < pieces)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fma((double)t[r][e], (double)t[r][e], ss);
+        c1 = block_factor(ss, sh.sum[0], a.F, a.eps);
+    }
     ss = 0.0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int p = tid + r * blockDim.x;
         if (p < pieces) {
-            float g[8];
-            if (a.post) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[r][e] *= c1;
-                if (a.post_gamma) {
-                    load8<false>(a.post_gamma, 8 * p, g);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) t[r][e] *= g[e];
-                }
+            float(&g1)[8] = pg[kAhead ? r : 0], (&g2)[8] = gt[kAhead ? r : 0];
+            if constexpr (!kAhead) {
+                load_gain(a.post_gamma, 8 * p, g1);
+                load_gain(gate, 8 * p, g2);
             }
-            if (a.gate) {
-                load8<false>(a.gate, blockIdx.x * a.gate_stride + 8 * p, g);
+            // a factor of 1 changes nothing, so what is absent needs no branch
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t[r][e] *= g[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[r][e] *= a.scale;
+            for (int e = 0; e < 8; ++e) t[r][e] = (((t[r][e] * c1) * g1[e]) * g2[e]) * a.scale;
             // ---- the residual stream, as it is stored
             if (a.res) {
-                load8<SB>(a.res, row + 8 * p, g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t[r][e] = g[e] + t[r][e];
+                for (int e = 0; e < 8; ++e) t[r][e] = res[r][e] + t[r][e];
                 store8<SB>(a.h, row + 8 * p, t[r]);
             }
 #pragma unroll
@@ -131,14 +142,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(const Block
     for (int r = 0; r < R; ++r) {
         const int p = tid + r * blockDim.x;
         if (p < pieces) {
-            float g[8];
+            float(&g)[8] = gm[kAhead ? r : 0];
+            if constexpr (!kAhead) load_gain(a.gamma, 8 * p, g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[r][e] *= c2;
-            if (a.gamma) {
-                load8<false>(a.gamma, 8 * p, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[r][e] *= g[e];
-            }
+            for (int e = 0; e < 8; ++e) t[r][e] = (t[r][e] * c2) * g[e];
 #pragma unroll
             for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(t[r][e]));
             if (a.v) {
@@ -197,9 +204,9 @@ void launch_r(const BlockNormArgs &a, int64_t N, int threads, int b_bf16, int s_
 
 hipError_t launch_block_norm(const BlockNormArgs &a, int64_t N, int b_bf16, int s_bf16,
                              hipStream_t st) {
-    // eight channels per thread up to 8192 channels, then up to 32
+    // eight channels per thread up to 4096, 16 up to 8192, then up to 32
     const int pieces = a.F >> 3;
-    const int r = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : 4;
+    const int r = pieces <= 512 ? 1 : pieces <= 1024 ? 2 : 4;
     const int threads = ((pieces + r - 1) / r + 63) / 64 * 64;
     if (r == 1) launch_r<1>(a, N, threads, b_bf16, s_bf16, st);
     else if (r == 2) launch_r<2>(a, N, threads, b_bf16, s_bf16, st);

@@ -44,16 +44,23 @@ struct Kv4Page {
     static constexpr int kBytes = 72 * D;
 };
 
-// The sequence of row r: the largest b with start[b] <= r (0 if there is none).
-// Always in [0, n), whatever start holds.
-__device__ __forceinline__ int64_t sequence_of(const int32_t *start, int64_t n, int64_t r) {
-    int64_t lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int64_t m = (lo + hi + 1) >> 1;
-        if (start[m] <= r) lo = m;
-        else hi = m - 1;
+// Tiles of ROWS rows, a sequence's own from start[b] * G / ROWS + SLACK * b on: the
+// sequence of tile x, the largest b for which that is at most x.  64 probes at a
+// time, the same x in every lane; the result is uniform and always in [0, n),
+// whatever start holds.
+template <int ROWS, int SLACK>
+__device__ __forceinline__ int sequence_of(const int32_t *start, int n, uint32_t G, uint32_t x) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0;   // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 63) >> 6, b = lo + lane * step;
+        const bool ok = lane * step < n && (uint32_t)start[b] * G / ROWS + SLACK * b <= x;
+        const int hits = __popcll(__ballot(ok));   // all probes up to the answer's
+        const int k = hits > 0 ? hits - 1 : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Tokens of sequence b that the cache can hold: kv_len held to [0, 64 max_pages].
@@ -62,24 +69,6 @@ __device__ __forceinline__ int64_t held_tokens(const Kv4Args &c, int64_t b) {
     return t < 0 ? 0 : t > most ? most : t;
 }
 
-// Row r of a call (a new token, or one to read): its place in the cache.
-struct Kv4Place {
-    int64_t rec;   // record index of kv head 0, or -1 if the row has no place
-    int in_page;
-};
-__device__ __forceinline__ Kv4Place place_of(const Kv4Args &c, int64_t r) {
-    Kv4Place p{-1, 0};
-    const int64_t b = sequence_of(c.q_start, c.n_seqs, r);
-    const int64_t first = c.q_start[b], end = c.q_start[b + 1];
-    const int64_t held = held_tokens(c, b);
-    const int64_t pos = held - (end - r);
-    if (r < first || r >= end || pos < 0 || pos >= held) return p;
-    const int64_t page = c.table[b * c.max_pages + pos / kPage];
-    if (page < 0 || page >= c.n_pages) return p;
-    p.rec = page * c.kv_heads;
-    p.in_page = (int)(pos % kPage);
-    return p;
-}
 // Whether row r belongs to one of the call's sequences at all.
 __device__ __forceinline__ bool row_in_call(const Kv4Args &c, int64_t r) {
     return r >= c.q_start[0] && r < c.q_start[c.n_seqs];

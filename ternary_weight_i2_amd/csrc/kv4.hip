@@ -1,9 +1,11 @@
 // kv4.hip -- the 4-bit key/value cache: quantising keys and values as they are
 // written, and reading them back (kv4.h: the quantiser and the layout).
 //
-// Eight lanes hold a group of 64 channels, eight channels each: its smallest
-// and largest value come from three DPP moves, every lane quantises its own
-// eight and stores them.  Both kernels are bound by HBM for prompts (5 or 3
+// A workgroup takes four positions of one sequence that lie side by side in a page
+// (a block of the value codes), all heads, keys and values.  Eight lanes hold a
+// group of 64 channels, eight channels each, of all four tokens: a group's ends come
+// from three DPP moves, and a lane's value codes are two stores of 8 bytes, 16 side
+// by side for a group.  Both kernels are bound by HBM for prompts (4.56 or 2.56
 // bytes a value with fp32 or bf16 rows) and by latency for single tokens.
 #include "kv4.h"
 
@@ -53,41 +55,92 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t *pair) {
     return codes;
 }
 
+// The four positions [base, base + 4) of a workgroup, and their rows in the call.
+struct Block4 {
+    int64_t rec;        // record index of kv head 0, or -1 if there is no page
+    int in_page;        // of base: a multiple of 4
+    int row;            // the call's row at base
+    uint32_t rows;      // bit t: the call has a row at base + t
+    uint32_t places;    // bit t: and the cache a place for it
+};
+__device__ __forceinline__ Block4 find_block(const Kv4Args &c, int64_t N) {
+    Block4 k{-1, 0, 0, 0, 0};
+    const int b = sequence_of<4, 2>(c.q_start, (int)c.n_seqs, 1, blockIdx.x);
+    const int first = c.q_start[b], end = c.q_start[b + 1];
+    const int tile = (int)(blockIdx.x - ((uint32_t)first / 4 + 2 * b));
+    if (tile < 0 || first < 0 || end <= first || end > N) return k;
+    const int held = (int)held_tokens(c, b), pos0 = held - (end - first);
+    const int base = (pos0 & ~3) + 4 * tile;
+    k.row = first + base - pos0;
+    for (int t = 0; t < 4; ++t)
+        if (base + t >= pos0 && base + t < held) k.rows |= 1u << t;
+    if (base < 0 || !k.rows) return k;   // base is a multiple of 4: all four lie before 0
+    const int page = c.table[b * c.max_pages + base / kPage];
+    if (page < 0 || page >= c.n_pages) return k;
+    k.rec = (int64_t)page * c.kv_heads;
+    k.in_page = base % kPage;
+    k.places = k.rows;
+    return k;
+}
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(kKvThreads) void kv4_append_kernel(
     const Kv4Args c, const void *k, const void *v, int64_t k_stride, int64_t v_stride, int64_t N) {
     using L = Kv4Page<D>;
-    // one lane: eight channels of a (token, head, key or value) row
-    const int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
-    const int p = (int)(i % (D / 8));
-    int64_t r = i / (D / 8);
-    const int is_v = (int)(r & 1);
-    r >>= 1;
-    const int head = (int)(r % c.kv_heads);
-    const int64_t token = r / c.kv_heads;
-    if (token >= N) return;   // whole groups of eight lanes leave together
-    const Kv4Place at = place_of(c, token);
-    if (at.rec < 0) return;
-    float x[8];
-    load8<BF16>(is_v ? v : k, token * (is_v ? v_stride : k_stride) + head * D + 8 * p, x);
-    uint32_t pair;
-    const uint32_t codes = quantise8(x, &pair);
-    uint8_t *rec = c.cache + (at.rec + head) * (int64_t)L::kBytes;
-    const int g = p >> 3, t = at.in_page;
-    if (!is_v) {
-        const int dw = t * (D / 8) + (p & 3) * L::kSteps + (p >> 2);
-        reinterpret_cast<uint32_t *>(rec)[dw] = codes;
-        if ((p & 7) == 0)
-            reinterpret_cast<uint32_t *>(rec + L::kKeyPairs)[t * L::kGroups + g] = pair;
-    } else {
-        uint16_t *w = reinterpret_cast<uint16_t *>(rec + L::kValues);
-        const int lane = 2 * (p & 7), blk = t >> 2;
-        w[((blk * 16 + lane) * L::kGroups + g) * 4 + (t & 3)] = (uint16_t)codes;
-        w[((blk * 16 + lane + 1) * L::kGroups + g) * 4 + (t & 3)] = (uint16_t)(codes >> 16);
-        if ((p & 7) == 0) {
-            uint16_t *m = reinterpret_cast<uint16_t *>(rec + L::kValuePairs);
-            m[(blk * L::kGroups + g) * 8 + (t & 3)] = (uint16_t)pair;
-            m[(blk * L::kGroups + g) * 8 + 4 + (t & 3)] = (uint16_t)(pair >> 16);
+    const Block4 at = find_block(c, N);
+    if (!at.places) return;   // the whole workgroup
+    const int lanes = c.kv_heads * 2 * (D / 8), t0 = at.in_page;
+    for (int i = threadIdx.x; i < lanes; i += blockDim.x) {   // whole groups of eight lanes
+        const int p = i % (D / 8), g = p >> 3, head = i / (D / 8) >> 1;
+        const bool is_v = i / (D / 8) & 1;
+        const void *src = is_v ? v : k;
+        const int64_t stride = is_v ? v_stride : k_stride;
+        float x[4][8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (at.places >> t & 1)
+                load8<BF16>(src, (at.row + t) * stride + head * D + 8 * p, x[t]);
+        uint32_t codes[4], pair[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) codes[t] = quantise8(x[t], &pair[t]);
+        uint8_t *rec = c.cache + (at.rec + head) * (int64_t)L::kBytes;
+        if (!is_v) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(rec) + t0 * (D / 8) + (p & 3) * L::kSteps + (p >> 2);
+            uint32_t *m = reinterpret_cast<uint32_t *>(rec + L::kKeyPairs) + t0 * L::kGroups + g;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (!(at.places >> t & 1)) continue;
+                w[t * (D / 8)] = codes[t];
+                if ((p & 7) == 0) m[t * L::kGroups] = pair[t];
+            }
+            continue;
+        }
+        // halfwords [token] of this lane's two value lanes, and [step, mid][token]
+        uint16_t *w = reinterpret_cast<uint16_t *>(rec + L::kValues) +
+                      ((t0 >> 2) * 16 + 2 * (p & 7)) * L::kGroups * 4 + g * 4;
+        uint16_t *m = reinterpret_cast<uint16_t *>(rec + L::kValuePairs) +
+                      ((t0 >> 2) * L::kGroups + g) * 8;
+        if (at.places == 15) {
+            auto low = [](uint32_t a, uint32_t b) { return (a & 0xffffu) | b << 16; };
+            auto high = [](uint32_t a, uint32_t b) { return a >> 16 | (b & 0xffff0000u); };
+            *reinterpret_cast<uint2 *>(w) = make_uint2(low(codes[0], codes[1]), low(codes[2], codes[3]));
+            *reinterpret_cast<uint2 *>(w + 4 * L::kGroups) =
+                make_uint2(high(codes[0], codes[1]), high(codes[2], codes[3]));
+            if ((p & 7) == 0)
+                *reinterpret_cast<uint4 *>(m) =
+                    make_uint4(low(pair[0], pair[1]), low(pair[2], pair[3]),
+                               high(pair[0], pair[1]), high(pair[2], pair[3]));
+            continue;
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (!(at.places >> t & 1)) continue;
+            w[t] = (uint16_t)codes[t];
+            w[4 * L::kGroups + t] = (uint16_t)(codes[t] >> 16);
+            if ((p & 7) == 0) {
+                m[t] = (uint16_t)pair[t];
+                m[4 + t] = (uint16_t)(pair[t] >> 16);
+            }
         }
     }
 }
@@ -97,54 +150,75 @@ __global__ __launch_bounds__(kKvThreads) void kv4_read_kernel(const Kv4Args c, v
                                                               int64_t N) {
 #pragma clang fp contract(off)
     using L = Kv4Page<D>;
-    const int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
-    const int p = (int)(i % (D / 8));
-    int64_t r = i / (D / 8);
-    const int is_v = (int)(r & 1);
-    r >>= 1;
-    const int head = (int)(r % c.kv_heads);
-    const int64_t token = r / c.kv_heads;
-    void *out = is_v ? v : k;
-    if (token >= N || !out || !row_in_call(c, token)) return;
-    const Kv4Place at = place_of(c, token);
-    float x[8];
+    const Block4 at = find_block(c, N);
+    if (!at.rows) return;   // the whole workgroup
+    const int lanes = c.kv_heads * 2 * (D / 8), t0 = at.in_page;
+    for (int i = threadIdx.x; i < lanes; i += blockDim.x) {
+        const int p = i % (D / 8), g = p >> 3, head = i / (D / 8) >> 1;
+        const bool is_v = i / (D / 8) & 1;
+        void *out = is_v ? v : k;
+        if (!out) continue;
+        uint32_t codes[4] = {0, 0, 0, 0}, pair[4] = {0, 0, 0, 0};   // zeros where there is no page
+        if (at.rec >= 0) {
+            const uint8_t *rec = c.cache + (at.rec + head) * (int64_t)L::kBytes;
+            if (!is_v) {
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(rec) + t0 * (D / 8) +
+                                    (p & 3) * L::kSteps + (p >> 2);
+                const uint32_t *m =
+                    reinterpret_cast<const uint32_t *>(rec + L::kKeyPairs) + t0 * L::kGroups + g;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-    if (at.rec >= 0) {
-        const uint8_t *rec = c.cache + (at.rec + head) * (int64_t)L::kBytes;
-        const int g = p >> 3, t = at.in_page;
-        uint32_t codes, pair;
-        if (!is_v) {
-            codes = reinterpret_cast<const uint32_t *>(
-                rec)[t * (D / 8) + (p & 3) * L::kSteps + (p >> 2)];
-            pair = reinterpret_cast<const uint32_t *>(rec + L::kKeyPairs)[t * L::kGroups + g];
-        } else {
-            const uint16_t *w = reinterpret_cast<const uint16_t *>(rec + L::kValues);
-            const uint16_t *m = reinterpret_cast<const uint16_t *>(rec + L::kValuePairs);
-            const int lane = 2 * (p & 7), blk = t >> 2;
-            codes = w[((blk * 16 + lane) * L::kGroups + g) * 4 + (t & 3)] |
-                    (uint32_t)w[((blk * 16 + lane + 1) * L::kGroups + g) * 4 + (t & 3)] << 16;
-            pair = m[(blk * L::kGroups + g) * 8 + (t & 3)] |
-                   (uint32_t)m[(blk * L::kGroups + g) * 8 + 4 + (t & 3)] << 16;
+                for (int t = 0; t < 4; ++t) {
+                    codes[t] = w[t * (D / 8)];
+                    pair[t] = m[t * L::kGroups];
+                }
+            } else {
+                const uint16_t *w = reinterpret_cast<const uint16_t *>(rec + L::kValues) +
+                                    ((t0 >> 2) * 16 + 2 * (p & 7)) * L::kGroups * 4 + g * 4;
+                const uint2 a = *reinterpret_cast<const uint2 *>(w);
+                const uint2 b = *reinterpret_cast<const uint2 *>(w + 4 * L::kGroups);
+                const uint4 m = *reinterpret_cast<const uint4 *>(
+                    rec + L::kValuePairs + ((t0 >> 2) * L::kGroups + g) * 16);
+                codes[0] = (a.x & 0xffffu) | b.x << 16;
+                codes[1] = a.x >> 16 | (b.x & 0xffff0000u);
+                codes[2] = (a.y & 0xffffu) | b.y << 16;
+                codes[3] = a.y >> 16 | (b.y & 0xffff0000u);
+                pair[0] = (m.x & 0xffffu) | m.z << 16;
+                pair[1] = m.x >> 16 | (m.z & 0xffff0000u);
+                pair[2] = (m.y & 0xffffu) | m.w << 16;
+                pair[3] = m.y >> 16 | (m.w & 0xffff0000u);
+            }
         }
-        const float step = (float)__builtin_bit_cast(_Float16, (uint16_t)pair);
-        const float mid = (float)__builtin_bit_cast(_Float16, (uint16_t)(pair >> 16));
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = mid + step * (float)((int)((codes >> (4 * e)) & 15u) - 8);
-    }
-    const int64_t o = (token * c.kv_heads + head) * D + 8 * p;
-    if constexpr (BF16) {
-        uint32_t w[4];
+        for (int t = 0; t < 4; ++t) {
+            if (!(at.rows >> t & 1)) continue;
+            const float step = (float)__builtin_bit_cast(_Float16, (uint16_t)pair[t]);
+            const float mid = (float)__builtin_bit_cast(_Float16, (uint16_t)(pair[t] >> 16));
+            float x[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = bf16_bits(x[2 * e]) | bf16_bits(x[2 * e + 1]) << 16;
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + o) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
+            for (int e = 0; e < 8; ++e)
+                x[e] = mid + step * (float)((int)((codes[t] >> (4 * e)) & 15u) - 8);
+            const int64_t o = ((int64_t)(at.row + t) * c.kv_heads + head) * D + 8 * p;
+            if constexpr (BF16) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = bf16_bits(x[2 * e]) | bf16_bits(x[2 * e + 1]) << 16;
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + o) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
+                f[0] = make_float4(x[0], x[1], x[2], x[3]);
+                f[1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
+        }
     }
+}
+
+// A sequence of n rows touches at most n / 4 + 2 blocks.
+dim3 block_grid(const Kv4Args &c, int64_t N) { return dim3((unsigned)(N / 4 + 2 * c.n_seqs)); }
+dim3 block_threads(const Kv4Args &c, int dim) {
+    const int lanes = c.kv_heads * 2 * (dim / 8);
+    return dim3(lanes < kKvThreads ? (lanes + 63) / 64 * 64 : kKvThreads);
 }
 
 }  // namespace
@@ -152,8 +226,7 @@ __global__ __launch_bounds__(kKvThreads) void kv4_read_kernel(const Kv4Args c, v
 hipError_t launch_kv4_append(const Kv4Args &c, const void *k, const void *v, int bf16,
                              int64_t k_stride, int64_t v_stride, int64_t N, int dim,
                              hipStream_t st) {
-    const int64_t lanes = N * c.kv_heads * 2 * (dim / 8);
-    const dim3 g((unsigned)((lanes + kKvThreads - 1) / kKvThreads)), t(kKvThreads);
+    const dim3 g = block_grid(c, N), t = block_threads(c, dim);
 #define KV4_APPEND(D, B) \
     hipLaunchKernelGGL((kv4_append_kernel<D, B>), g, t, 0, st, c, k, v, k_stride, v_stride, N)
     if (dim == 64) { if (bf16) KV4_APPEND(64, true); else KV4_APPEND(64, false); }
@@ -165,8 +238,7 @@ hipError_t launch_kv4_append(const Kv4Args &c, const void *k, const void *v, int
 
 hipError_t launch_kv4_read(const Kv4Args &c, void *k, void *v, int bf16, int64_t N, int dim,
                            hipStream_t st) {
-    const int64_t lanes = N * c.kv_heads * 2 * (dim / 8);
-    const dim3 g((unsigned)((lanes + kKvThreads - 1) / kKvThreads)), t(kKvThreads);
+    const dim3 g = block_grid(c, N), t = block_threads(c, dim);
 #define KV4_READ(D, B) hipLaunchKernelGGL((kv4_read_kernel<D, B>), g, t, 0, st, c, k, v, N)
     if (dim == 64) { if (bf16) KV4_READ(64, true); else KV4_READ(64, false); }
     else if (dim == 128) { if (bf16) KV4_READ(128, true); else KV4_READ(128, false); }
