@@ -595,7 +595,7 @@ BITNET_API int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t 
     g_last_error.clear();
     if (n_seqs == 0 || N == 0) return 0;
     const int64_t splits =
-        bitnet::attn4_plan(n_seqs, N, n_heads, n_kv_heads, max_kv, window, sinks).splits;
+        bitnet::attn4_plan(n_seqs, N, n_heads, n_kv_heads, head_dim, max_kv, window, sinks).splits;
     return splits > 1 ? splits * N * n_heads * (head_dim + 4) * 4 : 0;
 }
 
@@ -627,11 +627,11 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
         return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
                     (long long)workspace_bytes, (long long)need);
     const bitnet::Attn4Plan sp =
-        bitnet::attn4_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads, max_kv, window,
-                            sinks);
+        bitnet::attn4_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads, batch->head_dim, max_kv,
+                           window, sinks);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
                               scale * 1.4426950408889634f, (int)n_heads, sp.prompt,
-                              sp.splits, sp.chunk, (int)window, (int)sinks, 0};
+                              sp.wide, sp.splits, sp.chunk, (int)window, (int)sinks, 0};
     hipError_t e = bitnet::launch_attn4(a, dtype == BITNET_BF16, (int)batch->head_dim,
                                         static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);

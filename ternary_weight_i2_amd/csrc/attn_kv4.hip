@@ -41,11 +41,9 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;          // waves of a workgroup
-constexpr int kWanted = 512;      // workgroups that a launch is split into
+constexpr int kWanted = 512;       // workgroups that a launch is split into
 constexpr int kMaxSplits = 256;
-constexpr int kPromptFrom = 64;   // rows of a sequence, on average
-constexpr int kPromptChunk = 16;
+constexpr int kPromptFrom = 2048;
 constexpr int kJoinThreads = 1024;
 constexpr float kBehind = 8.0f, kUp = 7.0f;   // see attn4_kernel
 constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
@@ -252,9 +250,10 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[j][e]));
     top = quad_max(top);
-    // q times 2^k: the largest is in [2^14, 2^15); the sums of q times 2^(k - 11):
-    // the largest they can be is 2^10
-    const int k = top > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(top), 140) : 0;
+    // q times 2^k: the largest is in [2^14, 2^15) (a row of numbers below 2^-111
+    // stays smaller); the sums of q times 2^(k - 11): the largest they can be is 2^10
+    const int k = top > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(top), 126) : 0;
+    const float up = ldexpf(1.0f, k), up16 = up * 0.0625f;
     qs = fmaxf(ldexpf(a.scale_log2, (RAW ? 24 : 0) - k), 1.2e-38f);
     cf = h8{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
@@ -265,11 +264,12 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int ch = (e >> 1) + 4 * (e & 1);
-                sum += ldexpf(v[j][ch], k - 11);
-                const float z = ldexpf(v[j][ch], k - (RAW && (e & 2) ? 4 : 0));
+                const float z = v[j][ch] * (RAW && (e & 2) ? up16 : up);
                 const _Float16 hi = (_Float16)z;
                 qf[0][j][e] = hi;
                 if constexpr (!BF16) qf[1][j][e] = (_Float16)(z - (float)hi);
+                // up * 2^-11 first: a sum of 64 numbers below the largest fp32
+                sum = fmaf(v[j][ch], up * 0x1p-11f, sum);
             }
         sum = quad_sum(sum);
         // -8 (raw codes) and 1 times the sum, its upper term in the first 8 of 32
@@ -283,25 +283,25 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
     }
 }
 
-// A workgroup has 16 * RT rows, 16 to each of RT fragments, and its four waves
-// take turns at their pages.  RT is 1 for tokens; fp32 prompts have 2 where the
-// registers allow it, which shares what a page's codes cost to unpack.
-constexpr int prompt_rt(int dim) { return dim == 64 ? 2 : 1; }
-constexpr int least_waves(int dim, int rt, bool bf16) {   // to a SIMD, without spills
-    return dim == 256 ? 1 : dim * rt * (bf16 ? 1 : 2) <= 128 ? 3 : 2;
+// A workgroup has 16 * RT rows, 16 to each of RT fragments, and its WAVES waves
+// take turns at their pages.  RT is 2 for prompts of many rows, which shares what a
+// page's codes cost to unpack; eight waves serve a single short history, which is
+// then not split.
+constexpr int least_waves(int dim, int rt, bool bf16, int waves) {   // to a SIMD, without spills
+    return dim == 256 ? 1 : waves == 4 && dim * rt * (bf16 ? 1 : 2) <= 128 ? 3 : 2;
 }
 
-template <int D, bool BF16, int RT>
-__global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_kernel(
+template <int D, bool BF16, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void attn4_kernel(
     const Attn4Args a) {
     using L = Kv4Page<D>;
     constexpr int NG = L::kGroups, NS = L::kSteps, NT = BF16 ? 1 : 2, ROWS = 16 * RT;
     constexpr int SUBS = 2;   // 16-token quarters of a page that are worked on together
     constexpr int kCodeExp = BF16 ? 24 : 0;   // raw codes carry 2^-24, and every second pair 16
-    __shared__ __align__(16) uint32_t pairs_all[kWaves][2 * D];   // 8 D bytes a page
-    __shared__ __align__(16) uint32_t ones_all[kWaves][2];        // four fp16 ones
-    __shared__ __align__(16) float4 o_all[kWaves][RT * NG * 4][64];
-    __shared__ float m_all[kWaves][ROWS], l_all[kWaves][ROWS];
+    __shared__ __align__(16) uint32_t pairs_all[WAVES][2 * D];   // 8 D bytes a page
+    __shared__ __align__(16) uint32_t ones_all[WAVES][2];        // four fp16 ones
+    __shared__ __align__(16) float4 o_all[WAVES][RT * NG * 4][64];
+    __shared__ float m_all[WAVES][ROWS], l_all[WAVES][ROWS];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_k
         return;
     }
 
-    // ---- the pages of this split, every fourth to this wave.  64 table entries
+    // ---- the pages of this split, every WAVES-th to this wave.  64 table entries
     // at a time, one a lane, with a bit for each page that is there; they are
     // waited for before the pages, so that no wait of the loop takes in a page that
     // is on its way.  For the same reason a page is always loaded, at the end the
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_k
     int from = sh.begin + wave, ids = -1, id = 0, at_bit = 0;
     uint64_t there = 0;
     auto load_ids = [&]() {
-        const int mine = from + kWaves * lane;
+        const int mine = from + WAVES * lane;
         ids = mine < sh.end ? table[page_at(mine)] : -1;
         there = __ballot(ids >= 0 && ids < a.c.n_pages);
     };
@@ -343,15 +343,15 @@ __global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_k
     const uint8_t *rec = cache;
     auto next = [&]() {
         while (there == 0) {
-            if (from >= sh.end - 64 * kWaves) return -1;
-            from += 64 * kWaves;
+            if (from >= sh.end - 64 * WAVES) return -1;
+            from += 64 * WAVES;
             load_ids();
         }
         at_bit = __builtin_ctzll(there);
         there &= there - 1;
         id = __builtin_amdgcn_readlane(ids, at_bit);
         rec = cache + id * page_bytes;
-        return page_at(from + kWaves * at_bit) * kPage;
+        return page_at(from + WAVES * at_bit) * kPage;
     };
     // codes of the quarters that come next, and this lane's share of a page's pairs
     uint32_t raw_k[SUBS][D / 32], raw_v[SUBS][D / 32], raw_m[D / 32];
@@ -510,6 +510,7 @@ __global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_k
         const bool all_seen =
             t0 + kPage - 1 <= pos_first && (t0 >= low_last || t0 + kPage <= a.sinks);
         if (!all_seen) {
+            asm volatile("");   // a branch: most pages are seen by all rows
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -630,7 +631,7 @@ __global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_k
                     o[rt][g][i][e] = fmaf(o[rt][g][i][e], i & 1 ? up1 : up, rest);
         }
     }
-    // ---- join the waves: wave e takes the channels 4 e .. 4 e + 3 of every lane's 16
+    // ---- join the waves: each takes every WAVES-th four of a lane's channels
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         if (quad == 0) {
@@ -649,12 +650,12 @@ __global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_k
     for (int rt = 0; rt < RT; ++rt) {
         const int rr = 16 * rt + n;
         if (t.row0 + rr >= t.rows) continue;
-        float top = m_all[0][rr], f[kWaves];
+        float top = m_all[0][rr], f[WAVES];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_all[w][rr]);
+        for (int w = 1; w < WAVES; ++w) top = fmaxf(top, m_all[w][rr]);
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             f[w] = __builtin_amdgcn_exp2f(m_all[w][rr] - top);
             sum = fmaf(f[w], l_all[w][rr], sum);
         }
@@ -662,302 +663,19 @@ __global__ __launch_bounds__(64 * kWaves, least_waves(D, RT, BF16)) void attn4_k
         float *part = part_of<D>(a, split, line);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int u = 0; u < (4 * NG + WAVES - 1) / WAVES; ++u) {
+            const int it = wave + u * WAVES;
+            if (4 * NG % WAVES != 0 && it >= 4 * NG) continue;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                add_part(acc, f[w], o_all[w][(rt * NG + g) * 4 + wave][lane]);
-            const int ch = 64 * g + 16 * quad + 4 * wave;
+            for (int w = 0; w < WAVES; ++w) add_part(acc, f[w], o_all[w][rt * NG * 4 + it][lane]);
+            const int ch = 64 * (it >> 2) + 16 * quad + 4 * (it & 3);
             if (sh.shared) *reinterpret_cast<float4 *>(part + ch) = acc;
             else store_out<BF16>(a.out, line * D + ch, acc, inv);
         }
         if (a.splits > 1 && wave == 0 && quad == 0) {
             part[D] = top;
             part[D + 1] = sh.shared ? sum : kFinal;
-        }
-    }
-}
-
-// bf16 prompts: a workgroup has 32 rows in each of its four waves (16 at 256
-// channels), which share each page through LDS.  A page's codes become matrix
-// fragments once, a quarter by each wave, while the page before it is worked on,
-// and become the values themselves (one fp16 rounding, 11 bits), so that a score
-// needs nothing but the mask and the exponential after its product.
-template <int D>
-struct Prompt {
-    static constexpr int kRt = D == 256 ? 1 : 2;
-    static constexpr int kRows = 64 * kRt;
-};
-
-// One page's codes and pairs as a wave loads its quarter: 16 tokens of the keys,
-// and for the values the units (32 tokens, group) u = wave, wave + 4, ..
-template <int D>
-struct RawQuarter {
-    static constexpr int kUnits = D == 64 ? 1 : D / 128;
-    uint32_t k[D / 32], kp[D / 64];
-    uint32_t v[kUnits][2][2], vp[kUnits][2][4];
-};
-template <int D>
-__device__ __forceinline__ void load_quarter(const uint8_t *rec, int lane, int wave,
-                                             RawQuarter<D> &r) {
-    using L = Kv4Page<D>;
-    const int n = lane & 15, q = lane >> 4;
-    load_words(rec + (16 * wave + n) * L::kRow + q * (D / 8), r.k);
-    load_words(rec + L::kKeyPairs + (16 * wave + n) * 4 * L::kGroups, r.kp);
-#pragma unroll
-    for (int i = 0; i < RawQuarter<D>::kUnits; ++i) {
-        const int u = (wave + 4 * i) % (2 * L::kGroups), hf = u / L::kGroups, g = u % L::kGroups;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int blk = 4 * (2 * hf + b) + q;
-            load_words(rec + L::kValues + (blk * 16 + n) * (D / 8) + 8 * g, r.v[i][b]);
-            load_words(rec + L::kValuePairs + (blk * L::kGroups + g) * 16, r.vp[i][b]);
-        }
-    }
-}
-
-template <int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn4_prompt_kernel(const Attn4Args a) {
-    using L = Kv4Page<D>;
-    constexpr int NG = L::kGroups, NS = L::kSteps, RT = Prompt<D>::kRt, ROWS = Prompt<D>::kRows;
-    __shared__ h8 kfrag[2][4 * NS * 64], vfrag[2][8 * NG * 64];
-
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 15, quad = lane >> 4;
-    const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
-    // heads first, the last tiles before the first, as in attn4_kernel
-    const uint32_t x = blockIdx.x / (uint32_t)a.c.kv_heads;
-    const int kv_head = (int)(blockIdx.x - x * a.c.kv_heads);
-    const uint32_t tile = x / (uint32_t)a.splits;
-    const int split = (int)(x - tile * a.splits);
-    const Tile t = find_tile<ROWS>(a, a.tiles - 1 - tile, G);
-    if (t.rows == 0) return;   // the whole workgroup
-    const Share sh = share_of(a, t, split);
-    if (sh.begin == sh.end && split > 0) {
-        write_nothing<D>(a, t, sh, kv_head, G, split, ROWS);
-        return;
-    }
-
-    // the next page that is there, in every wave the same: 64 table entries at a
-    // time, one a lane
-    const int32_t *table = a.c.table + (int64_t)t.seq * a.c.max_pages;
-    auto page_at = [&](int i) { return i < t.sink_pages ? i : t.first + i - t.sink_pages; };
-    const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
-    const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
-    int from = sh.begin - 64, ids = -1, id = 0;
-    uint64_t there = 0;
-    auto next = [&]() {   // its first token, or -1
-        while (there == 0) {
-            if (from >= sh.end - 64) return -1;
-            from += 64;
-            const int mine = from + lane;
-            ids = mine < sh.end ? table[page_at(mine)] : -1;
-            there = __ballot(ids >= 0 && ids < a.c.n_pages);
-        }
-        const int j = __builtin_ctzll(there);
-        there &= there - 1;
-        id = __builtin_amdgcn_readlane(ids, j);
-        return page_at(from + j) * kPage;
-    };
-    RawQuarter<D> raw;
-    auto load = [&]() { load_quarter<D>(cache + id * page_bytes, lane, wave, raw); };
-    int t0 = next(), t1 = -1;
-    load();
-
-    // ---- this lane's rows and their queries
-    int pos[RT], low[RT];
-    h8 qf[RT][1][NS];
-    float qs[RT];
-    const uint32_t wave_row = t.row0 + wave * 16 * RT;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t row = min(wave_row + 16 * rt + n, t.rows - 1), tok = row / G;
-        pos[rt] = t.pos0 + (int)tok;
-        low[rt] = a.window > 0 ? pos[rt] - a.window + 1 : 0;
-        h8 unused;
-        load_query<D, true, false>(a, t.token0 + (int)tok, kv_head * (int)G + (int)(row - tok * G),
-                                   quad, qf[rt], unused, qs[rt]);
-    }
-    // the wave's first and last row
-    const int pos_first = t.pos0 + (int)(min(wave_row, t.rows - 1) / G);
-    const int pos_last = t.pos0 + (int)((min(wave_row + 16 * RT, t.rows) - 1) / G);
-    const int low_last = a.window > 0 ? pos_last - a.window + 1 : 0;
-
-    const uint32_t one = ones_1024();
-    // fragments of the loaded page, whose first token is t0, into buffer `to`
-    auto stage = [&](int t0, int to) {
-        if (t0 + kPage > t.held) {   // tokens behind the last have pairs of any value
-            const int left = t.held - t0;
-#pragma unroll
-            for (int i = 0; i < RawQuarter<D>::kUnits; ++i) {
-                const int hf = (wave + 4 * i) / NG;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int tok = 16 * (2 * hf + (w >> 1)) + 4 * quad + 2 * (w & 1);
-                    const uint32_t keep = tok + 1 < left ? 0xffffffffu : tok < left ? 0xffffu : 0u;
-                    raw.vp[i][w >> 1][w & 1] &= keep;
-                    raw.vp[i][w >> 1][2 + (w & 1)] &= keep;
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            h2 c[4];
-            codes8<false>(raw.k[j], one, c);
-            const h2 p = as_h2(raw.kp[j >> 1]), st = {p[0], p[0]}, md = {p[1], p[1]};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = __builtin_elementwise_fma(c[e], st, md);
-            kfrag[to][(wave * NS + j) * 64 + lane] = join(c[0], c[1], c[2], c[3]);
-        }
-#pragma unroll
-        for (int i = 0; i < RawQuarter<D>::kUnits; ++i) {
-            const int u = wave + 4 * i;
-            if (u >= 2 * NG) continue;
-            const int hf = u / NG, g = u % NG;
-            h2 c[4][4];   // [two tokens][channel]
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                codes8<false>(raw.v[i][w >> 1][w & 1], one, c[w]);
-                const h2 st = as_h2(raw.vp[i][w >> 1][w & 1]);
-                const h2 md = as_h2(raw.vp[i][w >> 1][2 + (w & 1)]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[w][e] = __builtin_elementwise_fma(c[w][e], st, md);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                vfrag[to][((hf * NG + g) * 4 + e) * 64 + lane] =
-                    join(c[0][e], c[1][e], c[2][e], c[3][e]);
-        }
-    };
-
-    // What is carried along the pages, as in attn4_kernel; `sums` has the sum of p
-    // in all its rows.
-    float m[RT];
-    f4 o[RT][NG][4], sums[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = kNoMax;
-        sums[rt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[rt][g][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    auto scores = [&](int buf, f4 (&s)[RT][4]) {
-#pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) s[rt][i4] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const h8 kf = kfrag[buf][(i4 * NS + j) * 64 + lane];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) s[rt][i4] = mfma(kf, qf[rt][0][j], s[rt][i4]);
-            }
-        }
-    };
-    auto weigh = [&](int t0, int buf, f4 (&s)[RT][4]) {
-        const bool all_seen =
-            t0 + kPage - 1 <= pos_first && (t0 >= low_last || t0 + kPage <= a.sinks);
-        if (!all_seen) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int i4 = 0; i4 < 4; ++i4)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = t0 + 16 * i4 + 4 * quad + e;
-                        const bool hidden = (j > pos[rt]) | ((j < low[rt]) & (j >= a.sinks));
-                        s[rt][i4][e] = hidden ? -INFINITY : s[rt][i4][e];
-                    }
-        }
-        h2 p[RT][8];   // pairs of tokens: two of each 16's four
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[rt][i4][e]);
-            top = quad_max(top) * qs[rt];
-            if (__any(top > m[rt] + kBehind)) {
-                const float m_new = fmaxf(m[rt], top), f = __builtin_amdgcn_exp2f(m[rt] - m_new);
-                sums[rt] *= f;
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[rt][g][i] *= f;
-                m[rt] = m_new;
-            }
-            const float ref = m[rt] - kUp;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const float p0 = s[rt][w >> 1][2 * (w & 1)], p1 = s[rt][w >> 1][2 * (w & 1) + 1];
-                p[rt][w] = h2{(_Float16)__builtin_amdgcn_exp2f(fmaf(p0, qs[rt], -ref)),
-                              (_Float16)__builtin_amdgcn_exp2f(fmaf(p1, qs[rt], -ref))};
-            }
-        }
-        const _Float16 o1 = (_Float16)1.0f;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            h8 pf[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                pf[rt] = join(p[rt][4 * hf], p[rt][4 * hf + 1], p[rt][4 * hf + 2], p[rt][4 * hf + 3]);
-                sums[rt] = mfma(h8{o1, o1, o1, o1, o1, o1, o1, o1}, pf[rt], sums[rt]);
-            }
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const h8 vf = vfrag[buf][((hf * NG + g) * 4 + i) * 64 + lane];
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) o[rt][g][i] = mfma(vf, pf[rt], o[rt][g][i]);
-                }
-        }
-    };
-
-    // one page in LDS being worked on, the next one in registers or on its way;
-    // what is staged behind the last is never used
-    if (t0 >= 0) {
-        stage(t0, 0);
-        t1 = next();
-        load();
-    }
-    for (int buf = 0; t0 >= 0; buf ^= 1) {
-        __syncthreads();   // the page is whole, and everyone is done with the other buffer
-        const int t2 = next();
-        f4 s[RT][4];
-        scores(buf, s);
-        stage(t1, buf ^ 1);
-        load();
-        if (t0 <= pos_last) weigh(t0, buf, s);
-        t0 = t1;
-        t1 = t2;
-    }
-
-    // ---- everything of a row is scaled by 2^(kUp - m)
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t r = wave_row + 16 * rt + n;
-        if (r >= t.rows) continue;
-        const int64_t line = line_of(a, t, r, kv_head, G);
-        float *part = part_of<D>(a, split, line);
-        const float l = sums[rt][0], inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int ch = 64 * g + 16 * quad + 4 * e;
-                const float4 w = make_float4(o[rt][g][0][e], o[rt][g][1][e], o[rt][g][2][e],
-                                             o[rt][g][3][e]);
-                if (sh.shared) *reinterpret_cast<float4 *>(part + ch) = w;
-                else store_out<true>(a.out, line * D + ch, w, inv);
-            }
-        if (a.splits > 1 && quad == 0) {
-            part[D] = m[rt];
-            part[D + 1] = sh.shared ? l : kFinal;
         }
     }
 }
@@ -1033,14 +751,14 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
 template <int D, bool BF16>
 void launch_d(Attn4Args a, hipStream_t st) {
     const int64_t G = a.heads / a.c.kv_heads;
-    constexpr int kRt = BF16 ? 1 : prompt_rt(D);
-    const int rows = !a.prompt ? 16 : BF16 ? Prompt<D>::kRows : 16 * kRt;
-    const int64_t tiles = a.N * G / rows + a.c.n_seqs;
+    constexpr int kRt = D <= 128 ? 2 : 1, kWide = D <= 128 ? 8 : 4;
+    const int64_t tiles = a.N * G / (16 * (a.prompt ? kRt : 1)) + a.c.n_seqs;
     a.tiles = (uint32_t)tiles;
-    const dim3 grid((unsigned)(tiles * a.c.kv_heads * a.splits)), block(64 * kWaves);
-    if (!a.prompt) hipLaunchKernelGGL((attn4_kernel<D, BF16, 1>), grid, block, 0, st, a);
-    else if (BF16) hipLaunchKernelGGL(attn4_prompt_kernel<D>, grid, block, 0, st, a);
-    else hipLaunchKernelGGL((attn4_kernel<D, false, kRt>), grid, block, 0, st, a);
+    const dim3 grid((unsigned)(tiles * a.c.kv_heads * a.splits));
+    if (a.prompt) hipLaunchKernelGGL((attn4_kernel<D, BF16, kRt, 4>), grid, dim3(256), 0, st, a);
+    else if (a.wide)
+        hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, kWide>), grid, dim3(64 * kWide), 0, st, a);
+    else hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 4>), grid, dim3(256), 0, st, a);
     if (a.splits > 1) {
         // few rows with many splits: whole workgroups of 1024 to a row
         const int64_t lines = a.N * a.heads;
@@ -1055,25 +773,29 @@ void launch_d(Attn4Args a, hipStream_t st) {
 
 }  // namespace
 
-Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t max_kv,
-                     int64_t window, int64_t sinks) {
-    // Prompts go where a sequence has kPromptFrom rows on average.  Chunks of
-    // pages, so that a batch's workgroups are alike however its lengths differ:
-    // enough of them for kWanted workgroups, each at least one page for every wave
-    // (prompts: kPromptChunk pages, since a workgroup has its rows to prepare).
+Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
+                     int64_t max_kv, int64_t window, int64_t sinks) {
+    // Two fragments of rows where one would make kPromptFrom workgroups: three
+    // prompts of 2048, 16 heads, 93 -> 84 us; below that its fewer workgroups lose
+    // (one prompt of 512: 8 us with one, 10 with two).
     const int64_t rows = N * (heads / kv_heads);
-    const bool prompt = rows >= kPromptFrom * n_seqs;
-    const int64_t tile = prompt ? 32 : 16, least = prompt ? kPromptChunk : kWaves;
+    const bool prompt = dim <= 128 && rows / 16 * kv_heads >= kPromptFrom;
+    const int64_t tile = prompt ? 32 : 16;
     const int64_t groups = (rows / tile + n_seqs) * kv_heads;
     int64_t pages = (max_kv + kPage - 1) / kPage;
     if (window > 0)   // what a tile's rows can see of it: the window before each, the sinks
         pages = std::min(pages, (window + tile) / kPage + 2 + (sinks + kPage - 1) / kPage);
+    // A workgroup to a compute unit and two pages to a wave: splitting costs more
+    // than it saves.
+    if (dim <= 128 && groups <= 256 && pages <= 16) return Attn4Plan{0, 1, 1, 16};
+    // Chunks of pages, so that a batch's workgroups are alike however its lengths
+    // differ: enough of them for kWanted workgroups, each a page for every wave.
     int64_t s = (kWanted + groups - 1) / groups;
     if (s > kMaxSplits) s = kMaxSplits;
     int64_t chunk = (pages + s - 1) / s;
-    chunk = chunk < least ? least : (chunk + kWaves - 1) / kWaves * kWaves;
+    chunk = chunk < 4 ? 4 : (chunk + 3) / 4 * 4;
     s = (pages + chunk - 1) / chunk;
-    return Attn4Plan{prompt ? 1 : 0, s < 1 ? 1 : (int)s, (int)chunk};
+    return Attn4Plan{prompt ? 1 : 0, 0, s < 1 ? 1 : (int)s, (int)chunk};
 }
 
 hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st) {

@@ -331,16 +331,16 @@ struct Attn4Args {
     float *part;           // per split, row: dim accumulators, then maximum and sum
     int64_t q_stride, N;
     float scale_log2;      // softmax scale times log2(e)
-    int heads, prompt, splits, chunk, window, sinks;
+    int heads, prompt, wide, splits, chunk, window, sinks;
     uint32_t tiles;        // set by the launch
 };
 // Which kernel a call's sizes take, how many workgroups share the pages of one
 // row tile, and how many pages each takes (the last one the rest).
 struct Attn4Plan {
-    int prompt, splits, chunk;
+    int prompt, wide, splits, chunk;
 };
-Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t max_kv,
-                     int64_t window, int64_t sinks);
+Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
+                     int64_t max_kv, int64_t window, int64_t sinks);
 hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st);
 
 // One-time weight conversion (AbsMean ternariser, sign/threshold packer).
