@@ -229,8 +229,8 @@ __device__ __forceinline__ float *part_of(const Attn4Args &a, int split, int64_t
 template <int D>
 __device__ __forceinline__ void write_nothing(const Attn4Args &a, const Tile &t, const Share &s,
                                               int kv_head, uint32_t G, int split, uint32_t rows) {
-    const uint32_t r = t.row0 + threadIdx.x;
-    if (s.shared && threadIdx.x < rows && r < t.rows)
+    const uint32_t lane = threadIdx.x & 63, r = t.row0 + lane;
+    if (s.shared && lane < rows && r < t.rows)
         part_of<D>(a, split, line_of(a, t, r, kv_head, G))[D + 1] = 0.0f;
 }
 
@@ -283,15 +283,15 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
     }
 }
 
-// A workgroup has 16 * RT rows, 16 to each of RT fragments, and its WAVES waves
-// take turns at their pages.  RT is 2 for prompts of many rows, which shares what a
-// page's codes cost to unpack; eight waves serve a single short history, which is
-// then not split.
+// A tile has 16 * RT rows, 16 to each of RT fragments; TURNS waves take turns at
+// its pages, and a workgroup has WAVES / TURNS tiles.  RT is 2 for prompts of many
+// rows, which shares what a page's codes cost to unpack; eight waves serve a single
+// short history, which is then not split.
 constexpr int least_waves(int dim, int rt, bool bf16, int waves) {   // to a SIMD, without spills
     return dim == 256 ? 1 : waves == 4 && dim * rt * (bf16 ? 1 : 2) <= 128 ? 3 : 2;
 }
 
-template <int D, bool BF16, int RT, int WAVES>
+template <int D, bool BF16, int RT, int WAVES, int TURNS>
 __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void attn4_kernel(
     const Attn4Args a) {
     using L = Kv4Page<D>;
@@ -314,15 +314,24 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     const int kv_head = (int)(blockIdx.x - x * a.c.kv_heads);
     const uint32_t tile = x / (uint32_t)a.splits;
     const int split = (int)(x - tile * a.splits);
-    const Tile t = find_tile<ROWS>(a, a.tiles - 1 - tile, G);
-    if (t.rows == 0) return;   // the whole workgroup
-    const Share sh = share_of(a, t, split);
-    if (sh.begin == sh.end && split > 0) {
-        write_nothing<D>(a, t, sh, kv_head, G, split, ROWS);
-        return;
+    constexpr int TEAMS = WAVES / TURNS;
+    const int team = wave / TURNS, turn = wave % TURNS;
+    Tile t = find_tile<ROWS>(a, a.tiles - 1 - (tile * TEAMS + team), G);
+    Share sh = share_of(a, t, split);
+    if constexpr (TEAMS == 1) {   // the whole workgroup leaves
+        if (t.rows == 0) return;
+        if (sh.begin == sh.end && split > 0) {
+            if (turn == 0) write_nothing<D>(a, t, sh, kv_head, G, split, ROWS);
+            return;
+        }
+    } else if (t.rows == 0) {   // a team without rows stays for the barrier
+        t.token0 = 0;
+        t.row0 = 0;
+        sh = Share{0, 0, false};
     }
+    const uint32_t last_row = t.rows > 0 ? t.rows - 1 : 0;
 
-    // ---- the pages of this split, every WAVES-th to this wave.  64 table entries
+    // ---- the pages of this split, every TURNS-th to this wave.  64 table entries
     // at a time, one a lane, with a bit for each page that is there; they are
     // waited for before the pages, so that no wait of the loop takes in a page that
     // is on its way.  For the same reason a page is always loaded, at the end the
@@ -332,10 +341,10 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     auto page_at = [&](int i) { return i < t.sink_pages ? i : t.first + i - t.sink_pages; };
     const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
     const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
-    int from = sh.begin + wave, ids = -1, id = 0, at_bit = 0;
+    int from = sh.begin + turn, ids = -1, id = 0, at_bit = 0;
     uint64_t there = 0;
     auto load_ids = [&]() {
-        const int mine = from + WAVES * lane;
+        const int mine = from + TURNS * lane;
         ids = mine < sh.end ? table[page_at(mine)] : -1;
         there = __ballot(ids >= 0 && ids < a.c.n_pages);
     };
@@ -343,15 +352,15 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     const uint8_t *rec = cache;
     auto next = [&]() {
         while (there == 0) {
-            if (from >= sh.end - 64 * WAVES) return -1;
-            from += 64 * WAVES;
+            if (from >= sh.end - 64 * TURNS) return -1;
+            from += 64 * TURNS;
             load_ids();
         }
         at_bit = __builtin_ctzll(there);
         there &= there - 1;
         id = __builtin_amdgcn_readlane(ids, at_bit);
         rec = cache + id * page_bytes;
-        return page_at(from + WAVES * at_bit) * kPage;
+        return page_at(from + TURNS * at_bit) * kPage;
     };
     // codes of the quarters that come next, and this lane's share of a page's pairs
     uint32_t raw_k[SUBS][D / 32], raw_v[SUBS][D / 32], raw_m[D / 32];
@@ -381,7 +390,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     float qs[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t row = min(t.row0 + 16 * rt + n, t.rows - 1), tok = row / G;
+        const uint32_t row = min(t.row0 + 16 * rt + n, last_row), tok = row / G;
         pos[rt] = t.pos0 + (int)tok;
         low[rt] = a.window > 0 ? pos[rt] - a.window + 1 : 0;   // may be negative
         load_query<D, BF16, BF16>(a, t.token0 + (int)tok, kv_head * (int)G + (int)(row - tok * G),
@@ -389,7 +398,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     }
     const int pos_first = t.pos0 + (int)(t.row0 / G);
     const int low_last = a.window > 0
-                             ? t.pos0 + (int)((min(t.row0 + ROWS, t.rows) - 1) / G) - a.window + 1
+                             ? t.pos0 + (int)(min(t.row0 + ROWS - 1, last_row) / G) - a.window + 1
                              : 0;
 
     // What is carried along the pages.  The weights p are 2^(x - m + 7), where m
@@ -631,7 +640,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
                     o[rt][g][i][e] = fmaf(o[rt][g][i][e], i & 1 ? up1 : up, rest);
         }
     }
-    // ---- join the waves: each takes every WAVES-th four of a lane's channels
+    // ---- join the waves: each takes every TURNS-th four of a lane's channels
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         if (quad == 0) {
@@ -650,30 +659,32 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     for (int rt = 0; rt < RT; ++rt) {
         const int rr = 16 * rt + n;
         if (t.row0 + rr >= t.rows) continue;
-        float top = m_all[0][rr], f[WAVES];
+        const int first = team * TURNS;
+        float top = m_all[first][rr], f[TURNS];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) top = fmaxf(top, m_all[w][rr]);
+        for (int w = 1; w < TURNS; ++w) top = fmaxf(top, m_all[first + w][rr]);
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(m_all[w][rr] - top);
-            sum = fmaf(f[w], l_all[w][rr], sum);
+        for (int w = 0; w < TURNS; ++w) {
+            f[w] = __builtin_amdgcn_exp2f(m_all[first + w][rr] - top);
+            sum = fmaf(f[w], l_all[first + w][rr], sum);
         }
         const int64_t line = line_of(a, t, t.row0 + rr, kv_head, G);
         float *part = part_of<D>(a, split, line);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-        for (int u = 0; u < (4 * NG + WAVES - 1) / WAVES; ++u) {
-            const int it = wave + u * WAVES;
-            if (4 * NG % WAVES != 0 && it >= 4 * NG) continue;
+        for (int u = 0; u < (4 * NG + TURNS - 1) / TURNS; ++u) {
+            const int it = turn + u * TURNS;
+            if (4 * NG % TURNS != 0 && it >= 4 * NG) continue;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) add_part(acc, f[w], o_all[w][rt * NG * 4 + it][lane]);
+            for (int w = 0; w < TURNS; ++w)
+                add_part(acc, f[w], o_all[first + w][rt * NG * 4 + it][lane]);
             const int ch = 64 * (it >> 2) + 16 * quad + 4 * (it & 3);
             if (sh.shared) *reinterpret_cast<float4 *>(part + ch) = acc;
             else store_out<BF16>(a.out, line * D + ch, acc, inv);
         }
-        if (a.splits > 1 && wave == 0 && quad == 0) {
+        if (a.splits > 1 && turn == 0 && quad == 0) {
             part[D] = top;
             part[D + 1] = sh.shared ? sum : kFinal;
         }
@@ -751,14 +762,24 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
 template <int D, bool BF16>
 void launch_d(Attn4Args a, hipStream_t st) {
     const int64_t G = a.heads / a.c.kv_heads;
-    constexpr int kRt = D <= 128 ? 2 : 1, kWide = D <= 128 ? 8 : 4;
-    const int64_t tiles = a.N * G / (16 * (a.prompt ? kRt : 1)) + a.c.n_seqs;
-    a.tiles = (uint32_t)tiles;
-    const dim3 grid((unsigned)(tiles * a.c.kv_heads * a.splits));
-    if (a.prompt) hipLaunchKernelGGL((attn4_kernel<D, BF16, kRt, 4>), grid, dim3(256), 0, st, a);
-    else if (a.wide)
-        hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, kWide>), grid, dim3(64 * kWide), 0, st, a);
-    else hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 4>), grid, dim3(256), 0, st, a);
+    const int64_t rows = a.N * G, per = a.c.kv_heads * a.splits;
+    if constexpr (D <= 128) {
+        if (a.prompt) {   // two tiles of 32 rows to a workgroup; those behind the last have none
+            a.tiles = (uint32_t)((rows / 32 + a.c.n_seqs + 1) / 2 * 2);
+            hipLaunchKernelGGL((attn4_kernel<D, BF16, 2, 4, 2>), dim3((unsigned)(a.tiles / 2 * per)),
+                               dim3(256), 0, st, a);
+            return;
+        }
+    }
+    a.tiles = (uint32_t)(rows / 16 + a.c.n_seqs);
+    const dim3 grid((unsigned)(a.tiles * per));
+    if constexpr (D <= 128) {
+        if (a.wide) {
+            hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 8, 8>), grid, dim3(512), 0, st, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 4, 4>), grid, dim3(256), 0, st, a);
     if (a.splits > 1) {
         // few rows with many splits: whole workgroups of 1024 to a row
         const int64_t lines = a.N * a.heads;
@@ -775,16 +796,15 @@ void launch_d(Attn4Args a, hipStream_t st) {
 
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
                      int64_t max_kv, int64_t window, int64_t sinks) {
-    // Two fragments of rows where one would make kPromptFrom workgroups: three
-    // prompts of 2048, 16 heads, 93 -> 84 us; below that its fewer workgroups lose
-    // (one prompt of 512: 8 us with one, 10 with two).
+    // Two fragments of rows where one would make kPromptFrom workgroups (three
+    // prompts of 2048, 16 heads: 92 -> 81 us; one prompt of 512 8 us with one, 10
+    // with two).  There are then enough workgroups without any split.
     const int64_t rows = N * (heads / kv_heads);
-    const bool prompt = dim <= 128 && rows / 16 * kv_heads >= kPromptFrom;
-    const int64_t tile = prompt ? 32 : 16;
-    const int64_t groups = (rows / tile + n_seqs) * kv_heads;
+    if (dim <= 128 && rows / 16 * kv_heads >= kPromptFrom) return Attn4Plan{1, 0, 1, 1 << 24};
+    const int64_t groups = (rows / 16 + n_seqs) * kv_heads;
     int64_t pages = (max_kv + kPage - 1) / kPage;
     if (window > 0)   // what a tile's rows can see of it: the window before each, the sinks
-        pages = std::min(pages, (window + tile) / kPage + 2 + (sinks + kPage - 1) / kPage);
+        pages = std::min(pages, (window + 16) / kPage + 2 + (sinks + kPage - 1) / kPage);
     // A workgroup to a compute unit and two pages to a wave: splitting costs more
     // than it saves.
     if (dim <= 128 && groups <= 256 && pages <= 16) return Attn4Plan{0, 1, 1, 16};
@@ -795,7 +815,7 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     int64_t chunk = (pages + s - 1) / s;
     chunk = chunk < 4 ? 4 : (chunk + 3) / 4 * 4;
     s = (pages + chunk - 1) / chunk;
-    return Attn4Plan{prompt ? 1 : 0, 0, s < 1 ? 1 : (int)s, (int)chunk};
+    return Attn4Plan{0, 0, s < 1 ? 1 : (int)s, (int)chunk};
 }
 
 hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st) {

@@ -167,9 +167,9 @@ def read(cache, table, kv_len, q_start, n, d):
     return out
 
 
-def attention(q, cache, table, kv_len, q_start, scale, window=0, sinks=0, half=False):
+def attention(q, cache, table, kv_len, q_start, scale, window=0, sinks=0, half=False, only=None):
     """-> (out binary64 [N][heads][d], bound on what the kernel may be off by); NaN
-    in rows of no sequence.  The bound is six standard deviations of roundings taken as
+    in rows of no sequence, and in those that `only` (a set of (row, head)) leaves out.  The bound is six standard deviations of roundings taken as
     independent, each at its largest, and the bf16 result's half step, 2^-8 of it:
 
     * weight t is off, relatively, by e_t, with e_t^2 the sum of
@@ -191,11 +191,15 @@ def attention(q, cache, table, kv_len, q_start, scale, window=0, sinks=0, half=F
         for g in range(kvh):
             k, v, there, mag, kmag = history(cache, table[b], held, g, d)
             for r, pos in rows:
+                if only is not None and not any((r, h) in only for h in range(g * heads // kvh, (g + 1) * heads // kvh)):
+                    continue
                 j = np.arange(held)
                 see = there & (j <= pos)
                 if window:
                     see &= (j > pos - window) | (j < sinks)
                 for h in range(g * heads // kvh, (g + 1) * heads // kvh):
+                    if only is not None and (r, h) not in only:
+                        continue
                     if not see.any():
                         out[r, h] = 0
                         tol[r, h] = 0
