@@ -643,3 +643,34 @@ def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window=
     if need < 0:
         raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
     return need
+
+
+def _matmuls(tokens, mats):
+    """y of every (packed, w_scale) in ``mats`` for fp32 / bf16 tokens [N][K] or
+    quantised ones (xq, s, xsum)."""
+    if not isinstance(tokens, tuple):
+        return [y for _, y in linear(tokens, mats, want_dot=False)[0]]
+    group = gemv_group if tokens[0].shape[0] <= GEMV_MAX_N else gemm_group
+    return [y for _, y in group(mats, *tokens, want_dot=False)]
+
+
+def attn_block(tokens, q, k, v, o, cache, table, kv_len, q_start, gamma=None, eps=1e-5, rotary=None,
+               window=0, sinks=0, max_kv=None):
+    """The attention block on I2_S weights and a 4-bit cache: q, k and v projections
+    (one grouped launch) -> keys and values appended to the cache -> attention over
+    it -> RMS sub-norm (gain gamma or 1) and int8 tokens -> the o projection.
+
+    tokens: fp32 / bf16 [N][hidden], or quantised as block_norm_quant gives them.
+    q, k, v, o: (packed, w_scale) pairs; head_dim and the kv heads are the cache's.
+    rotary: called with q [N][n_heads][head_dim] and k [N][n_kv_heads][head_dim]
+    (fp32), returns them with their positions applied.  The rest as in attn_kv4.
+    Returns y [N][hidden] fp32, the block's output for the next block_norm_quant."""
+    yq, yk, yv = _matmuls(tokens, [q, k, v])
+    N, kv_heads, dim = yq.shape[0], cache.shape[1], cache.shape[2] // 72
+    qh, kh, vh = yq.view(N, -1, dim), yk.view(N, kv_heads, dim), yv.view(N, kv_heads, dim)
+    if rotary is not None:
+        qh, kh = rotary(qh, kh)
+    kv4_append(cache, table, kv_len, q_start, kh, vh)
+    a = attn_kv4(qh, cache, table, kv_len, q_start, window=window, sinks=sinks, max_kv=max_kv)
+    _, _, inner = block_norm_quant(a.view(N, -1), gamma=gamma, eps=eps)
+    return _matmuls(inner, [o])[0]

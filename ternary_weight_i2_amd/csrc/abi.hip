@@ -626,12 +626,15 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
     if (workspace_bytes < need)
         return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
                     (long long)workspace_bytes, (long long)need);
+    // positions stay below 2^30, so no window or sink beyond says more
+    const int far = 1 << 30, win = (int)(window < far ? window : far);
+    const int first = (int)(sinks < far ? sinks : far);
     const bitnet::Attn4Plan sp =
         bitnet::attn4_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads, batch->head_dim, max_kv,
                            window, sinks);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
                               scale * 1.4426950408889634f, (int)n_heads, sp.prompt,
-                              sp.wide, sp.splits, sp.chunk, (int)window, (int)sinks, 0};
+                              sp.wide, sp.splits, sp.chunk, win, first, 0};
     hipError_t e = bitnet::launch_attn4(a, dtype == BITNET_BF16, (int)batch->head_dim,
                                         static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);

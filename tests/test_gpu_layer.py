@@ -327,6 +327,43 @@ def test_window_and_sinks(bn, window, sinks, dtype):
                window, sinks)
 
 
+def test_window_and_sinks_of_any_size(bn):
+    s = Seqs([200, 65], [3, 1], 1, 64, seed=13, fill=0xFF).fill()
+    top = 2 ** 31 - 1
+    for window, sinks in ((top, 0), (top, top), (64, top), (1, top)):
+        check_attn(bn, s, 2, window=window, sinks=sinks)
+
+
+def test_offsets_beyond_32_bits(bn):
+    """A cache of over 4 GiB, its last pages in use."""
+    s = Seqs([150, 70], [150, 2], 8, 256, seed=32, spare=0)
+    far = 2 ** 32 // (8 * 72 * 256) + 1 - 2
+    cache = torch.empty((far + s.n_pages, 8, 72 * 256), dtype=torch.uint8, device="cuda")
+    cache[far:] = dev(s.cache)
+    rest = [dev(np.where(s.table >= 0, s.table + far, -1)), dev(s.kv_len), dev(s.q_start)]
+    k, v = s.rows(s.n), s.rows(s.n)
+    bn.kv4_append(cache, *rest, dev(k), dev(v))
+    lo.append(s.cache, s.table, s.kv_len, s.q_start, k, v)
+    assert torch.equal(cache[far:], dev(s.cache))
+    assert torch.equal(bn.kv4_read(cache, *rest, s.n)[0], bn.kv4_read(*s.dev(), s.n)[0])
+    q = dev(s.rng.standard_normal((s.n, 8, 256)).astype(np.float32))
+    assert torch.equal(bn.attn_kv4(q, cache, *rest), bn.attn_kv4(q, *s.dev()))
+
+
+def test_workspace_given(bn):
+    s = Seqs([3000, 10], [1, 1], 1, 64, seed=33, fill=0xFF).fill(every=range(0, 3000, 7))
+    s.cache[s.cache == 0xFF] = 0
+    q = dev(s.rng.standard_normal((2, 2, 64)).astype(np.float32))
+    need = bn.attn_kv4_workspace(2, 2, 2, 1, 64, 64 * s.table.shape[1])
+    assert need > 0
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    want = bn.attn_kv4(q, *s.dev())
+    assert torch.equal(bn.attn_kv4(q, *s.dev(), workspace=ws[:need]), want)
+    assert (ws[need:] == 255).all()
+    with pytest.raises(ValueError, match="workspace"):
+        bn.attn_kv4(q, *s.dev(), workspace=ws[:need - 1])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_rows_that_see_nothing_and_absent_pages(bn, dtype):
     # more rows than tokens, a sequence without any, pages that are not there: the
@@ -455,6 +492,64 @@ def test_two_streams_at_once(bn):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(want[i], g) for g in got[i])
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("n_new,quantised", [([1, 1], True), ([1, 1], False), ([40, 30], True),
+                                             ([3, 2], False)])
+def test_a_layer_step(bn, n_new, quantised):
+    """Boundary, attention block, boundary, matmul, as a layer runs them: 2 kv heads and 8
+    query heads of 64 channels on ternary weights, histories already in the cache.  The block
+    is the chain of its calls bit for bit, and every stage is what the oracle makes of the
+    stage before."""
+    rng = np.random.default_rng(40 + len(n_new) + n_new[0])
+    hidden, d, kvh, heads = 256, 64, 2, 8
+    old = [90, 30]
+    s = Seqs([a + b for a, b in zip(old, n_new)], n_new, kvh, d, seed=41, fill=0xFF)
+    s.kv_len[:] = old
+    keep, s.q_start = s.q_start, np.array([0, *np.cumsum(old)], np.int32)
+    k0, v0 = s.rows(sum(old)), s.rows(sum(old))
+    lo.append(s.cache, s.table, s.kv_len, s.q_start, k0, v0)
+    s.kv_len, s.q_start = np.array([a + b for a, b in zip(old, n_new)], np.int32), keep
+    N = s.n
+    mats = {}
+    for name, m, kk in (("q", heads * d, hidden), ("k", kvh * d, hidden), ("v", kvh * d, hidden),
+                        ("o", hidden, heads * d), ("up", 512, hidden)):
+        w = rng.integers(-1, 2, (m, kk)).astype(np.int8)
+        mats[name] = (bn.pack(dev(w)), 0.05)
+    b, r = (dev(rng.standard_normal((N, hidden)).astype(np.float32)) for _ in range(2))
+    gamma = dev((1 + 0.2 * rng.standard_normal(hidden)).astype(np.float32))
+    sub = dev((1 + 0.2 * rng.standard_normal(heads * d)).astype(np.float32))
+    turn = lambda q, k: (q * 0.5, k.flip(2))  # noqa: E731  (any map of q and k)
+
+    h, v, tokens = bn.block_norm_quant(b, r, gamma=gamma, want_v=True)
+    x = tokens if quantised else v
+    c, *rest = s.dev()
+    y = bn.attn_block(x, *(mats[m] for m in "qkvo"), c, *rest, gamma=sub, rotary=turn, window=64, sinks=2)
+    # the same calls one by one
+    c2 = dev(s.cache)
+    (_, yq), (_, yk), (_, yv) = (bn.gemv_group if N <= 64 else bn.gemm_group)(
+        [mats[m] for m in "qkv"], *tokens)
+    qh, kh = turn(yq.view(N, heads, d), yk.view(N, kvh, d))
+    bn.kv4_append(c2, *rest, kh, yv.view(N, kvh, d))
+    a = bn.attn_kv4(qh, c2, *rest, window=64, sinks=2)
+    _, _, inner = bn.block_norm_quant(a.view(N, -1), gamma=sub)
+    y2 = (bn.gemv if N <= 64 else bn.gemm)(*mats["o"], *inner)[1]
+    assert torch.equal(c, c2) and torch.equal(y, y2)
+    # and each against the oracle
+    lo.append(s.cache, s.table, s.kv_len, s.q_start, host(kh), host(yv).reshape(N, kvh, d))
+    assert np.array_equal(c.cpu().numpy(), s.cache)
+    want, tol = lo.attention(host(qh), s.cache, s.table, s.kv_len, s.q_start, d ** -0.5, 64, 2)
+    assert (np.abs(host(a) - want) <= tol).all()
+    _, _, xq, xs, xsum = lo.block_norm(host(a).reshape(N, -1), gamma=host(sub))
+    assert np.array_equal(inner[0].cpu().numpy(), xq) and np.array_equal(host(inner[1]), xs)
+    h2, _, t2 = bn.block_norm_quant(y, h, post_norm=True, scale=0.3)
+    wh, _, wq, _, wsum = lo.block_norm(host(y), host(h), post=True, scale=0.3)
+    assert np.array_equal(host(h2), wh) and np.array_equal(t2[0].cpu().numpy(), wq)
+    assert np.array_equal(t2[2].cpu().numpy(), wsum)
+    up = (bn.gemv_group if N <= 64 else bn.gemm_group)([mats["up"]], *t2)[0][1]
+    assert torch.isfinite(up).all()
 
 
 def test_nothing_to_do(bn):
