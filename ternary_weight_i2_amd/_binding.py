@@ -502,10 +502,11 @@ def block_norm_quant(b, res=None, post_norm=False, post_gamma=None, gate=None, s
     gate_rows = gate is not None and gate.dim() != 1
     if out is None:
         h = torch.empty_like(res) if res is not None else None
-        v = torch.empty(shape, dtype=stream, device=dev) if want_v else None
-        q = (torch.empty(shape, dtype=torch.int8, device=dev),
-             torch.empty(N, dtype=f32, device=dev),
-             torch.empty(N, dtype=torch.int32, device=dev)) if want_q else None
+        v = torch.empty_like(b, dtype=stream) if want_v else None
+        q = None
+        if want_q:
+            xs = torch.empty(N, dtype=f32, device=dev)
+            q = (torch.empty_like(b, dtype=torch.int8), xs, torch.empty_like(xs, dtype=torch.int32))
     else:
         h, v, q = out
         if h is not None and res is None:

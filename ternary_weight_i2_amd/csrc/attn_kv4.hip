@@ -251,7 +251,9 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[j][e]));
     top = quad_max(top);
     // q times 2^k: the largest is in [2^14, 2^15) (a row of numbers below 2^-111
-    // stays smaller); the sums of q times 2^(k - 11): the largest they can be is 2^10
+    // stays smaller).  The sums of q: with raw codes times 2^(k - 24), the product's
+    // own scale (to 2^-25, 2^-16 of the largest q); else times 2^(k - 11), the
+    // largest they can be being 2^10, and scaled after their product.
     const int k = top > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(top), 126) : 0;
     const float up = ldexpf(1.0f, k), up16 = up * 0.0625f;
     qs = fmaxf(ldexpf(a.scale_log2, (RAW ? 24 : 0) - k), 1.2e-38f);
@@ -268,8 +270,7 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
                 const _Float16 hi = (_Float16)z;
                 qf[0][j][e] = hi;
                 if constexpr (!BF16) qf[1][j][e] = (_Float16)(z - (float)hi);
-                // up * 2^-11 first: a sum of 64 numbers below the largest fp32
-                sum = fmaf(v[j][ch], up * 0x1p-11f, sum);
+                sum = fmaf(v[j][ch], up * (RAW ? 0x1p-24f : 0x1p-11f), sum);
             }
         sum = quad_sum(sum);
         // -8 (raw codes) and 1 times the sum, its upper term in the first 8 of 32
@@ -408,6 +409,8 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     // group g, 2 g + 1 its middles, 2 NG + 1 ones.
     float m[RT];
     int E = -14;                 // every step so far is below 2^E
+    const bool steps_here = lane >= 32 && (D > 64 || !(lane & 1));   // see raw_m below
+    _Float16 down = steps_here ? pow2_f16(14) : (_Float16)1.0f;      // 2^-E for the steps
     f4 o[RT][NG][4], sums[RT];   // o[..][g][i][e]: channel 64 g + 16 quad + 4 e + i
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -442,20 +445,22 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
             }
         }
         // the largest step: lanes 32 on hold four steps, then four middles, and so on
-        const bool steps_here = lane >= 32 && (D > 64 || !(lane & 1));
         uint32_t smax = 0;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
             if (D == 64 || !(w & 2)) smax = max(smax, max(raw_m[w] & 0xffffu, raw_m[w] >> 16));
-        const int E_new = max(E, (wave_max_u16(steps_here ? (int)smax : 0) >> 10) - 14);
+        int E_new = E;
+        if (__any(steps_here && (int)smax >= (E + 15) << 10)) {
+            E_new = (wave_max_u16(steps_here ? (int)smax : 0) >> 10) - 14;
+            down = steps_here ? pow2_f16(-E_new) : (_Float16)1.0f;
+        }
         {
-            const _Float16 f = steps_here ? pow2_f16(-E_new) : (_Float16)1.0f;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int w = 0; w < D / 32; ++w)
                 pairs[lane * (D / 32) + w] =
-                    D == 64 || !(w & 2) ? __builtin_bit_cast(uint32_t, as_h2(raw_m[w]) * f)
+                    D == 64 || !(w & 2) ? __builtin_bit_cast(uint32_t, as_h2(raw_m[w]) * down)
                                         : raw_m[w];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -498,7 +503,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
                 const f4 rest = mfma(pf, cf[rt], f4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[rt][i4][e] = rest[e] * (BF16 ? 0x1p-13f : 0x1p11f);
+                    s[rt][i4][e] = BF16 ? rest[e] : rest[e] * 0x1p11f;
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
                         s[rt][i4][e] =
@@ -534,14 +539,13 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
         // ---- p
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            float top = -INFINITY;
+            float top = -INFINITY;   // of this lane's tokens: the row's only where it matters
 #pragma unroll
             for (int i4 = 0; i4 < SUBS; ++i4)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, s[rt][i4][e]);
-            top = quad_max(top) * qs[rt];
-            if (E_new > E || __any(top > m[rt] + kBehind)) {
-                const float m_new = fmaxf(m[rt], top);
+            if (E_new > E || __any(top * qs[rt] > m[rt] + kBehind)) {
+                const float m_new = fmaxf(m[rt], quad_max(top) * qs[rt]);
                 const float f = __builtin_amdgcn_exp2f(m[rt] - m_new), fs = ldexpf(f, E - E_new);
                 sums[rt][0] *= fs;
                 sums[rt][1] *= f;
@@ -810,7 +814,8 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     if (dim <= 128 && groups <= 256 && pages <= 16) return Attn4Plan{0, 1, 1, 16};
     // Chunks of pages, so that a batch's workgroups are alike however its lengths
     // differ: enough of them for kWanted workgroups, each a page for every wave.
-    int64_t s = (kWanted + groups - 1) / groups;
+    const int64_t wanted = dim == 256 ? kWanted / 2 : kWanted;   // one or two to a compute unit
+    int64_t s = (wanted + groups - 1) / groups;
     if (s > kMaxSplits) s = kMaxSplits;
     int64_t chunk = (pages + s - 1) / s;
     chunk = chunk < 4 ? 4 : (chunk + 3) / 4 * 4;
