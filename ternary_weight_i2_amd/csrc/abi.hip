@@ -9,6 +9,7 @@
 
 #include "bitnet_i2s.h"
 #include "common.h"
+#include "layer.h"
 
 #define BITNET_API extern "C" __attribute__((visibility("default")))
 

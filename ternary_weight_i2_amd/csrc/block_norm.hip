@@ -19,7 +19,7 @@
 // HBM for long prompts and the chain of loads and workgroup reductions (two
 // sums, one maximum, one sum of codes) for single tokens.  The workgroup's
 // width depends on F alone, so a token's result does not depend on N.
-#include "common.h"
+#include "layer.h"
 
 namespace bitnet {
 

@@ -66,6 +66,28 @@ __device__ __forceinline__ void window_totals(const FfnShared &sh, U128 *tot, ui
     *tot_cnt = D[4];
 }
 
+__device__ __forceinline__ double wave_sum_f64(double v) {   // exact here: integer multiples below 2^53
+    uint64_t b;
+    __builtin_memcpy(&b, &v, 8);
+    auto add = [&](uint64_t o) {
+        double x, y;
+        __builtin_memcpy(&x, &b, 8);
+        __builtin_memcpy(&y, &o, 8);
+        x += y;
+        __builtin_memcpy(&b, &x, 8);
+    };
+    add(dpp_u64<kDppXor1>(b));
+    add(dpp_u64<kDppXor2>(b));
+    add(dpp_u64<kDppHalfMirror>(b));
+    add(dpp_u64<kDppMirror>(b));
+    add(dpp_rows_u64<kDppRowBcast15, 0xA>(b));   // the rows a move skips add +0
+    add(dpp_rows_u64<kDppRowBcast31, 0xC>(b));
+    b = readlane63_u64(b);
+    double r;
+    __builtin_memcpy(&r, &b, 8);
+    return r;
+}
+
 // Level 1 of the window on the FP64 units (exact_sum.h, window_add_f64):
 // this thread's three bin sums and count.
 __device__ __forceinline__ void window_pass_f64(const float4 *hl, int nq, int b, Bins3 *acc,

@@ -25,7 +25,7 @@
 // code - 8 costs one packed fp16 addition.
 #pragma once
 
-#include "common.h"
+#include "layer.h"
 
 namespace bitnet {
 
