@@ -473,7 +473,6 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
         float s[RT][SUBS][4];
 #pragma unroll
         for (int i4 = 0; i4 < SUBS; ++i4) {
-            __builtin_amdgcn_sched_barrier(0);   // unpack one quarter at a time: registers
             h8 pf = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -592,7 +591,6 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
                                     sums[rt]);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                __builtin_amdgcn_sched_barrier(0);
                 h2 ps[RT][NT][4], c[4][4];   // p * step, and the codes [two tokens][channel]
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {

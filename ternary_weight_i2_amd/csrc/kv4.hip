@@ -32,7 +32,7 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t *pair) {
     float lo = kKv4Max, hi = -kKv4Max;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        x[e] = fminf(fmaxf(x[e], -kKv4Max), kKv4Max);   // a NaN becomes -kKv4Max
+        x[e] = __builtin_amdgcn_fmed3f(x[e], -kKv4Max, kKv4Max);   // a NaN becomes -kKv4Max
         lo = fminf(lo, x[e]);
         hi = fmaxf(hi, x[e]);
     }
@@ -43,12 +43,16 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t *pair) {
     const _Float16 step16 = (_Float16)fmaxf((hi - mid) * (1.0f / 7.0f), (mid - lo) * 0.125f);
     const float step = (float)step16;
     const float inv = step > 0.0f ? 1.0f / step : 0.0f;
-    uint32_t codes = 0;
+    // Adding 1.5 * 2^23 rounds the held value to an integer, half to even, and
+    // leaves it in the low bits above a constant; the constants of all eight are
+    // taken off at once.
+    constexpr uint32_t kMagic = 0x4b400000u;
+    uint32_t codes = 0u - kMagic * 0x11111111u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float t = (x[e] - mid) * inv;
-        const float c = fminf(fmaxf(rintf(t + 8.0f), 0.0f), 15.0f);
-        codes |= (uint32_t)c << (4 * e);
+        const float c = __builtin_amdgcn_fmed3f(t + 8.0f, 0.0f, 15.0f) + 12582912.0f;
+        codes += __float_as_uint(c) << (4 * e);
     }
     *pair = (uint32_t)__builtin_bit_cast(uint16_t, step16) |
             (uint32_t)__builtin_bit_cast(uint16_t, mid16) << 16;
