@@ -649,9 +649,12 @@ def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window=
 def _matmuls(tokens, mats):
     """y of every (packed, w_scale) in ``mats`` for fp32 / bf16 tokens [N][K] or
     quantised ones (xq, s, xsum)."""
+    x = tokens[0] if isinstance(tokens, tuple) else tokens
+    if x.shape[0] == 0:     # nothing to multiply, and empty tensors have no address
+        return [y for _, y in _mats_out(mats, 0, x.shape[1], x.device, False, True, None)]
     if not isinstance(tokens, tuple):
         return [y for _, y in linear(tokens, mats, want_dot=False)[0]]
-    group = gemv_group if tokens[0].shape[0] <= GEMV_MAX_N else gemm_group
+    group = gemv_group if x.shape[0] <= GEMV_MAX_N else gemm_group
     return [y for _, y in group(mats, *tokens, want_dot=False)]
 
 
@@ -668,10 +671,11 @@ def attn_block(tokens, q, k, v, o, cache, table, kv_len, q_start, gamma=None, ep
     Returns y [N][hidden] fp32, the block's output for the next block_norm_quant."""
     yq, yk, yv = _matmuls(tokens, [q, k, v])
     N, kv_heads, dim = yq.shape[0], cache.shape[1], cache.shape[2] // 72
-    qh, kh, vh = yq.view(N, -1, dim), yk.view(N, kv_heads, dim), yv.view(N, kv_heads, dim)
+    qh = yq.view(N, yq.shape[1] // dim, dim)
+    kh, vh = yk.view(N, kv_heads, dim), yv.view(N, kv_heads, dim)
     if rotary is not None:
         qh, kh = rotary(qh, kh)
     kv4_append(cache, table, kv_len, q_start, kh, vh)
     a = attn_kv4(qh, cache, table, kv_len, q_start, window=window, sinks=sinks, max_kv=max_kv)
-    _, _, inner = block_norm_quant(a.view(N, -1), gamma=gamma, eps=eps)
+    _, _, inner = block_norm_quant(a.view(yq.shape), gamma=gamma, eps=eps)
     return _matmuls(inner, [o])[0]

@@ -633,10 +633,13 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
     const bitnet::Attn4Plan sp =
         bitnet::attn4_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads, batch->head_dim, max_kv,
                            window, sinks);
+    if (sp.workgroups >= 1 << 24)   // of 256 threads: a launch has fewer than 2^32
+        return fail(BITNET_E_SHAPE, "%s: N=%lld, n_seqs=%lld are too many rows for one call", fn,
+                    (long long)N, (long long)batch->n_seqs);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
-                              scale * 1.4426950408889634f, (int)n_heads, sp.prompt,
-                              sp.wide, sp.splits, sp.chunk, win, first, 0};
-    hipError_t e = bitnet::launch_attn4(a, dtype == BITNET_BF16, (int)batch->head_dim,
+                              scale * 1.4426950408889634f, (int)n_heads, win, first, sp.splits,
+                              sp.chunk, (uint32_t)sp.tiles};
+    hipError_t e = bitnet::launch_attn4(a, sp, dtype == BITNET_BF16, (int)batch->head_dim,
                                         static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);
     return ok();

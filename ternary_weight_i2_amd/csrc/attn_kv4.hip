@@ -43,7 +43,7 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWanted = 512;       // workgroups that a launch is split into
 constexpr int kMaxSplits = 256;
-constexpr int kPromptFrom = 2048;
+constexpr int kPromptFrom = 2048, kPromptRows = 128;   // see attn4_plan
 constexpr int kJoinThreads = 1024;
 constexpr float kBehind = 8.0f, kUp = 7.0f;   // see attn4_kernel
 constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
@@ -165,10 +165,8 @@ __device__ __forceinline__ Tile find_tile(const Attn4Args &a, uint32_t x, uint32
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
-    static_assert(N == 1 || N == 2 || N == 4 || N == 8, "4, 8, 16 or 32 bytes");
-    if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else if constexpr (N == 2) {
+    static_assert(N == 2 || N == 4 || N == 8, "8, 16 or 32 bytes");
+    if constexpr (N == 2) {
         const uint2 a = *reinterpret_cast<const uint2 *>(p);
         w[0] = a.x; w[1] = a.y;
     } else {
@@ -762,32 +760,25 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
 }
 
 template <int D, bool BF16>
-void launch_d(Attn4Args a, hipStream_t st) {
-    const int64_t G = a.heads / a.c.kv_heads;
-    const int64_t rows = a.N * G, per = a.c.kv_heads * a.splits;
+void launch_d(const Attn4Args &a, const Attn4Plan &plan, hipStream_t st) {
+    const dim3 grid((unsigned)plan.workgroups);
     if constexpr (D <= 128) {
-        if (a.prompt) {   // two tiles of 32 rows to a workgroup; those behind the last have none
-            a.tiles = (uint32_t)((rows / 32 + a.c.n_seqs + 1) / 2 * 2);
-            hipLaunchKernelGGL((attn4_kernel<D, BF16, 2, 4, 2>), dim3((unsigned)(a.tiles / 2 * per)),
-                               dim3(256), 0, st, a);
+        if (plan.prompt) {
+            hipLaunchKernelGGL((attn4_kernel<D, BF16, 2, 4, 2>), grid, dim3(256), 0, st, a);
             return;
         }
-    }
-    a.tiles = (uint32_t)(rows / 16 + a.c.n_seqs);
-    const dim3 grid((unsigned)(a.tiles * per));
-    if constexpr (D <= 128) {
-        if (a.wide) {
+        if (plan.wide) {
             hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 8, 8>), grid, dim3(512), 0, st, a);
             return;
         }
     }
     hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 4, 4>), grid, dim3(256), 0, st, a);
-    if (a.splits > 1) {
+    if (plan.splits > 1) {
         // few rows with many splits: whole workgroups of 1024 to a row
         const int64_t lines = a.N * a.heads;
-        const int threads = a.splits > 16 ? kJoinThreads : 256, slots = threads / (D / 4);
+        const int threads = plan.splits > 16 ? kJoinThreads : 256, slots = threads / (D / 4);
         int par = 1;
-        while (par < slots && 2 * par < a.splits) par *= 2;
+        while (par < slots && 2 * par < plan.splits) par *= 2;
         const int64_t per = slots / par;
         hipLaunchKernelGGL((attn4_join_kernel<D, BF16>),
                            dim3((unsigned)((lines + per - 1) / per)), dim3(threads), 0, st, a, par);
@@ -796,20 +787,28 @@ void launch_d(Attn4Args a, hipStream_t st) {
 
 }  // namespace
 
+// Measured on the times of calls in a graph.
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
                      int64_t max_kv, int64_t window, int64_t sinks) {
-    // Two fragments of rows where one would make kPromptFrom workgroups (three
-    // prompts of 2048, 16 heads: 92 -> 81 us; one prompt of 512 8 us with one, 10
-    // with two).  There are then enough workgroups without any split.
     const int64_t rows = N * (heads / kv_heads);
-    if (dim <= 128 && rows / 16 * kv_heads >= kPromptFrom) return Attn4Plan{1, 0, 1, 1 << 24};
-    const int64_t groups = (rows / 16 + n_seqs) * kv_heads;
+    // Two fragments of rows, two tiles to a workgroup (those behind the last have
+    // no rows), where one fragment would make kPromptFrom workgroups (three prompts
+    // of 2048, 16 heads: 92 -> 81 us; one prompt of 512: 8 us with one, 10 with
+    // two) and sequences have kPromptRows rows on average, so that tiles are full
+    // (512 sequences of 8 rows at 1000 tokens: 89 us with one, 119 with two; of
+    // 128 rows 57 and 60 us either way round; 50 of 512 rows: 123 and 108).  There
+    // are then enough workgroups without any split.
+    if (dim <= 128 && rows / 16 * kv_heads >= kPromptFrom && rows >= kPromptRows * n_seqs) {
+        const int64_t tiles = (rows / 32 + n_seqs + 1) / 2 * 2;
+        return Attn4Plan{1, 0, 1, 1 << 24, tiles, tiles / 2 * kv_heads};
+    }
+    const int64_t tiles = rows / 16 + n_seqs, groups = tiles * kv_heads;
     int64_t pages = (max_kv + kPage - 1) / kPage;
     if (window > 0)   // what a tile's rows can see of it: the window before each, the sinks
         pages = std::min(pages, (window + 16) / kPage + 2 + (sinks + kPage - 1) / kPage);
     // A workgroup to a compute unit and two pages to a wave: splitting costs more
     // than it saves.
-    if (dim <= 128 && groups <= 256 && pages <= 16) return Attn4Plan{0, 1, 1, 16};
+    if (dim <= 128 && groups <= 256 && pages <= 16) return Attn4Plan{0, 1, 1, 16, tiles, groups};
     // Chunks of pages, so that a batch's workgroups are alike however its lengths
     // differ: enough of them for kWanted workgroups, each a page for every wave.
     const int64_t wanted = dim == 256 ? kWanted / 2 : kWanted;   // one or two to a compute unit
@@ -818,13 +817,14 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     int64_t chunk = (pages + s - 1) / s;
     chunk = chunk < 4 ? 4 : (chunk + 3) / 4 * 4;
     s = (pages + chunk - 1) / chunk;
-    return Attn4Plan{0, 0, s < 1 ? 1 : (int)s, (int)chunk};
+    s = s < 1 ? 1 : s;
+    return Attn4Plan{0, 0, (int)s, (int)chunk, tiles, groups * s};
 }
 
-hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st) {
-    if (dim == 64) { if (bf16) launch_d<64, true>(a, st); else launch_d<64, false>(a, st); }
-    else if (dim == 128) { if (bf16) launch_d<128, true>(a, st); else launch_d<128, false>(a, st); }
-    else { if (bf16) launch_d<256, true>(a, st); else launch_d<256, false>(a, st); }
+hipError_t launch_attn4(const Attn4Args &a, const Attn4Plan &p, int bf16, int dim, hipStream_t st) {
+    if (dim == 64) { if (bf16) launch_d<64, true>(a, p, st); else launch_d<64, false>(a, p, st); }
+    else if (dim == 128) { if (bf16) launch_d<128, true>(a, p, st); else launch_d<128, false>(a, p, st); }
+    else { if (bf16) launch_d<256, true>(a, p, st); else launch_d<256, false>(a, p, st); }
     return hipGetLastError();
 }
 

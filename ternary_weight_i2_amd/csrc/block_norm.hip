@@ -19,6 +19,8 @@
 // HBM for long prompts and the chain of loads and workgroup reductions (two
 // sums, one maximum, one sum of codes) for single tokens.  The workgroup's
 // width depends on F alone, so a token's result does not depend on N.
+#include <algorithm>
+
 #include "layer.h"
 
 namespace bitnet {
@@ -208,10 +210,33 @@ hipError_t launch_block_norm(const BlockNormArgs &a, int64_t N, int b_bf16, int 
     const int pieces = a.F >> 3;
     const int r = pieces <= 512 ? 1 : pieces <= 1024 ? 2 : 4;
     const int threads = ((pieces + r - 1) / r + 63) / 64 * 64;
-    if (r == 1) launch_r<1>(a, N, threads, b_bf16, s_bf16, st);
-    else if (r == 2) launch_r<2>(a, N, threads, b_bf16, s_bf16, st);
-    else launch_r<4>(a, N, threads, b_bf16, s_bf16, st);
-    return hipGetLastError();
+    // a launch has fewer than 2^32 threads: 2^21 tokens at a time
+    constexpr int64_t kTokens = 1 << 21;
+    for (int64_t n0 = 0; n0 < N; n0 += kTokens) {
+        const int64_t n = std::min(N - n0, kTokens), at = n0 * a.F;
+        auto rows = [&](auto *p, int bytes) {
+            using T = decltype(p);
+            return p ? (T)((uintptr_t)p + (uintptr_t)(at * bytes)) : p;
+        };
+        BlockNormArgs c = a;
+        const int sb = s_bf16 ? 2 : 4;
+        c.b = rows(a.b, b_bf16 ? 2 : 4);
+        c.res = rows(a.res, sb);
+        c.h = rows(a.h, sb);
+        c.v = rows(a.v, sb);
+        c.xq = rows(a.xq, 1);
+        if (a.gate) c.gate = a.gate + n0 * a.gate_stride;
+        if (a.xq) {
+            c.xs = a.xs + n0;
+            c.xsum = a.xsum + n0;
+        }
+        if (r == 1) launch_r<1>(c, n, threads, b_bf16, s_bf16, st);
+        else if (r == 2) launch_r<2>(c, n, threads, b_bf16, s_bf16, st);
+        else launch_r<4>(c, n, threads, b_bf16, s_bf16, st);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace bitnet

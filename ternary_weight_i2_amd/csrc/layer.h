@@ -92,16 +92,19 @@ struct Attn4Args {
     float *part;           // per split, row: dim accumulators, then maximum and sum
     int64_t q_stride, N;
     float scale_log2;      // softmax scale times log2(e)
-    int heads, prompt, wide, splits, chunk, window, sinks;
-    uint32_t tiles;        // set by the launch
+    int heads, window, sinks, splits, chunk;   // the last two and `tiles`: Attn4Plan
+    uint32_t tiles;
 };
 // Which kernel a call's sizes take, how many workgroups share the pages of one
-// row tile, and how many pages each takes (the last one the rest).
+// row tile, how many pages each takes (the last one the rest), the tiles of a kv
+// head and the workgroups of all.
 struct Attn4Plan {
     int prompt, wide, splits, chunk;
+    int64_t tiles, workgroups;
 };
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
                      int64_t max_kv, int64_t window, int64_t sinks);
-hipError_t launch_attn4(const Attn4Args &a, int bf16, int dim, hipStream_t st);
+hipError_t launch_attn4(const Attn4Args &a, const Attn4Plan &plan, int bf16, int dim,
+                        hipStream_t st);
 
 }  // namespace bitnet

@@ -92,6 +92,21 @@ def test_boundary_feeds_the_matmul_and_any_batch_gives_the_same(bn):
         assert torch.equal(qi[0], q[i]) and si[0] == s[i] and ti[0] == t[i]
 
 
+def test_boundary_of_more_tokens_than_a_launch_takes(bn):
+    """Over 2^21 tokens are several launches: the last tokens, and those on both sides of the
+    cut, as a call of their own gives them."""
+    N, F = 2 ** 21 + 5, 128
+    g = torch.Generator(device="cuda").manual_seed(4)
+    b, r = (torch.randn((N, F), generator=g, device="cuda").to(BF16) for _ in range(2))
+    gate = torch.rand((N, F), generator=g, device="cuda")
+    h, v, (q, s, t) = bn.block_norm_quant(b, r, gate=gate, want_v=True)
+    for first in (0, 2 ** 21 - 4, N - 8):
+        c = slice(first, first + 8)
+        h1, v1, (q1, s1, t1) = bn.block_norm_quant(b[c], r[c], gate=gate[c], want_v=True)
+        for x, y in ((h, h1), (v, v1), (q, q1), (s, s1), (t, t1)):
+            assert torch.equal(x[c], y)
+
+
 # ---------------------------------------------------------------- cache
 
 class Seqs:
@@ -317,6 +332,14 @@ def test_many_sequences(bn, n_seqs):
     want = lo.read(s.cache, s.table, s.kv_len, s.q_start, s.n, 64)
     for got, w in zip(bn.kv4_read(c, *rest, s.n), want):
         assert np.array_equal(host(got), w)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_large_batch_of_single_tokens(bn, dtype):
+    """Enough rows for a prompt's kernel, but few to each sequence."""
+    rng = np.random.default_rng(34)
+    check_attn(bn, Seqs(rng.integers(1, 30, 300), [1] * 300, 2, 64, seed=34, fill=0xFF).fill(), 128,
+               dtype, sample=800)
 
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (5, 1), (64, 4), (65, 64), (100, 70), (64, 300),
@@ -563,4 +586,7 @@ def test_nothing_to_do(bn):
     h, _, (q, _, _) = bn.block_norm_quant(torch.empty((0, 128), device="cuda"),
                                           torch.empty((0, 128), device="cuda"))
     assert h.shape == (0, 128) and q.shape == (0, 128)
+    wide, mat = ((bn.pack(torch.ones((m, 128), dtype=torch.int8, device="cuda")), 1.0) for m in (128, 64))
+    y = bn.attn_block(torch.empty((0, 128), device="cuda"), wide, mat, mat, wide, c, table, kv_len, q_start)
+    assert y.shape == (0, 128)
     assert np.array_equal(c.cpu().numpy(), s.cache)

@@ -118,6 +118,9 @@ def test_attention_validation(L):
     assert f(L, _batch(), ws=MIS) == E_ALIGN
     for bad in (255, 258, 0):
         assert f(L, _batch(), qs=bad) == E_SHAPE
+    # more workgroups than a launch takes
+    assert f(L, _batch(n_kv_heads=16, n_seqs=1 << 20), heads=16, N=1 << 20, qs=1024) == E_SHAPE
+    assert "too many" in L.bitnet_last_error().decode()
     # a long history is shared by several workgroups, which takes a workspace
     need = L.bitnet_attn_kv4_workspace(2, 3, 4, 2, 64, 64 * 100, 0, 0)
     assert need > 0
