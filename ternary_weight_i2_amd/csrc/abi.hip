@@ -3,6 +3,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <mutex>
 #include <string>
@@ -595,8 +596,10 @@ BITNET_API int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t 
     }
     g_last_error.clear();
     if (n_seqs == 0 || N == 0) return 0;
-    const int64_t splits =
-        bitnet::attn4_plan(n_seqs, N, n_heads, n_kv_heads, head_dim, max_kv, window, sinks).splits;
+    int64_t splits = 1;   // the larger of the two types
+    for (bool bf16 : {false, true})
+        splits = std::max<int64_t>(splits, bitnet::attn4_plan(n_seqs, N, n_heads, n_kv_heads, head_dim,
+                                                              max_kv, window, sinks, bf16).splits);
     return splits > 1 ? splits * N * n_heads * (head_dim + 4) * 4 : 0;
 }
 
@@ -632,7 +635,7 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
     const int first = (int)(sinks < far ? sinks : far);
     const bitnet::Attn4Plan sp =
         bitnet::attn4_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads, batch->head_dim, max_kv,
-                           window, sinks);
+                           window, sinks, dtype == BITNET_BF16);
     if (sp.workgroups >= 1 << 24)   // of 256 threads: a launch has fewer than 2^32
         return fail(BITNET_E_SHAPE, "%s: N=%lld, n_seqs=%lld are too many rows for one call", fn,
                     (long long)N, (long long)batch->n_seqs);

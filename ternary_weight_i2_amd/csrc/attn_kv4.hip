@@ -789,7 +789,7 @@ void launch_d(const Attn4Args &a, const Attn4Plan &plan, hipStream_t st) {
 
 // Measured on the times of calls in a graph.
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
-                     int64_t max_kv, int64_t window, int64_t sinks) {
+                     int64_t max_kv, int64_t window, int64_t sinks, bool bf16) {
     const int64_t rows = N * (heads / kv_heads);
     // Two fragments of rows, two tiles to a workgroup (those behind the last have
     // no rows), where one fragment would make kPromptFrom workgroups (three prompts
@@ -806,9 +806,12 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     int64_t pages = (max_kv + kPage - 1) / kPage;
     if (window > 0)   // what a tile's rows can see of it: the window before each, the sinks
         pages = std::min(pages, (window + 16) / kPage + 2 + (sinks + kPage - 1) / kPage);
-    // A workgroup to a compute unit and two pages to a wave: splitting costs more
-    // than it saves.
-    if (dim <= 128 && groups <= 256 && pages <= 16) return Attn4Plan{0, 1, 1, 16, tiles, groups};
+    // A workgroup to a compute unit and a few pages to a wave: splitting costs more
+    // than it saves (20/5 heads of 128, one token: fp32 9.4 us whole and 9.9 split at
+    // 12 pages, 11.7 and 9.9 at 13; bf16 8.7 and 9.2 at 18, 10.2 and 9.1 at 21).
+    const int64_t whole = bf16 ? 20 : 12;
+    if (dim <= 128 && groups <= 256 && pages <= whole)
+        return Attn4Plan{0, 1, 1, (int)whole, tiles, groups};
     // Chunks of pages, so that a batch's workgroups are alike however its lengths
     // differ: enough of them for kWanted workgroups, each a page for every wave.
     const int64_t wanted = dim == 256 ? kWanted / 2 : kWanted;   // one or two to a compute unit

@@ -103,7 +103,7 @@ struct Attn4Plan {
     int64_t tiles, workgroups;
 };
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
-                     int64_t max_kv, int64_t window, int64_t sinks);
+                     int64_t max_kv, int64_t window, int64_t sinks, bool bf16);
 hipError_t launch_attn4(const Attn4Args &a, const Attn4Plan &plan, int bf16, int dim,
                         hipStream_t st);
 
