@@ -41,7 +41,7 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWanted = 512;       // workgroups that a launch is split into
+constexpr int kUnits = 256;        // compute units
 constexpr int kMaxSplits = 256;
 constexpr int kPromptFrom = 2048, kPromptRows = 128;   // see attn4_plan
 constexpr int kJoinThreads = 1024;
@@ -286,12 +286,19 @@ __device__ __forceinline__ void load_query(const Attn4Args &a, int token, int he
 // its pages, and a workgroup has WAVES / TURNS tiles.  RT is 2 for prompts of many
 // rows, which shares what a page's codes cost to unpack; eight waves serve a single
 // short history, which is then not split.
-constexpr int least_waves(int dim, int rt, bool bf16, int waves) {   // to a SIMD, without spills
-    return dim == 256 ? 1 : waves == 4 && dim * rt * (bf16 ? 1 : 2) <= 128 ? 3 : 2;
+constexpr int least_waves(int dim, int rt, int waves) {   // to a SIMD
+    return waves == 4 && dim * rt <= 128 ? 3 : 2;
+}
+// Whether a tile's query lies in LDS (where the waves' results meet later) instead
+// of registers, so that a SIMD holds that many waves without spills: rows of 256
+// channels 2 in place of 1 (two prompts of 2048, 16/4 heads, bf16: 185 -> 110 us),
+// fp32 rows of 128 3 in place of 2 (one of 512, 20/5 heads: 18 -> 14 us).
+constexpr bool query_in_lds(int dim, bool bf16, int waves) {
+    return dim == 256 || (dim == 128 && !bf16 && waves == 4);
 }
 
 template <int D, bool BF16, int RT, int WAVES, int TURNS>
-__global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void attn4_kernel(
+__global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_kernel(
     const Attn4Args a) {
     using L = Kv4Page<D>;
     constexpr int NG = L::kGroups, NS = L::kSteps, NT = BF16 ? 1 : 2, ROWS = 16 * RT;
@@ -314,7 +321,8 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
     const uint32_t tile = x / (uint32_t)a.splits;
     const int split = (int)(x - tile * a.splits);
     constexpr int TEAMS = WAVES / TURNS;
-    const int team = wave / TURNS, turn = wave % TURNS;
+    // the waves that have a page more than the others are not the same of all splits
+    const int team = wave / TURNS, turn = (wave + split) % TURNS;
     Tile t = find_tile<ROWS>(a, a.tiles - 1 - (tile * TEAMS + team), G);
     Share sh = share_of(a, t, split);
     if constexpr (TEAMS == 1) {   // the whole workgroup leaves
@@ -394,6 +402,18 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
         low[rt] = a.window > 0 ? pos[rt] - a.window + 1 : 0;   // may be negative
         load_query<D, BF16, BF16>(a, t.token0 + (int)tok, kv_head * (int)G + (int)(row - tok * G),
                                   quad, qf[rt], cf[rt], qs[rt]);
+    }
+    constexpr bool kQueryInLds = query_in_lds(D, BF16, WAVES);
+    h8 *const q_lds = reinterpret_cast<h8 *>(o_all) + team * RT * NT * NS * 64 + lane;
+    if constexpr (kQueryInLds) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int n2 = 0; n2 < NT; ++n2)
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    if (j % TURNS == turn) q_lds[((rt * NT + n2) * NS + j) * 64] = qf[rt][n2][j];
+        __syncthreads();
     }
     const int pos_first = t.pos0 + (int)(t.row0 / G);
     const int low_last = a.window > 0
@@ -492,7 +512,9 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
 #pragma unroll
                         for (int n2 = 0; n2 < NT; ++n2)
                             acc[rt][g] =
-                                mfma(join(c[0], c[1], c[2], c[3]), qf[rt][n2][j], acc[rt][g]);
+                                mfma(join(c[0], c[1], c[2], c[3]),
+                                     kQueryInLds ? q_lds[((rt * NT + n2) * NS + j) * 64] : qf[rt][n2][j],
+                                     acc[rt][g]);
                 }
             }
 #pragma unroll
@@ -640,6 +662,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, BF16, WAVES)) void a
                     o[rt][g][i][e] = fmaf(o[rt][g][i][e], i & 1 ? up1 : up, rest);
         }
     }
+    if constexpr (kQueryInLds) __syncthreads();   // all queries read
     // ---- join the waves: each takes every TURNS-th four of a lane's channels
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -759,6 +782,13 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
     if (mine) store_out<BF16>(a.out, line * D + ch, acc, sum > 0.0f ? 1.0f / sum : 0.0f);
 }
 
+// LDS that leaves `per_cu` workgroups of four waves to a compute unit (0: as many as fit).
+template <int D>
+int spare_lds(int per_cu) {
+    constexpr int kLds = 160 * 1024, kOwn = 4 * (8 * D + 64 * D + 8 + 128);
+    return per_cu ? std::max(0, kLds / (per_cu + 1) + 1024 - kOwn) : 0;
+}
+
 template <int D, bool BF16>
 void launch_d(const Attn4Args &a, const Attn4Plan &plan, hipStream_t st) {
     const dim3 grid((unsigned)plan.workgroups);
@@ -772,7 +802,8 @@ void launch_d(const Attn4Args &a, const Attn4Plan &plan, hipStream_t st) {
             return;
         }
     }
-    hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 4, 4>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attn4_kernel<D, BF16, 1, 4, 4>), grid, dim3(256),
+                       spare_lds<D>(plan.per_cu), st, a);
     if (plan.splits > 1) {
         // few rows with many splits: whole workgroups of 1024 to a row
         const int64_t lines = a.N * a.heads;
@@ -800,7 +831,7 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     // are then enough workgroups without any split.
     if (dim <= 128 && rows / 16 * kv_heads >= kPromptFrom && rows >= kPromptRows * n_seqs) {
         const int64_t tiles = (rows / 32 + n_seqs + 1) / 2 * 2;
-        return Attn4Plan{1, 0, 1, 1 << 24, tiles, tiles / 2 * kv_heads};
+        return Attn4Plan{1, 0, 1, 1 << 24, 0, tiles, tiles / 2 * kv_heads};
     }
     const int64_t tiles = rows / 16 + n_seqs, groups = tiles * kv_heads;
     int64_t pages = (max_kv + kPage - 1) / kPage;
@@ -811,17 +842,26 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     // 12 pages, 11.7 and 9.9 at 13; bf16 8.7 and 9.2 at 18, 10.2 and 9.1 at 21).
     const int64_t whole = bf16 ? 20 : 12;
     if (dim <= 128 && groups <= 256 && pages <= whole)
-        return Attn4Plan{0, 1, 1, (int)whole, tiles, groups};
+        return Attn4Plan{0, 1, 1, (int)whole, 0, tiles, groups};
     // Chunks of pages, so that a batch's workgroups are alike however its lengths
-    // differ: enough of them for kWanted workgroups, each a page for every wave.
-    const int64_t wanted = dim == 256 ? kWanted / 2 : kWanted;   // one or two to a compute unit
-    int64_t s = (wanted + groups - 1) / groups;
-    if (s > kMaxSplits) s = kMaxSplits;
-    int64_t chunk = (pages + s - 1) / s;
-    chunk = chunk < 4 ? 4 : (chunk + 3) / 4 * 4;
-    s = (pages + chunk - 1) / chunk;
-    s = s < 1 ? 1 : s;
-    return Attn4Plan{0, 0, (int)s, (int)chunk, tiles, groups * s};
+    // differ, for all the workgroups with rows (of sequences of one length) that run
+    // at once, but none beyond: 32 sequences of 2000 tokens, 32/8 heads of 64 20.6 us
+    // at four to a compute unit and 18.3 at three; 8 of 4000, heads of 128, fp32 18.0
+    // at two, 21.1 at three.  A short chunk is a page for every wave or several.
+    const int64_t tall = (std::max<int64_t>(rows / n_seqs, 1) + 15) / 16;
+    const int64_t busy = std::min(n_seqs, N) * tall * kv_heads;
+    const int64_t at_once = kUnits * (dim == 64 ? 3 : dim == 256 && bf16 ? 1 : 2);
+    int64_t s = std::min<int64_t>(std::max<int64_t>(at_once / busy, 1), kMaxSplits);
+    int64_t chunk = std::max<int64_t>((pages + s - 1) / s, 4);
+    if (chunk < 16) chunk = (chunk + 3) / 4 * 4;
+    s = std::max<int64_t>((pages + chunk - 1) / chunk, 1);
+    // Up to two to a compute unit are kept at two: where three fit, the workgroups
+    // without rows between them let some units take three and others one (64
+    // sequences of 2000 tokens, 32/8 heads of 128, fp32 37.9 -> 32.2 us).  Whole
+    // bf16 histories are bound by HBM and want the third (64 of 4095, 64/8 heads:
+    // 43.3 us, held to two 49.9).
+    const bool hold = dim == 128 && busy * s <= 2 * kUnits && (s > 1 || !bf16);
+    return Attn4Plan{0, 0, (int)s, (int)chunk, hold ? 2 : 0, tiles, groups * s};
 }
 
 hipError_t launch_attn4(const Attn4Args &a, const Attn4Plan &p, int bf16, int dim, hipStream_t st) {

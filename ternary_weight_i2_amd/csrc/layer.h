@@ -96,10 +96,10 @@ struct Attn4Args {
     uint32_t tiles;
 };
 // Which kernel a call's sizes take, how many workgroups share the pages of one
-// row tile, how many pages each takes (the last one the rest), the tiles of a kv
-// head and the workgroups of all.
+// row tile, how many pages each takes (the last one the rest), how many may be on
+// a compute unit at once (0: any), the tiles of a kv head and the workgroups of all.
 struct Attn4Plan {
-    int prompt, wide, splits, chunk;
+    int prompt, wide, splits, chunk, per_cu;
     int64_t tiles, workgroups;
 };
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
