@@ -29,6 +29,17 @@
 // with 16 tokens of one row: that is exactly the fragment that the second
 // product (channels x rows) takes, so p never crosses lanes, and the running
 // maximum and the accumulators of a row all live in the same lanes.
+//
+// What bounds it.  A long history of few rows: HBM with bf16 rows (64 sequences of
+// up to 4096 tokens, 64/8 heads of 128: 175 MB in 40 us, 4.4 TB/s; a large copy
+// reaches 4.8), the vector operations with fp32 rows (131072 tokens, 20/5 heads: 94
+// MB in 25 us, and 5 us for the join): a page of 128 channels costs a wave about 600
+// of them (350 in bf16 calls) and 72 (38) matrix instructions, however many of its 16
+// rows are real; the unpacking is the largest part.  Prompts: the vector operations
+// again, of which 32 rows a wave share the unpacking (three of 2048 tokens, 16/8
+// heads of 128, bf16: 36 GF in 72 us, 500 TF).  Short histories: the chain of
+// dependent loads (lengths, table, page), a page or two of work and the join of the
+// waves (515 tokens, 20/5 heads, fp32: 9.2 us in a graph, 7 with one page).
 #include <algorithm>
 
 #include "kv4.h"
@@ -716,7 +727,8 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
 
 // Joins the splits of a row: D / 4 lanes to its channels, `par` (a power of
 // two) groups of them to its splits, always added in the same order.  A part
-// without a sum has no accumulators.
+// without a sum has no accumulators.  Bound by latency: 20 rows of 98 splits, 1 MB,
+// take 5 us, of which a launch is about 2.
 template <int D, bool BF16>
 __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Args a, int par) {
     constexpr int kLanes = D / 4, kMaxSlots = kJoinThreads / kLanes;
