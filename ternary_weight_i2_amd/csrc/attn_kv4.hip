@@ -149,17 +149,16 @@ template <int ROWS>
 __device__ __forceinline__ Tile find_tile(const Attn4Args &a, uint32_t x, uint32_t G) {
     Tile t;
     // a sequence has at least as many tiles to itself as its rows need
-    const int lo = sequence_of<ROWS, 1>(a.c.q_start, (int)a.c.n_seqs, G, x);
-    t.seq = lo;
-    const int begin = a.c.q_start[lo], end = a.c.q_start[lo + 1];
-    t.token0 = begin;
-    const bool good = begin >= 0 && end > begin && end <= (int)a.N;
-    t.rows = good ? (uint32_t)(end - begin) * G : 0;
-    const int tile = (int)(x - ((uint32_t)begin * G / ROWS + lo));
+    const SeqAt s = sequence_of<ROWS, 1>(a.c, G, x);
+    t.seq = s.seq;
+    t.token0 = s.begin;
+    const bool good = s.begin >= 0 && s.end > s.begin && s.end <= (int)a.N;
+    t.rows = good ? (uint32_t)(s.end - s.begin) * G : 0;
+    const int tile = (int)(x - ((uint32_t)s.begin * G / ROWS + s.seq));
     if (tile < 0) t.rows = 0;
     t.row0 = (uint32_t)tile * ROWS;
-    t.held = (int)held_tokens(a.c, lo);
-    t.pos0 = t.held - (end - begin);
+    t.held = s.held;
+    t.pos0 = t.held - (s.end - s.begin);
     t.pages = t.first = t.sink_pages = 0;
     if (t.row0 >= t.rows) {
         t.rows = 0;

@@ -45,28 +45,35 @@ struct Kv4Page {
 };
 
 // Tiles of ROWS rows, a sequence's own from start[b] * G / ROWS + SLACK * b on: the
-// sequence of tile x, the largest b for which that is at most x.  64 probes at a
-// time, the same x in every lane; the result is uniform and always in [0, n),
-// whatever start holds.
+// sequence of tile x, the largest b for which that is at most x; its rows [begin,
+// end) as q_start has them, and `held`, the tokens that the cache can hold of it,
+// kv_len held to [0, 64 max_pages].  64 probes at a time, the same x in every lane;
+// the last 64 bring the lengths with them, which saves a round trip.  The result is
+// uniform and seq in [0, n_seqs), whatever the arrays hold.
+struct SeqAt {
+    int seq, begin, end, held;
+};
 template <int ROWS, int SLACK>
-__device__ __forceinline__ int sequence_of(const int32_t *start, int n, uint32_t G, uint32_t x) {
+__device__ __forceinline__ SeqAt sequence_of(const Kv4Args &c, uint32_t G, uint32_t x) {
     const int lane = threadIdx.x & 63;
-    int lo = 0;   // the answer is in [lo, lo + n)
-    while (n > 1) {
+    auto at_most = [&](int b, int begin) { return (uint32_t)begin * G / ROWS + SLACK * b <= x; };
+    int lo = 0, n = (int)c.n_seqs;   // the answer is in [lo, lo + n)
+    while (n > 64) {
         const int step = (n + 63) >> 6, b = lo + lane * step;
-        const bool ok = lane * step < n && (uint32_t)start[b] * G / ROWS + SLACK * b <= x;
+        const bool ok = lane * step < n && at_most(b, c.q_start[b]);
         const int hits = __popcll(__ballot(ok));   // all probes up to the answer's
         const int k = hits > 0 ? hits - 1 : 0;
         lo += k * step;
         n = min(step, n - k * step);
     }
-    return __builtin_amdgcn_readfirstlane(lo);
-}
-
-// Tokens of sequence b that the cache can hold: kv_len held to [0, 64 max_pages].
-__device__ __forceinline__ int64_t held_tokens(const Kv4Args &c, int64_t b) {
-    const int64_t t = c.kv_len[b], most = c.max_pages * kPage;
-    return t < 0 ? 0 : t > most ? most : t;
+    const int b = lo + min(lane, n - 1);
+    const int begin = c.q_start[b], end = c.q_start[b + 1], len = c.kv_len[b];
+    const int hits = __popcll(__ballot(lane < n && at_most(b, begin)));
+    const int k = __builtin_amdgcn_readfirstlane(hits > 0 ? hits - 1 : 0);
+    const int64_t most = c.max_pages * kPage;   // up to 2^30
+    return SeqAt{__builtin_amdgcn_readfirstlane(lo) + k, __builtin_amdgcn_readlane(begin, k),
+                 __builtin_amdgcn_readlane(end, k),
+                 min(max(__builtin_amdgcn_readlane(len, k), 0), (int)most)};
 }
 
 // Whether row r belongs to one of the call's sequences at all.

@@ -64,29 +64,24 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t *pair) {
 
 // The four positions [base, base + 4) of a workgroup, and their rows in the call.
 struct Block4 {
-    int64_t rec;        // record index of kv head 0, or -1 if there is no page
+    int page;           // its entry in the table (or -1): not looked at before a page is
     int in_page;        // of base: a multiple of 4
     int row;            // the call's row at base
     uint32_t rows;      // bit t: the call has a row at base + t
-    uint32_t places;    // bit t: and the cache a place for it
+    __device__ bool cached(const Kv4Args &c) const { return page >= 0 && page < c.n_pages; }
 };
 __device__ __forceinline__ Block4 find_block(const Kv4Args &c, int64_t N) {
-    Block4 k{-1, 0, 0, 0, 0};
-    const int b = sequence_of<4, 2>(c.q_start, (int)c.n_seqs, 1, blockIdx.x);
-    const int first = c.q_start[b], end = c.q_start[b + 1];
-    const int tile = (int)(blockIdx.x - ((uint32_t)first / 4 + 2 * b));
-    if (tile < 0 || first < 0 || end <= first || end > N) return k;
-    const int held = (int)held_tokens(c, b), pos0 = held - (end - first);
-    const int base = (pos0 & ~3) + 4 * tile;
-    k.row = first + base - pos0;
+    Block4 k{-1, 0, 0, 0};
+    const SeqAt s = sequence_of<4, 2>(c, 1, blockIdx.x);
+    const int tile = (int)(blockIdx.x - ((uint32_t)s.begin / 4 + 2 * s.seq));
+    if (tile < 0 || s.begin < 0 || s.end <= s.begin || s.end > N) return k;
+    const int pos0 = s.held - (s.end - s.begin), base = (pos0 & ~3) + 4 * tile;
+    k.row = s.begin + base - pos0;
     for (int t = 0; t < 4; ++t)
-        if (base + t >= pos0 && base + t < held) k.rows |= 1u << t;
+        if (base + t >= pos0 && base + t < s.held) k.rows |= 1u << t;
     if (base < 0 || !k.rows) return k;   // base is a multiple of 4: all four lie before 0
-    const int page = c.table[b * c.max_pages + base / kPage];
-    if (page < 0 || page >= c.n_pages) return k;
-    k.rec = (int64_t)page * c.kv_heads;
+    k.page = c.table[s.seq * c.max_pages + base / kPage];
     k.in_page = base % kPage;
-    k.places = k.rows;
     return k;
 }
 
@@ -95,7 +90,7 @@ __global__ __launch_bounds__(kKvThreads) void kv4_append_kernel(
     const Kv4Args c, const void *k, const void *v, int64_t k_stride, int64_t v_stride, int64_t N) {
     using L = Kv4Page<D>;
     const Block4 at = find_block(c, N);
-    if (!at.places) return;   // the whole workgroup
+    if (!at.rows) return;   // the whole workgroup
     const int lanes = c.kv_heads * 2 * (D / 8), t0 = at.in_page;
     for (int i = threadIdx.x; i < lanes; i += blockDim.x) {   // whole groups of eight lanes
         const int p = i % (D / 8), g = p >> 3, head = i / (D / 8) >> 1;
@@ -105,18 +100,19 @@ __global__ __launch_bounds__(kKvThreads) void kv4_append_kernel(
         float x[4][8];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            if (at.places >> t & 1)
+            if (at.rows >> t & 1)
                 load8<BF16>(src, (at.row + t) * stride + head * D + 8 * p, x[t]);
         uint32_t codes[4], pair[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) codes[t] = quantise8(x[t], &pair[t]);
-        uint8_t *rec = c.cache + (at.rec + head) * (int64_t)L::kBytes;
+        if (!at.cached(c)) return;   // the whole workgroup; the rows are on their way by now
+        uint8_t *rec = c.cache + ((int64_t)at.page * c.kv_heads + head) * L::kBytes;
         if (!is_v) {
             uint32_t *w = reinterpret_cast<uint32_t *>(rec) + t0 * (D / 8) + (p & 3) * L::kSteps + (p >> 2);
             uint32_t *m = reinterpret_cast<uint32_t *>(rec + L::kKeyPairs) + t0 * L::kGroups + g;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                if (!(at.places >> t & 1)) continue;
+                if (!(at.rows >> t & 1)) continue;
                 w[t * (D / 8)] = codes[t];
                 if ((p & 7) == 0) m[t * L::kGroups] = pair[t];
             }
@@ -127,7 +123,7 @@ __global__ __launch_bounds__(kKvThreads) void kv4_append_kernel(
                       ((t0 >> 2) * 16 + 2 * (p & 7)) * L::kGroups * 4 + g * 4;
         uint16_t *m = reinterpret_cast<uint16_t *>(rec + L::kValuePairs) +
                       ((t0 >> 2) * L::kGroups + g) * 8;
-        if (at.places == 15) {
+        if (at.rows == 15) {
             auto low = [](uint32_t a, uint32_t b) { return (a & 0xffffu) | b << 16; };
             auto high = [](uint32_t a, uint32_t b) { return a >> 16 | (b & 0xffff0000u); };
             *reinterpret_cast<uint2 *>(w) = make_uint2(low(codes[0], codes[1]), low(codes[2], codes[3]));
@@ -141,7 +137,7 @@ __global__ __launch_bounds__(kKvThreads) void kv4_append_kernel(
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            if (!(at.places >> t & 1)) continue;
+            if (!(at.rows >> t & 1)) continue;
             w[t] = (uint16_t)codes[t];
             w[4 * L::kGroups + t] = (uint16_t)(codes[t] >> 16);
             if ((p & 7) == 0) {
@@ -166,8 +162,8 @@ __global__ __launch_bounds__(kKvThreads) void kv4_read_kernel(const Kv4Args c, v
         void *out = is_v ? v : k;
         if (!out) continue;
         uint32_t codes[4] = {0, 0, 0, 0}, pair[4] = {0, 0, 0, 0};   // zeros where there is no page
-        if (at.rec >= 0) {
-            const uint8_t *rec = c.cache + (at.rec + head) * (int64_t)L::kBytes;
+        if (at.cached(c)) {
+            const uint8_t *rec = c.cache + ((int64_t)at.page * c.kv_heads + head) * L::kBytes;
             if (!is_v) {
                 const uint32_t *w = reinterpret_cast<const uint32_t *>(rec) + t0 * (D / 8) +
                                     (p & 3) * L::kSteps + (p >> 2);
