@@ -500,27 +500,38 @@ def block_norm_quant(b, res=None, post_norm=False, post_gamma=None, gate=None, s
     if post_gamma is not None and not post_norm:
         raise ValueError("post_gamma without post_norm")
     gate_rows = gate is not None and gate.dim() != 1
-    if out is None:
-        h = torch.empty_like(res) if res is not None else None
-        v = torch.empty_like(b, dtype=stream) if want_v else None
-        q = None
+    if not b.is_contiguous():
+        raise ValueError("b must be contiguous")
+    res_at = _at(res, "res", stream, shape, dev)
+    h = v = q = h_at = v_at = xq_at = xs_at = xsum_at = None
+    if out is None:     # tensors made here need no checks
+        if res is not None:
+            h = torch.empty_like(res)
+            h_at = h.data_ptr()
+        if want_v:
+            v = torch.empty_like(b, dtype=stream)
+            v_at = v.data_ptr()
         if want_q:
             xs = torch.empty(N, dtype=f32, device=dev)
-            q = (torch.empty_like(b, dtype=torch.int8), xs, torch.empty_like(xs, dtype=torch.int32))
+            xq, xsum = torch.empty_like(b, dtype=torch.int8), torch.empty_like(xs, dtype=torch.int32)
+            q = (xq, xs, xsum)
+            xq_at, xs_at, xsum_at = xq.data_ptr(), xs.data_ptr(), xsum.data_ptr()
     else:
         h, v, q = out
         if h is not None and res is None:
             raise ValueError("h without res")
-    xq, xs, xsum = q if q is not None else (None, None, None)
-    if q is not None and (xq is None or xs is None or xsum is None):
-        raise ValueError("xq, x_scale and x_sum come together")
-    _launch(load().bitnet_block_norm_quant_i8, dev, _at(b, "b", b.dtype, shape, dev), bd,
+        h_at, v_at = _at(h, "h", stream, shape, dev), _at(v, "v", stream, shape, dev)
+        if q is not None:
+            xq, xs, xsum = q
+            if xq is None or xs is None or xsum is None:
+                raise ValueError("xq, x_scale and x_sum come together")
+            xq_at, xs_at = _at(xq, "xq", torch.int8, shape, dev), _at(xs, "x_scale", f32, (N,), dev)
+            xsum_at = _at(xsum, "x_sum", torch.int32, (N,), dev)
+    _launch(load().bitnet_block_norm_quant_i8, dev, b.data_ptr(), bd,
             1 if post_norm else 0, _at(post_gamma, "post_gamma", f32, (F,), dev),
             _at(gate, "gate", f32, shape if gate_rows else (F,), dev), F if gate_rows else 0, scale,
-            _at(res, "res", stream, shape, dev), _at(h, "h", stream, shape, dev), sd,
-            _at(gamma, "gamma", f32, (F,), dev), eps, N, F, _at(v, "v", stream, shape, dev),
-            _at(xq, "xq", torch.int8, shape, dev), _at(xs, "x_scale", f32, (N,), dev),
-            _at(xsum, "x_sum", torch.int32, (N,), dev))
+            res_at, h_at, sd, _at(gamma, "gamma", f32, (F,), dev), eps, N, F, v_at, xq_at, xs_at,
+            xsum_at)
     return h, v, q
 
 
@@ -587,14 +598,16 @@ def kv4_read(cache, table, kv_len, q_start, n, dtype=None, out=None):
     dev, shape = cache.device, (n, heads, dim)
     if out is None:
         dtype = dtype or torch.float32
-        out = (torch.empty(shape, dtype=dtype, device=dev),
-               torch.empty(shape, dtype=dtype, device=dev))
-    k, v = out
-    if k is None and v is None:
-        raise ValueError("k and v are both None")
-    dtype = dtype or (k if k is not None else v).dtype
-    _launch(load().bitnet_kv4_read, dev, batch, _at(k, "k", dtype, shape, dev),
-            _at(v, "v", dtype, shape, dev), _float_code(dtype, "out"), n)
+        k = torch.empty(shape, dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+        out, at = (k, v), (k.data_ptr(), v.data_ptr())
+    else:
+        k, v = out
+        if k is None and v is None:
+            raise ValueError("k and v are both None")
+        dtype = dtype or (k if k is not None else v).dtype
+        at = _at(k, "k", dtype, shape, dev), _at(v, "v", dtype, shape, dev)
+    _launch(load().bitnet_kv4_read, dev, batch, *at, _float_code(dtype, "out"), n)
     return out
 
 
@@ -625,6 +638,9 @@ def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, ma
         raise BitnetError(E_SHAPE, L.bitnet_last_error().decode(errors="replace"))
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
+        at = out.data_ptr()
+    else:
+        at = _at(out, "out", dtype, shape, dev)
     if workspace is None:
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -632,7 +648,7 @@ def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, ma
         raise ValueError(f"workspace must be {need} bytes of uint8 on {dev}")
     _launch(L.bitnet_attn_kv4, dev, batch, q.data_ptr(), stride, code, N, heads,
             dim ** -0.5 if scale is None else scale, window, sinks, max_kv,
-            _at(out, "out", dtype, shape, dev), None if workspace is None else _ptr(workspace),
+            at, None if workspace is None else _ptr(workspace),
             0 if workspace is None else workspace.numel())
     return out
 
