@@ -441,6 +441,19 @@ def test_any_expected_length_gives_the_same_attention(bn, dtype):
         s.rng.bit_generator.state = st
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_long_history_among_short_ones(bn, d, dtype):
+    """Chunks of pages of several lengths, fours and others, of which only the long history
+    fills more than one."""
+    rng = np.random.default_rng(35)
+    s = Seqs([*rng.integers(1, 65, 20), 1500, *rng.integers(1, 65, 20)], [1] * 41, 2, d, seed=35,
+             fill=0xFF).fill()
+    s.table = np.concatenate([s.table, np.full((41, 150), -1, np.int32)], 1)
+    for pages in (24, 60, 110, 170):
+        check_attn(bn, s, 4, dtype, max_kv=64 * pages)
+
+
 def test_queries_as_slices_and_out_given(bn):
     s = Seqs([100, 50], [3, 2], 2, 64, seed=20, fill=0xFF).fill()
     y = dev(s.rng.standard_normal((5, 8, 64)).astype(np.float32))
