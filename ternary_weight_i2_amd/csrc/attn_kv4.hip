@@ -805,7 +805,10 @@ void launch_d(const Attn4Args &a, const Attn4Plan &plan, hipStream_t st) {
     const dim3 grid((unsigned)plan.workgroups);
     if constexpr (D <= 128) {
         if (plan.prompt) {
-            hipLaunchKernelGGL((attn4_kernel<D, BF16, 2, 4, 2>), grid, dim3(256), 0, st, a);
+            if (plan.prompt == 2)
+                hipLaunchKernelGGL((attn4_kernel<D, BF16, 2, 4, 2>), grid, dim3(256), 0, st, a);
+            else
+                hipLaunchKernelGGL((attn4_kernel<D, BF16, 2, 4, 4>), grid, dim3(256), 0, st, a);
             return;
         }
         if (plan.wide) {
@@ -832,22 +835,29 @@ void launch_d(const Attn4Args &a, const Attn4Plan &plan, hipStream_t st) {
 // Measured on the times of calls in a graph.
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
                      int64_t max_kv, int64_t window, int64_t sinks, bool bf16) {
-    const int64_t rows = N * (heads / kv_heads);
-    // Two fragments of rows, two tiles to a workgroup (those behind the last have
-    // no rows), where one fragment would make kPromptFrom workgroups (three prompts
-    // of 2048, 16 heads: 92 -> 81 us; one prompt of 512: 8 us with one, 10 with
-    // two) and sequences have kPromptRows rows on average, so that tiles are full
-    // (512 sequences of 8 rows at 1000 tokens: 89 us with one, 119 with two; of
-    // 128 rows 57 and 60 us either way round; 50 of 512 rows: 123 and 108).  There
-    // are then enough workgroups without any split.
-    if (dim <= 128 && rows / 16 * kv_heads >= kPromptFrom && rows >= kPromptRows * n_seqs) {
-        const int64_t tiles = (rows / 32 + n_seqs + 1) / 2 * 2;
-        return Attn4Plan{1, 0, 1, 1 << 24, 0, tiles, tiles / 2 * kv_heads};
-    }
-    const int64_t tiles = rows / 16 + n_seqs, groups = tiles * kv_heads;
+    const int64_t rows = N * (heads / kv_heads), each = rows / 16 * kv_heads;
     int64_t pages = (max_kv + kPage - 1) / kPage;
     if (window > 0)   // what a tile's rows can see of it: the window before each, the sinks
         pages = std::min(pages, (window + 16) / kPage + 2 + (sinks + kPage - 1) / kPage);
+    // Two fragments of rows to a wave, if there are enough workgroups without any
+    // split and sequences have kPromptRows rows on average, so that tiles are full
+    // (512 sequences of 8 rows at 1000 tokens: 89 us with one fragment, 119 with two;
+    // of 128 rows 57 and 60 us either way round; 50 of 512 rows: 123 and 108).
+    // Where one fragment would make kPromptFrom workgroups, two tiles to a workgroup
+    // (those behind the last have no rows): three prompts of 2048, 16/8 heads of 128,
+    // 92 -> 81 us; 700 rows of 32/8 heads from nothing 18 us with one fragment, 21
+    // with two.  Over long histories, where one fragment would make more workgroups
+    // than run at once, all four waves on one tile: after 8000 tokens, 20/5 heads of
+    // 128, 640 rows 110 us with one fragment and 94 so, but 512 83 and 92; 2048 rows
+    // 285 us in pairs of tiles and 243 so, but a prompt of 4096 103 and 108.
+    const bool lengthy = pages >= 32 && 32 * pages >= each;
+    if (dim <= 128 && each >= (lengthy ? 3 * kUnits + 1 : kPromptFrom) &&
+        rows >= kPromptRows * n_seqs) {
+        const int at = lengthy ? 1 : 2;   // tiles to a workgroup
+        const int64_t tiles = (rows / 32 + n_seqs + at - 1) / at * at;
+        return Attn4Plan{at, 0, 1, 1 << 24, 0, tiles, tiles / at * kv_heads};
+    }
+    const int64_t tiles = rows / 16 + n_seqs, groups = tiles * kv_heads;
     // A workgroup to a compute unit and a few pages to a wave: splitting costs more
     // than it saves (20/5 heads of 128, one token: fp32 9.4 us whole and 9.9 split at
     // 12 pages, 11.7 and 9.9 at 13; bf16 8.7 and 9.2 at 18, 10.2 and 9.1 at 21).

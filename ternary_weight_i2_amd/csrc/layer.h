@@ -95,9 +95,10 @@ struct Attn4Args {
     int heads, window, sinks, splits, chunk;   // the last two and `tiles`: Attn4Plan
     uint32_t tiles;
 };
-// Which kernel a call's sizes take, how many workgroups share the pages of one
-// row tile, how many pages each takes (the last one the rest), how many may be on
-// a compute unit at once (0: any), the tiles of a kv head and the workgroups of all.
+// Which kernel a call's sizes take (prompt: its tiles to a workgroup, or 0), how many
+// workgroups share the pages of one row tile, how many pages each takes (the last one
+// the rest), how many may be on a compute unit at once (0: any), the tiles of a kv
+// head and the workgroups of all.
 struct Attn4Plan {
     int prompt, wide, splits, chunk, per_cu;
     int64_t tiles, workgroups;

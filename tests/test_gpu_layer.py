@@ -316,6 +316,20 @@ def test_many_rows(bn, d, dtype, window, sinks):
     assert np.abs(host(one).reshape(s.n, 2, 36, d) - w[:, :, None]).max() <= 2.0 ** (-7 if dtype is BF16 else -16) * np.abs(w).max()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2500, 3)])
+def test_many_rows_over_long_histories(bn, d, dtype, window, sinks):
+    """Over 16384 rows of long histories (here: what the table could hold) put all waves of a
+    workgroup on one tile of two fragments."""
+    s = Seqs([300, 1, 77, 0, 130, 2600], [200, 1, 33, 0, 30, 9], 2, d, seed=36, fill=0xFF,
+             gap=[(0, 1), (5, 3)])
+    s.fill(every=[p for p in range(2600) if p < 400 or p > 2300])
+    s.cache[s.cache == 0xFF] = 0
+    s.table = np.concatenate([s.table, np.full((6, 80 - s.table.shape[1]), -1, np.int32)], 1)
+    check_attn(bn, s, 124, dtype, window, sinks, sample=600)
+
+
 @pytest.mark.parametrize("n_seqs", [63, 64, 65, 130, 700])
 def test_many_sequences(bn, n_seqs):
     """Sequences are found 64 at a time: numbers around 64, and over 64 squared / 64."""
