@@ -31,9 +31,9 @@
 // maximum and the accumulators of a row all live in the same lanes.
 //
 // What bounds it.  A long history of few rows: HBM with bf16 rows (64 sequences of
-// up to 4096 tokens, 64/8 heads of 128: 175 MB in 40 us, 4.4 TB/s; a large copy
-// reaches 4.8), the vector operations with fp32 rows (131072 tokens, 20/5 heads: 94
-// MB in 25 us, and 5 us for the join): a page of 128 channels costs a wave about 600
+// up to 4096 tokens, 64/8 heads of 128: 175 MB in 36 to 41 us, the less of it the
+// last-level cache holds the more; a large copy reaches 4.8 TB/s), the vector operations with fp32 rows (131072 tokens, 20/5 heads: 94
+// MB in 26 us, and 5 us for the join): a page of 128 channels costs a wave about 600
 // of them (350 in bf16 calls) and 72 (38) matrix instructions, however many of its 16
 // rows are real; the unpacking is the largest part.  Prompts: the vector operations
 // again, of which 32 rows a wave share the unpacking (three of 2048 tokens, 16/8
