@@ -302,7 +302,9 @@ constexpr int least_waves(int dim, int rt, int waves) {   // to a SIMD
 // Whether a tile's query lies in LDS (where the waves' results meet later) instead
 // of registers, so that a SIMD holds that many waves without spills: rows of 256
 // channels 2 in place of 1 (two prompts of 2048, 16/4 heads, bf16: 185 -> 110 us),
-// fp32 rows of 128 3 in place of 2 (one of 512, 20/5 heads: 18 -> 14 us).
+// fp32 rows of 128 3 in place of 2 (one of 512, 20/5 heads: 18 -> 14 us).  fp32 rows
+// of 64 in two fragments spill a few registers for their third wave and gain by it
+// (four prompts of 2048, 32/8 heads: 200 -> 182 us), as much as from LDS.
 constexpr bool query_in_lds(int dim, bool bf16, int waves) {
     return dim == 256 || (dim == 128 && !bf16 && waves == 4);
 }
@@ -845,7 +847,7 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     // of 128 rows 57 and 60 us either way round; 50 of 512 rows: 123 and 108).
     // Where one fragment would make kPromptFrom workgroups, two tiles to a workgroup
     // (those behind the last have no rows): three prompts of 2048, 16/8 heads of 128,
-    // 92 -> 81 us; 700 rows of 32/8 heads from nothing 18 us with one fragment, 21
+    // 92 -> 81 us when it was added; 700 rows of 32/8 heads from nothing 18 us with one fragment, 21
     // with two.  Over long histories, where one fragment would make more workgroups
     // than run at once, all four waves on one tile: after 8000 tokens, 20/5 heads of
     // 128, 640 rows 110 us with one fragment and 94 so, but 512 83 and 92; 2048 rows
@@ -869,10 +871,15 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     // at once, but none beyond: 32 sequences of 2000 tokens, 32/8 heads of 64 20.6 us
     // at four to a compute unit and 18.3 at three; 8 of 4000, heads of 128, fp32 18.0
     // at two, 21.1 at three.  A short chunk is a page for every wave or several.
+    // Workgroups without rows, of sequences without any, cost time too, if little:
+    // at most 64 of all for each page (256 sequences, of which 8 have a row at 500
+    // tokens, 32/8 heads of 128: 14.9 -> 9.2 us; one at 4000: 53 -> 25; at 30000: 175
+    // -> 61).
     const int64_t tall = (std::max<int64_t>(rows / n_seqs, 1) + 15) / 16;
     const int64_t busy = std::min(n_seqs, N) * tall * kv_heads;
     const int64_t at_once = kUnits * (dim == 64 ? 3 : dim == 256 && bf16 ? 1 : 2);
-    int64_t s = std::min<int64_t>(std::max<int64_t>(at_once / busy, 1), kMaxSplits);
+    const int64_t most = std::min<int64_t>(64 * pages / groups, kMaxSplits);
+    int64_t s = std::max<int64_t>(std::min(at_once / busy, most), 1);
     int64_t chunk = std::max<int64_t>((pages + s - 1) / s, 4);
     if (chunk < 16) chunk = (chunk + 3) / 4 * 4;
     s = std::max<int64_t>((pages + chunk - 1) / chunk, 1);

@@ -468,6 +468,17 @@ def test_one_long_history_among_short_ones(bn, d, dtype):
         check_attn(bn, s, 4, dtype, max_kv=64 * pages)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_few_sequences_with_rows_among_many(bn, dtype):
+    """A step of a fixed number of sequences, of which most add no token."""
+    rng = np.random.default_rng(37)
+    new = np.zeros(200, np.int64)
+    new[[3, 77, 199]] = 1
+    kv_len = rng.integers(0, 100, 200)
+    kv_len[[3, 77, 199]] = 1500, 90, 600
+    check_attn(bn, Seqs(kv_len, new, 2, 64, seed=37, fill=0xFF).fill(), 8, dtype)
+
+
 def test_queries_as_slices_and_out_given(bn):
     s = Seqs([100, 50], [3, 2], 2, 64, seed=20, fill=0xFF).fill()
     y = dev(s.rng.standard_normal((5, 8, 64)).astype(np.float32))
