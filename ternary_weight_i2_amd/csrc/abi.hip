@@ -641,7 +641,7 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
                     (long long)N, (long long)batch->n_seqs);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
                               scale * 1.4426950408889634f, (int)n_heads, win, first, sp.splits,
-                              sp.chunk, (uint32_t)sp.tiles};
+                              (uint32_t)sp.tiles};
     hipError_t e = bitnet::launch_attn4(a, sp, dtype == BITNET_BF16, (int)batch->head_dim,
                                         static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);

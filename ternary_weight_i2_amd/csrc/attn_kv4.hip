@@ -208,19 +208,30 @@ __device__ __forceinline__ void store_out(void *out, int64_t at, float4 acc, flo
     }
 }
 
-// The pages [begin, end) of a tile's list that a split takes (the last one the
-// rest).  A tile whose pages are one split's has its result written by it; its part
-// then says so in place of a sum, and the join leaves the row alone.
+// The pages of a split: an even share, of at least a page for every wave and, where
+// it is short, the same number for each.
+__host__ __device__ inline int chunk_of(int pages, int splits) {
+    const int c = (int)((uint32_t)(pages + splits - 1) / (uint32_t)splits);
+    return c >= 16 ? c : c <= 4 ? 4 : (c + 3) & ~3;
+}
+// The pages [begin, end) of a tile's list that a split takes: shares of what this
+// tile's rows see, so a call captured for the longest history loses little on a
+// short one (8 sequences, 32/8 heads of 128, bf16, captured for 32768 tokens: at 4000
+// 14.3 us, as if captured for 4000, against 34.6 with shares of the longest; two pages
+// to a wave are not split, 8.9 against 11.0 us at 500).  A tile whose pages are one split's has its result written by it; its
+// part then says so in place of a sum, and the join leaves the row alone.
 constexpr float kFinal = -1.0f;
 struct Share {
     int begin, end;
     bool shared;
 };
 __device__ __forceinline__ Share share_of(const Attn4Args &a, const Tile &t, int split) {
+    const bool whole = a.splits == 1 || (a.splits > 2 && t.pages <= 8);
+    const int chunk = whole ? t.pages : chunk_of(t.pages, a.splits);
     Share s;
-    s.begin = min(split * a.chunk, t.pages);
-    s.end = split == a.splits - 1 ? t.pages : min(s.begin + a.chunk, t.pages);
-    s.shared = t.pages > a.chunk && a.splits > 1;
+    s.begin = min(split * chunk, t.pages);
+    s.end = min(s.begin + chunk, t.pages);
+    s.shared = t.pages > chunk;
     return s;
 }
 // The output line of a sequence's row r, and its part of a split.
@@ -857,7 +868,7 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
         rows >= kPromptRows * n_seqs) {
         const int at = lengthy ? 1 : 2;   // tiles to a workgroup
         const int64_t tiles = (rows / 32 + n_seqs + at - 1) / at * at;
-        return Attn4Plan{at, 0, 1, 1 << 24, 0, tiles, tiles / at * kv_heads};
+        return Attn4Plan{at, 0, 1, 0, tiles, tiles / at * kv_heads};
     }
     const int64_t tiles = rows / 16 + n_seqs, groups = tiles * kv_heads;
     // A workgroup to a compute unit and a few pages to a wave: splitting costs more
@@ -865,12 +876,12 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     // 12 pages, 11.7 and 9.9 at 13; bf16 8.7 and 9.2 at 18, 10.2 and 9.1 at 21).
     const int64_t whole = bf16 ? 20 : 12;
     if (dim <= 128 && groups <= 256 && pages <= whole)
-        return Attn4Plan{0, 1, 1, (int)whole, 0, tiles, groups};
+        return Attn4Plan{0, 1, 1, 0, tiles, groups};
     // Chunks of pages, so that a batch's workgroups are alike however its lengths
     // differ, for all the workgroups with rows (of sequences of one length) that run
     // at once, but none beyond: 32 sequences of 2000 tokens, 32/8 heads of 64 20.6 us
     // at four to a compute unit and 18.3 at three; 8 of 4000, heads of 128, fp32 18.0
-    // at two, 21.1 at three.  A short chunk is a page for every wave or several.
+    // at two, 21.1 at three.
     // Workgroups without rows, of sequences without any, cost time too, if little:
     // at most 64 of all for each page (256 sequences, of which 8 have a row at 500
     // tokens, 32/8 heads of 128: 14.9 -> 9.2 us; one at 4000: 53 -> 25; at 30000: 175
@@ -880,8 +891,7 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     const int64_t at_once = kUnits * (dim == 64 ? 3 : dim == 256 && bf16 ? 1 : 2);
     const int64_t most = std::min<int64_t>(64 * pages / groups, kMaxSplits);
     int64_t s = std::max<int64_t>(std::min(at_once / busy, most), 1);
-    int64_t chunk = std::max<int64_t>((pages + s - 1) / s, 4);
-    if (chunk < 16) chunk = (chunk + 3) / 4 * 4;
+    const int64_t chunk = chunk_of((int)pages, (int)s);
     s = std::max<int64_t>((pages + chunk - 1) / chunk, 1);
     // Up to two to a compute unit are kept at two: where three fit, the workgroups
     // without rows between them let some units take three and others one (64
@@ -889,7 +899,7 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     // bf16 histories are bound by HBM and want the third (64 of 4095, 64/8 heads:
     // 43.3 us, held to two 49.9).
     const bool hold = dim == 128 && busy * s <= 2 * kUnits && (s > 1 || !bf16);
-    return Attn4Plan{0, 0, (int)s, (int)chunk, hold ? 2 : 0, tiles, groups * s};
+    return Attn4Plan{0, 0, (int)s, hold ? 2 : 0, tiles, groups * s};
 }
 
 hipError_t launch_attn4(const Attn4Args &a, const Attn4Plan &p, int bf16, int dim, hipStream_t st) {

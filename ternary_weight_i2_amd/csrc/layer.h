@@ -92,15 +92,14 @@ struct Attn4Args {
     float *part;           // per split, row: dim accumulators, then maximum and sum
     int64_t q_stride, N;
     float scale_log2;      // softmax scale times log2(e)
-    int heads, window, sinks, splits, chunk;   // the last two and `tiles`: Attn4Plan
+    int heads, window, sinks, splits;   // splits and `tiles`: Attn4Plan
     uint32_t tiles;
 };
 // Which kernel a call's sizes take (prompt: its tiles to a workgroup, or 0), how many
-// workgroups share the pages of one row tile, how many pages each takes (the last one
-// the rest), how many may be on a compute unit at once (0: any), the tiles of a kv
-// head and the workgroups of all.
+// workgroups share the pages of one row tile, how many may be on a compute unit at
+// once (0: any), the tiles of a kv head and the workgroups of all.
 struct Attn4Plan {
-    int prompt, wide, splits, chunk, per_cu;
+    int prompt, wide, splits, per_cu;
     int64_t tiles, workgroups;
 };
 Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
