@@ -439,9 +439,11 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
         __syncthreads();
     }
     const int pos_first = t.pos0 + (int)(t.row0 / G);
-    const int low_last = a.window > 0
-                             ? t.pos0 + (int)(min(t.row0 + ROWS - 1, last_row) / G) - a.window + 1
-                             : 0;
+    const int pos_last = t.pos0 + (int)(min(t.row0 + ROWS - 1, last_row) / G);
+    const int low_last = a.window > 0 ? pos_last - a.window + 1 : 0;
+    // what some row of the tile sees: the positions [seen_from, seen_end) and the sinks
+    const int seen_from = a.window > 0 ? pos_first - a.window + 1 : 0, seen_end = pos_last + 1;
+    auto unseen = [&](int j) { return j >= seen_end || (j < seen_from && j >= a.sinks); };
 
     // What is carried along the pages.  The weights p are 2^(x - m + 7), where m
     // may stay up to 8 behind the largest x so that the accumulators are rescaled
@@ -472,16 +474,18 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
 
     while (t0 >= 0) {
         // ---- the page's pairs go through LDS, its steps divided by 2^E
-        if (t0 + kPage > t.held) {   // tokens behind the last have pairs of any value
-            const int left = t.held - t0;
+        // Where no row of the tile sees a token, none need have been written: its pairs
+        // may be of any value, and a weight of 0 would not silence them.  (Such a token is
+        // on the tile's last page, or where its window begins or its sinks end.)
+        if (t0 + kPage > seen_end || (t0 < seen_from && t0 + kPage > a.sinks)) {
             if (lane >= 32) {
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
                     // halfword i of the value pairs: token 4 (i / 8 / NG) + i % 4
                     const int h0 = (lane - 32) * (D / 16) + 2 * w;
-                    const int tok = 4 * (h0 / (8 * NG)) + (h0 & 3);
-                    if (tok >= left) raw_m[w] = 0;
-                    else if (tok + 1 >= left) raw_m[w] &= 0xffffu;
+                    const int j = t0 + 4 * (h0 / (8 * NG)) + (h0 & 3);
+                    if (unseen(j)) raw_m[w] &= 0xffff0000u;
+                    if (unseen(j + 1)) raw_m[w] &= 0xffffu;
                 }
             }
         }
