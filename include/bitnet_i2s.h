@@ -408,8 +408,9 @@ int bitnet_kv4_read(const bitnet_kv4_batch *batch, void *k, void *v, int dtype, 
  *   max_kv   the longest kv_len that is expected (at most 64 * max_pages): it
  *            decides how many workgroups share a sequence and so the workspace
  *            and the speed, not what is computed.
- *   out      [N][n_heads][head_dim] in dtype, 16-byte aligned.  A row that sees
- *            nothing gets zeros.
+ *   out      [N][n_heads][head_dim] in dtype, 16-byte aligned.  A row (one token,
+ *            one head) that sees nothing gets zeros; one whose q has a NaN or an
+ *            infinity is all NaN if it sees anything, and no other row is.
  *   workspace   device scratch of at least bitnet_attn_kv4_workspace bytes of the
  *            same sizes, 16-byte aligned (may be NULL where that is 0); used until the
  *            call's kernels have ended, so calls that may run at once need one

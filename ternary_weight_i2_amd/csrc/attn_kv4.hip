@@ -775,7 +775,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 if (s + i * par >= a.splits) ls[i] = 0.0f;
-                if (ls[i] > 0.0f) best = fmaxf(best, ms[i]);
+                // a sum that is no number goes on into the row, as without splits
+                if (ls[i] != 0.0f) best = fmaxf(best, ms[i]);
                 else os[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             const float f = __builtin_amdgcn_exp2f(top - best);
@@ -784,7 +785,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn4_join_kernel(const Attn4Arg
             top = best;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const float fi = ls[i] > 0.0f ? __builtin_amdgcn_exp2f(ms[i] - top) : 0.0f;
+                const float fi = ls[i] != 0.0f ? __builtin_amdgcn_exp2f(ms[i] - top) : 0.0f;
                 sum = fmaf(fi, ls[i], sum);
                 add_part(acc, fi, os[i]);
             }

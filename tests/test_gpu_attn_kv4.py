@@ -50,3 +50,24 @@ def test_hidden_places_of_many_rows(bn, d, dtype, heads, new, window):  # noqa: 
     """Prompts, with two tiles to a workgroup and with one."""
     s = seen_only(Seqs([2500, 140], [new, 30], 2, d, seed=52, fill=0xFF), window, 3)
     check_attn(bn, s, heads, dtype, window, 3, sample=500)
+
+
+# ---------------------------------------------------------------- queries that are no numbers
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("t", [100, 2000, 9000])       # eight waves, splits, many splits
+def test_a_query_that_is_no_number_gives_rows_that_are_none(bn, dtype, t):  # noqa: F811
+    """Those rows alone, whatever the launch; a row that sees nothing stays zero."""
+    s = Seqs([t, 0, 40], [2, 1, 1], 1, 64, seed=53, fill=0xFF).fill(every=range(t - 90, t))
+    s.cache[s.cache == 0xFF] = 0
+    q = host(dev(s.rng.standard_normal((4, 4, 64)).astype(np.float32), dtype))
+    want, tol = lo.attention(q, s.cache, s.table, s.kv_len, s.q_start, 0.125, half=dtype is BF16)
+    bad = np.zeros((4, 4), bool)
+    for row, head, ch, x in ((0, 1, 3, np.nan), (1, 0, 63, np.inf), (1, 3, 0, -np.inf), (3, 2, 40, np.nan)):
+        q[row, head, ch] = x
+        bad[row, head] = True
+    q[2, 0, 0] = np.nan                                  # the sequence without any token
+    got = host(bn.attn_kv4(dev(q, dtype), *s.dev()))
+    assert np.isnan(got[bad]).all()
+    assert (got[2] == 0).all()
+    assert (np.abs(got - want)[~bad] <= tol[~bad]).all()
