@@ -417,8 +417,11 @@ int bitnet_kv4_read(const bitnet_kv4_batch *batch, void *k, void *v, int dtype, 
  *            each.
  *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or n_seqs == 0 is a no-op.
  *
- * fp32 calls compute to about fp32 accuracy (fp32 sums; factors of 22 bits),
- * bf16 calls round q and the softmax weights to 11 bits and the output to bf16.
+ * Sums and maxima are fp32.  The softmax weights and their products with the
+ * cache's steps are carried in 22 bits by fp32 calls (q too) and in 11 by bf16
+ * calls, and no finer than 2^-27 (bf16: 2^-22) of a token's |mid| + 8 step at the
+ * row's largest weight.  Rows whose |q| or scaled scores reach 2^100 are
+ * unspecified.
  * Repeated calls with the same sizes give identical bits.
  */
 int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t n_heads,

@@ -617,7 +617,8 @@ def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, ma
     between tokens) over the 4-bit cache, for single tokens and prompts: row
     q_start[b] + i stands at position kv_len[b] - (q_start[b+1] - q_start[b]) + i
     and sees the positions up to its own; with a ``window`` the last ``window``
-    of them and the first ``sinks``.  A row that sees nothing gets zeros.
+    of them and the first ``sinks``.  A row that sees nothing gets zeros, one with a
+    NaN or an infinity in its q NaN.
 
     scale: 1 / sqrt(head_dim) if None.  max_kv: the longest kv_len expected (the
     table's capacity if None); it tunes the launch and changes no result beyond

@@ -19,11 +19,12 @@
 // second terms.  Its sums are then good to about 2^-17 (it aligns a subnormal's
 // product by the smallest normal exponent), far below what a bf16 result holds.
 //   fp32 calls make code - 8 a normal number, exactly, at nine operations.
-// q is scaled by a power of two per row, p * step by one per page (from the
-// largest step met so far, tracked like the maximum), so neither leaves fp16's
-// normal range; bf16 calls round q (8 bits), p and p * step once to fp16's 11 bits,
-// finer than the output, fp32 calls carry them as two fp16 terms (22 bits).  Sums,
-// maxima and accumulators are fp32.
+// q is scaled by a power of two per row, the steps by one that goes by the page, which
+// is visited again where its steps span too much for one, so both are normal numbers
+// in fp16; bf16 calls round p and p * step once to fp16's 11 bits, finer than the
+// output (q's 8 are exact), fp32 calls carry them and q as two fp16 terms (22 bits).
+// Both end at 2^-25, far below a row's largest weight (kUp).  Sums, maxima and
+// accumulators are fp32.
 //
 // The first product is taken transposed (tokens x rows), which leaves a lane
 // with 16 tokens of one row: that is exactly the fragment that the second
@@ -49,6 +50,7 @@ namespace bitnet {
 namespace {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef uint16_t us2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
@@ -56,9 +58,9 @@ constexpr int kUnits = 256;        // compute units
 constexpr int kMaxSplits = 256;
 constexpr int kPromptFrom = 2048, kPromptRows = 128;   // see attn4_plan
 constexpr int kJoinThreads = 1024;
-constexpr float kBehind = 8.0f, kUp = 7.0f;   // see attn4_kernel
 constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
 
+__device__ __forceinline__ us2 as_us2(uint32_t w) { return __builtin_bit_cast(us2, w); }
 __device__ __forceinline__ h2 as_h2(uint32_t w) { return __builtin_bit_cast(h2, w); }
 __device__ __forceinline__ h8 join(h2 a, h2 b, h2 c, h2 d) {
     return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
@@ -94,9 +96,16 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t one, h2 (&c)[4]) {
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-// 2^e as fp16, -24 <= e <= 15.
+// The steps in a word of two that are below `cut`; the others 0.
+__device__ __forceinline__ uint32_t steps_below(uint32_t w, uint32_t cut) {
+    return ((w & 0xffffu) < cut ? w & 0xffffu : 0) | (w >> 16 < cut ? w & 0xffff0000u : 0);
+}
+// 2^e as fp16 (0 where that has none so small), e <= 16.
+__device__ __forceinline__ uint32_t half_bits(int e) {
+    return e >= -14 ? (e + 15) << 10 : e >= -24 ? 1 << (e + 24) : 0;
+}
 __device__ __forceinline__ _Float16 pow2_f16(int e) {
-    return __builtin_bit_cast(_Float16, (uint16_t)(e >= -14 ? (e + 15) << 10 : 1 << (e + 24)));
+    return __builtin_bit_cast(_Float16, (uint16_t)half_bits(e));
 }
 
 // Over the four lanes that hold a row (l, l ^ 16, l ^ 32, l ^ 48): the swaps
@@ -325,6 +334,12 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
     const Attn4Args a) {
     using L = Kv4Page<D>;
     constexpr int NG = L::kGroups, NS = L::kSteps, NT = BF16 ? 1 : 2, ROWS = 16 * RT;
+    // The weights p are 2^(x - m + kUp), where m may stay up to kBehind behind the largest
+    // x so that the accumulators are rescaled seldom.  What fp16 holds of p ends at 2^-25,
+    // so a token's part is off by up to 2^-(25 + kUp) of its value at the largest weight:
+    // 2^-37 with fp32 rows, 2^-32 with bf16.  (7 bits for fp32 rows too would cost up to
+    // 1.5% less, but 2^-32 of a value of 20000 next to one of 0.01 is 2^-11 of that.)
+    constexpr float kUp = BF16 ? 7.0f : 12.0f, kBehind = 15.0f - kUp;
     constexpr int SUBS = 2;   // 16-token quarters of a page that are worked on together
     constexpr int kCodeExp = BF16 ? 24 : 0;   // raw codes carry 2^-24, and every second pair 16
     __shared__ __align__(16) uint32_t pairs_all[WAVES][2 * D];   // 8 D bytes a page
@@ -439,21 +454,22 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
         __syncthreads();
     }
     const int pos_first = t.pos0 + (int)(t.row0 / G);
-    const int pos_last = t.pos0 + (int)(min(t.row0 + ROWS - 1, last_row) / G);
-    const int low_last = a.window > 0 ? pos_last - a.window + 1 : 0;
-    // what some row of the tile sees: the positions [seen_from, seen_end) and the sinks
-    const int seen_from = a.window > 0 ? pos_first - a.window + 1 : 0, seen_end = pos_last + 1;
-    auto unseen = [&](int j) { return j >= seen_end || (j < seen_from && j >= a.sinks); };
+    const int low_last = a.window > 0
+                             ? t.pos0 + (int)(min(t.row0 + ROWS - 1, last_row) / G) - a.window + 1
+                             : 0;
+    // Tokens that may not have been written: behind the sequence's last, and those that the
+    // windows of all rows hide.  Pages from seen_from on, for seen_pages, have none.
+    const int seen_from = a.window > 0 ? max(pos_first - a.window + 1, 0) : 0;
+    const uint32_t seen_pages = (uint32_t)max(t.held - kPage + 1 - seen_from, 0);
+    auto unseen = [&](int j) { return j >= t.held || (j < seen_from && j >= a.sinks); };
 
-    // What is carried along the pages.  The weights p are 2^(x - m + 7), where m
-    // may stay up to 8 behind the largest x so that the accumulators are rescaled
-    // seldom; the steps in front of the second product are divided by 2^E.  `sums`
-    // is the product of p with what row n of 16 stands for: row 2 g the steps of
-    // group g, 2 g + 1 its middles, 2 NG + 1 ones.
+    // What is carried along the pages.  The steps in front of the second product are
+    // divided by 2^E.  `sums` is the product of p with what row n of 16 stands for: row
+    // 2 g the steps of group g, 2 g + 1 its middles, 2 NG + 1 ones.
     float m[RT];
-    int E = -14;                 // every step so far is below 2^E
+    int E = 2;                   // the steps of the page are below 2^E
     const bool steps_here = lane >= 32 && (D > 64 || !(lane & 1));   // see raw_m below
-    _Float16 down = steps_here ? pow2_f16(14) : (_Float16)1.0f;      // 2^-E for the steps
+    _Float16 down = steps_here ? pow2_f16(-E) : (_Float16)1.0f;      // 2^-E for the steps
     f4 o[RT][NG][4], sums[RT];   // o[..][g][i][e]: channel 64 g + 16 quad + 4 e + i
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -464,6 +480,15 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[rt][g][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    // Pages whose steps are all in [2^(E - 10), 2^E) are taken as they are: divided by 2^E
+    // they are normal numbers, and p * step is off by 2^(-15 - kUp) steps at most.  For other
+    // pages E changes (where it starts suits values of about 1), and where no E does for
+    // all steps of a page, those that are too small are left to another visit of it, in
+    // which nothing else counts (`cut`: what they are below; E falls by nine with each
+    // visit, down to -13, below which no step needs it).  As bits of fp16: `least` and
+    // `span`, [least, least + span).  Zeros are looked at, and change nothing.
+    auto least_of = [](int e) { return e > -13 ? half_bits(e - 10) : 0u; };
+    uint32_t least = least_of(E), span = half_bits(E) - least, cut = 0;
     if (lane < 2) ones[lane] = 0x3c003c00u;
     const uint32_t *sums_from[4];   // this lane's row of `sums`, for tokens 16 i + 4 quad ..
 #pragma unroll
@@ -474,30 +499,59 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
 
     while (t0 >= 0) {
         // ---- the page's pairs go through LDS, its steps divided by 2^E
-        // Where no row of the tile sees a token, none need have been written: its pairs
-        // may be of any value, and a weight of 0 would not silence them.  (Such a token is
-        // on the tile's last page, or where its window begins or its sinks end.)
-        if (t0 + kPage > seen_end || (t0 < seen_from && t0 + kPage > a.sinks)) {
-            if (lane >= 32) {
+        // lanes 32 on hold four steps, then four middles, and so on
+        auto is_steps = [](int w) { return D == 64 || !(w & 2); };
+        // what is not seen may have pairs of any value, which a weight of 0 would not silence
+        auto hide = [&](uint32_t by) {
+            if ((uint32_t)(t0 - seen_from) < seen_pages || lane < 32) return;
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    // halfword i of the value pairs: token 4 (i / 8 / NG) + i % 4
-                    const int h0 = (lane - 32) * (D / 16) + 2 * w;
-                    const int j = t0 + 4 * (h0 / (8 * NG)) + (h0 & 3);
-                    if (unseen(j)) raw_m[w] &= 0xffff0000u;
-                    if (unseen(j + 1)) raw_m[w] &= 0xffffu;
-                }
+            for (int w = 0; w < D / 32; ++w) {
+                // halfword i of the value pairs: token 4 (i / 8 / NG) + i % 4
+                const int h0 = (lane - 32) * (D / 16) + 2 * w;
+                const int j = t0 + 4 * (h0 / (8 * NG)) + (h0 & 3);
+                if (unseen(j)) raw_m[w] = (raw_m[w] & 0xffff0000u) | by;
+                if (unseen(j + 1)) raw_m[w] = (raw_m[w] & 0xffffu) | by << 16;
             }
-        }
-        // the largest step: lanes 32 on hold four steps, then four middles, and so on
-        uint32_t smax = 0;
+        };
+        hide(least);
+        us2 far = {0, 0};
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
-            if (D == 64 || !(w & 2)) smax = max(smax, max(raw_m[w] & 0xffffu, raw_m[w] >> 16));
+            if (is_steps(w))
+                far = __builtin_elementwise_max(far, as_us2(raw_m[w]) - as_us2(least * 0x10001u));
         int E_new = E;
-        if (__any(steps_here && (int)smax >= (E + 15) << 10)) {
-            E_new = (wave_max_u16(steps_here ? (int)smax : 0) >> 10) - 14;
-            down = steps_here ? pow2_f16(-E_new) : (_Float16)1.0f;
+        if (__any(steps_here && max((uint32_t)far[0], (uint32_t)far[1]) >= span)) {
+            hide(0);
+            uint32_t top = 0;
+            bool low = false;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                if (cut && lane >= 32)
+                    raw_m[w] = steps_here && is_steps(w) ? steps_below(raw_m[w], cut) : 0;
+                if (!steps_here || !is_steps(w)) continue;
+                top = max(top, max(raw_m[w] & 0xffffu, raw_m[w] >> 16));
+                low |= steps_below(raw_m[w], least) != 0;
+            }
+            if (lane < 2) ones[lane] = cut ? 0 : 0x3c003c00u;   // p counts once
+            const int most = wave_max_u16((int)top);
+            bool again = false;
+            if (most >= (int)half_bits(E) || __any(low)) {
+                E_new = min(most >> 10, 29) - 13;   // an octave to spare
+                least = least_of(E_new);
+                down = steps_here ? pow2_f16(-E_new) : (_Float16)1.0f;
+                low = false;
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    if (!steps_here || !is_steps(w)) continue;
+                    const uint32_t small = steps_below(raw_m[w], least);
+                    low |= small != 0;
+                    raw_m[w] ^= small;
+                }
+                again = __any(low);
+            }
+            span = cut || again ? 0 : half_bits(E_new) - least;   // 0: the next page is looked at
+            cut = again ? least : 0;
+            if (again) there |= (uint64_t)1 << at_bit;   // it is this one once more
         }
         {
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -590,7 +644,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
             for (int i4 = 0; i4 < SUBS; ++i4)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, s[rt][i4][e]);
-            if (E_new > E || __any(top * qs[rt] > m[rt] + kBehind)) {
+            if (E_new != E || __any(top * qs[rt] > m[rt] + kBehind)) {
                 const float m_new = fmaxf(m[rt], quad_max(top) * qs[rt]);
                 const float f = __builtin_amdgcn_exp2f(m[rt] - m_new), fs = ldexpf(f, E - E_new);
                 sums[rt][0] *= fs;
