@@ -415,7 +415,9 @@ int bitnet_kv4_read(const bitnet_kv4_batch *batch, void *k, void *v, int dtype, 
  *            same sizes, 16-byte aligned (may be NULL where that is 0); used until the
  *            call's kernels have ended, so calls that may run at once need one
  *            each.
- *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or n_seqs == 0 is a no-op.
+ *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or n_seqs == 0 is a no-op.  Calls of 2^24 or
+ *   more workgroups are refused, by bitnet_attn_kv4_workspace (-1) too: none with
+ *   N * n_heads / 16 + n_seqs * n_kv_heads below 2^24 is.
  *
  * Sums and maxima are fp32.  The softmax weights and their products with the
  * cache's steps are carried in 22 bits by fp32 calls (q too) and in 11 by bf16

@@ -597,9 +597,16 @@ BITNET_API int64_t bitnet_attn_kv4_workspace(int64_t n_seqs, int64_t N, int64_t 
     g_last_error.clear();
     if (n_seqs == 0 || N == 0) return 0;
     int64_t splits = 1;   // the larger of the two types
-    for (bool bf16 : {false, true})
-        splits = std::max<int64_t>(splits, bitnet::attn4_plan(n_seqs, N, n_heads, n_kv_heads, head_dim,
-                                                              max_kv, window, sinks, bf16).splits);
+    for (bool bf16 : {false, true}) {
+        const bitnet::Attn4Plan p = bitnet::attn4_plan(n_seqs, N, n_heads, n_kv_heads, head_dim,
+                                                       max_kv, window, sinks, bf16);
+        if (p.workgroups >= bitnet::kAttn4Workgroups) {
+            fail(BITNET_E_SHAPE, "%s: N=%lld, n_seqs=%lld are too many rows for one call", fn,
+                 (long long)N, (long long)n_seqs);
+            return -1;
+        }
+        splits = std::max<int64_t>(splits, p.splits);
+    }
     return splits > 1 ? splits * N * n_heads * (head_dim + 4) * 4 : 0;
 }
 
@@ -625,6 +632,7 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
         return fail(BITNET_E_ALIGN, "%s: out and workspace must be 16-byte aligned", fn);
     const int64_t need = bitnet_attn_kv4_workspace(batch->n_seqs, N, n_heads, batch->n_kv_heads,
                                                    batch->head_dim, max_kv, window, sinks);
+    if (need < 0) return BITNET_E_SHAPE;   // it has said why
     if (need > 0 && !workspace)
         return fail(BITNET_E_NULL, "%s: a workspace of %lld bytes is required", fn, (long long)need);
     if (workspace_bytes < need)
@@ -636,9 +644,6 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
     const bitnet::Attn4Plan sp =
         bitnet::attn4_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads, batch->head_dim, max_kv,
                            window, sinks, dtype == BITNET_BF16);
-    if (sp.workgroups >= 1 << 24)   // of 256 threads: a launch has fewer than 2^32
-        return fail(BITNET_E_SHAPE, "%s: N=%lld, n_seqs=%lld are too many rows for one call", fn,
-                    (long long)N, (long long)batch->n_seqs);
     const bitnet::Attn4Args a{kv4_args(batch), q, out, static_cast<float *>(workspace), q_stride, N,
                               scale * 1.4426950408889634f, (int)n_heads, win, first, sp.splits,
                               (uint32_t)sp.tiles};

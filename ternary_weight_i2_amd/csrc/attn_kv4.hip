@@ -948,7 +948,8 @@ Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
     const int64_t tall = (std::max<int64_t>(rows / n_seqs, 1) + 15) / 16;
     const int64_t busy = std::min(n_seqs, N) * tall * kv_heads;
     const int64_t at_once = kUnits * (dim == 64 ? 3 : dim == 256 && bf16 ? 1 : 2);
-    const int64_t most = std::min<int64_t>(64 * pages / groups, kMaxSplits);
+    const int64_t most = std::min<int64_t>({64 * pages / groups, kMaxSplits,
+                                            (kAttn4Workgroups - 1) / groups});
     int64_t s = std::max<int64_t>(std::min(at_once / busy, most), 1);
     const int64_t chunk = chunk_of((int)pages, (int)s);
     s = std::max<int64_t>((pages + chunk - 1) / chunk, 1);

@@ -98,6 +98,7 @@ struct Attn4Args {
 // Which kernel a call's sizes take (prompt: its tiles to a workgroup, or 0), how many
 // workgroups share the pages of one row tile, how many may be on a compute unit at
 // once (0: any), the tiles of a kv head and the workgroups of all.
+constexpr int64_t kAttn4Workgroups = 1 << 24;   // of 256 threads: a launch has fewer than 2^32
 struct Attn4Plan {
     int prompt, wide, splits, per_cu;
     int64_t tiles, workgroups;
