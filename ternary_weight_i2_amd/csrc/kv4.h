@@ -29,7 +29,6 @@
 
 namespace bitnet {
 
-constexpr int kPage = 64;    // tokens of a page
 constexpr int kGroup = 64;   // channels that share a (step, middle) pair
 constexpr float kKv4Max = 57344.0f;   // mid + 7 * step then stays below the largest fp16
 

@@ -3,6 +3,7 @@
 // (library-internal; not installed).
 #pragma once
 
+#include "attn_plan.h"
 #include "common.h"
 
 namespace bitnet {
@@ -95,16 +96,6 @@ struct Attn4Args {
     int heads, window, sinks, splits;   // splits and `tiles`: Attn4Plan
     uint32_t tiles;
 };
-// Which kernel a call's sizes take (prompt: its tiles to a workgroup, or 0), how many
-// workgroups share the pages of one row tile, how many may be on a compute unit at
-// once (0: any), the tiles of a kv head and the workgroups of all.
-constexpr int64_t kAttn4Workgroups = 1 << 24;   // of 256 threads: a launch has fewer than 2^32
-struct Attn4Plan {
-    int prompt, wide, splits, per_cu;
-    int64_t tiles, workgroups;
-};
-Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads, int64_t dim,
-                     int64_t max_kv, int64_t window, int64_t sinks, bool bf16);
 hipError_t launch_attn4(const Attn4Args &a, const Attn4Plan &plan, int bf16, int dim,
                         hipStream_t st);
 

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import layer_oracle as lo
+from attn_forms import FORMS
 from test_gpu_layer import BF16, F32, Seqs, bn, check_attn, dev, host  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -184,3 +185,21 @@ def test_values_of_nothing(bn, dtype):  # noqa: F811
     size = np.full(300, 0.5)
     size[64:128], size[130:300:2] = 0.0, 0.0
     check_positive(bn, unequal(Seqs([300, 100], [1, 3], 2, 128, seed=57), size, np.zeros(300, bool)), 8, dtype)
+
+
+# ---------------------------------------------------------------- every form of launch
+
+@pytest.mark.parametrize("form,d", [(f, d) for f, x in FORMS.items() for d in x["dims"]])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("window", [False, True])
+def test_every_form(bn, form, d, dtype, window):  # noqa: F811
+    """With a window and sinks, all that they hide unwritten, and without."""
+    f = FORMS[form]
+    w, sinks = (f["window"], f["sinks"]) if window else (0, 0)
+    s = Seqs(f["kv_len"], f["new"], f["kv_heads"], d, seed=58, fill=0xFF)
+    if window:
+        seen_only(s, w, sinks)
+    else:                                            # zeros where a long history has gaps
+        s.fill(every=[p for p in range(9000) if p < 300 or p % 8 == 0])
+        s.cache[s.cache == 0xFF] = 0
+    check_attn(bn, s, f["heads"], dtype, w, sinks, max_kv=f["max_kv"], sample=500)
