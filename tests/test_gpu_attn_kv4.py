@@ -203,3 +203,23 @@ def test_every_form(bn, form, d, dtype, window):  # noqa: F811
         s.fill(every=[p for p in range(9000) if p < 300 or p % 8 == 0])
         s.cache[s.cache == 0xFF] = 0
     check_attn(bn, s, f["heads"], dtype, w, sinks, max_kv=f["max_kv"], sample=500)
+
+
+# ---------------------------------------------------------------- very many sequences
+
+@pytest.mark.parametrize("n_seqs,empty", [(4096, 0.5), (4097, 0.5), (4097, 0.0), (5000, 0.9), (20000, 0.95)])
+def test_thousands_of_sequences(bn, n_seqs, empty):  # noqa: F811
+    """Sequences are found 64 at a time: over 4096 takes a further step of the search."""
+    rng = np.random.default_rng(n_seqs)
+    new = np.where(rng.random(n_seqs) < empty, 0, rng.integers(0, 3, n_seqs))
+    new[rng.integers(0, n_seqs, 3)] = 70
+    s = Seqs(new, new, 1, 64, seed=59, fill=0xFF)
+    k, v = s.rows(s.n), s.rows(s.n)
+    c, *rest = s.dev()
+    bn.kv4_append(c, *rest, dev(k), dev(v))
+    lo.append(s.cache, s.table, s.kv_len, s.q_start, k, v)
+    assert np.array_equal(c.cpu().numpy(), s.cache)
+    want = lo.read(s.cache, s.table, s.kv_len, s.q_start, s.n, 64)
+    for got, x in zip(bn.kv4_read(c, *rest, s.n), want):
+        assert np.array_equal(host(got), x)
+    check_attn(bn, s, 2, max_kv=128)
