@@ -380,6 +380,7 @@ typedef struct {
  *            k_stride elements (16-byte aligned, as the strides in bytes; a
  *            stride of at least a row, so slices of one merged projection do).
  *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or n_seqs == 0 is a no-op.
+ * The cache overlaps neither k nor v, nor any call's outputs or workspace.
  * If two rows have the same place (one page in two sequences' tables), what
  * that token holds afterwards is unspecified; other tokens are not touched.
  */

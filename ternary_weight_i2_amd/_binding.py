@@ -655,7 +655,8 @@ def attn_kv4(q, cache, table, kv_len, q_start, scale=None, window=0, sinks=0, ma
 
 
 def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window=0, sinks=0):
-    """Bytes of workspace that attn_kv4 takes for these sizes."""
+    """Bytes of workspace that attn_kv4 takes for these sizes: not fewer for a smaller
+    max_kv, so ask with the call's own (attn_kv4 takes at most the table's capacity)."""
     need = load().bitnet_attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv,
                                             window, sinks)
     if need < 0:
@@ -685,7 +686,8 @@ def attn_block(tokens, q, k, v, o, cache, table, kv_len, q_start, gamma=None, ep
     q, k, v, o: (packed, w_scale) pairs; head_dim and the kv heads are the cache's.
     rotary: called with q [N][n_heads][head_dim] and k [N][n_kv_heads][head_dim]
     (fp32), returns them with their positions applied.  The rest as in attn_kv4.
-    Returns y [N][hidden] fp32, the block's output for the next block_norm_quant."""
+    Returns y [N][hidden] fp32, the block's output for the next block_norm_quant; rows
+    of no sequence (padding) have no attention, and their y is unspecified."""
     yq, yk, yv = _matmuls(tokens, [q, k, v])
     N, kv_heads, dim = yq.shape[0], cache.shape[1], cache.shape[2] // 72
     qh = yq.view(N, yq.shape[1] // dim, dim)

@@ -33,14 +33,16 @@
 //
 // What bounds it.  A long history of few rows: HBM with bf16 rows (64 sequences of
 // up to 4096 tokens, 64/8 heads of 128: 175 MB in 36 to 41 us, the less of it the
-// last-level cache holds the more; a large copy reaches 4.8 TB/s), the vector operations with fp32 rows (131072 tokens, 20/5 heads: 94
-// MB in 26 us, and 5 us for the join): a page of 128 channels costs a wave about 600
+// last-level cache holds the more; a large copy reaches 4.8 TB/s), the vector
+// operations with fp32 rows (131072 tokens, 20/5 heads: 94 MB in 26 us, and 5 us for
+// the join; the batch of 64 in 61 us): a page of 128 channels costs a wave about 600
 // of them (350 in bf16 calls) and 72 (38) matrix instructions, however many of its 16
 // rows are real; the unpacking is the largest part.  Prompts: the vector operations
 // again, of which 32 rows a wave share the unpacking (three of 2048 tokens, 16/8
-// heads of 128, bf16: 36 GF in 72 us, 500 TF).  Short histories: the chain of
-// dependent loads (lengths, table, page), a page or two of work and the join of the
-// waves (515 tokens, 20/5 heads, fp32: 9.2 us in a graph, 7 with one page).
+// heads of 128, bf16: 36 GF in 72 us, 500 TF; they fill 71% of the cycles of a busy
+// compute unit, the matrix instructions 29%).  Short histories: the chain of dependent
+// loads (lengths, table, page), a page or two of work and the join of the
+// waves (515 tokens, 20/5 heads, fp32: 9.6 us in a graph).
 #include <algorithm>
 
 #include "kv4.h"

@@ -43,11 +43,11 @@ inline Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
     // of 128 rows 57 and 60 us either way round; 50 of 512 rows: 123 and 108).
     // Where one fragment would make kPromptFrom workgroups, two tiles to a workgroup
     // (those behind the last have no rows): three prompts of 2048, 16/8 heads of 128,
-    // 92 -> 81 us when it was added; 700 rows of 32/8 heads from nothing 18 us with one fragment, 21
-    // with two.  Over long histories, where one fragment would make more workgroups
-    // than run at once, all four waves on one tile: after 8000 tokens, 20/5 heads of
-    // 128, 640 rows 110 us with one fragment and 94 so, but 512 83 and 92; 2048 rows
-    // 285 us in pairs of tiles and 243 so, but a prompt of 4096 103 and 108.
+    // 92 -> 81 us when it was added; 700 rows of 32/8 heads from nothing 18 us with one
+    // fragment, 21 with two.  Over long histories, where one fragment would make more
+    // workgroups than run at once, all four waves on one tile: after 8000 tokens, 20/5
+    // heads of 128, 640 rows 110 us with one fragment and 97 so, but 512 83 and 92; 2048
+    // rows 292 us in pairs of tiles and 249 so, but a prompt of 4096 125 and 133.
     const bool lengthy = pages >= 32 && 32 * pages >= each;
     if (dim <= 128 && each >= (lengthy ? 3 * kUnits + 1 : kPromptFrom) &&
         rows >= kPromptRows * n_seqs) {

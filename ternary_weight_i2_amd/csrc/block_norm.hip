@@ -17,9 +17,11 @@
 // One workgroup per token keeps the token in registers between the steps, so
 // every input is read once and every output written once; what bounds it is
 // HBM for long prompts (4096 tokens of 2560, fp32 into a bf16 stream, a gate per
-// token: 136 MB in 28 us, 4.9 TB/s, what a large copy reaches) and the chain of
+// token: 136 MB in 28 us, 4.8 TB/s, what a large copy reaches) and the chain of
 // loads and workgroup reductions (two sums, one maximum, one sum of codes) for
-// single tokens (3.3 us at 2560; 64 tokens of 8192, norms on both sides: 6.8 us).
+// single tokens (3.4 us at 2560, of which the reductions are 1.0; 64 tokens of 8192,
+// norms on both sides, which leave three of four compute units idle: 6.7 us, of which
+// the reductions are 1.5).
 // The workgroup's width depends on F alone, so a token's result does not depend on
 // N; workgroups of half or twice the width took as long or up to 1.7 times it.
 #include <algorithm>

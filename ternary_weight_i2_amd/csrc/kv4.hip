@@ -7,9 +7,10 @@
 // from three DPP moves, and a lane's value codes are two stores of 8 bytes, 16 side
 // by side for a group.  Both kernels are bound by HBM for prompts (4.56 or 2.56
 // bytes a value with fp32 or bf16 rows): 6800 rows of 8 heads of 128, bf16, 35.6 MB
-// each way, are written in 12.5 us and read back in 10.1 (2.8 and 3.5 TB/s); 20000
-// fp32 rows of 5 heads read in 24 us (119 MB, 4.9 TB/s).  Single tokens are bound by
-// latency, the loads of the lengths, the table and the rows: 64 of them 3.9 and 3.1 us.
+// each way, are written in 12.8 us and read back in 10.1 (2.8 and 3.5 TB/s; in a graph
+// 11.0 and 9.3, where a copy that moves as much takes 6.1); 20000 fp32 rows of 5 heads
+// read in 24 us (119 MB, 4.9 TB/s).  Single tokens are bound by latency, the loads of
+// the lengths, the table and the rows: 64 of them 4.0 and 3.2 us.
 #include "kv4.h"
 
 namespace bitnet {
