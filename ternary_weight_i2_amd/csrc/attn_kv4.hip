@@ -451,9 +451,9 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
                              ? t.pos0 + (int)(min(t.row0 + ROWS - 1, last_row) / G) - a.window + 1
                              : 0;
     // Tokens that may not have been written: behind the sequence's last, and those that the
-    // windows of all rows hide.  Pages from seen_from on, for seen_pages, have none.
+    // windows of all rows hide.  Pages that begin in [seen_from, seen_from + seen) have none.
     const int seen_from = a.window > 0 ? max(pos_first - a.window + 1, 0) : 0;
-    const uint32_t seen_pages = (uint32_t)max(t.held - kPage + 1 - seen_from, 0);
+    const uint32_t seen = (uint32_t)max(t.held - kPage + 1 - seen_from, 0);
     auto unseen = [&](int j) { return j >= t.held || (j < seen_from && j >= a.sinks); };
 
     // What is carried along the pages.  The steps in front of the second product are
@@ -496,7 +496,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
         auto is_steps = [](int w) { return D == 64 || !(w & 2); };
         // what is not seen may have pairs of any value, which a weight of 0 would not silence
         auto hide = [&](uint32_t by) {
-            if ((uint32_t)(t0 - seen_from) < seen_pages || lane < 32) return;
+            if ((uint32_t)(t0 - seen_from) < seen || lane < 32) return;
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
                 // halfword i of the value pairs: token 4 (i / 8 / NG) + i % 4

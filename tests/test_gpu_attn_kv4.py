@@ -223,3 +223,35 @@ def test_thousands_of_sequences(bn, n_seqs, empty):  # noqa: F811
     for got, x in zip(bn.kv4_read(c, *rest, s.n), want):
         assert np.array_equal(host(got), x)
     check_attn(bn, s, 2, max_kv=128)
+
+
+# ---------------------------------------------------------------- captured
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_captured_with_pages_of_both_kinds(bn, dtype):  # noqa: F811
+    """A captured call, replayed over lengths that bring pages of one visit and of several,
+    ends under a window and none, gives the eager call's bits each time."""
+    size = np.where(np.arange(400) // 64 % 2, 0.3, 0.01)
+    size[30::64] = 2e4
+    s = unequal(Seqs([400, 260], [1, 1], 2, 128, seed=61), size, size > 1)
+    c, table, kv_len, q_start = s.dev()
+    q = dev(np.abs(s.rng.standard_normal((2, 8, 128))).astype(np.float32), dtype)
+
+    def run():
+        return [bn.attn_kv4(q, c, table, kv_len, q_start, window=w, sinks=3 if w else 0) for w in (0, 100)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for i in range(4):
+        kv_len.copy_(dev(np.array([400 - 61 * i, 60 + 50 * i], np.int32)))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        for a, b in zip(got, run()):
+            assert torch.equal(a, b) and torch.isfinite(a).all()
