@@ -53,6 +53,7 @@ extern "C" {
 #define BITNET_KV4_MAX_HEADS 1024   /* query heads, and kv heads, of a call    */
 #define BITNET_KV4_MAX_SEQS (1 << 20)  /* sequences of a call                  */
 #define BITNET_KV4_MAX_PAGES (1 << 24) /* pages of a sequence (2^30 tokens)    */
+#define BITNET_ROTARY_MAX_DIM 1024  /* channels of a head that positions turn   */
 
 typedef enum {
     BITNET_OK = 0,
@@ -435,6 +436,59 @@ int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int64_t q_stri
                     int64_t N, int64_t n_heads, float scale, int64_t window, int64_t sinks,
                     int64_t max_kv, void *out, void *workspace, int64_t workspace_bytes,
                     void *stream);
+
+/*
+ * Rotary positions.  Pair i of the first `rot` channels of a head's row, at position
+ * p, is turned by 2 pi frac(p * turns[i] / 2^64):
+ *   c = fp32(magnitude * cos), s = fp32(magnitude * sin)   (both from binary64)
+ *   (a, b) -> (fl(fl(a c) - fl(b s)), fl(fl(b c) + fl(a s))), rounded to the row's type;
+ * the other channels are copied.  turns[i] is the pair's frequency, in turns per position
+ * as a 64-bit fraction of one (base^(-2 i / rot) / (2 pi) * 2^64, say, or any other by
+ * which positions are scaled), so far positions lose nothing.
+ */
+typedef struct {
+    const int64_t *turns;   /* DEVICE [rot / 2], 8-byte aligned */
+    int64_t rot;            /* even, 2 .. head_dim */
+    int interleaved;        /* 0: pairs (i, i + rot/2); else (2 i, 2 i + 1) */
+    double magnitude;       /* positive and finite, below 1e30; 1 turns only */
+} bitnet_rotary_plan;
+
+/*
+ * bitnet_rotary -- rows at given positions.
+ *
+ *   x        rows of n_heads * head_dim fp32 or bf16 values, row n at x + n * x_stride
+ *            elements (16-byte aligned, as the strides in bytes; a stride of at least a
+ *            row); head_dim a multiple of 8, at most BITNET_ROTARY_MAX_DIM.
+ *   positions   DEVICE [N] int32 (negative ones turn the other way).
+ *   inverse  non-zero: by the negative angle (the magnitude the same), which is the
+ *            gradient of the forward call: dx from dout.
+ *   out      as x; it may be x itself with the same stride, and overlaps it in no
+ *            other way.
+ *   1 <= n_heads <= BITNET_KV4_MAX_HEADS, 0 <= N <= BITNET_GEMM_MAX_N; N == 0 is a no-op.
+ * A row with a NaN or an infinity has it, or a NaN, in the pair's two channels.
+ */
+int bitnet_rotary(const bitnet_rotary_plan *plan, const void *x, int64_t x_stride, int dtype,
+                  int64_t N, int64_t n_heads, int64_t head_dim, const int32_t *positions,
+                  int inverse, void *out, int64_t out_stride, void *stream);
+
+/*
+ * bitnet_rotary_kv4_append -- the step between a layer's projections and its attention in
+ * one launch: q turned, k turned and appended to the cache, v appended.
+ *
+ *   batch, k, v   as bitnet_kv4_append.
+ *   q, q_out      rows of n_heads * head_dim values as k; q_out may be q itself with the same
+ *                 stride, and overlaps nothing else.  Rows of no sequence are left as they are.
+ *   offset        DEVICE [n_seqs] int32 or NULL (0): a row at place p of the cache (see
+ *                 above) has the position p + offset[b], e.g. where tokens were evicted.
+ *   n_heads as bitnet_attn_kv4.
+ * The results are bitnet_rotary's of q and k and bitnet_kv4_append's of what that gives, bit
+ * for bit.
+ */
+int bitnet_rotary_kv4_append(const bitnet_kv4_batch *batch, const bitnet_rotary_plan *plan,
+                             const void *q, int64_t q_stride, void *q_out, int64_t out_stride,
+                             int64_t n_heads, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, int dtype, int64_t N, const int32_t *offset,
+                             void *stream);
 
 /* Thread-local description of the last non-OK status on this thread
  * (empty string if none).  The pointer stays valid until the next call on

@@ -46,6 +46,12 @@ class KV4Batch(ctypes.Structure):
                 ("n_seqs", ctypes.c_int64)]
 
 
+class RotaryPlan(ctypes.Structure):
+    """Mirror of bitnet_rotary_plan."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int64),
+                ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_double)]
+
+
 class BitnetError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"bitnet status {status}: {msg}")
@@ -140,6 +146,12 @@ def _open(path: str) -> ctypes.CDLL:
     L.bitnet_attn_kv4_workspace.restype = i64
     L.bitnet_attn_kv4.argtypes = [kv4, p, i64, i32, i64, i64, f32, i64, i64, i64, p, p, i64, p]
     L.bitnet_attn_kv4.restype = ctypes.c_int
+    plan = ctypes.POINTER(RotaryPlan)
+    L.bitnet_rotary.argtypes = [plan, p, i64, i32, i64, i64, i64, p, i32, p, i64, p]
+    L.bitnet_rotary.restype = ctypes.c_int
+    L.bitnet_rotary_kv4_append.argtypes = [kv4, plan, p, i64, p, i64, i64, p, i64, p, i64, i32, i64,
+                                           p, p]
+    L.bitnet_rotary_kv4_append.restype = ctypes.c_int
     for fn in ("bitnet_pack_i2s", "bitnet_quant_act_i8", "bitnet_gemv_i2s_i8",
                "bitnet_gemm_i2s_i8", "bitnet_gemv_i2s_lut", "bitnet_abi_version"):
         getattr(L, fn).restype = ctypes.c_int
@@ -589,6 +601,106 @@ def kv4_append(cache, table, kv_len, q_start, k, v):
             v.data_ptr(), _rows(v, "v", heads, dim, dev), _float_code(k.dtype, "k"), k.shape[0])
 
 
+class Rotary:
+    """Rotary positions: turns per position of each pair of channels (``turns`` [rot / 2]
+    int64 on the device, 64-bit fractions of a turn), the pairs (i, i + rot / 2) or
+    (2 i, 2 i + 1) (``interleaved``) of the first rot channels, and what cosine and sine
+    are multiplied by.  rotary_plan makes one from a base."""
+    __slots__ = ("turns", "interleaved", "magnitude", "_plan")
+
+    def __init__(self, turns, interleaved=False, magnitude=1.0):
+        import torch
+        if turns.dim() != 1 or turns.dtype != torch.int64 or not turns.is_contiguous():
+            raise TypeError("turns must be a contiguous 1-D int64 tensor")
+        self.turns, self.interleaved, self.magnitude = turns, bool(interleaved), float(magnitude)
+        self._plan = RotaryPlan(turns.data_ptr(), 2 * turns.shape[0], self.interleaved, self.magnitude)
+
+
+def rotary_plan(rot, base=10000.0, factor=1.0, length=0, low=1.0, high=32.0, freqs=None,
+                interleaved=False, magnitude=1.0, device="cuda"):
+    """A Rotary of ``rot`` channels: base^(-2 i / rot) radians per position, or ``freqs``
+    [rot / 2] (any numbers) in its place.  For contexts longer than trained for: ``factor``
+    divides every frequency (positions interpolated), or with ``length`` (the context
+    trained for) those that turn fewer than ``low`` times over it, none that turns more
+    than ``high`` times, and a share of it in between."""
+    import math
+
+    import torch
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot={rot} must be even and positive")
+    freqs = [base ** (-2 * i / rot) for i in range(rot // 2)] if freqs is None else [float(f) for f in freqs]
+    if len(freqs) != rot // 2 or not all(math.isfinite(f) for f in freqs):
+        raise ValueError(f"freqs must be {rot // 2} finite numbers")
+    if not factor > 0 or not length >= 0 or (length and not low < high):
+        raise ValueError("factor must be positive, length not negative and low below high")
+    turns = []
+    for f in freqs:
+        kept = 0.0
+        if length:
+            kept = min(max((length * abs(f) / (2 * math.pi) - low) / (high - low), 0.0), 1.0)
+        f *= kept + (1 - kept) / factor
+        t = int(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64     # whole turns fall away
+        turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    return Rotary(torch.tensor(turns, dtype=torch.int64, device=device), interleaved, magnitude)
+
+
+def _plan_of(plan, device):
+    if plan.turns.device != device:
+        raise ValueError(f"the plan's turns are on {plan.turns.device}, the rows on {device}")
+    return plan._plan
+
+
+def rotary(x, plan, positions, inverse=False, out=None):
+    """Rows x [N][heads][dim] (fp32 or bf16, any stride between tokens; dim a multiple of 8)
+    turned to ``positions`` [N] (int32, on the device) by a Rotary; ``inverse`` turns back,
+    which is the gradient's way.  ``out``: rows like x's, or x itself."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be 3-D [N][heads][dim]")
+    N, heads, dim = x.shape
+    dev = x.device
+    code, stride = _float_code(x.dtype, "x"), _rows(x, "x", heads, dim, dev)
+    if out is None:
+        out = torch.empty((N, heads, dim), dtype=x.dtype, device=dev)
+        to = heads * dim
+    else:
+        if out.dtype != x.dtype or out.shape != x.shape:
+            raise TypeError("out must have x's shape and type")
+        to = _rows(out, "out", heads, dim, dev)
+    _launch(load().bitnet_rotary, dev, _plan_of(plan, dev), x.data_ptr(), stride, code, N, heads, dim,
+            _at(positions, "positions", torch.int32, (N,), dev), 1 if inverse else 0, out.data_ptr(), to)
+    return out
+
+
+def rotary_kv4_append(cache, table, kv_len, q_start, q, k, v, plan, offset=None, out=None):
+    """q [N][n_heads][head_dim] and k [N][n_kv_heads][head_dim] turned to their positions by a
+    Rotary, k and v appended to the cache as kv4_append does: one launch.  A row's position is
+    its place in the cache plus ``offset`` [B] (int32, on the device) of its sequence.
+    Returns the turned q, in ``out`` if given (which may be q); rows of no sequence are left
+    as they are there."""
+    import torch
+    batch, kv_heads, dim = _kv4_batch(cache, table, kv_len, q_start)
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [N][n_heads][head_dim]")
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise TypeError("k and v must have the same shape and type")
+    if q.dtype != k.dtype or q.shape[0] != k.shape[0]:
+        raise TypeError("q and k must have the same type and as many rows")
+    N, heads, dev = q.shape[0], q.shape[1], cache.device
+    at_q, at_k, at_v = _rows(q, "q", heads, dim, dev), _rows(k, "k", kv_heads, dim, dev), _rows(v, "v", kv_heads, dim, dev)
+    if out is None:
+        out = torch.empty((N, heads, dim), dtype=q.dtype, device=dev)
+        to = heads * dim
+    else:
+        if out.dtype != q.dtype or out.shape != q.shape:
+            raise TypeError("out must have q's shape and type")
+        to = _rows(out, "out", heads, dim, dev)
+    _launch(load().bitnet_rotary_kv4_append, dev, batch, _plan_of(plan, dev), q.data_ptr(), at_q,
+            out.data_ptr(), to, heads, k.data_ptr(), at_k, v.data_ptr(), at_v, _float_code(q.dtype, "q"),
+            N, _at(offset, "offset", torch.int32, (batch.n_seqs,), dev))
+    return out
+
+
 def kv4_read(cache, table, kv_len, q_start, n, dtype=None, out=None):
     """What the cache holds at the last positions of each sequence (q_start as
     in kv4_append, n rows in all) -> (k, v) [n][n_kv_heads][head_dim], fp32 or
@@ -677,24 +789,30 @@ def _matmuls(tokens, mats):
 
 
 def attn_block(tokens, q, k, v, o, cache, table, kv_len, q_start, gamma=None, eps=1e-5, rotary=None,
-               window=0, sinks=0, max_kv=None):
+               window=0, sinks=0, max_kv=None, offset=None):
     """The attention block on I2_S weights and a 4-bit cache: q, k and v projections
     (one grouped launch) -> keys and values appended to the cache -> attention over
     it -> RMS sub-norm (gain gamma or 1) and int8 tokens -> the o projection.
 
     tokens: fp32 / bf16 [N][hidden], or quantised as block_norm_quant gives them.
     q, k, v, o: (packed, w_scale) pairs; head_dim and the kv heads are the cache's.
-    rotary: called with q [N][n_heads][head_dim] and k [N][n_kv_heads][head_dim]
-    (fp32), returns them with their positions applied.  The rest as in attn_kv4.
+    rotary: a Rotary (positions as in rotary_kv4_append, with its ``offset``), or called
+    with q [N][n_heads][head_dim] and k [N][n_kv_heads][head_dim] (fp32) and returns them with
+    their positions applied.  The rest as in attn_kv4.
     Returns y [N][hidden] fp32, the block's output for the next block_norm_quant; rows
     of no sequence (padding) have no attention, and their y is unspecified."""
     yq, yk, yv = _matmuls(tokens, [q, k, v])
     N, kv_heads, dim = yq.shape[0], cache.shape[1], cache.shape[2] // 72
     qh = yq.view(N, yq.shape[1] // dim, dim)
     kh, vh = yk.view(N, kv_heads, dim), yv.view(N, kv_heads, dim)
-    if rotary is not None:
-        qh, kh = rotary(qh, kh)
-    kv4_append(cache, table, kv_len, q_start, kh, vh)
+    if isinstance(rotary, Rotary):
+        qh = rotary_kv4_append(cache, table, kv_len, q_start, qh, kh, vh, rotary, offset, out=qh)
+    else:
+        if offset is not None:
+            raise ValueError("offset without a Rotary")
+        if rotary is not None:
+            qh, kh = rotary(qh, kh)
+        kv4_append(cache, table, kv_len, q_start, kh, vh)
     a = attn_kv4(qh, cache, table, kv_len, q_start, window=window, sinks=sinks, max_kv=max_kv)
     _, _, inner = block_norm_quant(a.view(yq.shape), gamma=gamma, eps=eps)
     return _matmuls(inner, [o])[0]

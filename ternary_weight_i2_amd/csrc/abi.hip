@@ -653,6 +653,86 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
     return ok();
 }
 
+static int check_plan(const char *fn, const bitnet_rotary_plan *p, int64_t dim) {
+    if (!p) return fail(BITNET_E_NULL, "%s: plan is NULL", fn);
+    if (p->rot < 2 || p->rot > dim || p->rot % 2 != 0)
+        return fail(BITNET_E_SHAPE, "%s: rot=%lld must be even and in [2, %lld]", fn,
+                    (long long)p->rot, (long long)dim);
+    if (!(p->magnitude > 0.0) || !(p->magnitude < 1e30))
+        return fail(BITNET_E_VALUE, "%s: magnitude must be positive and finite", fn);
+    return BITNET_OK;
+}
+static int check_turns(const char *fn, const bitnet_rotary_plan *p) {
+    if (!p->turns) return fail(BITNET_E_NULL, "%s: turns is NULL", fn);
+    if (!aligned(p->turns, 8)) return fail(BITNET_E_ALIGN, "%s: turns must be 8-byte aligned", fn);
+    return BITNET_OK;
+}
+
+BITNET_API int bitnet_rotary(const bitnet_rotary_plan *plan, const void *x, int64_t x_stride,
+                             int dtype, int64_t N, int64_t n_heads, int64_t head_dim,
+                             const int32_t *positions, int inverse, void *out, int64_t out_stride,
+                             void *stream) {
+    const char *fn = "bitnet_rotary";
+    if (dtype != BITNET_F32 && dtype != BITNET_BF16)
+        return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, dtype);
+    if (N < 0 || N > BITNET_GEMM_MAX_N)
+        return fail(BITNET_E_SHAPE, "%s: N=%lld outside [0, %d]", fn, (long long)N,
+                    BITNET_GEMM_MAX_N);
+    if (head_dim < 8 || head_dim > BITNET_ROTARY_MAX_DIM || head_dim % 8 != 0)
+        return fail(BITNET_E_SHAPE, "%s: head_dim=%lld must be a multiple of 8, at most %d", fn,
+                    (long long)head_dim, BITNET_ROTARY_MAX_DIM);
+    if (n_heads < 1 || n_heads > BITNET_KV4_MAX_HEADS)
+        return fail(BITNET_E_SHAPE, "%s: n_heads=%lld outside [1, %d]", fn, (long long)n_heads,
+                    BITNET_KV4_MAX_HEADS);
+    if (int s = check_plan(fn, plan, head_dim)) return s;
+    if (N == 0) return ok();
+    if (int s = check_turns(fn, plan)) return s;
+    const int64_t row = n_heads * head_dim;
+    if (int s = check_rows(fn, "x", x, x_stride, row, dtype)) return s;
+    if (int s = check_rows(fn, "out", out, out_stride, row, dtype)) return s;
+    if (out == x && out_stride != x_stride && N > 1)
+        return fail(BITNET_E_SHAPE, "%s: out is x with another stride", fn);
+    if (!positions) return fail(BITNET_E_NULL, "%s: positions is required", fn);
+    if (!aligned(positions, 4))
+        return fail(BITNET_E_ALIGN, "%s: positions must be 4-byte aligned", fn);
+    const bitnet::RotaryArgs r{plan->turns, plan->magnitude, inverse ? -1.0 : 1.0, (int)plan->rot,
+                               plan->interleaved != 0};
+    hipError_t e = bitnet::launch_rotary(r, x, x_stride, out, out_stride, dtype == BITNET_BF16, N,
+                                         (int)n_heads, (int)head_dim, positions,
+                                         static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+BITNET_API int bitnet_rotary_kv4_append(const bitnet_kv4_batch *batch,
+                                        const bitnet_rotary_plan *plan, const void *q,
+                                        int64_t q_stride, void *q_out, int64_t out_stride,
+                                        int64_t n_heads, const void *k, int64_t k_stride,
+                                        const void *v, int64_t v_stride, int dtype, int64_t N,
+                                        const int32_t *offset, void *stream) {
+    const char *fn = "bitnet_rotary_kv4_append";
+    if (int s = check_kv4(fn, batch, dtype, N)) return s;
+    if (int s = check_heads(fn, n_heads, batch->n_kv_heads)) return s;
+    if (int s = check_plan(fn, plan, batch->head_dim)) return s;
+    if (N == 0 || batch->n_seqs == 0) return ok();
+    if (int s = check_turns(fn, plan)) return s;
+    const int64_t row = batch->n_kv_heads * batch->head_dim, q_row = n_heads * batch->head_dim;
+    if (int s = check_rows(fn, "q", q, q_stride, q_row, dtype)) return s;
+    if (int s = check_rows(fn, "q_out", q_out, out_stride, q_row, dtype)) return s;
+    if (q_out == q && out_stride != q_stride && N > 1)
+        return fail(BITNET_E_SHAPE, "%s: q_out is q with another stride", fn);
+    if (int s = check_rows(fn, "k", k, k_stride, row, dtype)) return s;
+    if (int s = check_rows(fn, "v", v, v_stride, row, dtype)) return s;
+    if (!aligned(offset, 4)) return fail(BITNET_E_ALIGN, "%s: offset must be 4-byte aligned", fn);
+    const bitnet::RotaryArgs r{plan->turns, plan->magnitude, 1.0, (int)plan->rot,
+                               plan->interleaved != 0};
+    hipError_t e = bitnet::launch_rotary_append(
+        r, kv4_args(batch), q, q_stride, q_out, out_stride, (int)n_heads, k, k_stride, v, v_stride,
+        offset, dtype == BITNET_BF16, N, (int)batch->head_dim, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
 #ifdef BITNET_STAMPS
 // Instrumented build only (include/bitnet_i2s_stamps.h).
 namespace bitnet {

@@ -80,4 +80,121 @@ __device__ __forceinline__ bool row_in_call(const Kv4Args &c, int64_t r) {
     return r >= c.q_start[0] && r < c.q_start[c.n_seqs];
 }
 
+__device__ __forceinline__ float min8(float v) {   // over 8 aligned lanes
+    v = fminf(v, dpp_f32<kDppXor1>(v));
+    v = fminf(v, dpp_f32<kDppXor2>(v));
+    return fminf(v, dpp_f32<kDppHalfMirror>(v));
+}
+__device__ __forceinline__ float max8(float v) {
+    v = fmaxf(v, dpp_f32<kDppXor1>(v));
+    v = fmaxf(v, dpp_f32<kDppXor2>(v));
+    return fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+}
+
+// The group's pair (step in the low half) and this lane's eight codes.
+__device__ __forceinline__ uint32_t quantise8(float (&x)[8], uint32_t *pair) {
+#pragma clang fp contract(off)
+    float lo = kKv4Max, hi = -kKv4Max;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = __builtin_amdgcn_fmed3f(x[e], -kKv4Max, kKv4Max);   // a NaN becomes -kKv4Max
+        lo = fminf(lo, x[e]);
+        hi = fmaxf(hi, x[e]);
+    }
+    lo = min8(lo);
+    hi = max8(hi);
+    const _Float16 mid16 = (_Float16)(lo + (hi - lo) * (8.0f / 15.0f));
+    const float mid = (float)mid16;
+    const _Float16 step16 = (_Float16)fmaxf((hi - mid) * (1.0f / 7.0f), (mid - lo) * 0.125f);
+    const float step = (float)step16;
+    const float inv = step > 0.0f ? 1.0f / step : 0.0f;
+    // Adding 1.5 * 2^23 rounds the held value to an integer, half to even, and
+    // leaves it in the low bits above a constant; the constants of all eight are
+    // taken off at once.
+    constexpr uint32_t kMagic = 0x4b400000u;
+    uint32_t codes = 0u - kMagic * 0x11111111u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float t = (x[e] - mid) * inv;
+        const float c = __builtin_amdgcn_fmed3f(t + 8.0f, 0.0f, 15.0f) + 12582912.0f;
+        codes += __float_as_uint(c) << (4 * e);
+    }
+    *pair = (uint32_t)__builtin_bit_cast(uint16_t, step16) |
+            (uint32_t)__builtin_bit_cast(uint16_t, mid16) << 16;
+    return codes;
+}
+
+// The four positions [base, base + 4) of a workgroup, and their rows in the call.
+struct Block4 {
+    int page;           // its entry in the table (or -1): not looked at before a page is
+    int in_page;        // of base: a multiple of 4
+    int row;            // the call's row at base
+    uint32_t rows;      // bit t: the call has a row at base + t
+    int base, seq;      // its first position (negative: in front of the cache), its sequence
+    __device__ bool cached(const Kv4Args &c) const { return page >= 0 && page < c.n_pages; }
+};
+__device__ __forceinline__ Block4 find_block(const Kv4Args &c, int64_t N) {
+    Block4 k{-1, 0, 0, 0, 0, 0};
+    const SeqAt s = sequence_of<4, 2>(c, 1, blockIdx.x);
+    const int tile = (int)(blockIdx.x - ((uint32_t)s.begin / 4 + 2 * s.seq));
+    if (tile < 0 || s.begin < 0 || s.end <= s.begin || s.end > N) return k;
+    const int pos0 = s.held - (s.end - s.begin), base = (pos0 & ~3) + 4 * tile;
+    k.row = s.begin + base - pos0;
+    k.base = base;
+    k.seq = s.seq;
+    for (int t = 0; t < 4; ++t)
+        if (base + t >= pos0 && base + t < s.held) k.rows |= 1u << t;
+    if (base < 0 || !k.rows) return k;   // base is a multiple of 4: all four lie before 0
+    k.page = c.table[s.seq * c.max_pages + base / kPage];
+    k.in_page = base % kPage;
+    return k;
+}
+
+// A lane's codes and pairs of eight channels (8 p on) of four tokens, t0 on, into their
+// record: those tokens that `rows` has a bit for.
+template <int D>
+__device__ __forceinline__ void store_block4(uint8_t *rec, bool is_v, int t0, int p, uint32_t rows,
+                                             const uint32_t (&codes)[4], const uint32_t (&pair)[4]) {
+    using L = Kv4Page<D>;
+    const int g = p >> 3;
+    if (!is_v) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(rec) + t0 * (D / 8) + (p & 3) * L::kSteps + (p >> 2);
+        uint32_t *m = reinterpret_cast<uint32_t *>(rec + L::kKeyPairs) + t0 * L::kGroups + g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (!(rows >> t & 1)) continue;
+            w[t * (D / 8)] = codes[t];
+            if ((p & 7) == 0) m[t * L::kGroups] = pair[t];
+        }
+        return;
+    }
+    // halfwords [token] of this lane's two value lanes, and [step, mid][token]
+    uint16_t *w = reinterpret_cast<uint16_t *>(rec + L::kValues) +
+                  ((t0 >> 2) * 16 + 2 * (p & 7)) * L::kGroups * 4 + g * 4;
+    uint16_t *m = reinterpret_cast<uint16_t *>(rec + L::kValuePairs) +
+                  ((t0 >> 2) * L::kGroups + g) * 8;
+    if (rows == 15) {
+        auto low = [](uint32_t a, uint32_t b) { return (a & 0xffffu) | b << 16; };
+        auto high = [](uint32_t a, uint32_t b) { return a >> 16 | (b & 0xffff0000u); };
+        *reinterpret_cast<uint2 *>(w) = make_uint2(low(codes[0], codes[1]), low(codes[2], codes[3]));
+        *reinterpret_cast<uint2 *>(w + 4 * L::kGroups) =
+            make_uint2(high(codes[0], codes[1]), high(codes[2], codes[3]));
+        if ((p & 7) == 0)
+            *reinterpret_cast<uint4 *>(m) =
+                make_uint4(low(pair[0], pair[1]), low(pair[2], pair[3]),
+                           high(pair[0], pair[1]), high(pair[2], pair[3]));
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        if (!(rows >> t & 1)) continue;
+        w[t] = (uint16_t)codes[t];
+        w[4 * L::kGroups + t] = (uint16_t)(codes[t] >> 16);
+        if ((p & 7) == 0) {
+            m[t] = (uint16_t)pair[t];
+            m[4 + t] = (uint16_t)(pair[t] >> 16);
+        }
+    }
+}
+
 }  // namespace bitnet

@@ -37,6 +37,14 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
     const uint32_t u = __float_as_uint(v);
     return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
+// One value of a bf16 or fp32 row, read as fp32 and stored rounded to nearest even.
+template <bool BF16>
+__device__ __forceinline__ float load1(const void *p, int64_t i) {
+    if constexpr (BF16)
+        return __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16);
+    else
+        return static_cast<const float *>(p)[i];
+}
 // Eight consecutive values of a bf16 or fp32 row, as fp32.
 template <bool BF16>
 __device__ __forceinline__ void load8(const void *p, int64_t i, float (&x)[8]) {
@@ -86,6 +94,21 @@ hipError_t launch_kv4_append(const Kv4Args &c, const void *k, const void *v, int
                              hipStream_t st);
 hipError_t launch_kv4_read(const Kv4Args &c, void *k, void *v, int bf16, int64_t N, int dim,
                            hipStream_t st);
+// Rotary positions (rotary.hip): turns per position of each pair of channels, as 64-bit
+// fractions of one.
+struct RotaryArgs {
+    const int64_t *turns;
+    double magnitude, sign;   // sign: -1 turns back
+    int rot, interleaved;
+};
+hipError_t launch_rotary(const RotaryArgs &r, const void *x, int64_t x_stride, void *out,
+                         int64_t out_stride, int bf16, int64_t N, int heads, int dim,
+                         const int32_t *positions, hipStream_t st);
+hipError_t launch_rotary_append(const RotaryArgs &r, const Kv4Args &c, const void *q,
+                                int64_t q_stride, void *q_out, int64_t out_stride, int heads,
+                                const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                const int32_t *offset, int bf16, int64_t N, int dim,
+                                hipStream_t st);
 struct Attn4Args {
     Kv4Args c;
     const void *q;

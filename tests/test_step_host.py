@@ -1,0 +1,100 @@
+"""Host-side refusals of the operators around a decode step (CPU only: nothing is launched,
+fake pointers are never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+from test_layer_host import FAKE, MIS, OK, E_ALIGN, E_DTYPE, E_NULL, E_SHAPE, E_VALUE, _batch
+
+
+@pytest.fixture(scope="module")
+def L():
+    from ternary_weight_i2_amd import _binding
+    return _binding.load()
+
+
+def _plan(**kw):
+    from ternary_weight_i2_amd import RotaryPlan
+    return ctypes.byref(RotaryPlan(*dict(dict(turns=FAKE, rot=64, inter=0, magnitude=1.0), **kw).values()))
+
+
+ROTARY = {
+    "rotary": lambda L, plan=None, x=FAKE, xs=128, dt=0, N=3, heads=2, dim=64, at=FAKE, out=2 * FAKE, os=128:
+        L.bitnet_rotary(plan or _plan(), x, xs, dt, N, heads, dim, at, 0, out, os, None),
+    "append": lambda L, plan=None, b=None, x=FAKE, xs=256, dt=0, N=3, heads=4, out=2 * FAKE, os=256, k=FAKE, ks=128,
+        v=FAKE, vs=128, off=FAKE:
+        L.bitnet_rotary_kv4_append(b or _batch(), plan or _plan(), x, xs, out, os, heads, k, ks, v, vs, dt, N,
+                                   off, None),
+}
+
+
+@pytest.mark.parametrize("name", ROTARY)
+def test_rotary_validation(L, name):
+    f = ROTARY[name]
+    assert f(L, dt=2) == E_DTYPE
+    assert f(L, N=-1) == E_SHAPE and f(L, N=(1 << 21) + 1) == E_SHAPE
+    for rot in (0, -2, 3, 63, 66, 1 << 40):
+        assert f(L, plan=_plan(rot=rot)) == E_SHAPE
+    for m in (0.0, -1.0, float("inf"), float("nan"), 1e31):
+        assert f(L, plan=_plan(magnitude=m)) == E_VALUE
+    assert f(L, plan=_plan(turns=None)) == E_NULL and f(L, plan=_plan(turns=MIS)) == E_ALIGN
+    assert f(L, x=None) == E_NULL and f(L, out=None) == E_NULL
+    assert f(L, x=MIS) == E_ALIGN and f(L, out=MIS) == E_ALIGN
+    for s in ("xs", "os"):
+        for bad in (127, 0, -256, 1 << 41, 258):
+            assert f(L, **{s: bad}) == E_SHAPE
+    assert f(L, out=FAKE, os=512) == E_SHAPE        # in place with another stride
+    for heads in (0, -1, 1025):
+        assert f(L, heads=heads) == E_SHAPE
+    assert f(L, N=0, x=None, out=None) == OK and L.bitnet_last_error().decode() == ""
+
+
+def test_rotary_alone_validation(L):
+    f = ROTARY["rotary"]
+    for dim in (0, 4, 60, -64, 1032):
+        assert f(L, dim=dim, plan=_plan(rot=2)) == E_SHAPE
+    assert f(L, at=None) == E_NULL and f(L, at=FAKE + 2) == E_ALIGN
+    assert L.bitnet_rotary(None, FAKE, 128, 0, 3, 2, 64, FAKE, 0, FAKE, 128, None) == E_NULL
+
+
+def test_rotary_append_validation(L):
+    f = ROTARY["append"]
+    assert L.bitnet_rotary_kv4_append(None, _plan(), FAKE, 256, FAKE, 256, 4, FAKE, 128, FAKE, 128, 0, 3, None,
+                                      None) == E_NULL
+    assert f(L, b=_batch(head_dim=96)) == E_SHAPE and f(L, b=_batch(table=None)) == E_NULL
+    assert f(L, heads=3) == E_SHAPE
+    for p in ("k", "v"):
+        assert f(L, **{p: None}) == E_NULL and f(L, **{p: MIS}) == E_ALIGN
+        assert f(L, **{p + "s": 64}) == E_SHAPE
+    assert f(L, off=FAKE + 2) == E_ALIGN
+
+
+def test_rotary_binding_refuses():
+    import ternary_weight_i2_amd as bn
+    t = torch.zeros(32, dtype=torch.int64)
+    with pytest.raises(TypeError):
+        bn.Rotary(t.int())
+    with pytest.raises(TypeError):
+        bn.Rotary(torch.zeros((2, 4), dtype=torch.int64))
+    with pytest.raises(TypeError):
+        bn.Rotary(torch.zeros(64, dtype=torch.int64)[::2])
+    p, at = bn.Rotary(t), torch.zeros(3, dtype=torch.int32)
+    x = torch.zeros((3, 2, 64))
+    for bad in (dict(x=x[0]), dict(x=x.to(torch.float16)), dict(at=at.long()), dict(at=at[:2]), dict(x=x[:, :, :63]),
+                dict(x=x.transpose(0, 1)), dict(out=x[:2]), dict(out=x.bfloat16()), dict()):
+        with pytest.raises((ValueError, TypeError)):    # the last: not on a GPU
+            bn.rotary(bad.get("x", x), p, bad.get("at", at), out=bad.get("out"))
+    for kw in (dict(rot=3), dict(rot=0), dict(rot=4, freqs=[1.0]), dict(rot=4, freqs=[1.0, float("nan")]),
+               dict(rot=4, factor=0.0), dict(rot=4, length=-1), dict(rot=4, length=5, low=3, high=3)):
+        with pytest.raises(ValueError):
+            bn.rotary_plan(**kw, device="cpu")
+    c, table = torch.zeros((2, 1, 72 * 64), dtype=torch.uint8), torch.zeros((1, 1), dtype=torch.int32)
+    one, start = torch.ones(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    q, k = torch.zeros((1, 2, 64)), torch.zeros((1, 1, 64))
+    for bad in (dict(q=q.bfloat16()), dict(q=q[:0]), dict(v=k.bfloat16()), dict(off=one.long()), dict(out=k), dict()):
+        with pytest.raises((ValueError, TypeError)):
+            bn.rotary_kv4_append(c, table, one, start, bad.get("q", q), k, bad.get("v", k), p,
+                                 offset=bad.get("off"), out=bad.get("out"))
+    with pytest.raises((ValueError, TypeError)):        # a slice that no aligned load can take
+        bn.rotary(torch.zeros((3, 2, 65))[:, :, 1:], p, at)
