@@ -53,6 +53,7 @@ extern "C" {
 #define BITNET_KV4_MAX_HEADS 1024   /* query heads, and kv heads, of a call    */
 #define BITNET_KV4_MAX_SEQS (1 << 20)  /* sequences of a call                  */
 #define BITNET_KV4_MAX_PAGES (1 << 24) /* pages of a sequence (2^30 tokens)    */
+#define BITNET_W4_MAX_ROWS (1 << 24) /* rows of a matrix of 4-bit weights      */
 #define BITNET_ROTARY_MAX_DIM 1024  /* channels of a head that positions turn   */
 
 typedef enum {
@@ -489,6 +490,69 @@ int bitnet_rotary_kv4_append(const bitnet_kv4_batch *batch, const bitnet_rotary_
                              int64_t n_heads, const void *k, int64_t k_stride, const void *v,
                              int64_t v_stride, int dtype, int64_t N, const int32_t *offset,
                              void *stream);
+
+/*
+ * Matrices of 4-bit weights, for what a ternary model keeps finer than ternary (its output
+ * head, its embedding).  A weight is step * (code - 8): a code of 4 bits each, a step (fp16,
+ * of either sign) for each row and group of 32, 64 or 128 channels.
+ *
+ * Rows lie in tiles of 16 (rows behind the last are zeros), channels in blocks of 128, codes
+ * as dwords of 8 channels, the first in the low bits:
+ *   codes  [ceil(M/16)][K/128][4 quads][16 rows][4] dwords: dword (quad, row, j) has the
+ *          block's channels 32 j + 8 quad + 0..7
+ *   steps  [ceil(M/16)][K/128][16 rows][128/group] fp16
+ */
+typedef struct {
+    void *codes;            /* DEVICE, 16-byte aligned, ceil(M/16) * 8 * K bytes */
+    void *steps;            /* DEVICE, 16-byte aligned, ceil(M/16) * 32 * K / group bytes */
+    int64_t M;              /* 0 .. BITNET_W4_MAX_ROWS */
+    int64_t K;              /* as K of the other matmuls */
+    int64_t group;          /* 32, 64 or 128 */
+} bitnet_w4_matrix;
+
+/*
+ * bitnet_pack_w4 -- weights quantised into `mat`, group by group (every operation one
+ * fp32 rounding):
+ *   w is held to [-458528, 458528] (a NaN counts as 0); lo, hi the group's ends
+ *   step = fp16(max(hi * fp32(1/7), -lo / 8))   (a zero is +0)
+ *   code = clamp(round_half_even(w * fp32(1/step)), -8, 7) + 8; 8 if step is 0
+ *
+ *   w        [M][K] fp32 or bf16, 16-byte aligned.
+ *
+ * bitnet_pack_w4_codes -- weights that are 4-bit already: w [M][K] int8 in -8 .. 7 (held to
+ * that), 8-byte aligned, and their steps given [M][K/group] fp16, 2-byte aligned.
+ *
+ * Both only enqueue.  M == 0 is a no-op.
+ */
+int bitnet_pack_w4(const void *w, int dtype, const bitnet_w4_matrix *mat, void *stream);
+int bitnet_pack_w4_codes(const int8_t *w, const void *given, const bitnet_w4_matrix *mat,
+                         void *stream);
+
+/*
+ * bitnet_w4_rows -- rows of the matrix as fp32 or bf16 (the fp32 value rounded to nearest even):
+ * an embedding's lookup, or the weights read back.
+ *
+ *   ids      DEVICE [n] int32 row numbers, or NULL for rows 0 .. n-1.  One outside [0, M)
+ *            gives zeros.
+ *   out      [n][K], 16-byte aligned.  0 <= n <= BITNET_GEMM_MAX_N.
+ */
+int bitnet_w4_rows(const bitnet_w4_matrix *mat, const int32_t *ids, int64_t n, void *out,
+                   int dtype, void *stream);
+
+/*
+ * bitnet_linear_w4 -- y[n][m] = sum_k x[n][k] * weight[m][k], for one token and for many.
+ *
+ *   x        [N][K] fp32 or bf16, 16-byte aligned.
+ *   y        [N][M] fp32, 4-byte aligned.
+ *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or M == 0 is a no-op.
+ * A token's channels are carried in 22 bits (fp32; bf16 exactly) and no finer than 2^-40 of
+ * the largest of their 128 (bf16: 2^-39); products and sums are fp32, so where the sum of
+ * |x * weight| reaches 2^127 the result is unspecified.  A token with a NaN
+ * or an infinity gives unspecified results, in its own row only.  Repeated calls give
+ * identical bits.
+ */
+int bitnet_linear_w4(const void *x, int dtype, int64_t N, const bitnet_w4_matrix *mat, float *y,
+                     void *stream);
 
 /* Thread-local description of the last non-OK status on this thread
  * (empty string if none).  The pointer stays valid until the next call on

@@ -52,6 +52,12 @@ class RotaryPlan(ctypes.Structure):
                 ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_double)]
 
 
+class W4Desc(ctypes.Structure):
+    """Mirror of bitnet_w4_matrix."""
+    _fields_ = [("codes", ctypes.c_void_p), ("steps", ctypes.c_void_p), ("M", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("group", ctypes.c_int64)]
+
+
 class BitnetError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"bitnet status {status}: {msg}")
@@ -152,6 +158,11 @@ def _open(path: str) -> ctypes.CDLL:
     L.bitnet_rotary_kv4_append.argtypes = [kv4, plan, p, i64, p, i64, i64, p, i64, p, i64, i32, i64,
                                            p, p]
     L.bitnet_rotary_kv4_append.restype = ctypes.c_int
+    w4 = ctypes.POINTER(W4Desc)
+    for fn, args in (("bitnet_pack_w4", [p, i32, w4, p]), ("bitnet_pack_w4_codes", [p, p, w4, p]),
+                     ("bitnet_w4_rows", [w4, p, i64, p, i32, p]),
+                     ("bitnet_linear_w4", [p, i32, i64, w4, p, p])):
+        getattr(L, fn).argtypes, getattr(L, fn).restype = args, ctypes.c_int
     for fn in ("bitnet_pack_i2s", "bitnet_quant_act_i8", "bitnet_gemv_i2s_i8",
                "bitnet_gemm_i2s_i8", "bitnet_gemv_i2s_lut", "bitnet_abi_version"):
         getattr(L, fn).restype = ctypes.c_int
@@ -774,6 +785,105 @@ def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window=
     if need < 0:
         raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
     return need
+
+
+class W4Matrix:
+    """A matrix of 4-bit weights [M][K] as pack_w4 lays it out: ``codes`` uint8
+    [ceil(M/16)][K/128][64][16], ``steps`` fp16 [ceil(M/16)][K/128][16][128/group], and the number of its
+    ``rows`` M (all of the tiles' if None)."""
+    __slots__ = ("codes", "steps", "rows", "k", "group", "_desc")
+
+    def __init__(self, codes, steps, rows=None):
+        import torch
+        if codes.dim() != 4 or codes.dtype != torch.uint8 or codes.shape[2:] != (64, 16):
+            raise TypeError("codes must be uint8 [tiles][K/128][64][16]")
+        if steps.dim() != 4 or steps.dtype != torch.float16 or steps.shape[3] not in (1, 2, 4) or \
+                steps.shape[:3] != (codes.shape[0], codes.shape[1], 16):
+            raise TypeError("steps must be float16 [tiles][K/128][16][128/group]")
+        if steps.device != codes.device or not codes.is_contiguous() or not steps.is_contiguous():
+            raise ValueError("codes and steps must be contiguous, on one device")
+        tiles, blocks = codes.shape[:2]
+        self.rows = 16 * tiles if rows is None else rows
+        if not 16 * (tiles - 1) < self.rows <= 16 * tiles and (tiles or self.rows):
+            raise ValueError(f"{self.rows} rows are not {tiles} tiles of 16")
+        self.codes, self.steps, self.k, self.group = codes, steps, 128 * blocks, 128 // steps.shape[3]
+        self._desc = W4Desc(codes.data_ptr(), steps.data_ptr(), self.rows, self.k, self.group)
+
+    @classmethod
+    def empty(cls, rows, k, group=64, device="cuda"):
+        """An uninitialised matrix, for pack_w4's ``out``."""
+        import torch
+        if k % 128 or group not in (32, 64, 128):
+            raise ValueError(f"K={k} must be a multiple of 128 and group={group} 32, 64 or 128")
+        tiles = -(-rows // 16)
+        return cls(torch.empty((tiles, k // 128, 64, 16), dtype=torch.uint8, device=device),
+                   torch.empty((tiles, k // 128, 16, 128 // group), dtype=torch.float16, device=device), rows)
+
+
+def _w4_out(out, shape, group, device):
+    if out is None:
+        return W4Matrix.empty(*shape, group, device)
+    if (out.rows, out.k, out.group) != (*shape, group) or out.codes.device != device:
+        raise ValueError(f"out must be a {shape[0]} x {shape[1]} matrix of group {group} on {device}")
+    return out
+
+
+def pack_w4(w, group=64, out=None):
+    """fp32 or bf16 weights w[M][K] (cuda) -> a W4Matrix: 4 bits a weight and a step for each
+    ``group`` (32, 64 or 128) channels of a row."""
+    if w.dim() != 2 or not w.is_contiguous():
+        raise TypeError("w must be 2-D [M][K] and contiguous")
+    code = _float_code(w.dtype, "w")
+    out = _w4_out(out, tuple(w.shape), group, w.device)
+    _launch(load().bitnet_pack_w4, w.device, w.data_ptr(), code, out._desc)
+    return out
+
+
+def pack_w4_codes(w, steps, out=None):
+    """Weights that are 4-bit already: int8 w[M][K] in -8 .. 7 and fp16 steps [M][K/group] ->
+    a W4Matrix."""
+    import torch
+    if w.dim() != 2 or w.dtype != torch.int8 or not w.is_contiguous():
+        raise TypeError("w must be int8 [M][K] and contiguous")
+    M, K = w.shape
+    if steps.dim() != 2 or steps.shape[1] == 0 or K % steps.shape[1]:
+        raise ValueError("steps must be 2-D [M][K/group]")
+    group = K // steps.shape[1]
+    at = _at(steps, "steps", torch.float16, (M, K // group), w.device)
+    out = _w4_out(out, (M, K), group, w.device)
+    _launch(load().bitnet_pack_w4_codes, w.device, w.data_ptr(), at, out._desc)
+    return out
+
+
+def w4_rows(mat, ids=None, dtype=None, out=None):
+    """Rows ``ids`` (int32, on the device; all rows if None) of a W4Matrix as fp32 or bf16
+    [n][K]: an embedding's lookup.  An id outside the matrix gives zeros."""
+    import torch
+    dev = mat.codes.device
+    n = mat.rows if ids is None else ids.shape[0]
+    if out is None:
+        dtype = dtype or torch.float32
+        out = torch.empty((n, mat.k), dtype=dtype, device=dev)
+    at = _at(out, "out", dtype or out.dtype, (n, mat.k), dev)
+    _launch(load().bitnet_w4_rows, dev, mat._desc, _at(ids, "ids", torch.int32, (n,), dev), n, at,
+            _float_code(out.dtype, "out"))
+    return out
+
+
+def linear_w4(x, mat, out=None):
+    """x [N][K] (fp32 or bf16, any N) times a W4Matrix -> y [N][M] fp32."""
+    import torch
+    if x.dim() != 2 or x.shape[1] != mat.k:
+        raise ValueError(f"x must be 2-D [N][{mat.k}], got {tuple(x.shape)}")
+    N, dev = x.shape[0], mat.codes.device
+    at = _at(x, "x", x.dtype, x.shape, dev)
+    if out is None:
+        out = torch.empty((N, mat.rows), dtype=torch.float32, device=dev)
+        to = out.data_ptr()
+    else:
+        to = _at(out, "out", torch.float32, (N, mat.rows), dev)
+    _launch(load().bitnet_linear_w4, dev, at, _float_code(x.dtype, "x"), N, mat._desc, to)
+    return out
 
 
 def _matmuls(tokens, mats):

@@ -733,6 +733,95 @@ BITNET_API int bitnet_rotary_kv4_append(const bitnet_kv4_batch *batch,
     return ok();
 }
 
+static int check_w4(const char *fn, const bitnet_w4_matrix *m) {
+    if (!m) return fail(BITNET_E_NULL, "%s: mat is NULL", fn);
+    if (m->M < 0 || m->M > BITNET_W4_MAX_ROWS)
+        return fail(BITNET_E_SHAPE, "%s: M=%lld outside [0, %d]", fn, (long long)m->M,
+                    BITNET_W4_MAX_ROWS);
+    if (int s = check_k(fn, m->K)) return s;
+    if (m->group != 32 && m->group != 64 && m->group != 128)
+        return fail(BITNET_E_SHAPE, "%s: group=%lld must be 32, 64 or 128", fn, (long long)m->group);
+    if (m->M == 0) return BITNET_OK;
+    if (!m->codes || !m->steps) return fail(BITNET_E_NULL, "%s: codes and steps are required", fn);
+    if (!aligned(m->codes, 16) || !aligned(m->steps, 16))
+        return fail(BITNET_E_ALIGN, "%s: codes and steps must be 16-byte aligned", fn);
+    return BITNET_OK;
+}
+static bitnet::W4Args w4_args(const bitnet_w4_matrix *m) {
+    return bitnet::W4Args{static_cast<const uint8_t *>(m->codes),
+                          static_cast<const uint16_t *>(m->steps), (int)m->M, (int)m->K,
+                          (int)(128 / m->group)};
+}
+static int pack_w4(const char *fn, const void *w, int form, const void *given,
+                   const bitnet_w4_matrix *m, void *stream) {
+    hipError_t e = bitnet::launch_w4_pack(w, form, static_cast<const uint16_t *>(given), m->M, m->K,
+                                          (int)(128 / m->group), static_cast<uint8_t *>(m->codes),
+                                          static_cast<uint16_t *>(m->steps),
+                                          static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+BITNET_API int bitnet_pack_w4(const void *w, int dtype, const bitnet_w4_matrix *mat, void *stream) {
+    const char *fn = "bitnet_pack_w4";
+    if (dtype != BITNET_F32 && dtype != BITNET_BF16)
+        return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, dtype);
+    if (int s = check_w4(fn, mat)) return s;
+    if (mat->M == 0) return ok();
+    if (!w) return fail(BITNET_E_NULL, "%s: w is required", fn);
+    if (!aligned(w, 16)) return fail(BITNET_E_ALIGN, "%s: w must be 16-byte aligned", fn);
+    return pack_w4(fn, w, dtype == BITNET_BF16, nullptr, mat, stream);
+}
+
+BITNET_API int bitnet_pack_w4_codes(const int8_t *w, const void *given, const bitnet_w4_matrix *mat,
+                                    void *stream) {
+    const char *fn = "bitnet_pack_w4_codes";
+    if (int s = check_w4(fn, mat)) return s;
+    if (mat->M == 0) return ok();
+    if (!w || !given) return fail(BITNET_E_NULL, "%s: w and given are required", fn);
+    if (!aligned(w, 8) || !aligned(given, 2))
+        return fail(BITNET_E_ALIGN, "%s: w must be 8-byte and given 2-byte aligned", fn);
+    return pack_w4(fn, w, 2, given, mat, stream);
+}
+
+BITNET_API int bitnet_w4_rows(const bitnet_w4_matrix *mat, const int32_t *ids, int64_t n, void *out,
+                              int dtype, void *stream) {
+    const char *fn = "bitnet_w4_rows";
+    if (dtype != BITNET_F32 && dtype != BITNET_BF16)
+        return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, dtype);
+    if (n < 0 || n > BITNET_GEMM_MAX_N)
+        return fail(BITNET_E_SHAPE, "%s: n=%lld outside [0, %d]", fn, (long long)n,
+                    BITNET_GEMM_MAX_N);
+    if (int s = check_w4(fn, mat)) return s;
+    if (n == 0) return ok();
+    if (!out) return fail(BITNET_E_NULL, "%s: out is required", fn);
+    if (!aligned(out, 16)) return fail(BITNET_E_ALIGN, "%s: out must be 16-byte aligned", fn);
+    if (!aligned(ids, 4)) return fail(BITNET_E_ALIGN, "%s: ids must be 4-byte aligned", fn);
+    hipError_t e = bitnet::launch_w4_rows(w4_args(mat), ids, n, out, dtype == BITNET_BF16,
+                                          static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+BITNET_API int bitnet_linear_w4(const void *x, int dtype, int64_t N, const bitnet_w4_matrix *mat,
+                                float *y, void *stream) {
+    const char *fn = "bitnet_linear_w4";
+    if (dtype != BITNET_F32 && dtype != BITNET_BF16)
+        return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, dtype);
+    if (N < 0 || N > BITNET_GEMM_MAX_N)
+        return fail(BITNET_E_SHAPE, "%s: N=%lld outside [0, %d]", fn, (long long)N,
+                    BITNET_GEMM_MAX_N);
+    if (int s = check_w4(fn, mat)) return s;
+    if (N == 0 || mat->M == 0) return ok();
+    if (!x || !y) return fail(BITNET_E_NULL, "%s: x and y are required", fn);
+    if (!aligned(x, 16) || !aligned(y, 4))
+        return fail(BITNET_E_ALIGN, "%s: x must be 16-byte and y 4-byte aligned", fn);
+    hipError_t e = bitnet::launch_w4_linear(w4_args(mat), x, dtype == BITNET_BF16, N, y,
+                                            static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
 #ifdef BITNET_STAMPS
 // Instrumented build only (include/bitnet_i2s_stamps.h).
 namespace bitnet {

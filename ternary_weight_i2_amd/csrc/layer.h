@@ -64,6 +64,21 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, float (&x)[8]) {
     }
 }
 
+// Stores eight values, bf16 rounded to nearest even.
+template <bool BF16>
+__device__ __forceinline__ void store8_values(void *p, int64_t i, const float (&x)[8]) {
+    if constexpr (BF16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = bf16_bits(x[2 * e]) | bf16_bits(x[2 * e + 1]) << 16;
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+        f[0] = make_float4(x[0], x[1], x[2], x[3]);
+        f[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
 // ---- launchers (each returns the hipError_t of its launch) ---------------
 // The boundary between two blocks: norm, gate, scale, residual, norm, tokens;
 // one workgroup per token (F a multiple of 128, at most 32768).
@@ -109,6 +124,18 @@ hipError_t launch_rotary_append(const RotaryArgs &r, const Kv4Args &c, const voi
                                 const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                 const int32_t *offset, int bf16, int64_t N, int dim,
                                 hipStream_t st);
+// A matrix of 4-bit weights (w4.hip has its layout); groups: steps of a row's 128 channels.
+struct W4Args {
+    const uint8_t *codes;
+    const uint16_t *steps;
+    int M, K, groups;
+};
+hipError_t launch_w4_pack(const void *w, int form, const uint16_t *given, int64_t M, int64_t K,
+                          int groups, uint8_t *codes, uint16_t *steps, hipStream_t st);
+hipError_t launch_w4_rows(const W4Args &w, const int32_t *ids, int64_t n, void *out, int bf16,
+                          hipStream_t st);
+hipError_t launch_w4_linear(const W4Args &w, const void *x, int bf16, int64_t N, float *y,
+                            hipStream_t st);
 struct Attn4Args {
     Kv4Args c;
     const void *q;

@@ -61,19 +61,6 @@ __device__ __forceinline__ void put1(void *p, int64_t i, float v) {
     if constexpr (BF16) static_cast<uint16_t *>(p)[i] = (uint16_t)bf16_bits(v);
     else static_cast<float *>(p)[i] = v;
 }
-template <bool BF16>
-__device__ __forceinline__ void put8(void *p, int64_t i, const float (&x)[8]) {
-    if constexpr (BF16) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = bf16_bits(x[2 * e]) | bf16_bits(x[2 * e + 1]) << 16;
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-}
 
 // How a row is cut into a thread's items.  kHalves: eight pairs (i, i + rot/2), read and
 // written as two runs of eight channels, rot a multiple of 16; kNeighbours: eight
@@ -104,13 +91,13 @@ __device__ __forceinline__ void turn_item(const void *x, int64_t xi, void *out, 
                 a[e] = t.x;
                 b[e] = t.y;
             }
-            put8<BF16>(out, oi + 8 * j, a);
-            put8<BF16>(out, oi + rot / 2 + 8 * j, b);
+            store8_values<BF16>(out, oi + 8 * j, a);
+            store8_values<BF16>(out, oi + rot / 2 + 8 * j, b);
         } else {
             const int ch = rot + 8 * (j - rot / 16);
             float a[8];
             load8<BF16>(x, xi + ch, a);
-            put8<BF16>(out, oi + ch, a);
+            store8_values<BF16>(out, oi + ch, a);
         }
     } else if constexpr (CUT == kNeighbours) {
         float a[8];
@@ -122,7 +109,7 @@ __device__ __forceinline__ void turn_item(const void *x, int64_t xi, void *out, 
             a[e] = t.x;
             a[e + 1] = t.y;
         }
-        put8<BF16>(out, oi + 8 * j, a);
+        store8_values<BF16>(out, oi + 8 * j, a);
     } else {
         const int h = rot / 2;
         if (j < h) {

@@ -38,3 +38,59 @@ def rotate(x, turns, positions, interleaved=False, magnitude=1.0, inverse=False,
         p, q = lo.times(x[..., b], c), lo.times(x[..., a], s)
         out[..., b] = (p.astype(F8) + q.astype(F8)).astype(F4)
     return lo.bf16(out) if half else out
+
+
+# ---------------------------------------------------------------- 4-bit weights
+
+W4_TOP = F4(7 * 65504.0)
+
+
+def w4_quantise(w, group):
+    """w [M][K] -> codes [M][K] in -8..7 and steps [M][K / group] (fp16)."""
+    w = np.where(np.isnan(w), F4(0), np.clip(np.asarray(w, F4), -W4_TOP, W4_TOP))
+    g = w.reshape(w.shape[0], -1, group)
+    # a step of 0 is +0: one of the two ends is
+    step = (np.maximum(lo.times(g.max(2), F4(1 / 7)), lo.times(g.min(2), F4(-0.125))) + F4(0)).astype(np.float16)
+    with np.errstate(divide="ignore"):
+        inv = np.where(step > 0, F4(1) / step.astype(F4), F4(0))
+    code = np.clip(np.rint(lo.times(g, inv[..., None])), -8, 7)
+    return code.reshape(w.shape).astype(np.int8), step
+
+
+def w4_layout(codes, steps):
+    """codes [M][K] in -8..7, steps [M][K / group] -> the arrays that a matrix consists of."""
+    M, K = codes.shape
+    tiles, blocks, per = -(-M // 16), K // 128, 128 * steps.shape[1] // K
+    c = np.zeros((16 * tiles, K), np.int64)
+    c[:M] = codes
+    s = np.zeros((16 * tiles, steps.shape[1]), np.float16)
+    s[:M] = steps
+    out = np.zeros((tiles, blocks, 64, 16), np.uint8)
+    for quad in range(4):
+        for row in range(16):
+            for j in range(4):
+                for e in range(8):
+                    col = 128 * np.arange(blocks) + 32 * j + 8 * quad + e
+                    code = (c[row::16][:, col] + 8).astype(np.uint8)
+                    out[:, :, quad * 16 + row, 4 * j + e // 2] |= code << (4 * (e % 2))
+    return out, s.reshape(tiles, 16, blocks, per).transpose(0, 2, 1, 3).copy()
+
+
+def w4_values(codes, steps):
+    return (codes.astype(F8).reshape(codes.shape[0], steps.shape[1], -1) * steps.astype(F8)[..., None]).reshape(codes.shape)
+
+
+def w4_linear(x, w, group, half):
+    """y in binary64 and a bound on what the product may be off by:
+    * x is carried in two fp16 terms: hi is off by 2^-12 of its value, and what is left by
+      2^-12 of that, 2^-24; 2^-23 covers both, and 2^-41 of the block's largest is the
+      half step of the smallest fp16 at a largest of 2^15 (bf16: nothing, and 2^-40);
+    * step * scale is exact; K + K / group + 16 fp32 roundings of at most 2^-24 of sum |x w|
+      each, taken as independent: six standard deviations."""
+    a, b = np.asarray(x, F8), np.asarray(w, F8)
+    mag = np.abs(a) @ np.abs(b).T
+    K = a.shape[1]
+    top = np.abs(a.reshape(len(a), -1, 128)).max(2)
+    tol = (0 if half else 2.0 ** -23) * mag
+    tol += 2.0 ** (-40 if half else -41) * (top @ np.abs(b).reshape(len(b), -1, 128).sum(2).T)
+    return a @ b.T, tol + 6 * np.sqrt(K + K // group + 16) * 2.0 ** -24 * mag

@@ -98,3 +98,88 @@ def test_rotary_binding_refuses():
                                  offset=bad.get("off"), out=bad.get("out"))
     with pytest.raises((ValueError, TypeError)):        # a slice that no aligned load can take
         bn.rotary(torch.zeros((3, 2, 65))[:, :, 1:], p, at)
+
+
+# ---------------------------------------------------------------- 4-bit weights
+
+def _mat(**kw):
+    from ternary_weight_i2_amd import W4Desc
+    return ctypes.byref(W4Desc(*dict(dict(codes=FAKE, steps=FAKE, M=20, K=256, group=64), **kw).values()))
+
+
+W4 = {
+    "pack": lambda L, m=None, dt=0, w=FAKE: L.bitnet_pack_w4(w, dt, m or _mat(), None),
+    "codes": lambda L, m=None, w=FAKE, s=FAKE: L.bitnet_pack_w4_codes(w, s, m or _mat(), None),
+    "rows": lambda L, m=None, dt=0, ids=FAKE, n=3, out=FAKE: L.bitnet_w4_rows(m or _mat(), ids, n, out, dt, None),
+    "linear": lambda L, m=None, dt=0, x=FAKE, N=3, y=FAKE: L.bitnet_linear_w4(x, dt, N, m or _mat(), y, None),
+}
+
+
+@pytest.mark.parametrize("name", W4)
+def test_w4_matrix_validation(L, name):
+    f = W4[name]
+    assert f(L, _mat(M=-1)) == E_SHAPE and f(L, _mat(M=(1 << 24) + 1)) == E_SHAPE
+    for k in (0, 64, 100, -128, 32768 + 128):
+        assert f(L, _mat(K=k)) == E_SHAPE
+    for g in (0, 16, 48, 256, -64):
+        assert f(L, _mat(group=g)) == E_SHAPE
+    for p in ("codes", "steps"):
+        assert f(L, _mat(**{p: None})) == E_NULL and f(L, _mat(**{p: MIS})) == E_ALIGN
+    if name != "codes":
+        assert f(L, dt=2) == E_DTYPE
+    if name != "rows":
+        assert f(L, _mat(M=0, codes=None, steps=None)) == OK
+    assert {"pack": L.bitnet_pack_w4, "codes": L.bitnet_pack_w4_codes}.get(
+        name, lambda *a: E_NULL)(FAKE, 0 if name == "pack" else FAKE, None, None) == E_NULL
+
+
+def test_w4_operand_validation(L):
+    assert W4["pack"](L, w=None) == E_NULL and W4["pack"](L, w=MIS) == E_ALIGN
+    assert W4["codes"](L, w=None) == E_NULL and W4["codes"](L, s=None) == E_NULL
+    assert W4["codes"](L, w=MIS) == E_ALIGN and W4["codes"](L, s=FAKE + 1) == E_ALIGN
+    f = W4["rows"]
+    assert f(L, n=-1) == E_SHAPE and f(L, n=(1 << 21) + 1) == E_SHAPE
+    assert f(L, out=None) == E_NULL and f(L, out=MIS) == E_ALIGN and f(L, ids=FAKE + 2) == E_ALIGN
+    assert f(L, n=0, out=None) == OK
+    f = W4["linear"]
+    assert f(L, N=-1) == E_SHAPE and f(L, N=(1 << 21) + 1) == E_SHAPE
+    assert f(L, x=None) == E_NULL and f(L, y=None) == E_NULL
+    assert f(L, x=MIS) == E_ALIGN and f(L, y=FAKE + 2) == E_ALIGN
+    assert f(L, N=0, x=None, y=None) == OK and L.bitnet_last_error().decode() == ""
+
+
+def test_w4_binding_refuses():
+    import ternary_weight_i2_amd as bn
+    m = bn.W4Matrix.empty(20, 256, 64, device="cpu")
+    assert m.codes.shape == (2, 2, 64, 16) and m.steps.shape == (2, 2, 16, 2) and (m.rows, m.k, m.group) == (20, 256, 64)
+    assert bn.W4Matrix(m.codes, m.steps).rows == 32
+    for rows in (16, 33, 0, -1):
+        with pytest.raises(ValueError):
+            bn.W4Matrix(m.codes, m.steps, rows)
+    for c, s in ((m.codes[:1], m.steps), (m.codes.view(2, 2, 16, 64), m.steps), (m.codes.to(torch.int8), m.steps),
+                 (m.codes, m.steps.float()), (m.codes, m.steps[..., :0]), (m.codes, m.steps.view(2, 2, 32, 1)),
+                 (m.codes.transpose(0, 1), m.steps)):
+        with pytest.raises((TypeError, ValueError)):
+            bn.W4Matrix(c, s, 20)
+    for k, g in ((100, 64), (256, 16), (256, 256)):
+        with pytest.raises(ValueError):
+            bn.W4Matrix.empty(4, k, g, device="cpu")
+    x = torch.zeros((3, 256))
+    for bad in (x[:, :128], x[0], x.half(), torch.zeros((256, 3)).t(), x):    # the last: not on a GPU
+        with pytest.raises((TypeError, ValueError)):
+            bn.linear_w4(bad, m)
+    with pytest.raises(ValueError):
+        bn.linear_w4(x, m, out=torch.zeros((3, 21)))
+    with pytest.raises(TypeError):
+        bn.linear_w4(x, m, out=torch.zeros((3, 20), dtype=torch.bfloat16))
+    for w, g in ((x[0], 64), (x.half(), 64), (x, 48), (x.t(), 64), (x[:, :100].contiguous(), 64), (x, 64)):
+        with pytest.raises((TypeError, ValueError)):
+            bn.pack_w4(w, g)
+    with pytest.raises(ValueError):
+        bn.pack_w4(x, 64, out=m)
+    w, s = torch.zeros((3, 256), dtype=torch.int8), torch.zeros((3, 4), dtype=torch.float16)
+    for a, b in ((w.int(), s), (w, s.float()), (w, s[:2]), (w, s[:, :3].contiguous()), (w, s[:, :0])):
+        with pytest.raises((TypeError, ValueError)):
+            bn.pack_w4_codes(a, b)
+    with pytest.raises(TypeError):
+        bn.w4_rows(m, torch.zeros(3, dtype=torch.int64))
