@@ -554,6 +554,65 @@ int bitnet_w4_rows(const bitnet_w4_matrix *mat, const int32_t *ids, int64_t n, v
 int bitnet_linear_w4(const void *x, int dtype, int64_t N, const bitnet_w4_matrix *mat, float *y,
                      void *stream);
 
+/*
+ * What attention weighed the cache's tokens with, and eviction by it.  A token's weight in a kv
+ * head is one fp32 number; weights lie beside the cache as [n_pages][n_kv_heads]
+ * [BITNET_KV4_PAGE] in the caller's memory, 16-byte aligned, and need no initialisation.
+ *
+ * bitnet_kv4_weigh -- adds the softmax weights of a call's rows to the tokens they see:
+ *   out[t] = (t before the sequence's first row ? decay * weights[t] : 0)
+ *            + the sum over its rows, and the heads that share the kv head, of p_t
+ * for every position t < kv_len of each sequence that has rows in the call, on a page that
+ * is there; nothing else of out is written.  The rows' own tokens begin at 0, so what was in
+ * memory does not matter.  p are the weights of bitnet_attn_kv4 with the same arguments; the
+ * call does not need its results and may run before or after it.
+ *
+ *   batch, q, q_stride, dtype, N, n_heads, scale, window, sinks, max_kv   as bitnet_attn_kv4.
+ *   decay    finite, not negative; with 0 the weights are not read (NULL will do).
+ *   out      may be weights itself, and overlaps them in no other way.
+ *   workspace   device scratch of at least bitnet_kv4_weigh_workspace bytes (-1: sizes out
+ *            of range) of the same sizes, 16-byte aligned; used until the call's kernels have
+ *            ended, so calls that may run at once need one each.
+ * A row that sees nothing or whose q has a NaN or an infinity adds nothing.  Where two
+ * sequences with rows have one page, its weights are unspecified.  q is carried in 22 bits
+ * (fp32; bf16 exactly), all else in fp32 (a p below 2^-126 of the row's largest may count as
+ * 0); rows whose |q| or scaled scores reach 2^100 are
+ * unspecified.  Repeated calls with the same sizes give identical bits.
+ */
+int64_t bitnet_kv4_weigh_workspace(int64_t n_seqs, int64_t N, int64_t n_heads, int64_t n_kv_heads,
+                                   int64_t max_kv, int64_t window, int64_t sinks);
+
+int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, int64_t q_stride, int dtype,
+                     int64_t N, int64_t n_heads, float scale, int64_t window, int64_t sinks,
+                     int64_t max_kv, const float *weights, float decay, float *out, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/*
+ * bitnet_kv4_evict -- copies what is kept of each sequence to the pages of another table.
+ * Of the tokens at positions below kv_len whose page is there, min(their number, keep) are
+ * kept, in each kv head its own: the first `sinks` positions, the last `recent` ones, and
+ * of the others those of the largest weight (a NaN counts as -infinity; of equal ones the
+ * first).  They stay in order and take the places 0, 1, ... of new_table, with their weights.
+ * The old pages are left as they are.
+ *
+ *   batch       cache, table and kv_len; q_start is not looked at.
+ *   weights     [n_pages][n_kv_heads][BITNET_KV4_PAGE], read at the old pages, written at
+ *               the new ones.
+ *   new_table   DEVICE [n_seqs][new_max_pages] int32.  No page of it may be one that the call
+ *               reads (of any sequence), or that it has twice: what they then hold is
+ *               unspecified.  Tokens of a page that is absent in it are dropped.
+ *   keep        1 .. 64 * new_max_pages; sinks and recent not negative, together at most keep.
+ *   new_len     DEVICE [n_seqs] int32: the number of tokens kept.  (The rows' positions, which
+ *               keys carry, do not change: the next row's is kv_len[b], not new_len[b], which
+ *               is what the offsets of bitnet_rotary_kv4_append are for.)
+ *   index       DEVICE [n_seqs][n_kv_heads][keep] int32: the position that each token had; -1
+ *               behind the last.
+ * n_seqs == 0 is a no-op.
+ */
+int bitnet_kv4_evict(const bitnet_kv4_batch *batch, float *weights, const int32_t *new_table,
+                     int64_t new_max_pages, int64_t keep, int64_t sinks, int64_t recent,
+                     int32_t *new_len, int32_t *index, void *stream);
+
 /* Thread-local description of the last non-OK status on this thread
  * (empty string if none).  The pointer stays valid until the next call on
  * the same thread. */

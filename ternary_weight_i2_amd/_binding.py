@@ -158,6 +158,12 @@ def _open(path: str) -> ctypes.CDLL:
     L.bitnet_rotary_kv4_append.argtypes = [kv4, plan, p, i64, p, i64, i64, p, i64, p, i64, i32, i64,
                                            p, p]
     L.bitnet_rotary_kv4_append.restype = ctypes.c_int
+    L.bitnet_kv4_weigh_workspace.argtypes = [i64] * 7
+    L.bitnet_kv4_weigh_workspace.restype = i64
+    L.bitnet_kv4_weigh.argtypes = [kv4, p, i64, i32, i64, i64, f32, i64, i64, i64, p, f32, p, p, i64, p]
+    L.bitnet_kv4_weigh.restype = ctypes.c_int
+    L.bitnet_kv4_evict.argtypes = [kv4, p, p, i64, i64, i64, i64, p, p, p]
+    L.bitnet_kv4_evict.restype = ctypes.c_int
     w4 = ctypes.POINTER(W4Desc)
     for fn, args in (("bitnet_pack_w4", [p, i32, w4, p]), ("bitnet_pack_w4_codes", [p, p, w4, p]),
                      ("bitnet_w4_rows", [w4, p, i64, p, i32, p]),
@@ -568,8 +574,8 @@ def kv4_cache(n_pages, n_kv_heads, head_dim, device="cuda"):
     return torch.empty((n_pages, n_kv_heads, 72 * head_dim), dtype=torch.uint8, device=device)
 
 
-def _kv4_batch(cache, table, kv_len, q_start):
-    """Cache and sequences -> (bitnet_kv4_batch, kv heads, head_dim)."""
+def _kv4_batch(cache, table, kv_len, q_start, rows=True):
+    """Cache and sequences (without ``rows``: no q_start) -> (bitnet_kv4_batch, kv heads, head_dim)."""
     import torch
     i32 = torch.int32
     if cache.dim() != 3 or cache.dtype != torch.uint8 or cache.shape[2] % 72:
@@ -579,7 +585,7 @@ def _kv4_batch(cache, table, kv_len, q_start):
         raise ValueError("table must be 2-D [n_seqs][max_pages]")
     B, P = table.shape
     n_pages, heads, rec = cache.shape
-    if kv_len is None or q_start is None:
+    if kv_len is None or (rows and q_start is None):
         raise ValueError("kv_len and q_start are required")
     at = _at(table, "table", i32, (B, P), dev)
     lens, start = _at(kv_len, "kv_len", i32, (B,), dev), _at(q_start, "q_start", i32, (B + 1,), dev)
@@ -787,6 +793,83 @@ def attn_kv4_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window=
     return need
 
 
+def kv4_weights(cache):
+    """The array that kv4_weigh and kv4_evict keep beside a cache: fp32 [n_pages][n_kv_heads]
+    [64], uninitialised (a token's weight begins at 0 in the call that weighs its row)."""
+    import torch
+    return torch.empty((*cache.shape[:2], KV4_PAGE), dtype=torch.float32, device=cache.device)
+
+
+def kv4_weigh(weights, q, cache, table, kv_len, q_start, decay=1.0, scale=None, window=0, sinks=0,
+              max_kv=None, out=None, workspace=None):
+    """Adds what each cached token is weighed with by the attention of q's rows (the softmax
+    weights of attn_kv4 with the same arguments, summed over the rows and the heads that
+    share a kv head) to ``decay`` times its weight so far; tokens of the rows themselves begin
+    at 0.  ``weights`` fp32 [n_pages][n_kv_heads][64] is updated, or with ``out`` left as it is (None will do with
+    a decay of 0).  Sequences without rows keep theirs.  workspace: as in attn_kv4
+    (kv4_weigh_workspace bytes).  Returns out."""
+    import torch
+    batch, kv_heads, dim = _kv4_batch(cache, table, kv_len, q_start)
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [N][n_heads][head_dim]")
+    L, dev = load(), cache.device
+    N, heads = q.shape[0], q.shape[1]
+    code, stride = _float_code(q.dtype, "q"), _rows(q, "q", heads, dim, dev)
+    shape = (*cache.shape[:2], KV4_PAGE)
+    at = _at(weights, "weights", torch.float32, shape, dev)
+    if out is None:
+        out = weights
+    to = _at(out, "out", torch.float32, shape, dev)
+    most = KV4_PAGE * batch.max_pages
+    max_kv = most if max_kv is None else min(max_kv, most)
+    need = L.bitnet_kv4_weigh_workspace(batch.n_seqs, N, heads, kv_heads, max_kv, window, sinks)
+    if need < 0:
+        raise BitnetError(E_SHAPE, L.bitnet_last_error().decode(errors="replace"))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
+        raise ValueError(f"workspace must be {need} bytes of uint8 on {dev}")
+    _launch(L.bitnet_kv4_weigh, dev, batch, q.data_ptr(), stride, code, N, heads,
+            dim ** -0.5 if scale is None else scale, window, sinks, max_kv, at, decay, to,
+            _ptr(workspace), workspace.numel())
+    return out
+
+
+def kv4_weigh_workspace(n_seqs, n, n_heads, n_kv_heads, max_kv, window=0, sinks=0):
+    """Bytes of workspace that kv4_weigh takes for these sizes, with the call's own max_kv."""
+    need = load().bitnet_kv4_weigh_workspace(n_seqs, n, n_heads, n_kv_heads, max_kv, window, sinks)
+    if need < 0:
+        raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
+    return need
+
+
+def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0, out=None):
+    """Copies what is kept of each sequence to the pages of ``new_table`` [B][new_max_pages], kv
+    head by kv head: its first ``sinks`` tokens, its last ``recent`` ones, and of the others
+    those of the largest weight, ``keep`` in all (or all there are), in order, weights and all.  The new pages must be
+    none that a sequence of the call has; the old ones are left as they are, to be handed out again.
+
+    Returns (new_len [B], index [B][n_kv_heads][keep]: the places that the tokens had, -1
+    behind the last), int32, in ``out`` if given.  The step after goes on with new_table and new_len; its
+    positions are kv_len - new_len further on (rotary_kv4_append's offset)."""
+    import torch
+    i32, dev = torch.int32, cache.device
+    if weights is None or new_table is None or new_table.dim() != 2:
+        raise ValueError("weights and a 2-D new_table are required")
+    batch, heads, _ = _kv4_batch(cache, table, kv_len, None, rows=False)
+    B = batch.n_seqs
+    at_w = _at(weights, "weights", torch.float32, (*cache.shape[:2], KV4_PAGE), dev)
+    if out is None:
+        new_len = torch.empty(B, dtype=i32, device=dev)
+        index = torch.empty((B, heads, max(keep, 0)), dtype=i32, device=dev)
+    else:
+        new_len, index = out
+    _launch(load().bitnet_kv4_evict, dev, batch, at_w,
+            _at(new_table, "new_table", i32, (B, new_table.shape[1]), dev), new_table.shape[1], keep, sinks, recent,
+            _at(new_len, "new_len", i32, (B,), dev), _at(index, "index", i32, (B, heads, keep), dev))
+    return new_len, index
+
+
 class W4Matrix:
     """A matrix of 4-bit weights [M][K] as pack_w4 lays it out: ``codes`` uint8
     [ceil(M/16)][K/128][64][16], ``steps`` fp16 [ceil(M/16)][K/128][16][128/group], and the number of its
@@ -899,7 +982,7 @@ def _matmuls(tokens, mats):
 
 
 def attn_block(tokens, q, k, v, o, cache, table, kv_len, q_start, gamma=None, eps=1e-5, rotary=None,
-               window=0, sinks=0, max_kv=None, offset=None):
+               window=0, sinks=0, max_kv=None, offset=None, weights=None, decay=1.0):
     """The attention block on I2_S weights and a 4-bit cache: q, k and v projections
     (one grouped launch) -> keys and values appended to the cache -> attention over
     it -> RMS sub-norm (gain gamma or 1) and int8 tokens -> the o projection.
@@ -908,9 +991,13 @@ def attn_block(tokens, q, k, v, o, cache, table, kv_len, q_start, gamma=None, ep
     q, k, v, o: (packed, w_scale) pairs; head_dim and the kv heads are the cache's.
     rotary: a Rotary (positions as in rotary_kv4_append, with its ``offset``), or called
     with q [N][n_heads][head_dim] and k [N][n_kv_heads][head_dim] (fp32) and returns them with
-    their positions applied.  The rest as in attn_kv4.
+    their positions applied.
+    weights: what kv4_weigh keeps of each cached token, updated by this step's attention
+    (with ``decay``).  The rest as in attn_kv4.
     Returns y [N][hidden] fp32, the block's output for the next block_norm_quant; rows
     of no sequence (padding) have no attention, and their y is unspecified."""
+    if offset is not None and not isinstance(rotary, Rotary):
+        raise ValueError("offset without a Rotary")
     yq, yk, yv = _matmuls(tokens, [q, k, v])
     N, kv_heads, dim = yq.shape[0], cache.shape[1], cache.shape[2] // 72
     qh = yq.view(N, yq.shape[1] // dim, dim)
@@ -918,11 +1005,11 @@ def attn_block(tokens, q, k, v, o, cache, table, kv_len, q_start, gamma=None, ep
     if isinstance(rotary, Rotary):
         qh = rotary_kv4_append(cache, table, kv_len, q_start, qh, kh, vh, rotary, offset, out=qh)
     else:
-        if offset is not None:
-            raise ValueError("offset without a Rotary")
         if rotary is not None:
             qh, kh = rotary(qh, kh)
         kv4_append(cache, table, kv_len, q_start, kh, vh)
+    if weights is not None:
+        kv4_weigh(weights, qh, cache, table, kv_len, q_start, decay, window=window, sinks=sinks, max_kv=max_kv)
     a = attn_kv4(qh, cache, table, kv_len, q_start, window=window, sinks=sinks, max_kv=max_kv)
     _, _, inner = block_norm_quant(a.view(yq.shape), gamma=gamma, eps=eps)
     return _matmuls(inner, [o])[0]

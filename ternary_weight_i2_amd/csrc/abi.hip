@@ -497,7 +497,8 @@ BITNET_API int bitnet_block_norm_quant_i8(const void *b, int b_dtype, int post,
 }
 
 // Validate a cache descriptor and a call's row count (shared by the cache calls).
-static int check_kv4(const char *fn, const bitnet_kv4_batch *c, int dtype, int64_t N) {
+static int check_kv4(const char *fn, const bitnet_kv4_batch *c, int dtype, int64_t N,
+                     bool rows = true) {
     if (!c) return fail(BITNET_E_NULL, "%s: batch is NULL", fn);
     if (dtype != BITNET_F32 && dtype != BITNET_BF16)
         return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, dtype);
@@ -519,11 +520,11 @@ static int check_kv4(const char *fn, const bitnet_kv4_batch *c, int dtype, int64
         return fail(BITNET_E_SHAPE, "%s: n_seqs=%lld outside [0, %d]", fn, (long long)c->n_seqs,
                     BITNET_KV4_MAX_SEQS);
     if (N == 0 || c->n_seqs == 0) return BITNET_OK;
-    if (!c->cache || !c->table || !c->kv_len || !c->q_start)
+    if (!c->cache || !c->table || !c->kv_len || (rows && !c->q_start))
         return fail(BITNET_E_NULL, "%s: cache, table, kv_len and q_start are required", fn);
     if (!aligned(c->cache, 16))
         return fail(BITNET_E_ALIGN, "%s: cache must be 16-byte aligned", fn);
-    if (!aligned(c->table, 4) || !aligned(c->kv_len, 4) || !aligned(c->q_start, 4))
+    if (!aligned(c->table, 4) || !aligned(c->kv_len, 4) || (rows && !aligned(c->q_start, 4)))
         return fail(BITNET_E_ALIGN, "%s: table, kv_len and q_start must be 4-byte aligned", fn);
     return BITNET_OK;
 }
@@ -649,6 +650,97 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
                               (uint32_t)sp.tiles};
     hipError_t e = bitnet::launch_attn4(a, sp, dtype == BITNET_BF16, (int)batch->head_dim,
                                         static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+BITNET_API int64_t bitnet_kv4_weigh_workspace(int64_t n_seqs, int64_t N, int64_t n_heads,
+                                              int64_t n_kv_heads, int64_t max_kv, int64_t window,
+                                              int64_t sinks) {
+    const char *fn = "bitnet_kv4_weigh_workspace";
+    if (check_heads(fn, n_heads, n_kv_heads)) return -1;
+    if (n_seqs < 0 || n_seqs > BITNET_KV4_MAX_SEQS || N < 0 || N > BITNET_GEMM_MAX_N ||
+        max_kv < 0 || max_kv > (int64_t)BITNET_KV4_MAX_PAGES * BITNET_KV4_PAGE || window < 0 ||
+        window > 0x7fffffffLL || sinks < 0 || sinks > 0x7fffffffLL) {
+        fail(BITNET_E_SHAPE, "%s: sizes out of range", fn);
+        return -1;
+    }
+    g_last_error.clear();
+    if (n_seqs == 0 || N == 0) return 0;
+    return bitnet::weigh_plan(n_seqs, N, n_heads, n_kv_heads, max_kv, window, sinks).splits * N *
+           n_heads * 8;
+}
+
+BITNET_API int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, int64_t q_stride,
+                                int dtype, int64_t N, int64_t n_heads, float scale, int64_t window,
+                                int64_t sinks, int64_t max_kv, const float *weights, float decay,
+                                float *out, void *workspace, int64_t workspace_bytes,
+                                void *stream) {
+    const char *fn = "bitnet_kv4_weigh";
+    if (int s = check_kv4(fn, batch, dtype, N)) return s;
+    if (int s = check_heads(fn, n_heads, batch->n_kv_heads)) return s;
+    if (!(scale > 0.0f) || !(scale < 3.4e38f))
+        return fail(BITNET_E_VALUE, "%s: scale must be positive and finite", fn);
+    if (!(decay >= 0.0f) || !(decay < 3.4e38f))
+        return fail(BITNET_E_VALUE, "%s: decay must be finite and not negative", fn);
+    if (window < 0 || sinks < 0 || window > 0x7fffffffLL || sinks > 0x7fffffffLL)
+        return fail(BITNET_E_SHAPE, "%s: window=%lld, sinks=%lld out of range", fn,
+                    (long long)window, (long long)sinks);
+    if (max_kv < 0 || max_kv > batch->max_pages * BITNET_KV4_PAGE)
+        return fail(BITNET_E_SHAPE, "%s: max_kv=%lld outside [0, 64 * max_pages]", fn,
+                    (long long)max_kv);
+    if (N == 0 || batch->n_seqs == 0) return ok();
+    if (int s = check_rows(fn, "q", q, q_stride, n_heads * batch->head_dim, dtype)) return s;
+    if (!out || (!weights && decay != 0.0f))
+        return fail(BITNET_E_NULL, "%s: out, and weights with a decay, are required", fn);
+    if (!aligned(out, 16) || !aligned(weights, 16) || !aligned(workspace, 16))
+        return fail(BITNET_E_ALIGN, "%s: weights, out and workspace must be 16-byte aligned", fn);
+    const bitnet::WeighPlan p = bitnet::weigh_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads,
+                                                   max_kv, window, sinks);
+    const int64_t need = p.splits * N * n_heads * 8;
+    if (!workspace)
+        return fail(BITNET_E_NULL, "%s: a workspace of %lld bytes is required", fn, (long long)need);
+    if (workspace_bytes < need)
+        return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
+                    (long long)workspace_bytes, (long long)need);
+    const int far = 1 << 30, win = (int)(window < far ? window : far);   // as bitnet_attn_kv4
+    const bitnet::WeighArgs a{kv4_args(batch), q, weights, out, static_cast<float2 *>(workspace),
+                              q_stride, N, scale * 1.4426950408889634f, decay, (int)n_heads, win,
+                              (int)(sinks < far ? sinks : far), p.splits};
+    hipError_t e = bitnet::launch_kv4_weigh(a, p, dtype == BITNET_BF16, (int)batch->head_dim,
+                                            static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(fn, e);
+    return ok();
+}
+
+BITNET_API int bitnet_kv4_evict(const bitnet_kv4_batch *batch, float *weights,
+                                const int32_t *new_table, int64_t new_max_pages, int64_t keep,
+                                int64_t sinks, int64_t recent, int32_t *new_len, int32_t *index,
+                                void *stream) {
+    const char *fn = "bitnet_kv4_evict";
+    if (int s = check_kv4(fn, batch, BITNET_F32, 1, false)) return s;
+    if (new_max_pages < 1 || new_max_pages > BITNET_KV4_MAX_PAGES)
+        return fail(BITNET_E_SHAPE, "%s: new_max_pages=%lld outside [1, %d]", fn,
+                    (long long)new_max_pages, BITNET_KV4_MAX_PAGES);
+    if (keep < 1 || keep > new_max_pages * BITNET_KV4_PAGE)
+        return fail(BITNET_E_SHAPE, "%s: keep=%lld outside [1, 64 * new_max_pages]", fn,
+                    (long long)keep);
+    if (sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks)
+        return fail(BITNET_E_SHAPE, "%s: sinks=%lld and recent=%lld are more than keep=%lld", fn,
+                    (long long)sinks, (long long)recent, (long long)keep);
+    if (batch->n_seqs == 0) return ok();
+    if (!weights || !new_table || !new_len || !index)
+        return fail(BITNET_E_NULL, "%s: weights, new_table, new_len and index are required", fn);
+    if (!aligned(weights, 16))
+        return fail(BITNET_E_ALIGN, "%s: weights must be 16-byte aligned", fn);
+    if (!aligned(new_table, 4) || !aligned(new_len, 4) || !aligned(index, 4))
+        return fail(BITNET_E_ALIGN, "%s: new_table, new_len and index must be 4-byte aligned", fn);
+    const bitnet::EvictArgs a{static_cast<uint8_t *>(batch->cache), weights, batch->table,
+                              batch->kv_len, new_table, new_len, index, batch->n_pages,
+                              batch->max_pages, new_max_pages, batch->n_seqs,
+                              (int)batch->n_kv_heads, (int)keep, (int)sinks, (int)recent};
+    hipError_t e = bitnet::launch_kv4_evict(a, (int)batch->head_dim,
+                                            static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);
     return ok();
 }

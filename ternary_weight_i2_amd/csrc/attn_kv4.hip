@@ -53,7 +53,7 @@ namespace bitnet {
 namespace {
 
 constexpr int kJoinThreads = 1024;
-constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
+
 
 // The steps in a word of two that are below `cut`; the others 0.
 __device__ __forceinline__ uint32_t steps_below(uint32_t w, uint32_t cut) {
@@ -67,32 +67,6 @@ __device__ __forceinline__ _Float16 pow2_f16(int e) {
     return __builtin_bit_cast(_Float16, (uint16_t)half_bits(e));
 }
 
-// Over the four lanes that hold a row (l, l ^ 16, l ^ 32, l ^ 48): the swaps
-// hand every lane its own and its partner's value.
-__device__ __forceinline__ void partners16(float v, float &a, float &b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
-                                                    false);
-    a = __uint_as_float(r[0]);
-    b = __uint_as_float(r[1]);
-}
-__device__ __forceinline__ void partners32(float v, float &a, float &b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
-                                                    false);
-    a = __uint_as_float(r[0]);
-    b = __uint_as_float(r[1]);
-}
-__device__ __forceinline__ float quad_max(float v) {
-    float a, b;
-    partners16(v, a, b);
-    partners32(fmaxf(a, b), a, b);
-    return fmaxf(a, b);
-}
-__device__ __forceinline__ float quad_sum(float v) {
-    float a, b;
-    partners16(v, a, b);
-    partners32(a + b, a, b);
-    return a + b;
-}
 // The wave's largest of small non-negative integers, in a scalar register.
 __device__ __forceinline__ int wave_max_u16(int v) {
     v = max(v, dpp_i32<kDppXor1>(v));
@@ -102,58 +76,6 @@ __device__ __forceinline__ int wave_max_u16(int v) {
     v = max(v, dpp_rows_i32<kDppRowBcast15, 0xA>(v));
     v = max(v, dpp_rows_i32<kDppRowBcast31, 0xC>(v));
     return __builtin_amdgcn_readlane(v, 63);
-}
-
-// The tile (ROWS rows of one sequence) that a workgroup works on, and the pages
-// its rows see: the first `sink_pages`, then from `first` to the last.
-struct Tile {
-    int seq, token0, held;      // token0: the sequence's first query token
-    uint32_t rows, row0;
-    int pos0;                   // position of row 0's token
-    int first, sink_pages, pages;
-};
-
-template <int ROWS>
-__device__ __forceinline__ Tile find_tile(const Attn4Args &a, uint32_t x, uint32_t G) {
-    Tile t;
-    // a sequence has at least as many tiles to itself as its rows need
-    const SeqAt s = sequence_of<ROWS, 1>(a.c, G, x);
-    t.seq = s.seq;
-    t.token0 = s.begin;
-    const bool good = s.begin >= 0 && s.end > s.begin && s.end <= (int)a.N;
-    t.rows = good ? (uint32_t)(s.end - s.begin) * G : 0;
-    const int tile = (int)(x - ((uint32_t)s.begin * G / ROWS + s.seq));
-    if (tile < 0) t.rows = 0;
-    t.row0 = (uint32_t)tile * ROWS;
-    t.held = s.held;
-    t.pos0 = t.held - (s.end - s.begin);
-    t.pages = t.first = t.sink_pages = 0;
-    if (t.row0 >= t.rows) {
-        t.rows = 0;
-        return t;
-    }
-    const uint32_t last_row = min(t.row0 + ROWS, t.rows) - 1;
-    const int pos_a = t.pos0 + (int)(t.row0 / G), pos_b = t.pos0 + (int)(last_row / G);
-    if (pos_b < 0) return t;
-    t.first = a.window > 0 && pos_a >= a.window ? (pos_a - a.window + 1) / kPage : 0;
-    t.sink_pages = min((a.sinks + kPage - 1) / kPage, t.first);
-    t.pages = t.sink_pages + pos_b / kPage - t.first + 1;
-    return t;
-}
-
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
-    static_assert(N == 2 || N == 4 || N == 8, "8, 16 or 32 bytes");
-    if constexpr (N == 2) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(p);
-        w[0] = a.x; w[1] = a.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const uint4 a = reinterpret_cast<const uint4 *>(p)[i];
-            w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
-        }
-    }
 }
 
 __device__ __forceinline__ void add_part(float4 &acc, float f, const float4 &o) {
@@ -314,7 +236,7 @@ __global__ __launch_bounds__(64 * WAVES, least_waves(D, RT, WAVES)) void attn4_k
     constexpr int TEAMS = WAVES / TURNS;
     // the waves that have a page more than the others are not the same of all splits
     const int team = wave / TURNS, turn = (wave + split) % TURNS;
-    Tile t = find_tile<ROWS>(a, a.tiles - 1 - (tile * TEAMS + team), G);
+    Tile t = find_tile<ROWS>(a.c, a.N, a.window, a.sinks, a.tiles - 1 - (tile * TEAMS + team), G);
     Share sh = share_of(a, t, split);
     if constexpr (TEAMS == 1) {   // the whole workgroup leaves
         if (t.rows == 0) return;

@@ -88,4 +88,31 @@ inline Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
     return Attn4Plan{0, 0, (int)s, hold ? 2 : 0, tiles, groups * s};
 }
 
+// kv4_weigh.hip: the tiles of 16 rows, the shares of the pages that each tile's rows see, the
+// workgroups that share a sequence's pages, and whether a page's rows are shared by waves.
+struct WeighPlan {
+    int64_t tiles;
+    int splits, chunks, shared;
+};
+inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
+                            int64_t max_kv, int64_t window, int64_t sinks) {
+    const int64_t rows = N * (heads / kv_heads), pages = std::max<int64_t>((max_kv + kPage - 1) / kPage, 1);
+    int64_t seen = pages;
+    if (window > 0) seen = std::min(pages, (window + 16) / kPage + 2 + (sinks + kPage - 1) / kPage);
+    WeighPlan p;
+    p.tiles = rows / 16 + n_seqs;
+    // four workgroups to a compute unit, and a page at least for every wave
+    const int64_t tall = (std::max<int64_t>(rows / n_seqs, 1) + 15) / 16;
+    const int64_t busy = std::min(n_seqs, N) * tall * kv_heads;
+    // (and no more units of either kind than a launch has workgroups, with many empty sequences)
+    constexpr int64_t kMost = 1 << 22;
+    p.splits = (int)std::max<int64_t>(
+        std::min({4 * kUnits / busy, seen / 4, (int64_t)64, kMost / (p.tiles * kv_heads)}), 1);
+    // Rows of several tiles are shared by the waves.
+    p.shared = rows >= 4 * 16 * n_seqs;
+    p.chunks = (int)std::max<int64_t>(
+        std::min(p.shared ? pages : (pages + 3) / 4, kMost / (n_seqs * kv_heads)), 1);
+    return p;
+}
+
 }  // namespace bitnet

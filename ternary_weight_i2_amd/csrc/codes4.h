@@ -47,4 +47,46 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Over the four lanes that hold a row (l, l ^ 16, l ^ 32, l ^ 48): the swaps
+// hand every lane its own and its partner's value.
+__device__ __forceinline__ void partners16(float v, float &a, float &b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void partners32(float v, float &a, float &b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float quad_max(float v) {
+    float a, b;
+    partners16(v, a, b);
+    partners32(fmaxf(a, b), a, b);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    float a, b;
+    partners16(v, a, b);
+    partners32(a + b, a, b);
+    return a + b;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
+    static_assert(N == 2 || N == 4 || N == 8, "8, 16 or 32 bytes");
+    if constexpr (N == 2) {
+        const uint2 a = *reinterpret_cast<const uint2 *>(p);
+        w[0] = a.x; w[1] = a.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 a = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+        }
+    }
+}
+
 }  // namespace bitnet

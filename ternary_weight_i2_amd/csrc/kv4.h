@@ -80,6 +80,46 @@ __device__ __forceinline__ bool row_in_call(const Kv4Args &c, int64_t r) {
     return r >= c.q_start[0] && r < c.q_start[c.n_seqs];
 }
 
+constexpr float kNoMax = -3.0e38f; // a running maximum before the first visible token
+
+// The tile (ROWS rows of one sequence) that a workgroup works on, and the pages
+// its rows see: the first `sink_pages`, then from `first` to the last.
+struct Tile {
+    int seq, token0, held;      // token0: the sequence's first query token
+    uint32_t rows, row0;
+    int pos0;                   // position of row 0's token
+    int first, sink_pages, pages;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Tile find_tile(const Kv4Args &c, int64_t N, int window, int sinks,
+                                          uint32_t x, uint32_t G) {
+    Tile t;
+    // a sequence has at least as many tiles to itself as its rows need
+    const SeqAt s = sequence_of<ROWS, 1>(c, G, x);
+    t.seq = s.seq;
+    t.token0 = s.begin;
+    const bool good = s.begin >= 0 && s.end > s.begin && s.end <= (int)N;
+    t.rows = good ? (uint32_t)(s.end - s.begin) * G : 0;
+    const int tile = (int)(x - ((uint32_t)s.begin * G / ROWS + s.seq));
+    if (tile < 0) t.rows = 0;
+    t.row0 = (uint32_t)tile * ROWS;
+    t.held = s.held;
+    t.pos0 = t.held - (s.end - s.begin);
+    t.pages = t.first = t.sink_pages = 0;
+    if (t.row0 >= t.rows) {
+        t.rows = 0;
+        return t;
+    }
+    const uint32_t last_row = min(t.row0 + ROWS, t.rows) - 1;
+    const int pos_a = t.pos0 + (int)(t.row0 / G), pos_b = t.pos0 + (int)(last_row / G);
+    if (pos_b < 0) return t;
+    t.first = window > 0 && pos_a >= window ? (pos_a - window + 1) / kPage : 0;
+    t.sink_pages = min((sinks + kPage - 1) / kPage, t.first);
+    t.pages = t.sink_pages + pos_b / kPage - t.first + 1;
+    return t;
+}
+
 __device__ __forceinline__ float min8(float v) {   // over 8 aligned lanes
     v = fminf(v, dpp_f32<kDppXor1>(v));
     v = fminf(v, dpp_f32<kDppXor2>(v));

@@ -136,6 +136,29 @@ hipError_t launch_w4_rows(const W4Args &w, const int32_t *ids, int64_t n, void *
                           hipStream_t st);
 hipError_t launch_w4_linear(const W4Args &w, const void *x, int bf16, int64_t N, float *y,
                             hipStream_t st);
+// The attention weights of a call's rows, summed by cached token (kv4_weigh.hip).
+struct WeighArgs {
+    Kv4Args c;
+    const void *q;
+    const float *old;
+    float *out;
+    float2 *part;          // per split and row: maximum and sum
+    int64_t q_stride, N;
+    float scale_log2, decay;
+    int heads, window, sinks, splits;
+};
+hipError_t launch_kv4_weigh(const WeighArgs &a, const WeighPlan &plan, int bf16, int dim,
+                            hipStream_t st);
+// The tokens of the largest weight, moved to other pages (kv4_evict.hip).
+struct EvictArgs {
+    uint8_t *cache;
+    float *weights;
+    const int32_t *table, *kv_len, *new_table;
+    int32_t *new_len, *index;
+    int64_t n_pages, max_pages, new_pages, n_seqs;
+    int kv_heads, keep, sinks, recent;
+};
+hipError_t launch_kv4_evict(const EvictArgs &a, int dim, hipStream_t st);
 struct Attn4Args {
     Kv4Args c;
     const void *q;

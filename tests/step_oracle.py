@@ -94,3 +94,92 @@ def w4_linear(x, w, group, half):
     tol = (0 if half else 2.0 ** -23) * mag
     tol += 2.0 ** (-40 if half else -41) * (top @ np.abs(b).reshape(len(b), -1, 128).sum(2).T)
     return a @ b.T, tol + 6 * np.sqrt(K + K // group + 16) * 2.0 ** -24 * mag
+
+
+# ---------------------------------------------------------------- weights of cached tokens
+
+def weigh(weights, q, cache, table, kv_len, q_start, scale, decay=1.0, window=0, sinks=0):
+    """weights [pages][heads][64] -> (the new ones in binary64, what they may be off by, whether
+    the call writes them).  What a row's weight p_t may be off by, relatively:
+    * e_t, with e_t^2 the sum of (2^-22 scale |q * mag_t|_2)^2 (q in 22 bits, mag = |mid| + 8 step
+      being what a channel's two terms are made of), n (2^-24 scale sum |q_d| mag_td)^2 (the logit's
+      n = D + 2 D / 64 + 4 fp32 sums) and (2^-22 (1 + |x_t|))^2 (2^z and its argument);
+    * and as much as its denominator, sum_s p_s e_s and the sum's own roundings, 2^-22.
+    Six standard deviations of these, taken as independent between rows, and of the sums over
+    rows, 2^-24 of the result each, of which there are the rows', 20 and the old weight's.  A
+    weight below 2^-126 of its row's largest is none of fp32's normal numbers and may be 0."""
+    N, heads, d = q.shape
+    kvh = cache.shape[1]
+    out, tol = np.array(weights, F8), np.zeros(weights.shape)
+    written = np.zeros(weights.shape, bool)
+    u = 2.0 ** -24
+    for b in range(len(kv_len)):
+        rows, held = lo.rows_of(kv_len, q_start, b, table.shape[1])
+        if not rows:
+            continue
+        first = held - len(rows)
+        j = np.arange(held)
+        for g in range(kvh):
+            k, _, there, _, kmag = lo.history(cache, table[b], held, g, d)
+            got, var = np.zeros(held), np.zeros(held)
+            for r, pos in rows:
+                see = there & (j <= pos)
+                if window:
+                    see &= (j > pos - window) | (j < sinks)
+                for h in range(g * heads // kvh, (g + 1) * heads // kvh):
+                    qr = q[r, h].astype(F8)
+                    if not see.any() or not np.isfinite(qr).all():
+                        continue
+                    x = scale * (k[see] @ qr)
+                    p = np.exp(x - x.max())
+                    p /= p.sum()
+                    qa = np.abs(qr)
+                    e = np.sqrt((4 * u * scale) ** 2 * (kmag[see] ** 2 @ qa ** 2)
+                                + (d + 2 * (d // 64) + 4) * (u * scale * (kmag[see] @ qa)) ** 2
+                                + (4 * u) ** 2 * (1 + np.abs(x)) ** 2)
+                    got[see] += p
+                    var[see] += (p * (e + p @ e + 4 * u)) ** 2
+            at = (table[b, j // 64], g, j % 64)
+            at = tuple(np.broadcast_to(a, j.shape)[there] for a in at)
+            old = np.where((j < first)[there], decay * np.nan_to_num(weights[at].astype(F8)), 0.0) if decay else 0.0
+            new = got[there] + old
+            out[at], written[at] = new, True
+            n = len(rows) * heads // kvh
+            tol[at] = 6 * np.sqrt(var[there] + (n + 21) * (u * np.abs(new)) ** 2) + n * 2.0 ** -126
+    return out, tol, written
+
+
+def token_bytes(d, t):
+    """Where a record has token t: the bytes of its key, then of its value, in order."""
+    g = d // 64
+    key = [t * d // 2 + i for i in range(d // 2)] + [64 * d + t * 4 * g + i for i in range(4 * g)]
+    a, e = t // 4, t % 4
+    code = [32 * d + 2 * (((a * 16 + i) * g + p) * 4 + e) + s for i in range(16) for p in range(g) for s in range(2)]
+    pair = [68 * d + 2 * ((a * g + p) * 8 + 4 * kind + e) + s for p in range(g) for kind in range(2) for s in range(2)]
+    return np.array(key + code + pair)
+
+
+def evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0):
+    """In place -> (new_len, index)."""
+    pages, heads, d = len(cache), cache.shape[1], cache.shape[2] // 72
+    B = len(kv_len)
+    new_len, index = np.zeros(B, np.int32), np.full((B, heads, keep), -1, np.int32)
+    before, w0 = cache.copy(), weights.copy()
+    where = [token_bytes(d, t) for t in range(64)]
+    for b in range(B):
+        held = min(max(int(kv_len[b]), 0), 64 * table.shape[1])
+        t = np.array([i for i in range(held) if 0 <= table[b, i // 64] < pages], np.int64)
+        new_len[b] = min(len(t), keep)
+        for h in range(heads):
+            w = np.array([w0[table[b, i // 64], h, i % 64] for i in t], F8)
+            w[np.isnan(w)] = -np.inf
+            spared = (t < sinks) | (t >= held - recent)
+            order = sorted(range(len(t)), key=lambda i: (not spared[i], -w[i] if not spared[i] else 0, t[i]))
+            kept = np.sort(t[order[:new_len[b]]])
+            index[b, h, :len(kept)] = kept
+            for to, i in enumerate(kept):
+                page = new_table[b, to // 64]
+                if 0 <= page < pages:
+                    cache[page, h, where[to % 64]] = before[table[b, i // 64], h, where[i % 64]]
+                    weights[page, h, to % 64] = w0[table[b, i // 64], h, i % 64]
+    return new_len, index

@@ -183,3 +183,82 @@ def test_w4_binding_refuses():
             bn.pack_w4_codes(a, b)
     with pytest.raises(TypeError):
         bn.w4_rows(m, torch.zeros(3, dtype=torch.int64))
+
+
+# ---------------------------------------------------------------- weights of cached tokens, eviction
+
+def _weigh(L, b=None, q=FAKE, qs=256, dt=0, N=3, heads=4, scale=0.125, window=0, sinks=0, max_kv=64, w=FAKE,
+           decay=1.0, out=FAKE, ws=FAKE, wb=1 << 20):
+    return L.bitnet_kv4_weigh(b or _batch(), q, qs, dt, N, heads, scale, window, sinks, max_kv, w, decay, out, ws, wb,
+                              None)
+
+
+def test_weigh_validation(L):
+    f = _weigh
+    assert f(L, _batch(n_kv_heads=0)) == E_SHAPE and f(L, _batch(q_start=None)) == E_NULL
+    assert f(L, dt=2) == E_DTYPE and f(L, N=-1) == E_SHAPE
+    for heads in (0, 3, -2, 1026):
+        assert f(L, heads=heads) == E_SHAPE
+    for bad in (0.0, -1.0, float("inf"), float("nan")):
+        assert f(L, scale=bad) == E_VALUE
+    for bad in (-0.5, float("inf"), float("nan")):
+        assert f(L, decay=bad) == E_VALUE
+    for k in ("window", "sinks"):
+        assert f(L, **{k: -1}) == E_SHAPE and f(L, **{k: 1 << 31}) == E_SHAPE
+    assert f(L, max_kv=-1) == E_SHAPE and f(L, max_kv=193) == E_SHAPE
+    for p in ("q", "out", "w", "ws"):
+        assert f(L, **{p: None}) == E_NULL and f(L, **{p: MIS}) == E_ALIGN
+    for bad in (255, 258, 0):
+        assert f(L, qs=bad) == E_SHAPE
+    need = L.bitnet_kv4_weigh_workspace(2, 3, 4, 2, 64, 0, 0)
+    assert need >= 3 * 4 * 8 and f(L, wb=need - 1) == E_SHAPE
+    assert f(L, N=0, q=None, ws=None) == OK and f(L, _batch(n_seqs=0), q=None) == OK
+    for bad in ((-1, 3, 4, 2, 64, 0, 0), (2, -1, 4, 2, 64, 0, 0), (2, 3, 3, 2, 64, 0, 0), (2, 3, 4, 2, -1, 0, 0),
+                (2, 3, 4, 2, (1 << 30) + 1, 0, 0), (2, 3, 4, 2, 64, -1, 0), (2, 3, 4, 2, 64, 0, -1)):
+        assert L.bitnet_kv4_weigh_workspace(*bad) == -1
+    assert L.bitnet_kv4_weigh_workspace(0, 3, 4, 2, 64, 0, 0) == 0
+
+
+def _evict(L, b=None, w=FAKE, nt=FAKE, cap=3, keep=64, sinks=4, recent=8, nl=FAKE, idx=FAKE):
+    return L.bitnet_kv4_evict(b or _batch(q_start=None), w, nt, cap, keep, sinks, recent, nl, idx, None)
+
+
+def test_evict_validation(L):
+    f = _evict
+    assert f(L, _batch(head_dim=80)) == E_SHAPE and f(L, _batch(table=None)) == E_NULL
+    assert f(L, _batch(q_start=None, kv_len=FAKE + 2)) == E_ALIGN
+    assert f(L, cap=0) == E_SHAPE and f(L, cap=(1 << 24) + 1) == E_SHAPE
+    for keep in (0, -1, 193):
+        assert f(L, keep=keep) == E_SHAPE
+    for sinks, recent in ((-1, 0), (0, -1), (65, 0), (0, 65), (60, 5), (1 << 62, 1 << 62)):
+        assert f(L, sinks=sinks, recent=recent) == E_SHAPE
+    for p in ("w", "nt", "nl", "idx"):
+        assert f(L, **{p: None}) == E_NULL
+        assert f(L, **{p: MIS if p == "w" else FAKE + 2}) == E_ALIGN
+    assert L.bitnet_kv4_evict(None, FAKE, FAKE, 3, 64, 0, 0, FAKE, FAKE, None) == E_NULL
+    assert f(L, _batch(n_seqs=0, q_start=None), w=None) == OK
+
+
+def test_weigh_and_evict_binding_refuses():
+    import ternary_weight_i2_amd as bn
+    c, table = torch.zeros((2, 1, 72 * 64), dtype=torch.uint8), torch.zeros((1, 1), dtype=torch.int32)
+    one, start = torch.ones(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    q, w = torch.zeros((1, 2, 64)), torch.zeros((2, 1, 64))
+    assert bn.kv4_weights(c).shape == (2, 1, 64)
+    for bad in (dict(w=w[:1]), dict(w=w.bfloat16()), dict(q=q[0]), dict(q=q.half()), dict(out=w[:1]),
+                dict(ws=torch.empty(3, dtype=torch.uint8)), dict()):
+        with pytest.raises((ValueError, TypeError)):
+            bn.kv4_weigh(bad.get("w", w), bad.get("q", q), c, table, one, start, out=bad.get("out"),
+                         workspace=bad.get("ws"))
+    for bad in (dict(w=None), dict(w=w[:1]), dict(nt=None), dict(nt=table[0]), dict(nt=table.long()), dict(kv=one.long()),
+                dict(nt=torch.zeros((2, 1), dtype=torch.int32)), dict(out=(one, one)), dict()):
+        with pytest.raises((ValueError, TypeError)):
+            bn.kv4_evict(c, bad.get("w", w), table, bad.get("kv", one), bad.get("nt", table), 5, out=bad.get("out"))
+    from ternary_weight_i2_amd import _binding
+    for k in (dict(weights=w), dict()):   # an offset is only for a Rotary
+        with pytest.raises((ValueError, TypeError)):
+            bn.attn_block(torch.zeros((1, 256)), *[(torch.zeros((64, 64), dtype=torch.uint8), 1.0)] * 4, c, table, one,
+                          start, offset=one, **k)
+    assert _binding.kv4_weigh_workspace(1, 1, 2, 1, 64) > 0
+    with pytest.raises(bn.BitnetError):
+        _binding.kv4_weigh_workspace(1, 1, 3, 2, 64)
