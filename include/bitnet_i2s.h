@@ -544,6 +544,10 @@ int bitnet_w4_rows(const bitnet_w4_matrix *mat, const int32_t *ids, int64_t n, v
  *
  *   x        [N][K] fp32 or bf16, 16-byte aligned.
  *   y        [N][M] fp32, 4-byte aligned.
+ *   workspace   device scratch of at least bitnet_linear_w4_workspace bytes (-1: sizes out
+ *            of range) of the same sizes, 16-byte aligned (may be NULL where that is 0, as for up
+ *            to 16 tokens); used until the call's kernels have ended, so calls that may run at
+ *            once need one each.
  *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or M == 0 is a no-op.
  * A token's channels are carried in 22 bits (fp32; bf16 exactly) and no finer than 2^-40 of
  * the largest of their 128 (bf16: 2^-39); products and sums are fp32, so where the sum of
@@ -551,8 +555,10 @@ int bitnet_w4_rows(const bitnet_w4_matrix *mat, const int32_t *ids, int64_t n, v
  * or an infinity gives unspecified results, in its own row only.  Repeated calls give
  * identical bits.
  */
+int64_t bitnet_linear_w4_workspace(int64_t N, int64_t M, int64_t K);
+
 int bitnet_linear_w4(const void *x, int dtype, int64_t N, const bitnet_w4_matrix *mat, float *y,
-                     void *stream);
+                     void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * What attention weighed the cache's tokens with, and eviction by it.  A token's weight in a kv

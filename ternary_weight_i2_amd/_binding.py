@@ -167,8 +167,9 @@ def _open(path: str) -> ctypes.CDLL:
     w4 = ctypes.POINTER(W4Desc)
     for fn, args in (("bitnet_pack_w4", [p, i32, w4, p]), ("bitnet_pack_w4_codes", [p, p, w4, p]),
                      ("bitnet_w4_rows", [w4, p, i64, p, i32, p]),
-                     ("bitnet_linear_w4", [p, i32, i64, w4, p, p])):
+                     ("bitnet_linear_w4", [p, i32, i64, w4, p, p, i64, p])):
         getattr(L, fn).argtypes, getattr(L, fn).restype = args, ctypes.c_int
+    L.bitnet_linear_w4_workspace.argtypes, L.bitnet_linear_w4_workspace.restype = [i64] * 3, i64
     for fn in ("bitnet_pack_i2s", "bitnet_quant_act_i8", "bitnet_gemv_i2s_i8",
                "bitnet_gemm_i2s_i8", "bitnet_gemv_i2s_lut", "bitnet_abi_version"):
         getattr(L, fn).restype = ctypes.c_int
@@ -870,6 +871,9 @@ def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0,
     return new_len, index
 
 
+W4_FEW = 16                # linear_w4: up to so many tokens take no workspace
+
+
 class W4Matrix:
     """A matrix of 4-bit weights [M][K] as pack_w4 lays it out: ``codes`` uint8
     [ceil(M/16)][K/128][64][16], ``steps`` fp16 [ceil(M/16)][K/128][16][128/group], and the number of its
@@ -953,8 +957,10 @@ def w4_rows(mat, ids=None, dtype=None, out=None):
     return out
 
 
-def linear_w4(x, mat, out=None):
-    """x [N][K] (fp32 or bf16, any N) times a W4Matrix -> y [N][M] fp32."""
+def linear_w4(x, mat, out=None, workspace=None):
+    """x [N][K] (fp32 or bf16, any N) times a W4Matrix -> y [N][M] fp32.  workspace: a uint8
+    tensor for calls that must not allocate (linear_w4_workspace bytes, none up to 16 tokens);
+    one for each call that may run at once."""
     import torch
     if x.dim() != 2 or x.shape[1] != mat.k:
         raise ValueError(f"x must be 2-D [N][{mat.k}], got {tuple(x.shape)}")
@@ -965,8 +971,24 @@ def linear_w4(x, mat, out=None):
         to = out.data_ptr()
     else:
         to = _at(out, "out", torch.float32, (N, mat.rows), dev)
-    _launch(load().bitnet_linear_w4, dev, at, _float_code(x.dtype, "x"), N, mat._desc, to)
+    ws, size = None, 0
+    if N > W4_FEW:
+        need = linear_w4_workspace(N, mat.rows, mat.k)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
+            raise ValueError(f"workspace must be {need} bytes of uint8 on {dev}")
+        ws, size = _ptr(workspace), workspace.numel()
+    _launch(load().bitnet_linear_w4, dev, at, _float_code(x.dtype, "x"), N, mat._desc, to, ws, size)
     return out
+
+
+def linear_w4_workspace(n, rows, k):
+    """Bytes of workspace that linear_w4 takes for n tokens and a matrix of rows x k."""
+    need = load().bitnet_linear_w4_workspace(n, rows, k)
+    if need < 0:
+        raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
+    return need
 
 
 def _matmuls(tokens, mats):

@@ -895,8 +895,21 @@ BITNET_API int bitnet_w4_rows(const bitnet_w4_matrix *mat, const int32_t *ids, i
     return ok();
 }
 
+BITNET_API int64_t bitnet_linear_w4_workspace(int64_t N, int64_t M, int64_t K) {
+    const char *fn = "bitnet_linear_w4_workspace";
+    if (check_k(fn, K)) return -1;
+    if (N < 0 || N > BITNET_GEMM_MAX_N || M < 0 || M > BITNET_W4_MAX_ROWS) {
+        fail(BITNET_E_SHAPE, "%s: sizes out of range", fn);
+        return -1;
+    }
+    g_last_error.clear();
+    if (N == 0 || M == 0) return 0;
+    const int64_t shares = bitnet::w4_plan(N, M, K).shares;
+    return shares > 1 ? shares * N * M * 4 : 0;
+}
+
 BITNET_API int bitnet_linear_w4(const void *x, int dtype, int64_t N, const bitnet_w4_matrix *mat,
-                                float *y, void *stream) {
+                                float *y, void *workspace, int64_t workspace_bytes, void *stream) {
     const char *fn = "bitnet_linear_w4";
     if (dtype != BITNET_F32 && dtype != BITNET_BF16)
         return fail(BITNET_E_DTYPE, "%s: unknown dtype %d", fn, dtype);
@@ -906,9 +919,17 @@ BITNET_API int bitnet_linear_w4(const void *x, int dtype, int64_t N, const bitne
     if (int s = check_w4(fn, mat)) return s;
     if (N == 0 || mat->M == 0) return ok();
     if (!x || !y) return fail(BITNET_E_NULL, "%s: x and y are required", fn);
-    if (!aligned(x, 16) || !aligned(y, 4))
-        return fail(BITNET_E_ALIGN, "%s: x must be 16-byte and y 4-byte aligned", fn);
+    if (!aligned(x, 16) || !aligned(y, 4) || !aligned(workspace, 16))
+        return fail(BITNET_E_ALIGN, "%s: x and workspace must be 16-byte and y 4-byte aligned", fn);
+    const bitnet::W4Plan p = bitnet::w4_plan(N, mat->M, mat->K);
+    const int64_t need = p.shares > 1 ? p.shares * N * mat->M * 4 : 0;
+    if (need > 0 && !workspace)
+        return fail(BITNET_E_NULL, "%s: a workspace of %lld bytes is required", fn, (long long)need);
+    if (workspace_bytes < need)
+        return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
+                    (long long)workspace_bytes, (long long)need);
     hipError_t e = bitnet::launch_w4_linear(w4_args(mat), x, dtype == BITNET_BF16, N, y,
+                                            static_cast<float *>(workspace), p,
                                             static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);
     return ok();

@@ -5,6 +5,7 @@
 
 #include "attn_plan.h"
 #include "common.h"
+#include "w4_plan.h"
 
 namespace bitnet {
 
@@ -135,7 +136,7 @@ hipError_t launch_w4_pack(const void *w, int form, const uint16_t *given, int64_
 hipError_t launch_w4_rows(const W4Args &w, const int32_t *ids, int64_t n, void *out, int bf16,
                           hipStream_t st);
 hipError_t launch_w4_linear(const W4Args &w, const void *x, int bf16, int64_t N, float *y,
-                            hipStream_t st);
+                            float *part, const W4Plan &plan, hipStream_t st);
 // The attention weights of a call's rows, summed by cached token (kv4_weigh.hip).
 struct WeighArgs {
     Kv4Args c;

@@ -272,6 +272,7 @@ __global__ __launch_bounds__(kW4Threads) void w4_linear_kernel(const W4Args w, c
                     for (int tt = 0; tt < TT; ++tt)
                         s[tt] = *reinterpret_cast<const f4 *>(sc + (lb * TT + tt) * 16 + 4 * quad);
                     const uint32_t word[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                    f4 block[TT];
 #pragma unroll
                     for (int g = 0; g < GS; ++g) {
                         f4 acc[TT];
@@ -292,8 +293,13 @@ __global__ __launch_bounds__(kW4Threads) void w4_linear_kernel(const W4Args w, c
 #pragma unroll
                         for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) sum[tt][e] = fmaf(acc[tt][e], step * s[tt][e], sum[tt][e]);
+                            for (int e = 0; e < 4; ++e)
+                                block[tt][e] = g == 0 ? acc[tt][e] * step : fmaf(acc[tt][e], step, block[tt][e]);
                     }
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[tt][e] = fmaf(block[tt][e], s[tt][e], sum[tt][e]);
                     const bool here = b + u + kAhead < now.to;
                     load(u, here ? now : next, here ? b + u + kAhead : next.from + u);
                 }
@@ -334,6 +340,149 @@ __global__ __launch_bounds__(kW4Threads) void w4_linear_kernel(const W4Args w, c
     }
 }
 
+// More tokens than 16: a workgroup has 16 * TT tokens and eight waves of RT tiles each, over
+// a share of the blocks (blockIdx.z).  The tokens' operands are made `CB` blocks at a time in
+// one half of the LDS while the matrix instructions read the other half: the values for it
+// are on their way meanwhile, and so is each block of weights a turn ahead of its use.
+// Token t of the 16 bytes (j, quad) = p lies in slot (t + 4 p) mod 16 TT, so that the lanes
+// that write eight channels each of a few tokens spread over all banks.
+template <bool BF16, int TT, int GS, int RT>
+__global__ __launch_bounds__(kW4Threads, 2) void w4_wide_kernel(const W4Args w, const void *x, int64_t N,
+                                                                float *y, float *part) {
+    constexpr int NT = BF16 ? 1 : 2, CB = 4 / NT, TOK = 16 * TT;
+    constexpr int kPieces = CB * TOK * 16 / kW4Threads;   // of 8 channels, for a thread
+    __shared__ h8 xs[2][CB * 16 * NT][TOK];
+    __shared__ __align__(16) float sc[2][CB][TOK];
+    const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t tok0 = (int64_t)blockIdx.y * TOK;
+    const int toks = (int)min(N - tok0, (int64_t)TOK);
+    const int nblk = w.K / 128, tiles = (w.M + 15) / 16;
+    const int begin = (int)((int64_t)nblk * blockIdx.z / gridDim.z), end = (int)((int64_t)nblk * (blockIdx.z + 1) / gridDim.z);
+    const int tile0 = ((int)blockIdx.x * kW4Waves + wave) * RT;
+    using Word = typename StepWord<GS>::type;
+    uint4 raw[CB][RT];
+    Word st[CB][RT];
+    auto load_weights = [&](int c, int blk) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int64_t at = (int64_t)min(tile0 + r, tiles - 1) * nblk + min(blk, end - 1);
+            raw[c][r] = reinterpret_cast<const uint4 *>(w.codes)[at * 64 + lane];
+            st[c][r] = reinterpret_cast<const Word *>(w.steps)[at * 16 + n];
+        }
+    };
+    float v[kPieces][8];
+    const int p = threadIdx.x & 15, u0 = threadIdx.x >> 4;   // piece i: unit u0 + 32 i, a token's block
+    auto load_tokens = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int u = u0 + 32 * i, blk = min(b0 + u / TOK, end - 1), t = min(u % TOK, toks - 1);
+            load8<BF16>(x, (tok0 + t) * w.K + (int64_t)blk * 128 + 8 * p, v[i]);
+        }
+    };
+    auto put_tokens = [&](int half) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int u = u0 + 32 * i, blk = u / TOK, t = u % TOK;
+            h8 h[NT];
+            const float down = halves_of<NT>(v[i], h);
+#pragma unroll
+            for (int k = 0; k < NT; ++k) xs[half][(blk * 4 + (p >> 2)) * NT * 4 + k * 4 + (p & 3)][(t + 4 * p) % TOK] = h[k];
+            if (p == 0) sc[half][blk][t] = down;
+        }
+    };
+    load_tokens(begin);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) load_weights(c, begin + c);
+    put_tokens(0);
+    __syncthreads();
+    const uint32_t one = ones_1024();
+    f4 sum[RT][TT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) sum[r][tt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    int half = 0;
+    for (int b0 = begin; b0 < end; b0 += CB, half ^= 1) {
+        const bool more = b0 + CB < end;
+        if (more) load_tokens(b0 + CB);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+            if (b0 + c >= end) continue;
+            f4 block[RT][TT];
+#pragma unroll
+            for (int g = 0; g < GS; ++g) {
+                f4 acc[RT][TT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt) acc[r][tt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = g * 4 / GS; j < (g + 1) * 4 / GS; ++j) {
+                    h8 wq[RT];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const uint32_t word = j == 0 ? raw[c][r].x : j == 1 ? raw[c][r].y : j == 2 ? raw[c][r].z : raw[c][r].w;
+                        h2 q[4];
+                        codes8<false>(word, one, q);
+                        wq[r] = join(q[0], q[1], q[2], q[3]);
+                    }
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int k = 0; k < NT; ++k) {
+                            const h8 a = xs[half][(c * 4 + j) * NT * 4 + k * 4 + quad][(16 * tt + n + 4 * (4 * j + quad)) % TOK];
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) acc[r][tt] = mfma(a, wq[r], acc[r][tt]);
+                        }
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float step = step_of(st[c][r], g);
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            block[r][tt][e] = g == 0 ? acc[r][tt][e] * step : fmaf(acc[r][tt][e], step, block[r][tt][e]);
+                }
+            }
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                const f4 s = *reinterpret_cast<const f4 *>(&sc[half][c][16 * tt + 4 * quad]);
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[r][tt][e] = fmaf(block[r][tt][e], s[e], sum[r][tt][e]);
+            }
+            load_weights(c, b0 + c + CB);
+        }
+        if (more) put_tokens(half ^ 1);
+        __syncthreads();
+    }
+    float *const out = gridDim.z > 1 ? part + (int64_t)blockIdx.z * N * w.M : y;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int m = (tile0 + r) * 16 + n;
+        if (m < w.M)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 16 * tt + 4 * quad + e;
+                    if (t < toks) out[(tok0 + t) * w.M + m] = sum[r][tt][e];
+                }
+    }
+}
+
+// y = the shares' sums, added in their order.
+__global__ __launch_bounds__(256) void w4_join_kernel(const float *part, int64_t values, int shares, float *y) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < values; i += (int64_t)gridDim.x * 256) {
+        float s = part[i];
+        for (int k = 1; k < shares; ++k) s += part[k * values + i];
+        y[i] = s;
+    }
+}
+
 template <int FORM>
 void launch_pack_form(int groups, dim3 g, hipStream_t st, const void *w, const uint16_t *given, int64_t M,
                       int64_t K, uint8_t *codes, uint16_t *steps) {
@@ -343,27 +492,50 @@ void launch_pack_form(int groups, dim3 g, hipStream_t st, const void *w, const u
 #undef W4_PACK
 }
 
-template <bool BF16, int TT>
-void launch_linear_t(const W4Args &w, const void *x, int64_t N, float *y, hipStream_t st) {
-    constexpr int NT = BF16 ? 1 : 2, kLds = 64 * 1024;
-    const int toks = (int)std::min<int64_t>(N, 16 * TT), nblk = w.K / 128, tiles = (w.M + 15) / 16;
-    const int block_bytes = 256 * NT * toks + 64 * TT, red = kW4Waves * TT * 1024;
-    const int chunk = std::max(1, std::min(nblk, (kLds - red) / block_bytes));
+template <bool BF16>
+void launch_few(const W4Args &w, const void *x, int64_t N, float *y, hipStream_t st) {
+    constexpr int NT = BF16 ? 1 : 2, kLds = 64 * 1024, kRed = kW4Waves * 1024;
+    const int nblk = w.K / 128, tiles = (w.M + 15) / 16, block_bytes = 256 * NT * (int)N + 64;
+    const int chunk = std::min(nblk, (kLds - kRed) / block_bytes);
     // two workgroups to a compute unit, and the waves of one on as many tiles as leave none idle
     const int64_t groups = 512;
     int wk = 1;
-    while (wk < kW4Waves && 2 * wk <= std::min(chunk, nblk) && (int64_t)tiles * wk < groups * kW4Waves) wk *= 2;
+    while (wk < kW4Waves && 2 * wk <= chunk && (int64_t)tiles * wk < groups * kW4Waves) wk *= 2;
     const int slots = kW4Waves / wk;
     const int64_t need = (tiles + slots - 1) / slots;
     const int64_t grid = std::min(need, groups);
     const int iters = (int)((need + grid - 1) / grid);
-    const dim3 g((unsigned)grid, (unsigned)((N + 16 * TT - 1) / (16 * TT)));
-    const size_t lds = (size_t)chunk * block_bytes + red;
-#define W4_LINEAR(GS)                                                                             \
-    hipLaunchKernelGGL((w4_linear_kernel<BF16, TT, GS>), g, dim3(kW4Threads), lds, st, w, x, N, y, \
-                       wk, chunk, iters)
-    if (w.groups == 1) W4_LINEAR(1); else if (w.groups == 2) W4_LINEAR(2); else W4_LINEAR(4);
-#undef W4_LINEAR
+    const size_t lds = (size_t)chunk * block_bytes + kRed;
+#define W4_FEW(GS)                                                                                     \
+    hipLaunchKernelGGL((w4_linear_kernel<BF16, 1, GS>), dim3((unsigned)grid), dim3(kW4Threads), lds, st, \
+                       w, x, N, y, wk, chunk, iters)
+    if (w.groups == 1) W4_FEW(1); else if (w.groups == 2) W4_FEW(2); else W4_FEW(4);
+#undef W4_FEW
+}
+
+template <bool BF16, int TT, int RT>
+void launch_wide(const W4Args &w, const void *x, int64_t N, float *y, float *part, dim3 g, hipStream_t st) {
+#define W4_WIDE(GS) \
+    hipLaunchKernelGGL((w4_wide_kernel<BF16, TT, GS, RT>), g, dim3(kW4Threads), 0, st, w, x, N, y, part)
+    if (w.groups == 1) W4_WIDE(1); else if (w.groups == 2) W4_WIDE(2); else W4_WIDE(4);
+#undef W4_WIDE
+}
+template <bool BF16>
+void launch_many(const W4Args &w, const void *x, int64_t N, float *y, float *part, const W4Plan &p,
+                 hipStream_t st) {
+    const dim3 g((unsigned)p.rows, (unsigned)p.tokens, (unsigned)p.shares);
+    if (p.tt == 2) {
+        if (p.rt == 2) launch_wide<BF16, 2, 2>(w, x, N, y, part, g, st);
+        else launch_wide<BF16, 2, 1>(w, x, N, y, part, g, st);
+    } else {
+        if (p.rt == 2) launch_wide<BF16, 4, 2>(w, x, N, y, part, g, st);
+        else launch_wide<BF16, 4, 1>(w, x, N, y, part, g, st);
+    }
+    if (p.shares > 1) {
+        const int64_t values = N * w.M;
+        hipLaunchKernelGGL(w4_join_kernel, dim3((unsigned)std::min<int64_t>((values + 255) / 256, 1 << 16)), dim3(256),
+                           0, st, part, values, p.shares, y);
+    }
 }
 
 }  // namespace
@@ -385,11 +557,11 @@ hipError_t launch_w4_rows(const W4Args &w, const int32_t *ids, int64_t n, void *
     return hipGetLastError();
 }
 
-hipError_t launch_w4_linear(const W4Args &w, const void *x, int bf16, int64_t N, float *y, hipStream_t st) {
-#define W4_TOKENS(TT) \
-    if (bf16) launch_linear_t<true, TT>(w, x, N, y, st); else launch_linear_t<false, TT>(w, x, N, y, st)
-    if (N <= 16) { W4_TOKENS(1); } else if (N <= 32) { W4_TOKENS(2); } else { W4_TOKENS(4); }
-#undef W4_TOKENS
+hipError_t launch_w4_linear(const W4Args &w, const void *x, int bf16, int64_t N, float *y, float *part,
+                            const W4Plan &p, hipStream_t st) {
+    if (p.tt == 1) { if (bf16) launch_few<true>(w, x, N, y, st); else launch_few<false>(w, x, N, y, st); }
+    else if (bf16) launch_many<true>(w, x, N, y, part, p, st);
+    else launch_many<false>(w, x, N, y, part, p, st);
     return hipGetLastError();
 }
 

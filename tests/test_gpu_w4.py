@@ -207,6 +207,27 @@ def test_captured_and_on_another_stream(bn):
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_shares_of_the_channels_and_given_scratch(bn, dtype):
+    """Sizes for one share and for many, one tile of rows to a wave and two; scratch of any content."""
+    rng = np.random.default_rng(8)
+    for N, M, K in ((17, 40, 128), (20, 40, 32768), (64, 300, 12800), (33, 5000, 1408), (64, 4200, 2560), (130, 4100, 4096)):
+        codes = rng.integers(-8, 8, (M, K)).astype(np.int8)
+        steps = rng.choice([1.0, 2.0, -1.0], (M, K // 64)).astype(np.float16)
+        mat = bn.pack_w4_codes(dev(codes), dev(steps))
+        x = np.zeros((N, K), np.float32)
+        for t in range(N):
+            x[t, rng.permutation(K)[:16]] = rng.integers(-15, 16, 16)
+        need = bn.linear_w4_workspace(N, M, K)
+        ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        y = bn.linear_w4(dev(x, dtype), mat, workspace=ws)
+        assert np.array_equal(host(y), (x.astype(np.float64) @ so.w4_values(codes, steps).T).astype(np.float32))
+        assert (ws[need:] == 0xFF).all()
+        if need:
+            with pytest.raises(ValueError):
+                bn.linear_w4(dev(x, dtype), mat, workspace=ws[:need - 1])
+
+
 def test_nothing_to_multiply(bn):
     mat = bn.pack_w4(torch.ones((20, 128), device="cuda"))
     assert bn.linear_w4(torch.empty((0, 128), device="cuda"), mat).shape == (0, 20)

@@ -111,7 +111,8 @@ W4 = {
     "pack": lambda L, m=None, dt=0, w=FAKE: L.bitnet_pack_w4(w, dt, m or _mat(), None),
     "codes": lambda L, m=None, w=FAKE, s=FAKE: L.bitnet_pack_w4_codes(w, s, m or _mat(), None),
     "rows": lambda L, m=None, dt=0, ids=FAKE, n=3, out=FAKE: L.bitnet_w4_rows(m or _mat(), ids, n, out, dt, None),
-    "linear": lambda L, m=None, dt=0, x=FAKE, N=3, y=FAKE: L.bitnet_linear_w4(x, dt, N, m or _mat(), y, None),
+    "linear": lambda L, m=None, dt=0, x=FAKE, N=3, y=FAKE, ws=None, wb=0:
+        L.bitnet_linear_w4(x, dt, N, m or _mat(), y, ws, wb, None),
 }
 
 
@@ -146,6 +147,13 @@ def test_w4_operand_validation(L):
     assert f(L, x=None) == E_NULL and f(L, y=None) == E_NULL
     assert f(L, x=MIS) == E_ALIGN and f(L, y=FAKE + 2) == E_ALIGN
     assert f(L, N=0, x=None, y=None) == OK and L.bitnet_last_error().decode() == ""
+    need = L.bitnet_linear_w4_workspace(20, 20, 8192)
+    big = lambda **kw: f(L, _mat(K=8192), N=20, **kw)  # noqa: E731
+    assert need >= 2 * 20 * 20 * 4 and big() == E_NULL and big(ws=FAKE, wb=need - 1) == E_SHAPE
+    assert f(L, ws=MIS) == E_ALIGN
+    assert L.bitnet_linear_w4_workspace(16, 1 << 24, 32768) == 0 == L.bitnet_linear_w4_workspace(0, 5, 128)
+    for bad in ((-1, 5, 128), (5, -1, 128), (5, 5, 100), ((1 << 21) + 1, 5, 128), (5, (1 << 24) + 1, 128)):
+        assert L.bitnet_linear_w4_workspace(*bad) == -1
 
 
 def test_w4_binding_refuses():
