@@ -545,9 +545,8 @@ int bitnet_w4_rows(const bitnet_w4_matrix *mat, const int32_t *ids, int64_t n, v
  *   x        [N][K] fp32 or bf16, 16-byte aligned.
  *   y        [N][M] fp32, 4-byte aligned.
  *   workspace   device scratch of at least bitnet_linear_w4_workspace bytes (-1: sizes out
- *            of range) of the same sizes, 16-byte aligned (may be NULL where that is 0, as for up
- *            to 16 tokens); used until the call's kernels have ended, so calls that may run at
- *            once need one each.
+ *            of range) of the same sizes, 16-byte aligned (may be NULL where that is 0); used
+ *            until the call's kernels have ended, so calls that may run at once need one each.
  *   0 <= N <= BITNET_GEMM_MAX_N; N == 0 or M == 0 is a no-op.
  * A token's channels are carried in 22 bits (fp32; bf16 exactly) and no finer than 2^-40 of
  * the largest of their 128 (bf16: 2^-39); products and sums are fp32, so where the sum of

@@ -871,9 +871,6 @@ def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0,
     return new_len, index
 
 
-W4_FEW = 16                # linear_w4: up to so many tokens take no workspace
-
-
 class W4Matrix:
     """A matrix of 4-bit weights [M][K] as pack_w4 lays it out: ``codes`` uint8
     [ceil(M/16)][K/128][64][16], ``steps`` fp16 [ceil(M/16)][K/128][16][128/group], and the number of its
@@ -959,7 +956,7 @@ def w4_rows(mat, ids=None, dtype=None, out=None):
 
 def linear_w4(x, mat, out=None, workspace=None):
     """x [N][K] (fp32 or bf16, any N) times a W4Matrix -> y [N][M] fp32.  workspace: a uint8
-    tensor for calls that must not allocate (linear_w4_workspace bytes, none up to 16 tokens);
+    tensor for calls that must not allocate (linear_w4_workspace bytes, often none);
     one for each call that may run at once."""
     import torch
     if x.dim() != 2 or x.shape[1] != mat.k:
@@ -971,15 +968,15 @@ def linear_w4(x, mat, out=None, workspace=None):
         to = out.data_ptr()
     else:
         to = _at(out, "out", torch.float32, (N, mat.rows), dev)
-    ws, size = None, 0
-    if N > W4_FEW:
-        need = linear_w4_workspace(N, mat.rows, mat.k)
+    L = load()
+    need, ws = L.bitnet_linear_w4_workspace(N, mat.rows, mat.k), None
+    if need > 0:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         elif workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
             raise ValueError(f"workspace must be {need} bytes of uint8 on {dev}")
-        ws, size = _ptr(workspace), workspace.numel()
-    _launch(load().bitnet_linear_w4, dev, at, _float_code(x.dtype, "x"), N, mat._desc, to, ws, size)
+        ws = _ptr(workspace)
+    _launch(L.bitnet_linear_w4, dev, at, _float_code(x.dtype, "x"), N, mat._desc, to, ws, max(need, 0))
     return out
 
 

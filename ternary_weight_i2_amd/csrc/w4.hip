@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kW4Threads = 512;
 constexpr int kW4Waves = kW4Threads / 64;
-constexpr int kAhead = 4;                 // blocks of 1 KB that a wave has on the way
 constexpr float kW4Max = 7.0f * 65504.0f; // 7 steps of the largest fp16
 
 // ---------------------------------------------------------------- quantiser
@@ -166,191 +165,19 @@ __device__ __forceinline__ float step_of(const uint2 &w, int g) {
     return (float)as_h2(g < 2 ? w.x : w.y)[g & 1];
 }
 
-// The tokens of blockIdx.y (up to 16 * TT) times tiles of rows.  WK of a workgroup's eight
-// waves share a tile's blocks; the others have tiles of their own, every gridDim.x * 8 / WK
-// on.  The tokens lie in LDS as operands: all of their channels if they fit, else `chunk`
-// blocks at a time.
-template <bool BF16, int TT, int GS>
-__global__ __launch_bounds__(kW4Threads) void w4_linear_kernel(const W4Args w, const void *x, int64_t N,
-                                                               float *y, int wk, int chunk, int iters) {
-    constexpr int NT = BF16 ? 1 : 2;
-    extern __shared__ __align__(16) uint8_t lds[];
-    const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tok0 = (int64_t)blockIdx.y * 16 * TT;
-    const int toks = (int)min(N - tok0, (int64_t)(16 * TT));
-    const int nblk = w.K / 128, tiles = (w.M + 15) / 16;
-    h8 *const xs = reinterpret_cast<h8 *>(lds);            // [block][j][term][quad][token]
-    float *const sc = reinterpret_cast<float *>(lds + (size_t)chunk * 256 * NT * toks);   // [block][16 TT]
-    float4 *const red = reinterpret_cast<float4 *>(sc + chunk * 16 * TT);                 // [wave][TT][lane]
-
-    // ---- this wave's blocks: shares of the chunks, tile by tile
-    const int part = wave % wk, slot = wave / wk, slots = kW4Waves / wk;
-    const int chunks = (nblk + chunk - 1) / chunk;
-    auto tile_at = [&](int it) { return ((int)blockIdx.x + it * (int)gridDim.x) * slots + slot; };
-    struct Run { int tile, from, to; };
-    auto run_at = [&](int it, int c) {
-        const int b0 = c * chunk, cnt = min(chunk, nblk - b0);
-        return Run{min(tile_at(it), tiles - 1), b0 + cnt * part / wk, b0 + cnt * (part + 1) / wk};
-    };
-    using Word = typename StepWord<GS>::type;
-    uint4 raw[kAhead];
-    Word st[kAhead];
-    auto load = [&](int u, const Run &r, int blk) {
-        const int64_t at = (int64_t)r.tile * nblk + min(blk, nblk - 1);
-        raw[u] = reinterpret_cast<const uint4 *>(w.codes)[at * 64 + lane];
-        st[u] = reinterpret_cast<const Word *>(w.steps)[at * 16 + n];
-    };
-    auto after = [&](int it, int c) {   // the run that follows, or the same at the end
-        if (c + 1 < chunks) return run_at(it, c + 1);
-        return it + 1 < iters ? run_at(it + 1, 0) : run_at(it, c);
-    };
-    Run now = run_at(0, 0);
-    {
-        const Run next = after(0, 0);
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const bool here = now.from + u < now.to;
-            load(u, here ? now : next, here ? now.from + u : next.from + u);
-        }
-    }
-    const uint32_t one = ones_1024();
-
-    auto stage = [&](int c) {
-        const int b0 = c * chunk, cnt = min(chunk, nblk - b0), p = threadIdx.x & 15;
-        const int units = cnt * toks;   // (block, token): 16 lanes with 8 channels each
-        constexpr int kBatch = 4, kStep = kW4Threads / 16;
-        for (int u0 = threadIdx.x >> 4; u0 < units; u0 += kBatch * kStep) {
-            float v[kBatch][8];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int u = min(u0 + i * kStep, units - 1), blk = u / toks, t = u - blk * toks;
-                load8<BF16>(x, (tok0 + t) * w.K + (b0 + blk) * 128 + 8 * p, v[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int u = u0 + i * kStep;
-                if (u >= units) break;   // the same for the 16 lanes
-                const int blk = u / toks, t = u - blk * toks;
-                h8 h[NT];
-                const float down = halves_of<NT>(v[i], h);
-#pragma unroll
-                for (int k = 0; k < NT; ++k)
-                    xs[(((blk * 4 + (p >> 2)) * NT + k) * 4 + (p & 3)) * toks + t] = h[k];
-                if (p == 0) sc[blk * 16 * TT + t] = down;
-            }
-        }
-    };
-    if (chunks == 1) {
-        stage(0);
-        __syncthreads();
-    }
-    int tok[TT];   // the operand's token of this lane: those behind the last are repeated
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) tok[tt] = min(16 * tt + n, toks - 1);
-
-    for (int it = 0; it < iters; ++it) {
-        f4 sum[TT];
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) sum[tt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int c = 0; c < chunks; ++c) {
-            if (chunks > 1) {
-                __syncthreads();
-                stage(c);
-                __syncthreads();
-            }
-            now = run_at(it, c);
-            const Run next = after(it, c);
-            for (int b = now.from; b < now.to; b += kAhead) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (b + u >= now.to) continue;   // the slot holds the next run's block
-                    const int lb = b + u - c * chunk;
-                    const h8 *const xb = xs + lb * 16 * NT * toks + quad * toks;
-                    f4 s[TT];
-#pragma unroll
-                    for (int tt = 0; tt < TT; ++tt)
-                        s[tt] = *reinterpret_cast<const f4 *>(sc + (lb * TT + tt) * 16 + 4 * quad);
-                    const uint32_t word[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-                    f4 block[TT];
-#pragma unroll
-                    for (int g = 0; g < GS; ++g) {
-                        f4 acc[TT];
-#pragma unroll
-                        for (int tt = 0; tt < TT; ++tt) acc[tt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int j = g * 4 / GS; j < (g + 1) * 4 / GS; ++j) {
-                            h2 q[4];
-                            codes8<false>(word[j], one, q);
-                            const h8 wq = join(q[0], q[1], q[2], q[3]);
-#pragma unroll
-                            for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                                for (int k = 0; k < NT; ++k)
-                                    acc[tt] = mfma(xb[(j * NT + k) * 4 * toks + tok[tt]], wq, acc[tt]);
-                        }
-                        const float step = step_of(st[u], g);
-#pragma unroll
-                        for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                block[tt][e] = g == 0 ? acc[tt][e] * step : fmaf(acc[tt][e], step, block[tt][e]);
-                    }
-#pragma unroll
-                    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[tt][e] = fmaf(block[tt][e], s[tt][e], sum[tt][e]);
-                    const bool here = b + u + kAhead < now.to;
-                    load(u, here ? now : next, here ? b + u + kAhead : next.from + u);
-                }
-            }
-            // slots that a short run had no block for
-            if (now.to - now.from < kAhead)
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    if (now.from + u >= now.to) load(u, next, next.from + u);
-        }
-        // ---- the tile's rows: lane (n, quad) has row n of tokens 4 quad + e
-        const int tile = tile_at(it), m = tile * 16 + n;
-        if (wk > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt)
-                red[(wave * TT + tt) * 64 + lane] = make_float4(sum[tt][0], sum[tt][1], sum[tt][2], sum[tt][3]);
-            __syncthreads();
-            if (part == 0)
-#pragma unroll
-                for (int tt = 0; tt < TT; ++tt)
-                    for (int k = 1; k < wk; ++k) {
-                        const float4 o = red[((wave + k) * TT + tt) * 64 + lane];
-                        sum[tt][0] += o.x;
-                        sum[tt][1] += o.y;
-                        sum[tt][2] += o.z;
-                        sum[tt][3] += o.w;
-                    }
-        }
-        if (part == 0 && m < w.M)
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * tt + 4 * quad + e;
-                    if (t < toks) y[(tok0 + t) * w.M + m] = sum[tt][e];
-                }
-    }
-}
-
-// More tokens than 16: a workgroup has 16 * TT tokens and eight waves of RT tiles each, over
-// a share of the blocks (blockIdx.z).  The tokens' operands are made `CB` blocks at a time in
-// one half of the LDS while the matrix instructions read the other half: the values for it
-// are on their way meanwhile, and so is each block of weights a turn ahead of its use.
-// Token t of the 16 bytes (j, quad) = p lies in slot (t + 4 p) mod 16 TT, so that the lanes
-// that write eight channels each of a few tokens spread over all banks.
-template <bool BF16, int TT, int GS, int RT>
-__global__ __launch_bounds__(kW4Threads, 2) void w4_wide_kernel(const W4Args w, const void *x, int64_t N,
-                                                                float *y, float *part) {
-    constexpr int NT = BF16 ? 1 : 2, CB = 4 / NT, TOK = 16 * TT;
-    constexpr int kPieces = CB * TOK * 16 / kW4Threads;   // of 8 channels, for a thread
+// A workgroup has 16 * TT tokens and eight waves over a share of the blocks (blockIdx.z).  WK of
+// the waves share a tile's blocks, so that few rows have many waves; or a wave has RT tiles,
+// which halves what it reads of the operands in LDS (w4_plan.h chooses).
+// The tokens' operands are made CB blocks at a time in one half of the LDS while the matrix
+// instructions read the other half: the values for it are on their way meanwhile, and so is
+// each block of weights a turn ahead of its use.  Token t of the 16 bytes (j, quad) = p lies
+// in slot (t + 4 p) mod 16 TT, so that the lanes that write eight channels each of a few tokens
+// spread over all banks.
+template <bool BF16, int TT, int GS, int RT, int WK>
+__global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w, const void *x, int64_t N,
+                                                                  float *y, float *part) {
+    constexpr int NT = BF16 ? 1 : 2, CB = WK == 4 ? 8 : WK == 2 ? 8 / NT : 4 / NT, TOK = 16 * TT, OWN = CB / WK;
+    constexpr int kPieces = CB * TOK * 16 / kW4Threads;   // of 8 channels, at most for a thread
     __shared__ h8 xs[2][CB * 16 * NT][TOK];
     __shared__ __align__(16) float sc[2][CB][TOK];
     const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
@@ -359,44 +186,53 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_wide_kernel(const W4Args w, 
     const int toks = (int)min(N - tok0, (int64_t)TOK);
     const int nblk = w.K / 128, tiles = (w.M + 15) / 16;
     const int begin = (int)((int64_t)nblk * blockIdx.z / gridDim.z), end = (int)((int64_t)nblk * (blockIdx.z + 1) / gridDim.z);
-    const int tile0 = ((int)blockIdx.x * kW4Waves + wave) * RT;
+    const int turn = wave % WK;   // of the waves of a tile: its blocks are turn, turn + WK, ...
+    const int tile0 = ((int)blockIdx.x * (kW4Waves / WK) + wave / WK) * RT;
     using Word = typename StepWord<GS>::type;
-    uint4 raw[CB][RT];
-    Word st[CB][RT];
-    auto load_weights = [&](int c, int blk) {
+    uint4 raw[OWN][RT];
+    Word st[OWN][RT];
+    auto load_weights = [&](int i, int b0) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const int64_t at = (int64_t)min(tile0 + r, tiles - 1) * nblk + min(blk, end - 1);
-            raw[c][r] = reinterpret_cast<const uint4 *>(w.codes)[at * 64 + lane];
-            st[c][r] = reinterpret_cast<const Word *>(w.steps)[at * 16 + n];
+            const int64_t at = (int64_t)min(tile0 + r, tiles - 1) * nblk + min(b0 + i * WK + turn, end - 1);
+            raw[i][r] = reinterpret_cast<const uint4 *>(w.codes)[at * 64 + lane];
+            st[i][r] = reinterpret_cast<const Word *>(w.steps)[at * 16 + n];
         }
     };
-    float v[kPieces][8];
+    uint4 v[kPieces][NT];   // eight channels as they are
     const int p = threadIdx.x & 15, u0 = threadIdx.x >> 4;   // piece i: unit u0 + 32 i, a token's block
     auto load_tokens = [&](int b0) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int u = u0 + 32 * i, blk = min(b0 + u / TOK, end - 1), t = min(u % TOK, toks - 1);
-            load8<BF16>(x, (tok0 + t) * w.K + (int64_t)blk * 128 + 8 * p, v[i]);
+            const int u = u0 + 32 * i, c = u / TOK, t = min(u % TOK, toks - 1);
+            const int64_t at = (tok0 + t) * w.K + (int64_t)min(b0 + c, end - 1) * 128 + 8 * p;
+#pragma unroll
+            for (int k = 0; k < NT; ++k) v[i][k] = reinterpret_cast<const uint4 *>(x)[at / (8 / NT) + k];
         }
     };
     auto put_tokens = [&](int half) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int u = u0 + 32 * i, blk = u / TOK, t = u % TOK;
+            const int u = u0 + 32 * i, c = u / TOK, t = u % TOK;
+            if (TT == 1 && t >= toks) continue;   // the same for the 16 lanes
             h8 h[NT];
-            const float down = halves_of<NT>(v[i], h);
+            float f[8];
+            load8<BF16>(v[i], 0, f);
+            const float down = halves_of<NT>(f, h);
 #pragma unroll
-            for (int k = 0; k < NT; ++k) xs[half][(blk * 4 + (p >> 2)) * NT * 4 + k * 4 + (p & 3)][(t + 4 * p) % TOK] = h[k];
-            if (p == 0) sc[half][blk][t] = down;
+            for (int k = 0; k < NT; ++k) xs[half][(c * 4 + (p >> 2)) * NT * 4 + k * 4 + (p & 3)][(t + 4 * p) % TOK] = h[k];
+            if (p == 0) sc[half][c][t] = down;
         }
     };
     load_tokens(begin);
 #pragma unroll
-    for (int c = 0; c < CB; ++c) load_weights(c, begin + c);
+    for (int i = 0; i < OWN; ++i) load_weights(i, begin);
     put_tokens(0);
     __syncthreads();
     const uint32_t one = ones_1024();
+    int tok[TT];   // the operand's token of this lane: the last one again behind it
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) tok[tt] = (TT == 1 ? min(n, toks - 1) : 16 * tt + n) + 4 * quad;
     f4 sum[RT][TT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -407,7 +243,8 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_wide_kernel(const W4Args w, 
         const bool more = b0 + CB < end;
         if (more) load_tokens(b0 + CB);
 #pragma unroll
-        for (int c = 0; c < CB; ++c) {
+        for (int i = 0; i < OWN; ++i) {
+            const int c = i * WK + turn;
             if (b0 + c >= end) continue;
             f4 block[RT][TT];
 #pragma unroll
@@ -422,7 +259,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_wide_kernel(const W4Args w, 
                     h8 wq[RT];
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const uint32_t word = j == 0 ? raw[c][r].x : j == 1 ? raw[c][r].y : j == 2 ? raw[c][r].z : raw[c][r].w;
+                        const uint32_t word = j == 0 ? raw[i][r].x : j == 1 ? raw[i][r].y : j == 2 ? raw[i][r].z : raw[i][r].w;
                         h2 q[4];
                         codes8<false>(word, one, q);
                         wq[r] = join(q[0], q[1], q[2], q[3]);
@@ -431,14 +268,14 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_wide_kernel(const W4Args w, 
                     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                         for (int k = 0; k < NT; ++k) {
-                            const h8 a = xs[half][(c * 4 + j) * NT * 4 + k * 4 + quad][(16 * tt + n + 4 * (4 * j + quad)) % TOK];
+                            const h8 a = xs[half][(c * 4 + j) * NT * 4 + k * 4 + quad][(tok[tt] + 16 * j) % TOK];
 #pragma unroll
                             for (int r = 0; r < RT; ++r) acc[r][tt] = mfma(a, wq[r], acc[r][tt]);
                         }
                 }
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const float step = step_of(st[c][r], g);
+                    const float step = step_of(st[i][r], g);
 #pragma unroll
                     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
@@ -454,10 +291,25 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_wide_kernel(const W4Args w, 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sum[r][tt][e] = fmaf(block[r][tt][e], s[e], sum[r][tt][e]);
             }
-            load_weights(c, b0 + c + CB);
+            load_weights(i, b0 + CB);
         }
         if (more) put_tokens(half ^ 1);
         __syncthreads();
+    }
+    if constexpr (WK > 1) {   // the waves of a tile, in their order
+        f4 *const red = reinterpret_cast<f4 *>(xs);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) red[((wave * RT + r) * TT + tt) * 64 + lane] = sum[r][tt];
+        __syncthreads();
+        if (turn != 0) return;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                for (int k = 1; k < WK; ++k) sum[r][tt] += red[(((wave + k) * RT + r) * TT + tt) * 64 + lane];
     }
     float *const out = gridDim.z > 1 ? part + (int64_t)blockIdx.z * N * w.M : y;
 #pragma unroll
@@ -492,50 +344,25 @@ void launch_pack_form(int groups, dim3 g, hipStream_t st, const void *w, const u
 #undef W4_PACK
 }
 
-template <bool BF16>
-void launch_few(const W4Args &w, const void *x, int64_t N, float *y, hipStream_t st) {
-    constexpr int NT = BF16 ? 1 : 2, kLds = 64 * 1024, kRed = kW4Waves * 1024;
-    const int nblk = w.K / 128, tiles = (w.M + 15) / 16, block_bytes = 256 * NT * (int)N + 64;
-    const int chunk = std::min(nblk, (kLds - kRed) / block_bytes);
-    // two workgroups to a compute unit, and the waves of one on as many tiles as leave none idle
-    const int64_t groups = 512;
-    int wk = 1;
-    while (wk < kW4Waves && 2 * wk <= chunk && (int64_t)tiles * wk < groups * kW4Waves) wk *= 2;
-    const int slots = kW4Waves / wk;
-    const int64_t need = (tiles + slots - 1) / slots;
-    const int64_t grid = std::min(need, groups);
-    const int iters = (int)((need + grid - 1) / grid);
-    const size_t lds = (size_t)chunk * block_bytes + kRed;
-#define W4_FEW(GS)                                                                                     \
-    hipLaunchKernelGGL((w4_linear_kernel<BF16, 1, GS>), dim3((unsigned)grid), dim3(kW4Threads), lds, st, \
-                       w, x, N, y, wk, chunk, iters)
-    if (w.groups == 1) W4_FEW(1); else if (w.groups == 2) W4_FEW(2); else W4_FEW(4);
-#undef W4_FEW
-}
-
-template <bool BF16, int TT, int RT>
-void launch_wide(const W4Args &w, const void *x, int64_t N, float *y, float *part, dim3 g, hipStream_t st) {
-#define W4_WIDE(GS) \
-    hipLaunchKernelGGL((w4_wide_kernel<BF16, TT, GS, RT>), g, dim3(kW4Threads), 0, st, w, x, N, y, part)
-    if (w.groups == 1) W4_WIDE(1); else if (w.groups == 2) W4_WIDE(2); else W4_WIDE(4);
-#undef W4_WIDE
+template <bool BF16, int TT, int RT, int WK>
+void launch_linear_t(const W4Args &w, const void *x, int64_t N, float *y, float *part, const W4Plan &p,
+                     hipStream_t st) {
+    const dim3 g((unsigned)p.rows, (unsigned)p.tokens, (unsigned)p.shares), t(kW4Threads);
+#define W4_LINEAR(GS) \
+    hipLaunchKernelGGL((w4_linear_kernel<BF16, TT, GS, RT, WK>), g, t, 0, st, w, x, N, y, part)
+    if (w.groups == 1) W4_LINEAR(1); else if (w.groups == 2) W4_LINEAR(2); else W4_LINEAR(4);
+#undef W4_LINEAR
 }
 template <bool BF16>
-void launch_many(const W4Args &w, const void *x, int64_t N, float *y, float *part, const W4Plan &p,
-                 hipStream_t st) {
-    const dim3 g((unsigned)p.rows, (unsigned)p.tokens, (unsigned)p.shares);
-    if (p.tt == 2) {
-        if (p.rt == 2) launch_wide<BF16, 2, 2>(w, x, N, y, part, g, st);
-        else launch_wide<BF16, 2, 1>(w, x, N, y, part, g, st);
-    } else {
-        if (p.rt == 2) launch_wide<BF16, 4, 2>(w, x, N, y, part, g, st);
-        else launch_wide<BF16, 4, 1>(w, x, N, y, part, g, st);
-    }
-    if (p.shares > 1) {
-        const int64_t values = N * w.M;
-        hipLaunchKernelGGL(w4_join_kernel, dim3((unsigned)std::min<int64_t>((values + 255) / 256, 1 << 16)), dim3(256),
-                           0, st, part, values, p.shares, y);
-    }
+void launch_linear(const W4Args &w, const void *x, int64_t N, float *y, float *part, const W4Plan &p,
+                   hipStream_t st) {
+    if (p.tt == 1 && p.wk == 4) launch_linear_t<BF16, 1, 1, 4>(w, x, N, y, part, p, st);
+    else if (p.tt == 1 && p.wk == 2) launch_linear_t<BF16, 1, 1, 2>(w, x, N, y, part, p, st);
+    else if (p.tt == 1) launch_linear_t<BF16, 1, 1, 1>(w, x, N, y, part, p, st);
+    else if (p.tt == 2 && p.rt == 2) launch_linear_t<BF16, 2, 2, 1>(w, x, N, y, part, p, st);
+    else if (p.tt == 2) launch_linear_t<BF16, 2, 1, 1>(w, x, N, y, part, p, st);
+    else if (p.rt == 2) launch_linear_t<BF16, 4, 2, 1>(w, x, N, y, part, p, st);
+    else launch_linear_t<BF16, 4, 1, 1>(w, x, N, y, part, p, st);
 }
 
 }  // namespace
@@ -559,9 +386,13 @@ hipError_t launch_w4_rows(const W4Args &w, const int32_t *ids, int64_t n, void *
 
 hipError_t launch_w4_linear(const W4Args &w, const void *x, int bf16, int64_t N, float *y, float *part,
                             const W4Plan &p, hipStream_t st) {
-    if (p.tt == 1) { if (bf16) launch_few<true>(w, x, N, y, st); else launch_few<false>(w, x, N, y, st); }
-    else if (bf16) launch_many<true>(w, x, N, y, part, p, st);
-    else launch_many<false>(w, x, N, y, part, p, st);
+    if (bf16) launch_linear<true>(w, x, N, y, part, p, st);
+    else launch_linear<false>(w, x, N, y, part, p, st);
+    if (p.shares > 1) {
+        const int64_t values = N * w.M;
+        hipLaunchKernelGGL(w4_join_kernel, dim3((unsigned)std::min<int64_t>((values + 255) / 256, 1 << 16)), dim3(256),
+                           0, st, part, values, p.shares, y);
+    }
     return hipGetLastError();
 }
 

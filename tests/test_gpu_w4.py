@@ -211,7 +211,7 @@ def test_captured_and_on_another_stream(bn):
 def test_shares_of_the_channels_and_given_scratch(bn, dtype):
     """Sizes for one share and for many, one tile of rows to a wave and two; scratch of any content."""
     rng = np.random.default_rng(8)
-    for N, M, K in ((17, 40, 128), (20, 40, 32768), (64, 300, 12800), (33, 5000, 1408), (64, 4200, 2560), (130, 4100, 4096)):
+    for N, M, K in ((1, 100, 8192), (16, 3000, 4096), (5, 20000, 256), (3, 12000, 4480), (17, 40, 128), (20, 40, 32768), (64, 300, 12800), (33, 5000, 1408), (64, 4200, 2560), (130, 4100, 4096)):
         codes = rng.integers(-8, 8, (M, K)).astype(np.int8)
         steps = rng.choice([1.0, 2.0, -1.0], (M, K // 64)).astype(np.float16)
         mat = bn.pack_w4_codes(dev(codes), dev(steps))

@@ -152,6 +152,7 @@ def test_w4_operand_validation(L):
     assert need >= 2 * 20 * 20 * 4 and big() == E_NULL and big(ws=FAKE, wb=need - 1) == E_SHAPE
     assert f(L, ws=MIS) == E_ALIGN
     assert L.bitnet_linear_w4_workspace(16, 1 << 24, 32768) == 0 == L.bitnet_linear_w4_workspace(0, 5, 128)
+    assert L.bitnet_linear_w4_workspace(16, 0, 32768) == 0
     for bad in ((-1, 5, 128), (5, -1, 128), (5, 5, 100), ((1 << 21) + 1, 5, 128), (5, (1 << 24) + 1, 128)):
         assert L.bitnet_linear_w4_workspace(*bad) == -1
 
