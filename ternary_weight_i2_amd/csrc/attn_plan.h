@@ -89,10 +89,10 @@ inline Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
 }
 
 // kv4_weigh.hip: the tiles of 16 rows, the shares of the pages that each tile's rows see, the
-// workgroups that share a sequence's pages, and whether a page's rows are shared by waves.
+// workgroups that share a sequence's pages, and whether its rows are many (a workgroup to a page).
 struct WeighPlan {
     int64_t tiles;
-    int splits, chunks, shared;
+    int splits, chunks, many;
 };
 inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
                             int64_t max_kv, int64_t window, int64_t sinks) {
@@ -108,10 +108,9 @@ inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
     constexpr int64_t kMost = 1 << 22;
     p.splits = (int)std::max<int64_t>(
         std::min({4 * kUnits / busy, seen / 4, (int64_t)64, kMost / (p.tiles * kv_heads)}), 1);
-    // Rows of several tiles are shared by the waves.
-    p.shared = rows >= 4 * 16 * n_seqs;
-    p.chunks = (int)std::max<int64_t>(
-        std::min(p.shared ? pages : (pages + 3) / 4, kMost / (n_seqs * kv_heads)), 1);
+    p.many = rows >= 4 * 16 * n_seqs;
+    const int64_t parts = p.many ? pages : std::min(pages / 4, 4 * kUnits / (std::min(n_seqs, N) * kv_heads));
+    p.chunks = (int)std::max<int64_t>(std::min(parts, kMost / (n_seqs * kv_heads)), 1);
     return p;
 }
 

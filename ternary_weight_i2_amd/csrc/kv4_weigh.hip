@@ -7,10 +7,10 @@
 // rows of one problem as in attn_kv4.hip.
 //
 // Two launches.  The first gives each row's maximum m and sum, a workgroup to 16 rows and
-// a share of the pages that they see, its waves taking turns at the pages.  The second has
-// a wave to a page (or a workgroup, where there are many rows): it goes over the rows that
-// see the page and keeps the page's 64 sums in registers, so no token is added to by two
-// waves and the order of the sums is fixed.  Between them lie 8 bytes a row and share.
+// a share of the pages that they see, its waves taking turns at the pages.  The second sums
+// by token: few rows with a wave to every fourth page of a share, many rows with a workgroup
+// to a page, so no token is added to by two of them and the order of the sums is fixed.
+// Between the launches lie 8 bytes a row and share; the keys are read by both.
 //
 // q . k_t = sum_g step_tg (q_g . (code_tg - 8)) + mid_tg sum(q_g), the products of codes on
 // the fp16 matrix instruction (q scaled by a power of two a row, in two fp16 terms of 22
@@ -66,34 +66,38 @@ __device__ __forceinline__ void load_query(Query<D, BF16> &q, const void *p, int
     }
 }
 
-// A page's keys as they are loaded: this lane's codes of token 16 i + n, 8 channels of
-// every 32, and the pairs of tokens 16 i + 4 quad + 0..3.
+// A page's keys as they are loaded: this lane's codes of tokens 16 i + n, 8 channels of
+// every 32, and the pairs of token `lane`, which the wave shares through LDS.
 template <int D>
 struct Keys {
     static constexpr int NS = D / 32, NG = D / 64;
-    uint32_t code[4][NS], pair[4][4 * NG];
+    uint32_t code[4][NS], pair[NG];
 };
 template <int D>
-__device__ __forceinline__ void load_keys(Keys<D> &k, const uint8_t *rec, int n, int quad) {
+__device__ __forceinline__ void load_keys(Keys<D> &k, const uint8_t *rec, int lane) {
     using L = Kv4Page<D>;
+    const int n = lane & 15, quad = lane >> 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
         load_words(rec + (16 * i + n) * L::kRow + quad * (D / 8), k.code[i]);
-        const uint4 *p = reinterpret_cast<const uint4 *>(rec + L::kKeyPairs + (16 * i + 4 * quad) * L::kGroups * 4);
+    const uint32_t *p = reinterpret_cast<const uint32_t *>(rec + L::kKeyPairs) + lane * L::kGroups;
 #pragma unroll
-        for (int g = 0; g < L::kGroups; ++g) {
-            const uint4 a = p[g];
-            k.pair[i][4 * g] = a.x;
-            k.pair[i][4 * g + 1] = a.y;
-            k.pair[i][4 * g + 2] = a.z;
-            k.pair[i][4 * g + 3] = a.w;
-        }
-    }
+    for (int g = 0; g < L::kGroups; ++g) k.pair[g] = p[g];
+}
+// The page's pairs into the wave's part of the LDS.
+template <int D>
+__device__ __forceinline__ void share_pairs(const Keys<D> &k, uint32_t *pairs, int lane) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int g = 0; g < Keys<D>::NG; ++g) pairs[lane * Keys<D>::NG + g] = k.pair[g];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 // x of token 16 i + 4 quad + e and this lane's row, in s[i][e].
 template <int D, bool BF16>
-__device__ __forceinline__ void scores(const Keys<D> &k, const Query<D, BF16> &q, uint32_t one,
-                                       float (&s)[4][4]) {
+__device__ __forceinline__ void scores(const Keys<D> &k, const uint32_t *pairs, const Query<D, BF16> &q,
+                                       uint32_t one, int quad, float (&s)[4][4]) {
     using Q = Query<D, BF16>;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -115,7 +119,7 @@ __device__ __forceinline__ void scores(const Keys<D> &k, const Query<D, BF16> &q
             float x = 0.0f;
 #pragma unroll
             for (int g = 0; g < Q::NG; ++g) {
-                const h2 p = as_h2(k.pair[i][e * Q::NG + g]);   // (step, middle)
+                const h2 p = as_h2(pairs[(16 * i + 4 * quad + e) * Q::NG + g]);   // (step, middle)
                 x = fmaf((float)p[0], acc[g][e], fmaf((float)p[1], q.sum[g], x));
             }
             s[i][e] = x * q.scale;
@@ -135,10 +139,56 @@ __device__ __forceinline__ void hide(float (&s)[4][4], int t0, int quad, int pos
         }
 }
 
+// The pages of a tile's list (find_tile) that a wave takes, every kWeighWaves-th from `from`
+// on: those that are there, 64 table entries at a time, one a lane.
+struct Walk {
+    const int32_t *table;
+    int64_t n_pages;
+    int first, sink_pages, from, end, mine, id;
+    uint64_t there;
+    __device__ int page_at(int i) const { return i < sink_pages ? i : first + i - sink_pages; }
+    __device__ void entries() {
+        const int i = from + kWeighWaves * (int)(threadIdx.x & 63);
+        mine = i < end ? table[page_at(i)] : -1;
+        there = __ballot(mine >= 0 && mine < n_pages);
+    }
+    // The next page's first token, or -1; `id` stays one that can be loaded.
+    __device__ int next() {
+        while (there == 0) {
+            if (from >= end - 64 * kWeighWaves) return -1;
+            from += 64 * kWeighWaves;
+            entries();
+        }
+        const int bit = __builtin_ctzll(there);
+        there &= there - 1;
+        id = __builtin_amdgcn_readlane(mine, bit);
+        return page_at(from + kWeighWaves * bit) * kPage;
+    }
+};
+__device__ __forceinline__ Walk walk_of(const Kv4Args &c, const Tile &t, int begin, int end, int wave) {
+    Walk w{c.table + (int64_t)t.seq * c.max_pages, c.n_pages, t.first, t.sink_pages, begin + wave, end, -1, 0, 0};
+    w.entries();
+    return w;
+}
+
+// What of a page t0 all 16 rows see, or none needs to be hidden from: the first row's
+// position and the last row's window.
+struct Seen {
+    int pos_first, low_last, sinks;
+    __device__ bool all(int t0) const {
+        return t0 + kPage - 1 <= pos_first && (t0 >= low_last || t0 + kPage <= sinks);
+    }
+};
+__device__ __forceinline__ Seen seen_of(const WeighArgs &a, const Tile &t, uint32_t G) {
+    const uint32_t last = min(t.row0 + 15, t.rows - 1);
+    return Seen{t.pos0 + (int)(t.row0 / G), a.window > 0 ? t.pos0 + (int)(last / G) - a.window + 1 : 0, a.sinks};
+}
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighArgs a, int64_t units) {
     using L = Kv4Page<D>;
     __shared__ float m_all[kWeighWaves][16], l_all[kWeighWaves][16];
+    __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
     const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
@@ -156,38 +206,39 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighA
         const int begin = min(split * chunk, t.pages), end = min(begin + chunk, t.pages);
         float m = kNoMax, l = 0.0f;
         if (begin < end) {
+            Walk w = walk_of(a.c, t, begin, end, wave);
+            const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
+            const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
+            int t0 = w.next();
+            Keys<D> k;
+            load_keys(k, cache + w.id * page_bytes, lane);
             Query<D, BF16> q;
             load_query(q, a.q, (t.token0 + (int64_t)tok) * a.q_stride + head * D + 8 * quad, a.scale_log2);
             const int pos = t.pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
-            const int32_t *table = a.c.table + (int64_t)t.seq * a.c.max_pages;
-            for (int from = begin + wave; from < end; from += 64 * kWeighWaves) {
-                // 64 table entries of this wave at a time, one a lane
-                const int i = from + kWeighWaves * lane;
-                const int mine = i < end ? table[i < t.sink_pages ? i : t.first + i - t.sink_pages] : -1;
-                uint64_t there = __ballot(mine >= 0 && mine < a.c.n_pages);
-                while (there) {
-                    const int bit = __builtin_ctzll(there);
-                    there &= there - 1;
-                    const int at = from + kWeighWaves * bit, id = __builtin_amdgcn_readlane(mine, bit);
-                    const int t0 = (at < t.sink_pages ? at : t.first + at - t.sink_pages) * kPage;
-                    Keys<D> k;
-                    load_keys(k, a.c.cache + ((int64_t)id * a.c.kv_heads + kv_head) * L::kBytes, n, quad);
-                    float s[4][4];
-                    scores(k, q, one, s);
+            const Seen seen = seen_of(a, t, G);
+            while (t0 >= 0) {
+                share_pairs(k, pairs_all[wave], lane);
+                float s[4][4];
+                scores(k, pairs_all[wave], q, one, quad, s);
+                const int t1 = w.next();   // a page is always loaded, at the end the last one again
+                load_keys(k, cache + w.id * page_bytes, lane);
+                if (!seen.all(t0)) {
+                    asm volatile("");   // a branch: most pages are seen by all rows
                     hide(s, t0, quad, pos, low, a.sinks);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i4][e]);
-                    const float m_new = fmaxf(m, top);
-                    l *= __builtin_amdgcn_exp2f(m - m_new);
-                    m = m_new;
-#pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) l += __builtin_amdgcn_exp2f(s[i4][e] - m);
                 }
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][e]);
+                const float m_new = fmaxf(m, top);
+                l *= __builtin_amdgcn_exp2f(m - m_new);
+                m = m_new;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) l += __builtin_amdgcn_exp2f(s[i][e] - m);
+                t0 = t1;
             }
         }
         // a row's four lanes, then the waves
@@ -211,97 +262,206 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighA
     }
 }
 
-// PAGES pages to a workgroup: one for each wave, or one whose rows the waves share.
-template <int D, bool BF16, int PAGES>
-__global__ __launch_bounds__(kWeighThreads) void weigh_pages_kernel(const WeighArgs a, int chunks,
-                                                                    int64_t units) {
+// A row's maximum and one over its sum; 0 for a row that sees nothing, is no number or none
+// of the tile's.
+struct Row {
+    float max, inv;
+};
+__device__ __forceinline__ Row row_of(const WeighArgs &a, int64_t line, bool real) {
+    float2 ml = a.part[line];
+    for (int s = 1; s < a.splits; ++s) {
+        const float2 o = a.part[s * a.N * a.heads + line];
+        const float best = fmaxf(ml.x, o.x);
+        ml.y = ml.y * __builtin_amdgcn_exp2f(ml.x - best) + o.y * __builtin_amdgcn_exp2f(o.x - best);
+        ml.x = best;
+    }
+    const bool good = real && ml.y > 0.0f && ml.y < INFINITY;
+    return Row{good ? ml.x : 0.0f, good ? 1.0f / ml.y : 0.0f};
+}
+__device__ __forceinline__ void add_weights(const float (&x)[4][4], const Row &r, float (&w)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float p = __builtin_amdgcn_exp2f(x[i][e] - r.max);
+            w[i][e] = r.inv > 0.0f ? fmaf(p, r.inv, w[i][e]) : w[i][e];   // p may be no number
+        }
+}
+// Over the 16 rows; lane n of a quad keeps token 16 (n / 4) + 4 quad + n % 4.
+__device__ __forceinline__ float sum_rows(const float (&w)[4][4], int n) {
+    float mine = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float v = w[i][e];
+            v += dpp_f32<kDppXor1>(v);
+            v += dpp_f32<kDppXor2>(v);
+            v += dpp_f32<kDppHalfMirror>(v);
+            v += dpp_f32<kDppMirror>(v);
+            if (n == 4 * i + e) mine = v;
+        }
+    return mine;
+}
+__device__ __forceinline__ int place_of(int lane) {
+    return 16 * ((lane & 15) >> 2) + 4 * (lane >> 4) + (lane & 3);
+}
+
+// Few rows: a workgroup has a share of a sequence's pages, its waves taking turns, and a
+// tile's queries stay in registers.  The pages that the first tile does not see get their
+// old weights; what another tile adds, it adds to what its own lanes have written.
+template <int D, bool BF16>
+__global__ __launch_bounds__(kWeighThreads) void weigh_few_kernel(const WeighArgs a, int chunks, int64_t units) {
     using L = Kv4Page<D>;
-    __shared__ float w_all[PAGES == 1 ? kWeighWaves : 1][64];
-    const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
+    __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
+    const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4, place = place_of(lane);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
     const uint32_t one = ones_1024();
-    constexpr uint32_t kTurns = PAGES == 1 ? kWeighWaves : 1;
-    const uint32_t turn = PAGES == 1 ? wave : 0;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const int64_t u = unit / a.c.kv_heads;
-        const int kv_head = (int)(unit - u * a.c.kv_heads), seq = (int)(u / chunks), chunk = (int)(u - (int64_t)seq * chunks);
+        const int kv_head = (int)(unit - u * a.c.kv_heads), seq = (int)(u / chunks), part = (int)(u - (int64_t)seq * chunks);
         const int begin = a.c.q_start[seq], end = a.c.q_start[seq + 1];
-        const int64_t most = a.c.max_pages * kPage;
-        const int held = min(max(a.c.kv_len[seq], 0), (int)most);
+        const int held = min(max(a.c.kv_len[seq], 0), (int)(a.c.max_pages * kPage));
+        if (begin < 0 || end <= begin || end > a.N) continue;   // the whole workgroup
+        const int pages = (held + kPage - 1) / kPage, chunk = (pages + chunks - 1) / chunks;
+        const int p0 = min(part * chunk, pages), p1 = min(p0 + chunk, pages);   // this workgroup's
+        if (p0 == p1) continue;
+        const int pos0 = held - (end - begin);
+        const uint32_t rows = (uint32_t)(end - begin) * G;
+        const int32_t *table = a.c.table + (int64_t)seq * a.c.max_pages;
+        const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
+        const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
+        auto weight_at = [&](int id) { return ((int64_t)id * a.c.kv_heads + kv_head) * kPage + place; };
+        // A wave has the pages p0 + wave + 4 k, whichever tile and list they are of, so what it
+        // adds to has been written by itself.
+        for (uint32_t r = 0; r * 16 < rows; ++r) {
+            const uint32_t row0 = r * 16, last = min(row0 + 15, rows - 1), mine = row0 + n, row = min(mine, last), tok = row / G;
+            const int pos_a = pos0 + (int)(row0 / G), pos_b = pos0 + (int)(last / G);
+            // the pages that its rows see: [0, sink_end) and [win, see_end)
+            const int see_end = pos_b < 0 ? 0 : min(pos_b / kPage + 1, pages);
+            const int win = a.window > 0 && pos_a >= a.window ? (pos_a - a.window + 1) / kPage : 0;
+            const int sink_end = min((a.sinks + kPage - 1) / kPage, win);
+            auto sees = [&](int p) { return p < sink_end || (p >= win && p < see_end); };
+            const int head = kv_head * (int)G + (int)(row - tok * G);
+            const int pos = pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
+            Row rs{0.0f, 0.0f};
+            Query<D, BF16> q;
+            bool have = false;
+            for (int from = p0 + wave; from < p1; from += 64 * kWeighWaves) {
+                const int i = from + kWeighWaves * lane;
+                const int ids = i < p1 ? table[i] : -1;
+                const uint64_t there = __ballot(ids >= 0 && ids < a.c.n_pages);
+                uint64_t seen = __ballot(i < p1 && sees(i)) & there;
+                uint64_t rest = r == 0 ? there & ~seen : 0;
+                if (seen) {
+                    auto page = [&](uint64_t &bits, int &id) {   // the next one of them, or the last again
+                        if (!bits) return -1;
+                        const int bit = __builtin_ctzll(bits);
+                        bits &= bits - 1;
+                        id = __builtin_amdgcn_readlane(ids, bit);
+                        return (from + kWeighWaves * bit) * kPage;
+                    };
+                    int id = 0, t0 = page(seen, id);
+                    Keys<D> k;
+                    load_keys(k, cache + id * page_bytes, lane);
+                    if (!have) {
+                        have = true;
+                        rs = row_of(a, (int64_t)(begin + (int)tok) * a.heads + head, mine < rows);
+                        load_query(q, a.q, (begin + (int64_t)tok) * a.q_stride + head * D + 8 * quad, a.scale_log2);
+                    }
+                    const Seen all{pos_a, a.window > 0 ? pos_b - a.window + 1 : 0, a.sinks};
+                    while (t0 >= 0) {
+                        const int64_t at = weight_at(id);
+                        const bool write = t0 + place < held;
+                        float was = 0.0f, factor = 1.0f;
+                        if (write) {
+                            if (r > 0) was = a.out[at];
+                            else if (t0 + place < pos0 && a.decay != 0.0f) was = a.old[at], factor = a.decay;
+                        }
+                        share_pairs(k, pairs_all[wave], lane);
+                        float x[4][4], w[4][4] = {};
+                        scores(k, pairs_all[wave], q, one, quad, x);
+                        const int t1 = page(seen, id);
+                        load_keys(k, cache + id * page_bytes, lane);
+                        if (!all.all(t0)) {
+                            asm volatile("");
+                            hide(x, t0, quad, pos, low, a.sinks);
+                        }
+                        add_weights(x, rs, w);
+                        const float sum = sum_rows(w, n);
+                        if (write) a.out[at] = fmaf(factor, was, sum);
+                        t0 = t1;
+                    }
+                }
+                while (rest) {
+                    const int bit = __builtin_ctzll(rest);
+                    rest &= rest - 1;
+                    const int t0 = (from + kWeighWaves * bit) * kPage;
+                    const int64_t at = weight_at(__builtin_amdgcn_readlane(ids, bit));
+                    if (a.out == a.old && a.decay == 1.0f && t0 + kPage <= pos0) continue;   // they stay
+                    if (t0 + place < held)
+                        a.out[at] = t0 + place < pos0 && a.decay != 0.0f ? a.decay * a.old[at] : 0.0f;
+                }
+            }
+        }
+    }
+}
+
+// Many rows: a workgroup to a page, its waves taking turns at the tiles of rows that see it.
+template <int D, bool BF16>
+__global__ __launch_bounds__(kWeighThreads) void weigh_many_kernel(const WeighArgs a, int chunks, int64_t units) {
+    using L = Kv4Page<D>;
+    __shared__ float w_all[kWeighWaves][64];
+    __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
+    const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4, place = place_of(lane);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
+    const uint32_t one = ones_1024();
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t u = unit / a.c.kv_heads;
+        const int kv_head = (int)(unit - u * a.c.kv_heads), seq = (int)(u / chunks), part = (int)(u - (int64_t)seq * chunks);
+        const int begin = a.c.q_start[seq], end = a.c.q_start[seq + 1];
+        const int held = min(max(a.c.kv_len[seq], 0), (int)(a.c.max_pages * kPage));
         if (begin < 0 || end <= begin || end > a.N) continue;   // the whole workgroup
         const int pos0 = held - (end - begin);
         const uint32_t rows = (uint32_t)(end - begin) * G;
-        for (int first = chunk * PAGES; first * kPage < held; first += chunks * PAGES) {
-            const int t0 = (first + (PAGES == 1 ? 0 : wave)) * kPage;
-            const int id = t0 < held ? a.c.table[seq * a.c.max_pages + t0 / kPage] : -1;
-            const bool there = id >= 0 && id < a.c.n_pages;
+        for (int t0 = part * kPage; t0 < held; t0 += chunks * kPage) {
+            const int id = a.c.table[seq * a.c.max_pages + t0 / kPage];
+            if (id < 0 || id >= a.c.n_pages) continue;   // the whole workgroup
+            // the rows that see the page: from position t0 on, and not beyond the window
+            uint32_t r0 = t0 > pos0 ? (uint32_t)(t0 - pos0) * G / 16 : 0, r1 = (rows + 15) / 16;
+            if (a.window > 0 && t0 >= a.sinks) {
+                const int64_t last = (int64_t)t0 + kPage - 1 + a.window - 1 - pos0;   // the last token that does
+                r1 = last < 0 ? 0 : (uint32_t)min((int64_t)r1, ((last + 1) * G + 15) / 16);
+            }
+            Keys<D> k;
+            if (r0 < r1) {
+                load_keys(k, a.c.cache + ((int64_t)id * a.c.kv_heads + kv_head) * L::kBytes, lane);
+                share_pairs(k, pairs_all[wave], lane);
+            }
             float w[4][4] = {};
-            if (there) {
-                // the rows that see the page: from position t0 on, and not beyond the window
-                uint32_t r0 = t0 > pos0 ? (uint32_t)(t0 - pos0) * G / 16 : 0, r1 = (rows + 15) / 16;
-                if (a.window > 0 && t0 >= a.sinks) {
-                    const int64_t last = (int64_t)t0 + kPage - 1 + a.window - 1 - pos0;   // the last token that does
-                    r1 = last < 0 ? 0 : (uint32_t)min((int64_t)r1, ((last + 1) * G + 15) / 16);
-                }
-                Keys<D> k;
-                if (r0 < r1)
-                    load_keys(k, a.c.cache + ((int64_t)id * a.c.kv_heads + kv_head) * L::kBytes, n, quad);
-                for (uint32_t r = r0 + turn; r < r1; r += kTurns) {
-                    const uint32_t mine = r * 16 + n, row = min(mine, rows - 1), tok = row / G;
-                    const int head = kv_head * (int)G + (int)(row - tok * G);
-                    const int64_t line = (int64_t)(begin + (int)tok) * a.heads + head;
-                    float2 ml = a.part[line];
-                    for (int s = 1; s < a.splits; ++s) {
-                        const float2 o = a.part[s * a.N * a.heads + line];
-                        const float best = fmaxf(ml.x, o.x);
-                        ml.y = ml.y * __builtin_amdgcn_exp2f(ml.x - best) + o.y * __builtin_amdgcn_exp2f(o.x - best);
-                        ml.x = best;
-                    }
-                    Query<D, BF16> q;
-                    load_query(q, a.q, (begin + (int64_t)tok) * a.q_stride + head * D + 8 * quad, a.scale_log2);
-                    const int pos = pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
-                    float x[4][4];
-                    scores(k, q, one, x);
-                    hide(x, t0, quad, pos, low, a.sinks);
-                    // a row that sees nothing, or is no number, adds nothing; nor one behind the last
-                    const bool good = ml.y > 0.0f && ml.y < INFINITY && mine < rows;
-                    const float inv = good ? 1.0f / ml.y : 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float p = __builtin_amdgcn_exp2f(x[i][e] - ml.x);
-                            w[i][e] = good ? fmaf(p, inv, w[i][e]) : w[i][e];
-                        }
-                }
+            for (uint32_t r = r0 + wave; r < r1; r += kWeighWaves) {
+                const uint32_t mine = r * 16 + n, row = min(mine, rows - 1), tok = row / G;
+                const int head = kv_head * (int)G + (int)(row - tok * G);
+                Query<D, BF16> q;
+                load_query(q, a.q, (begin + (int64_t)tok) * a.q_stride + head * D + 8 * quad, a.scale_log2);
+                const Row rs = row_of(a, (int64_t)(begin + (int)tok) * a.heads + head, mine < rows);
+                const int pos = pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
+                float x[4][4];
+                scores(k, pairs_all[wave], q, one, quad, x);
+                hide(x, t0, quad, pos, low, a.sinks);
+                add_weights(x, rs, w);
             }
-            // over the 16 rows; lane n of a quad keeps token 16 (n / 4) + 4 quad + n % 4
-            float mine = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = w[i][e];
-                    v += dpp_f32<kDppXor1>(v);
-                    v += dpp_f32<kDppXor2>(v);
-                    v += dpp_f32<kDppHalfMirror>(v);
-                    v += dpp_f32<kDppMirror>(v);
-                    if (n == 4 * i + e) mine = v;
-                }
-            const int place = 16 * (n >> 2) + 4 * quad + (n & 3);
-            if constexpr (PAGES == 1) {
-                __syncthreads();
-                w_all[wave][place] = mine;
-                __syncthreads();
-                mine = 0.0f;
-                for (int k = 0; k < kWeighWaves; ++k) mine += w_all[k][place];
-                if (wave != 0) continue;   // barriers are ahead of it for every wave
-            }
-            if (there && t0 + place < held) {
+            __syncthreads();   // the last page's have been read
+            w_all[wave][place] = sum_rows(w, n);
+            __syncthreads();
+            if (wave == 0 && t0 + place < held) {
+                float sum = w_all[0][place];
+                for (int i = 1; i < kWeighWaves; ++i) sum += w_all[i][place];
                 const int64_t at = ((int64_t)id * a.c.kv_heads + kv_head) * kPage + place;
-                if (t0 + place < pos0 && a.decay != 0.0f) mine = fmaf(a.decay, a.old[at], mine);
-                a.out[at] = mine;
+                if (t0 + place < pos0 && a.decay != 0.0f) sum = fmaf(a.decay, a.old[at], sum);
+                a.out[at] = sum;
             }
         }
     }
@@ -315,11 +475,8 @@ void launch_weigh_d(const WeighArgs &a, const WeighPlan &p, hipStream_t st) {
                        dim3(kWeighThreads), 0, st, a, stats);
     const int64_t units = a.c.n_seqs * p.chunks * a.c.kv_heads;
     const dim3 g((unsigned)std::min(units, kMost));
-    if (p.shared)
-        hipLaunchKernelGGL((weigh_pages_kernel<D, BF16, 1>), g, dim3(kWeighThreads), 0, st, a, p.chunks, units);
-    else
-        hipLaunchKernelGGL((weigh_pages_kernel<D, BF16, kWeighWaves>), g, dim3(kWeighThreads), 0, st, a, p.chunks,
-                           units);
+    if (p.many) hipLaunchKernelGGL((weigh_many_kernel<D, BF16>), g, dim3(kWeighThreads), 0, st, a, p.chunks, units);
+    else hipLaunchKernelGGL((weigh_few_kernel<D, BF16>), g, dim3(kWeighThreads), 0, st, a, p.chunks, units);
 }
 
 }  // namespace
