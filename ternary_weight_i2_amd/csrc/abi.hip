@@ -706,7 +706,7 @@ BITNET_API int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, in
     const int far = 1 << 30, win = (int)(window < far ? window : far);   // as bitnet_attn_kv4
     const bitnet::WeighArgs a{kv4_args(batch), q, weights, out, static_cast<float2 *>(workspace),
                               q_stride, N, scale * 1.4426950408889634f, decay, (int)n_heads, win,
-                              (int)(sinks < far ? sinks : far), p.splits};
+                              (int)(sinks < far ? sinks : far), p.splits, p.share};
     hipError_t e = bitnet::launch_kv4_weigh(a, p, dtype == BITNET_BF16, (int)batch->head_dim,
                                             static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);

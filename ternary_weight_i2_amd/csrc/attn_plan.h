@@ -88,29 +88,33 @@ inline Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
     return Attn4Plan{0, 0, (int)s, hold ? 2 : 0, tiles, groups * s};
 }
 
-// kv4_weigh.hip: the tiles of 16 rows, the shares of the pages that each tile's rows see, the
-// workgroups that share a sequence's pages, and whether its rows are many (a workgroup to a page).
+// kv4_weigh.hip: the tiles of 16 rows; the pages of a share (of what a tile's rows see, and of a
+// sequence's pages where its rows are few), how many of them there are for the longest
+// sequence, and whether rows are many (a workgroup to a page).
 struct WeighPlan {
     int64_t tiles;
-    int splits, chunks, many;
+    int share, splits, chunks, many;
 };
 inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
                             int64_t max_kv, int64_t window, int64_t sinks) {
+    // workgroups of a launch; more units take turns, so empty sequences make no more than these
+    constexpr int64_t kMost = 1 << 22;
     const int64_t rows = N * (heads / kv_heads), pages = std::max<int64_t>((max_kv + kPage - 1) / kPage, 1);
     int64_t seen = pages;
     if (window > 0) seen = std::min(pages, (window + 16) / kPage + 2 + (sinks + kPage - 1) / kPage);
     WeighPlan p;
     p.tiles = rows / 16 + n_seqs;
-    // four workgroups to a compute unit, and a page at least for every wave
+    // Shares of a fixed number of pages, so that the workgroups of ragged sequences are alike, at
+    // most 4 to a compute unit for sequences of one length and 128 to a tile, and a page at least for every wave.
     const int64_t tall = (std::max<int64_t>(rows / n_seqs, 1) + 15) / 16;
     const int64_t busy = std::min(n_seqs, N) * tall * kv_heads;
-    // (and no more units of either kind than a launch has workgroups, with many empty sequences)
-    constexpr int64_t kMost = 1 << 22;
-    p.splits = (int)std::max<int64_t>(
-        std::min({4 * kUnits / busy, seen / 4, (int64_t)64, kMost / (p.tiles * kv_heads)}), 1);
+    const int64_t share = std::max((busy * seen + 4 * kUnits - 1) / (4 * kUnits), (seen + 127) / 128);
+    p.share = (int)std::min<int64_t>(std::max<int64_t>((share + 3) / 4 * 4, 4), 1 << 24);
     p.many = rows >= 4 * 16 * n_seqs;
-    const int64_t parts = p.many ? pages : std::min(pages / 4, 4 * kUnits / (std::min(n_seqs, N) * kv_heads));
-    p.chunks = (int)std::max<int64_t>(std::min(parts, kMost / (n_seqs * kv_heads)), 1);
+    p.splits = (int)std::max<int64_t>(
+        std::min((seen + p.share - 1) / p.share, kMost / (p.tiles * kv_heads)), 1);
+    p.chunks = (int)std::max<int64_t>(
+        std::min(p.many ? pages : (pages + p.share - 1) / p.share, kMost / (n_seqs * kv_heads)), 1);
     return p;
 }
 

@@ -27,6 +27,10 @@ namespace {
 constexpr int kWeighThreads = 256;
 constexpr int kWeighWaves = kWeighThreads / 64;
 
+// Waves to a SIMD: four where the registers spill little for it (64 bf16 tokens, heads of 128:
+// 72 -> 62 us in all; fp32 rows 24.6 us with three and 28.9 with four for the first launch).
+constexpr int least_waves(int dim, bool bf16) { return dim == 256 ? 2 : dim == 128 && !bf16 ? 3 : 4; }
+
 // A row's query: 8 channels of every 32 in this lane (quad), times 2^k; the sums of its
 // groups at the same scale; and what makes a product of them a power of two's exponent.
 template <int D, bool BF16>
@@ -36,11 +40,24 @@ struct Query {
     float sum[NG], scale;
 };
 template <int D, bool BF16>
-__device__ __forceinline__ void load_query(Query<D, BF16> &q, const void *p, int64_t at, float scale_log2) {
+struct RawQuery {   // as it is loaded
+    static constexpr int NW = BF16 ? 1 : 2;
+    uint4 v[D / 32][NW];
+};
+template <int D, bool BF16>
+__device__ __forceinline__ void load_query(RawQuery<D, BF16> &r, const void *p, int64_t at) {
+    constexpr int NW = RawQuery<D, BF16>::NW;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+        for (int k = 0; k < NW; ++k) r.v[j][k] = reinterpret_cast<const uint4 *>(p)[(at + 32 * j) * NW / 8 + k];
+}
+template <int D, bool BF16>
+__device__ __forceinline__ void make_query(Query<D, BF16> &q, const RawQuery<D, BF16> &r, float scale_log2) {
     using Q = Query<D, BF16>;
     float v[Q::NS][8], top = 0.0f;
 #pragma unroll
-    for (int j = 0; j < Q::NS; ++j) load8<BF16>(p, at + 32 * j, v[j]);
+    for (int j = 0; j < Q::NS; ++j) load8<BF16>(r.v[j], 0, v[j]);
 #pragma unroll
     for (int j = 0; j < Q::NS; ++j)
 #pragma unroll
@@ -94,7 +111,7 @@ __device__ __forceinline__ void share_pairs(const Keys<D> &k, uint32_t *pairs, i
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
-// x of token 16 i + 4 quad + e and this lane's row, in s[i][e].
+// x / q.scale of token 16 i + 4 quad + e and this lane's row, in s[i][e].
 template <int D, bool BF16>
 __device__ __forceinline__ void scores(const Keys<D> &k, const uint32_t *pairs, const Query<D, BF16> &q,
                                        uint32_t one, int quad, float (&s)[4][4]) {
@@ -122,7 +139,7 @@ __device__ __forceinline__ void scores(const Keys<D> &k, const uint32_t *pairs, 
                 const h2 p = as_h2(pairs[(16 * i + 4 * quad + e) * Q::NG + g]);   // (step, middle)
                 x = fmaf((float)p[0], acc[g][e], fmaf((float)p[1], q.sum[g], x));
             }
-            s[i][e] = x * q.scale;
+            s[i][e] = x;
         }
     }
 }
@@ -185,7 +202,7 @@ __device__ __forceinline__ Seen seen_of(const WeighArgs &a, const Tile &t, uint3
 }
 
 template <int D, bool BF16>
-__global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighArgs a, int64_t units) {
+__global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_stats_kernel(const WeighArgs a, int64_t units) {
     using L = Kv4Page<D>;
     __shared__ float m_all[kWeighWaves][16], l_all[kWeighWaves][16];
     __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
@@ -202,8 +219,8 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighA
         const uint32_t row = min(t.row0 + n, t.rows - 1), tok = row / G;
         const int head = kv_head * (int)G + (int)(row - tok * G);
         const int64_t line = (int64_t)(t.token0 + (int)tok) * a.heads + head;
-        const int chunk = (t.pages + a.splits - 1) / a.splits;
-        const int begin = min(split * chunk, t.pages), end = min(begin + chunk, t.pages);
+        // (the last share has what is more than expected)
+        const int begin = min(split * a.share, t.pages), end = split == a.splits - 1 ? t.pages : min(begin + a.share, t.pages);
         float m = kNoMax, l = 0.0f;
         if (begin < end) {
             Walk w = walk_of(a.c, t, begin, end, wave);
@@ -212,8 +229,10 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighA
             int t0 = w.next();
             Keys<D> k;
             load_keys(k, cache + w.id * page_bytes, lane);
+            RawQuery<D, BF16> raw;
+            load_query(raw, a.q, (t.token0 + (int64_t)tok) * a.q_stride + head * D + 8 * quad);
             Query<D, BF16> q;
-            load_query(q, a.q, (t.token0 + (int64_t)tok) * a.q_stride + head * D + 8 * quad, a.scale_log2);
+            make_query(q, raw, a.scale_log2);
             const int pos = t.pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
             const Seen seen = seen_of(a, t, G);
             while (t0 >= 0) {
@@ -231,13 +250,13 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighA
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][e]);
-                const float m_new = fmaxf(m, top);
+                const float m_new = fmaxf(m, top * q.scale);
                 l *= __builtin_amdgcn_exp2f(m - m_new);
                 m = m_new;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) l += __builtin_amdgcn_exp2f(s[i][e] - m);
+                    for (int e = 0; e < 4; ++e) l += __builtin_amdgcn_exp2f(fmaf(s[i][e], q.scale, -m));
                 t0 = t1;
             }
         }
@@ -267,41 +286,58 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_stats_kernel(const WeighA
 struct Row {
     float max, inv;
 };
-__device__ __forceinline__ Row row_of(const WeighArgs &a, int64_t line, bool real) {
-    float2 ml = a.part[line];
-    for (int s = 1; s < a.splits; ++s) {
-        const float2 o = a.part[s * a.N * a.heads + line];
-        const float best = fmaxf(ml.x, o.x);
-        ml.y = ml.y * __builtin_amdgcn_exp2f(ml.x - best) + o.y * __builtin_amdgcn_exp2f(o.x - best);
-        ml.x = best;
+__device__ __forceinline__ Row row_of(const WeighArgs &a, int64_t line, bool real, int quad) {
+    // the four lanes of a row take turns at its shares, four loads at a time
+    const int64_t stride = a.N * a.heads;
+    float m = kNoMax, l = 0.0f;
+    for (int s0 = quad; s0 < a.splits; s0 += 16) {
+        float2 o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = a.part[min(s0 + 4 * i, a.splits - 1) * stride + line];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (s0 + 4 * i >= a.splits) continue;
+            const float best = fmaxf(m, o[i].x);
+            l = l * __builtin_amdgcn_exp2f(m - best) + o[i].y * __builtin_amdgcn_exp2f(o[i].x - best);
+            m = best;
+        }
     }
-    const bool good = real && ml.y > 0.0f && ml.y < INFINITY;
-    return Row{good ? ml.x : 0.0f, good ? 1.0f / ml.y : 0.0f};
+    const float best = quad_max(m);
+    l = quad_sum(l * __builtin_amdgcn_exp2f(m - best));
+    const bool good = real && l > 0.0f && l < INFINITY;
+    return Row{good ? best : 0.0f, good ? 1.0f / l : 0.0f};
 }
-__device__ __forceinline__ void add_weights(const float (&x)[4][4], const Row &r, float (&w)[4][4]) {
+__device__ __forceinline__ void add_weights(float (&x)[4][4], float scale, const Row &r, float (&w)[4][4]) {
+    if (__any(r.inv == 0.0f))   // their scores may be no numbers
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = r.inv > 0.0f ? x[i][e] : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float p = __builtin_amdgcn_exp2f(x[i][e] - r.max);
-            w[i][e] = r.inv > 0.0f ? fmaf(p, r.inv, w[i][e]) : w[i][e];   // p may be no number
-        }
+        for (int e = 0; e < 4; ++e)
+            w[i][e] = fmaf(__builtin_amdgcn_exp2f(fmaf(x[i][e], scale, -r.max)), r.inv, w[i][e]);
 }
-// Over the 16 rows; lane n of a quad keeps token 16 (n / 4) + 4 quad + n % 4.
+// Over the 16 rows; lane n of a quad keeps token 16 (n / 4) + 4 quad + n % 4: lanes hand each
+// other the half of the values that the other keeps.
+template <int CTRL, int HALF>
+__device__ __forceinline__ void fold(float (&v)[16], bool upper) {
+#pragma unroll
+    for (int k = 0; k < HALF; ++k) {
+        const float keep = upper ? v[k + HALF] : v[k], give = upper ? v[k] : v[k + HALF];
+        v[k] = keep + dpp_f32<CTRL>(give);
+    }
+}
 __device__ __forceinline__ float sum_rows(const float (&w)[4][4], int n) {
-    float mine = 0.0f;
+    float v[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float v = w[i][e];
-            v += dpp_f32<kDppXor1>(v);
-            v += dpp_f32<kDppXor2>(v);
-            v += dpp_f32<kDppHalfMirror>(v);
-            v += dpp_f32<kDppMirror>(v);
-            if (n == 4 * i + e) mine = v;
-        }
-    return mine;
+    for (int k = 0; k < 16; ++k) v[k] = w[k >> 2][k & 3];
+    fold<kDppMirror, 8>(v, n & 8);
+    fold<kDppHalfMirror, 4>(v, n & 4);
+    fold<kDppXor2, 2>(v, n & 2);
+    fold<kDppXor1, 1>(v, n & 1);
+    return v[0];
 }
 __device__ __forceinline__ int place_of(int lane) {
     return 16 * ((lane & 15) >> 2) + 4 * (lane >> 4) + (lane & 3);
@@ -311,7 +347,7 @@ __device__ __forceinline__ int place_of(int lane) {
 // tile's queries stay in registers.  The pages that the first tile does not see get their
 // old weights; what another tile adds, it adds to what its own lanes have written.
 template <int D, bool BF16>
-__global__ __launch_bounds__(kWeighThreads) void weigh_few_kernel(const WeighArgs a, int chunks, int64_t units) {
+__global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few_kernel(const WeighArgs a, int chunks, int64_t units) {
     using L = Kv4Page<D>;
     __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
     const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4, place = place_of(lane);
@@ -324,8 +360,8 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_few_kernel(const WeighArg
         const int begin = a.c.q_start[seq], end = a.c.q_start[seq + 1];
         const int held = min(max(a.c.kv_len[seq], 0), (int)(a.c.max_pages * kPage));
         if (begin < 0 || end <= begin || end > a.N) continue;   // the whole workgroup
-        const int pages = (held + kPage - 1) / kPage, chunk = (pages + chunks - 1) / chunks;
-        const int p0 = min(part * chunk, pages), p1 = min(p0 + chunk, pages);   // this workgroup's
+        const int pages = (held + kPage - 1) / kPage;   // the last share has what is more than expected
+        const int p0 = min(part * a.share, pages), p1 = part == chunks - 1 ? pages : min(p0 + a.share, pages);
         if (p0 == p1) continue;
         const int pos0 = held - (end - begin);
         const uint32_t rows = (uint32_t)(end - begin) * G;
@@ -367,8 +403,10 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_few_kernel(const WeighArg
                     load_keys(k, cache + id * page_bytes, lane);
                     if (!have) {
                         have = true;
-                        rs = row_of(a, (int64_t)(begin + (int)tok) * a.heads + head, mine < rows);
-                        load_query(q, a.q, (begin + (int64_t)tok) * a.q_stride + head * D + 8 * quad, a.scale_log2);
+                        RawQuery<D, BF16> raw;
+                        load_query(raw, a.q, (begin + (int64_t)tok) * a.q_stride + head * D + 8 * quad);
+                        rs = row_of(a, (int64_t)(begin + (int)tok) * a.heads + head, mine < rows, quad);
+                        make_query(q, raw, a.scale_log2);
                     }
                     const Seen all{pos_a, a.window > 0 ? pos_b - a.window + 1 : 0, a.sinks};
                     while (t0 >= 0) {
@@ -388,7 +426,7 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_few_kernel(const WeighArg
                             asm volatile("");
                             hide(x, t0, quad, pos, low, a.sinks);
                         }
-                        add_weights(x, rs, w);
+                        add_weights(x, q.scale, rs, w);
                         const float sum = sum_rows(w, n);
                         if (write) a.out[at] = fmaf(factor, was, sum);
                         t0 = t1;
@@ -410,7 +448,7 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_few_kernel(const WeighArg
 
 // Many rows: a workgroup to a page, its waves taking turns at the tiles of rows that see it.
 template <int D, bool BF16>
-__global__ __launch_bounds__(kWeighThreads) void weigh_many_kernel(const WeighArgs a, int chunks, int64_t units) {
+__global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const WeighArgs a, int chunks, int64_t units) {
     using L = Kv4Page<D>;
     __shared__ float w_all[kWeighWaves][64];
     __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
@@ -441,17 +479,34 @@ __global__ __launch_bounds__(kWeighThreads) void weigh_many_kernel(const WeighAr
                 share_pairs(k, pairs_all[wave], lane);
             }
             float w[4][4] = {};
+            // a tile's queries are on their way while those before are worked on
+            RawQuery<D, BF16> raw;
+            uint32_t tok = 0, head = 0;   // of the queries on their way
+            auto ask = [&](uint32_t r) {
+                const uint32_t row = min(r * 16 + n, rows - 1);
+                tok = row / G;
+                head = kv_head * G + row - tok * G;
+                load_query(raw, a.q, (begin + (int64_t)tok) * a.q_stride + (int)head * D + 8 * quad);
+            };
+            if (r0 < r1) ask(min(r0 + wave, r1 - 1));
             for (uint32_t r = r0 + wave; r < r1; r += kWeighWaves) {
-                const uint32_t mine = r * 16 + n, row = min(mine, rows - 1), tok = row / G;
-                const int head = kv_head * (int)G + (int)(row - tok * G);
+                uint32_t o = one;
+                if constexpr (D == 256) asm volatile("" : "+v"(o));   // unpacked again: too many to be kept
+                const uint32_t mine = r * 16 + n, last = min(r * 16 + 15, rows - 1);
                 Query<D, BF16> q;
-                load_query(q, a.q, (begin + (int64_t)tok) * a.q_stride + head * D + 8 * quad, a.scale_log2);
-                const Row rs = row_of(a, (int64_t)(begin + (int)tok) * a.heads + head, mine < rows);
-                const int pos = pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
+                make_query(q, raw, a.scale_log2);
+                const int64_t line = (begin + (int64_t)tok) * a.heads + head;
+                ask(min(r + kWeighWaves, r1 - 1));
+                const Row rs = row_of(a, line, mine < rows, quad);
+                const int pos = pos0 + (int)(min(mine, last) / G), low = a.window > 0 ? pos - a.window + 1 : 0;
                 float x[4][4];
-                scores(k, pairs_all[wave], q, one, quad, x);
-                hide(x, t0, quad, pos, low, a.sinks);
-                add_weights(x, rs, w);
+                scores(k, pairs_all[wave], q, o, quad, x);
+                const Seen all{pos0 + (int)(r * 16 / G), a.window > 0 ? pos0 + (int)(last / G) - a.window + 1 : 0, a.sinks};
+                if (!all.all(t0)) {
+                    asm volatile("");
+                    hide(x, t0, quad, pos, low, a.sinks);
+                }
+                add_weights(x, q.scale, rs, w);
             }
             __syncthreads();   // the last page's have been read
             w_all[wave][place] = sum_rows(w, n);

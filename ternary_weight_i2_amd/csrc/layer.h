@@ -146,7 +146,7 @@ struct WeighArgs {
     float2 *part;          // per split and row: maximum and sum
     int64_t q_stride, N;
     float scale_log2, decay;
-    int heads, window, sinks, splits;
+    int heads, window, sinks, splits, share;   // splits and share: WeighPlan
 };
 hipError_t launch_kv4_weigh(const WeighArgs &a, const WeighPlan &plan, int bf16, int dim,
                             hipStream_t st);
