@@ -158,7 +158,7 @@ def _open(path: str) -> ctypes.CDLL:
     L.bitnet_rotary_kv4_append.argtypes = [kv4, plan, p, i64, p, i64, i64, p, i64, p, i64, i32, i64,
                                            p, p]
     L.bitnet_rotary_kv4_append.restype = ctypes.c_int
-    L.bitnet_kv4_weigh_workspace.argtypes = [i64] * 7
+    L.bitnet_kv4_weigh_workspace.argtypes = [i64] * 8
     L.bitnet_kv4_weigh_workspace.restype = i64
     L.bitnet_kv4_weigh.argtypes = [kv4, p, i64, i32, i64, i64, f32, i64, i64, i64, p, f32, p, p, i64, p]
     L.bitnet_kv4_weigh.restype = ctypes.c_int
@@ -823,7 +823,7 @@ def kv4_weigh(weights, q, cache, table, kv_len, q_start, decay=1.0, scale=None, 
     to = _at(out, "out", torch.float32, shape, dev)
     most = KV4_PAGE * batch.max_pages
     max_kv = most if max_kv is None else min(max_kv, most)
-    need = L.bitnet_kv4_weigh_workspace(batch.n_seqs, N, heads, kv_heads, max_kv, window, sinks)
+    need = L.bitnet_kv4_weigh_workspace(batch.n_seqs, N, heads, kv_heads, dim, max_kv, window, sinks)
     if need < 0:
         raise BitnetError(E_SHAPE, L.bitnet_last_error().decode(errors="replace"))
     if workspace is None:
@@ -836,9 +836,9 @@ def kv4_weigh(weights, q, cache, table, kv_len, q_start, decay=1.0, scale=None, 
     return out
 
 
-def kv4_weigh_workspace(n_seqs, n, n_heads, n_kv_heads, max_kv, window=0, sinks=0):
+def kv4_weigh_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window=0, sinks=0):
     """Bytes of workspace that kv4_weigh takes for these sizes, with the call's own max_kv."""
-    need = load().bitnet_kv4_weigh_workspace(n_seqs, n, n_heads, n_kv_heads, max_kv, window, sinks)
+    need = load().bitnet_kv4_weigh_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window, sinks)
     if need < 0:
         raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
     return need

@@ -655,20 +655,22 @@ BITNET_API int bitnet_attn_kv4(const bitnet_kv4_batch *batch, const void *q, int
 }
 
 BITNET_API int64_t bitnet_kv4_weigh_workspace(int64_t n_seqs, int64_t N, int64_t n_heads,
-                                              int64_t n_kv_heads, int64_t max_kv, int64_t window,
-                                              int64_t sinks) {
+                                              int64_t n_kv_heads, int64_t head_dim,
+                                              int64_t max_kv, int64_t window, int64_t sinks) {
     const char *fn = "bitnet_kv4_weigh_workspace";
     if (check_heads(fn, n_heads, n_kv_heads)) return -1;
     if (n_seqs < 0 || n_seqs > BITNET_KV4_MAX_SEQS || N < 0 || N > BITNET_GEMM_MAX_N ||
         max_kv < 0 || max_kv > (int64_t)BITNET_KV4_MAX_PAGES * BITNET_KV4_PAGE || window < 0 ||
-        window > 0x7fffffffLL || sinks < 0 || sinks > 0x7fffffffLL) {
+        window > 0x7fffffffLL || sinks < 0 || sinks > 0x7fffffffLL ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256)) {
         fail(BITNET_E_SHAPE, "%s: sizes out of range", fn);
         return -1;
     }
     g_last_error.clear();
     if (n_seqs == 0 || N == 0) return 0;
-    return bitnet::weigh_plan(n_seqs, N, n_heads, n_kv_heads, max_kv, window, sinks).splits * N *
-           n_heads * 8;
+    // of the two types, fp32 takes the more
+    return bitnet::weigh_plan(n_seqs, N, n_heads, n_kv_heads, head_dim, max_kv, window, sinks, false)
+        .bytes;
 }
 
 BITNET_API int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, int64_t q_stride,
@@ -695,18 +697,22 @@ BITNET_API int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, in
         return fail(BITNET_E_NULL, "%s: out, and weights with a decay, are required", fn);
     if (!aligned(out, 16) || !aligned(weights, 16) || !aligned(workspace, 16))
         return fail(BITNET_E_ALIGN, "%s: weights, out and workspace must be 16-byte aligned", fn);
-    const bitnet::WeighPlan p = bitnet::weigh_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads,
-                                                   max_kv, window, sinks);
-    const int64_t need = p.splits * N * n_heads * 8;
+    const bitnet::WeighPlan p =
+        bitnet::weigh_plan(batch->n_seqs, N, n_heads, batch->n_kv_heads, batch->head_dim, max_kv,
+                           window, sinks, dtype == BITNET_BF16);
+    const int64_t need = bitnet_kv4_weigh_workspace(batch->n_seqs, N, n_heads, batch->n_kv_heads,
+                                                    batch->head_dim, max_kv, window, sinks);
     if (!workspace)
         return fail(BITNET_E_NULL, "%s: a workspace of %lld bytes is required", fn, (long long)need);
     if (workspace_bytes < need)
         return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
                     (long long)workspace_bytes, (long long)need);
     const int far = 1 << 30, win = (int)(window < far ? window : far);   // as bitnet_attn_kv4
-    const bitnet::WeighArgs a{kv4_args(batch), q, weights, out, static_cast<float2 *>(workspace),
-                              q_stride, N, scale * 1.4426950408889634f, decay, (int)n_heads, win,
-                              (int)(sinks < far ? sinks : far), p.splits, p.share};
+    char *const ws = static_cast<char *>(workspace);
+    const bitnet::WeighArgs a{kv4_args(batch), q, weights, out, reinterpret_cast<float2 *>(ws),
+                              p.many ? reinterpret_cast<uint4 *>(ws + p.kept_at) : nullptr,
+                              reinterpret_cast<float *>(ws + p.sums_at), q_stride, N, scale * 1.4426950408889634f, decay, (int)n_heads, win,
+                              (int)(sinks < far ? sinks : far), p.splits};
     hipError_t e = bitnet::launch_kv4_weigh(a, p, dtype == BITNET_BF16, (int)batch->head_dim,
                                             static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);

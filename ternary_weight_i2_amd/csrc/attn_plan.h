@@ -88,15 +88,18 @@ inline Attn4Plan attn4_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
     return Attn4Plan{0, 0, (int)s, hold ? 2 : 0, tiles, groups * s};
 }
 
-// kv4_weigh.hip: the tiles of 16 rows; the pages of a share (of what a tile's rows see, and of a
-// sequence's pages where its rows are few), how many of them there are for the longest
-// sequence, and whether rows are many (a workgroup to a page).
+// kv4_weigh.hip: the tiles of 16 rows; the shares of the pages that a tile's rows see, and of a
+// sequence's pages where its rows are few; whether rows are many (a workgroup to a page) and
+// the parts that they are then in.
 struct WeighPlan {
     int64_t tiles;
-    int share, splits, chunks, many;
+    int splits, chunks, many, parts;
+    // the workspace: rows' maxima and sums, the queries as operands, the parts' sums
+    int64_t kept_at, sums_at, bytes;
 };
 inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv_heads,
-                            int64_t max_kv, int64_t window, int64_t sinks) {
+                            int64_t dim, int64_t max_kv, int64_t window, int64_t sinks,
+                            bool bf16) {
     // workgroups of a launch; more units take turns, so empty sequences make no more than these
     constexpr int64_t kMost = 1 << 22;
     const int64_t rows = N * (heads / kv_heads), pages = std::max<int64_t>((max_kv + kPage - 1) / kPage, 1);
@@ -104,17 +107,25 @@ inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
     if (window > 0) seen = std::min(pages, (window + 16) / kPage + 2 + (sinks + kPage - 1) / kPage);
     WeighPlan p;
     p.tiles = rows / 16 + n_seqs;
-    // Shares of a fixed number of pages, so that the workgroups of ragged sequences are alike, at
-    // most 4 to a compute unit for sequences of one length and 128 to a tile, and a page at least for every wave.
+    // Four workgroups to a compute unit and a page at least for every wave; at most 128 shares of
+    // a tile, which each of its rows joins.  (Shares of a fixed number of pages, so that ragged
+    // sequences have workgroups of one size, took longer: 64 sequences of 820 to 4096
+    // tokens 70 us with 32 pages and 77 with 16, two even shares of each 62.)
     const int64_t tall = (std::max<int64_t>(rows / n_seqs, 1) + 15) / 16;
-    const int64_t busy = std::min(n_seqs, N) * tall * kv_heads;
-    const int64_t share = std::max((busy * seen + 4 * kUnits - 1) / (4 * kUnits), (seen + 127) / 128);
-    p.share = (int)std::min<int64_t>(std::max<int64_t>((share + 3) / 4 * 4, 4), 1 << 24);
+    const int64_t busy = std::min(n_seqs, N) * tall * kv_heads, few = std::min(n_seqs, N) * kv_heads;
     p.many = rows >= 4 * 16 * n_seqs;
     p.splits = (int)std::max<int64_t>(
-        std::min((seen + p.share - 1) / p.share, kMost / (p.tiles * kv_heads)), 1);
+        std::min({4 * kUnits / busy, seen / 4, (int64_t)128, kMost / (p.tiles * kv_heads)}), 1);
     p.chunks = (int)std::max<int64_t>(
-        std::min(p.many ? pages : (pages + p.share - 1) / p.share, kMost / (n_seqs * kv_heads)), 1);
+        std::min(p.many ? pages : std::min(pages / 4, 4 * kUnits / few), kMost / (n_seqs * kv_heads)), 1);
+    // Where pages are few, their rows in parts of eight tiles or more, for 8 workgroups to a unit.
+    p.parts = p.many ? (int)std::max<int64_t>(
+                           std::min(8 * kUnits / (n_seqs * p.chunks * kv_heads), tall / 8), 1)
+                     : 1;
+    const int64_t pieces = (bf16 ? 1 : 2) * dim / 32 + (dim == 256 ? 2 : 1);   // kept_pieces
+    p.kept_at = (p.splits * N * heads * 8 + 15) / 16 * 16;
+    p.sums_at = p.kept_at + (p.many ? p.tiles * kv_heads * pieces * 1024 : 0);
+    p.bytes = p.sums_at + (p.parts > 1 ? n_seqs * p.chunks * kv_heads * p.parts * kPage * 4 : 0);
     return p;
 }
 

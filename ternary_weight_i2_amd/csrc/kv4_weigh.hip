@@ -83,6 +83,40 @@ __device__ __forceinline__ void make_query(Query<D, BF16> &q, const RawQuery<D, 
     }
 }
 
+// Queries as the first launch leaves them for a second one of many rows: [tile][16 bytes
+// of `Query`][lane] and, behind the operands, the scale and the sums.
+template <int D, bool BF16>
+constexpr int kept_pieces = Query<D, BF16>::NT * Query<D, BF16>::NS + (D == 256 ? 2 : 1);
+template <int D, bool BF16>
+__device__ __forceinline__ void keep_query(uint4 *p, const Query<D, BF16> &q, int lane) {
+    using Q = Query<D, BF16>;
+#pragma unroll
+    for (int t = 0; t < Q::NT; ++t)
+#pragma unroll
+        for (int j = 0; j < Q::NS; ++j) p[(t * Q::NS + j) * 64 + lane] = __builtin_bit_cast(uint4, q.f[t][j]);
+    uint32_t w[8] = {__float_as_uint(q.scale)};
+#pragma unroll
+    for (int g = 0; g < Q::NG; ++g) w[1 + g] = __float_as_uint(q.sum[g]);
+    p[Q::NT * Q::NS * 64 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (D == 256) p[(Q::NT * Q::NS + 1) * 64 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+template <int D, bool BF16>
+__device__ __forceinline__ void kept_query(Query<D, BF16> &q, const uint4 *p, int lane) {
+    using Q = Query<D, BF16>;
+#pragma unroll
+    for (int t = 0; t < Q::NT; ++t)
+#pragma unroll
+        for (int j = 0; j < Q::NS; ++j) q.f[t][j] = __builtin_bit_cast(h8, p[(t * Q::NS + j) * 64 + lane]);
+    const uint4 a = p[Q::NT * Q::NS * 64 + lane];
+    q.scale = __uint_as_float(a.x);
+    q.sum[0] = __uint_as_float(a.y);
+    if constexpr (Q::NG > 1) q.sum[1] = __uint_as_float(a.z);
+    if constexpr (Q::NG > 2) {
+        q.sum[2] = __uint_as_float(a.w);
+        q.sum[3] = __uint_as_float(p[(Q::NT * Q::NS + 1) * 64 + lane].x);
+    }
+}
+
 // A page's keys as they are loaded: this lane's codes of tokens 16 i + n, 8 channels of
 // every 32, and the pairs of token `lane`, which the wave shares through LDS.
 template <int D>
@@ -201,6 +235,11 @@ __device__ __forceinline__ Seen seen_of(const WeighArgs &a, const Tile &t, uint3
     return Seen{t.pos0 + (int)(t.row0 / G), a.window > 0 ? t.pos0 + (int)(last / G) - a.window + 1 : 0, a.sinks};
 }
 
+// The pages of one of `shares` even shares, at least one for every wave.
+__device__ __forceinline__ int share_of(int pages, int shares) {
+    return max((int)((uint32_t)(pages + shares - 1) / (uint32_t)shares), kWeighWaves);
+}
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_stats_kernel(const WeighArgs a, int64_t units) {
     using L = Kv4Page<D>;
@@ -219,8 +258,7 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_sta
         const uint32_t row = min(t.row0 + n, t.rows - 1), tok = row / G;
         const int head = kv_head * (int)G + (int)(row - tok * G);
         const int64_t line = (int64_t)(t.token0 + (int)tok) * a.heads + head;
-        // (the last share has what is more than expected)
-        const int begin = min(split * a.share, t.pages), end = split == a.splits - 1 ? t.pages : min(begin + a.share, t.pages);
+        const int share = share_of(t.pages, a.splits), begin = min(split * share, t.pages), end = min(begin + share, t.pages);
         float m = kNoMax, l = 0.0f;
         if (begin < end) {
             Walk w = walk_of(a.c, t, begin, end, wave);
@@ -233,6 +271,8 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_sta
             load_query(raw, a.q, (t.token0 + (int64_t)tok) * a.q_stride + head * D + 8 * quad);
             Query<D, BF16> q;
             make_query(q, raw, a.scale_log2);
+            if (a.kept && split == 0 && wave == 0)
+                keep_query(a.kept + ((u / a.splits) * a.c.kv_heads + kv_head) * (kept_pieces<D, BF16> * 64), q, lane);
             const int pos = t.pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
             const Seen seen = seen_of(a, t, G);
             while (t0 >= 0) {
@@ -360,8 +400,8 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
         const int begin = a.c.q_start[seq], end = a.c.q_start[seq + 1];
         const int held = min(max(a.c.kv_len[seq], 0), (int)(a.c.max_pages * kPage));
         if (begin < 0 || end <= begin || end > a.N) continue;   // the whole workgroup
-        const int pages = (held + kPage - 1) / kPage;   // the last share has what is more than expected
-        const int p0 = min(part * a.share, pages), p1 = part == chunks - 1 ? pages : min(p0 + a.share, pages);
+        const int pages = (held + kPage - 1) / kPage, share = share_of(pages, chunks);
+        const int p0 = min(part * share, pages), p1 = min(p0 + share, pages);
         if (p0 == p1) continue;
         const int pos0 = held - (end - begin);
         const uint32_t rows = (uint32_t)(end - begin) * G;
@@ -432,23 +472,33 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
                         t0 = t1;
                     }
                 }
-                while (rest) {
-                    const int bit = __builtin_ctzll(rest);
-                    rest &= rest - 1;
-                    const int t0 = (from + kWeighWaves * bit) * kPage;
-                    const int64_t at = weight_at(__builtin_amdgcn_readlane(ids, bit));
-                    if (a.out == a.old && a.decay == 1.0f && t0 + kPage <= pos0) continue;   // they stay
-                    if (t0 + place < held)
-                        a.out[at] = t0 + place < pos0 && a.decay != 0.0f ? a.decay * a.old[at] : 0.0f;
+                while (rest) {   // pages that no row of the first tile sees, four at a time
+                    int64_t at[4];
+                    float was[4];
+                    bool write[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int bit = rest ? __builtin_ctzll(rest) : 0, t0 = (from + kWeighWaves * bit) * kPage;
+                        at[e] = weight_at(__builtin_amdgcn_readlane(ids, bit));
+                        // (weights that stay are not written)
+                        write[e] = rest && t0 + place < held && !(a.out == a.old && a.decay == 1.0f && t0 + kPage <= pos0);
+                        was[e] = write[e] && t0 + place < pos0 && a.decay != 0.0f ? a.old[at[e]] : 0.0f;
+                        rest &= rest - 1;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (write[e]) a.out[at[e]] = a.decay * was[e];
                 }
             }
         }
     }
 }
 
-// Many rows: a workgroup to a page, its waves taking turns at the tiles of rows that see it.
+// Many rows: a workgroup to a page and, where pages are few, to one of `parts` parts of the
+// rows that see it, whose sums are then left in a.sums; its waves take turns at the tiles.
 template <int D, bool BF16>
-__global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const WeighArgs a, int chunks, int64_t units) {
+__global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const WeighArgs a, int chunks, int parts,
+                                                                      int64_t units) {
     using L = Kv4Page<D>;
     __shared__ float w_all[kWeighWaves][64];
     __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
@@ -457,14 +507,16 @@ __global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const Weig
     const uint32_t G = (uint32_t)a.heads / (uint32_t)a.c.kv_heads;
     const uint32_t one = ones_1024();
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t u = unit / a.c.kv_heads;
-        const int kv_head = (int)(unit - u * a.c.kv_heads), seq = (int)(u / chunks), part = (int)(u - (int64_t)seq * chunks);
+        const int64_t v = unit / parts, u = v / a.c.kv_heads;
+        const int part = (int)(unit - v * parts), kv_head = (int)(v - u * a.c.kv_heads);
+        const int seq = (int)(u / chunks), chunk = (int)(u - (int64_t)seq * chunks);
         const int begin = a.c.q_start[seq], end = a.c.q_start[seq + 1];
         const int held = min(max(a.c.kv_len[seq], 0), (int)(a.c.max_pages * kPage));
         if (begin < 0 || end <= begin || end > a.N) continue;   // the whole workgroup
         const int pos0 = held - (end - begin);
         const uint32_t rows = (uint32_t)(end - begin) * G;
-        for (int t0 = part * kPage; t0 < held; t0 += chunks * kPage) {
+        const uint32_t tile0 = (uint32_t)begin * G / 16 + seq;   // the sequence's first (find_tile)
+        for (int t0 = chunk * kPage; t0 < held; t0 += chunks * kPage) {
             const int id = a.c.table[seq * a.c.max_pages + t0 / kPage];
             if (id < 0 || id >= a.c.n_pages) continue;   // the whole workgroup
             // the rows that see the page: from position t0 on, and not beyond the window
@@ -473,40 +525,43 @@ __global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const Weig
                 const int64_t last = (int64_t)t0 + kPage - 1 + a.window - 1 - pos0;   // the last token that does
                 r1 = last < 0 ? 0 : (uint32_t)min((int64_t)r1, ((last + 1) * G + 15) / 16);
             }
-            Keys<D> k;
-            if (r0 < r1) {
-                load_keys(k, a.c.cache + ((int64_t)id * a.c.kv_heads + kv_head) * L::kBytes, lane);
-                share_pairs(k, pairs_all[wave], lane);
+            // (pages beyond the expected ones have no place for parts)
+            const bool whole = parts == 1 || t0 >= chunks * kPage;
+            if (whole && part > 0) continue;
+            if (!whole && r0 < r1) {
+                const uint32_t share = (r1 - r0 + parts - 1) / parts;
+                r0 = min(r0 + part * share, r1);
+                r1 = min(r0 + share, r1);
             }
             float w[4][4] = {};
-            // a tile's queries are on their way while those before are worked on
-            RawQuery<D, BF16> raw;
-            uint32_t tok = 0, head = 0;   // of the queries on their way
-            auto ask = [&](uint32_t r) {
-                const uint32_t row = min(r * 16 + n, rows - 1);
-                tok = row / G;
-                head = kv_head * G + row - tok * G;
-                load_query(raw, a.q, (begin + (int64_t)tok) * a.q_stride + (int)head * D + 8 * quad);
-            };
-            if (r0 < r1) ask(min(r0 + wave, r1 - 1));
-            for (uint32_t r = r0 + wave; r < r1; r += kWeighWaves) {
-                uint32_t o = one;
-                if constexpr (D == 256) asm volatile("" : "+v"(o));   // unpacked again: too many to be kept
-                const uint32_t mine = r * 16 + n, last = min(r * 16 + 15, rows - 1);
-                Query<D, BF16> q;
-                make_query(q, raw, a.scale_log2);
-                const int64_t line = (begin + (int64_t)tok) * a.heads + head;
-                ask(min(r + kWeighWaves, r1 - 1));
-                const Row rs = row_of(a, line, mine < rows, quad);
-                const int pos = pos0 + (int)(min(mine, last) / G), low = a.window > 0 ? pos - a.window + 1 : 0;
-                float x[4][4];
-                scores(k, pairs_all[wave], q, o, quad, x);
-                const Seen all{pos0 + (int)(r * 16 / G), a.window > 0 ? pos0 + (int)(last / G) - a.window + 1 : 0, a.sinks};
-                if (!all.all(t0)) {
-                    asm volatile("");
-                    hide(x, t0, quad, pos, low, a.sinks);
+            if (r0 < r1) {
+                Keys<D> k;
+                load_keys(k, a.c.cache + ((int64_t)id * a.c.kv_heads + kv_head) * L::kBytes, lane);
+                // a tile's queries are on their way while those before are worked on
+                Query<D, BF16> next;
+                auto ask = [&](uint32_t r) {
+                    kept_query(next, a.kept + ((int64_t)(tile0 + r) * a.c.kv_heads + kv_head) * (kept_pieces<D, BF16> * 64), lane);
+                };
+                ask(min(r0 + wave, r1 - 1));
+                share_pairs(k, pairs_all[wave], lane);
+                for (uint32_t r = r0 + wave; r < r1; r += kWeighWaves) {
+                    uint32_t o = one;
+                    if constexpr (D == 256) asm volatile("" : "+v"(o));   // unpacked again: too many to be kept
+                    const uint32_t mine = r * 16 + n, last = min(r * 16 + 15, rows - 1), row = min(mine, last), tok = row / G;
+                    const Row rs = row_of(a, (begin + (int64_t)tok) * a.heads + kv_head * (int)G + (int)(row - tok * G),
+                                          mine < rows, quad);
+                    const Query<D, BF16> q = next;
+                    ask(min(r + kWeighWaves, r1 - 1));
+                    const int pos = pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
+                    float x[4][4];
+                    scores(k, pairs_all[wave], q, o, quad, x);
+                    const Seen all{pos0 + (int)(r * 16 / G), a.window > 0 ? pos0 + (int)(last / G) - a.window + 1 : 0, a.sinks};
+                    if (!all.all(t0)) {
+                        asm volatile("");
+                        hide(x, t0, quad, pos, low, a.sinks);
+                    }
+                    add_weights(x, q.scale, rs, w);
                 }
-                add_weights(x, q.scale, rs, w);
             }
             __syncthreads();   // the last page's have been read
             w_all[wave][place] = sum_rows(w, n);
@@ -515,10 +570,34 @@ __global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const Weig
                 float sum = w_all[0][place];
                 for (int i = 1; i < kWeighWaves; ++i) sum += w_all[i][place];
                 const int64_t at = ((int64_t)id * a.c.kv_heads + kv_head) * kPage + place;
-                if (t0 + place < pos0 && a.decay != 0.0f) sum = fmaf(a.decay, a.old[at], sum);
-                a.out[at] = sum;
+                if (!whole) {
+                    a.sums[unit * kPage + place] = sum;
+                } else {
+                    if (t0 + place < pos0 && a.decay != 0.0f) sum = fmaf(a.decay, a.old[at], sum);
+                    a.out[at] = sum;
+                }
             }
         }
+    }
+}
+
+// The parts' sums, in their order, and the old weights: a wave to a page.
+__global__ __launch_bounds__(kWeighThreads) void weigh_join_kernel(const WeighArgs a, int chunks, int parts, int64_t units) {
+    const int place = threadIdx.x & 63;
+    for (int64_t v = (int64_t)blockIdx.x * kWeighWaves + (threadIdx.x >> 6); v < units; v += (int64_t)gridDim.x * kWeighWaves) {
+        const int64_t u = v / a.c.kv_heads;
+        const int kv_head = (int)(v - u * a.c.kv_heads), seq = (int)(u / chunks), t0 = (int)(u - (int64_t)seq * chunks) * kPage;
+        const int begin = a.c.q_start[seq], end = a.c.q_start[seq + 1];
+        const int held = min(max(a.c.kv_len[seq], 0), (int)(a.c.max_pages * kPage));
+        if (begin < 0 || end <= begin || end > a.N || t0 + place >= held) continue;
+        const int id = a.c.table[seq * a.c.max_pages + t0 / kPage];
+        if (id < 0 || id >= a.c.n_pages) continue;
+        const int64_t at = ((int64_t)id * a.c.kv_heads + kv_head) * kPage + place;
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) sum += a.sums[(v * parts + i) * kPage + place];
+        if (t0 + place < held - (end - begin) && a.decay != 0.0f) sum = fmaf(a.decay, a.old[at], sum);
+        a.out[at] = sum;
     }
 }
 
@@ -528,10 +607,16 @@ void launch_weigh_d(const WeighArgs &a, const WeighPlan &p, hipStream_t st) {
     const int64_t stats = p.tiles * a.splits * a.c.kv_heads;
     hipLaunchKernelGGL((weigh_stats_kernel<D, BF16>), dim3((unsigned)std::min(stats, kMost)),
                        dim3(kWeighThreads), 0, st, a, stats);
-    const int64_t units = a.c.n_seqs * p.chunks * a.c.kv_heads;
+    const int64_t pages = a.c.n_seqs * p.chunks * a.c.kv_heads, units = pages * p.parts;
     const dim3 g((unsigned)std::min(units, kMost));
-    if (p.many) hipLaunchKernelGGL((weigh_many_kernel<D, BF16>), g, dim3(kWeighThreads), 0, st, a, p.chunks, units);
-    else hipLaunchKernelGGL((weigh_few_kernel<D, BF16>), g, dim3(kWeighThreads), 0, st, a, p.chunks, units);
+    if (!p.many) {
+        hipLaunchKernelGGL((weigh_few_kernel<D, BF16>), g, dim3(kWeighThreads), 0, st, a, p.chunks, units);
+        return;
+    }
+    hipLaunchKernelGGL((weigh_many_kernel<D, BF16>), g, dim3(kWeighThreads), 0, st, a, p.chunks, p.parts, units);
+    if (p.parts > 1)
+        hipLaunchKernelGGL(weigh_join_kernel, dim3((unsigned)((pages + kWeighWaves - 1) / kWeighWaves)), dim3(kWeighThreads), 0,
+                           st, a, p.chunks, p.parts, pages);
 }
 
 }  // namespace

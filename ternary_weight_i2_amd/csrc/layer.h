@@ -144,9 +144,11 @@ struct WeighArgs {
     const float *old;
     float *out;
     float2 *part;          // per split and row: maximum and sum
+    uint4 *kept;           // many rows: the queries as operands
+    float *sums;           // many rows, few pages: the parts' sums
     int64_t q_stride, N;
     float scale_log2, decay;
-    int heads, window, sinks, splits, share;   // splits and share: WeighPlan
+    int heads, window, sinks, splits;   // splits: WeighPlan
 };
 hipError_t launch_kv4_weigh(const WeighArgs &a, const WeighPlan &plan, int bf16, int dim,
                             hipStream_t st);

@@ -79,6 +79,18 @@ def test_weigh_many_pages_few_expected_and_many_splits(bn):
         check_weigh(bn, s, 2, max_kv=max_kv)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_weigh_rows_in_parts(bn, d, dtype):
+    """Prompts of many rows over few pages, whose rows several workgroups share; more pages
+    than expected, which one of them then has; windows; an absent page."""
+    check_weigh(bn, Seqs([700, 333], [600, 333], 1, d, seed=30, fill=0xFF, gap=[(0, 3)]).fill(), 3, dtype, decay=0.5)
+    s = Seqs([640], [500], 2, d, seed=31).fill()
+    for max_kv in (None, 70, 0):
+        check_weigh(bn, s, 8, dtype, max_kv=max_kv)
+    check_weigh(bn, s, 8, dtype, window=100, sinks=3)
+
+
 def test_weigh_leaves_what_is_not_its_own(bn):
     """Absent pages, rows in front of the first sequence and behind the last, sequences without
     rows, rows before the first position, unwritten memory."""
@@ -122,7 +134,7 @@ def test_weigh_without_old_weights_and_given_scratch(bn):
     w.fill_(float("nan"))
     a = bn.kv4_weigh(w, q, c, *rest, decay=0.0, out=torch.zeros_like(w))
     b = bn.kv4_weigh(None, q, c, *rest, decay=0.0, out=torch.zeros_like(w))
-    need = bn.kv4_weigh_workspace(2, 10, 4, 2, 128)
+    need = bn.kv4_weigh_workspace(2, 10, 4, 2, 64, 128)
     ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
     d = bn.kv4_weigh(None, q, c, *rest, decay=0.0, max_kv=128, out=torch.zeros_like(w), workspace=ws)
     assert torch.equal(a, b) and torch.equal(a, d) and torch.isfinite(a).all()
@@ -163,7 +175,7 @@ def test_weigh_captured_and_on_two_streams(bn):
     kv_len.sub_(3)
     q = dev(s.rng.standard_normal((2, 8, 64)).astype(np.float32))
     w = torch.zeros((s.n_pages, 2, 64), device="cuda")
-    need = bn.kv4_weigh_workspace(2, 2, 8, 2, 320)
+    need = bn.kv4_weigh_workspace(2, 2, 8, 2, 64, 320)
     ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
     call = lambda out, k: bn.kv4_weigh(w, q, c, table, kv_len, q_start, max_kv=320, out=out, workspace=ws[k])  # noqa: E731
     out = torch.zeros_like(w)

@@ -219,13 +219,14 @@ def test_weigh_validation(L):
         assert f(L, **{p: None}) == E_NULL and f(L, **{p: MIS}) == E_ALIGN
     for bad in (255, 258, 0):
         assert f(L, qs=bad) == E_SHAPE
-    need = L.bitnet_kv4_weigh_workspace(2, 3, 4, 2, 64, 0, 0)
+    need = L.bitnet_kv4_weigh_workspace(2, 3, 4, 2, 64, 64, 0, 0)
     assert need >= 3 * 4 * 8 and f(L, wb=need - 1) == E_SHAPE
     assert f(L, N=0, q=None, ws=None) == OK and f(L, _batch(n_seqs=0), q=None) == OK
-    for bad in ((-1, 3, 4, 2, 64, 0, 0), (2, -1, 4, 2, 64, 0, 0), (2, 3, 3, 2, 64, 0, 0), (2, 3, 4, 2, -1, 0, 0),
-                (2, 3, 4, 2, (1 << 30) + 1, 0, 0), (2, 3, 4, 2, 64, -1, 0), (2, 3, 4, 2, 64, 0, -1)):
+    for bad in ((-1, 3, 4, 2, 64, 64, 0, 0), (2, -1, 4, 2, 64, 64, 0, 0), (2, 3, 3, 2, 64, 64, 0, 0),
+                (2, 3, 4, 2, 64, -1, 0, 0), (2, 3, 4, 2, 64, (1 << 30) + 1, 0, 0), (2, 3, 4, 2, 64, 64, -1, 0),
+                (2, 3, 4, 2, 64, 64, 0, -1), (2, 3, 4, 2, 96, 64, 0, 0)):
         assert L.bitnet_kv4_weigh_workspace(*bad) == -1
-    assert L.bitnet_kv4_weigh_workspace(0, 3, 4, 2, 64, 0, 0) == 0
+    assert L.bitnet_kv4_weigh_workspace(0, 3, 4, 2, 64, 64, 0, 0) == 0
 
 
 def _evict(L, b=None, w=FAKE, nt=FAKE, cap=3, keep=64, sinks=4, recent=8, nl=FAKE, idx=FAKE):
@@ -268,6 +269,6 @@ def test_weigh_and_evict_binding_refuses():
         with pytest.raises((ValueError, TypeError)):
             bn.attn_block(torch.zeros((1, 256)), *[(torch.zeros((64, 64), dtype=torch.uint8), 1.0)] * 4, c, table, one,
                           start, offset=one, **k)
-    assert _binding.kv4_weigh_workspace(1, 1, 2, 1, 64) > 0
+    assert _binding.kv4_weigh_workspace(1, 1, 2, 1, 64, 64) > 0
     with pytest.raises(bn.BitnetError):
-        _binding.kv4_weigh_workspace(1, 1, 3, 2, 64)
+        _binding.kv4_weigh_workspace(1, 1, 3, 2, 64, 64)
