@@ -17,6 +17,7 @@ namespace {
 constexpr int kChooseThreads = 1024;
 constexpr int kChooseWaves = kChooseThreads / 64;
 constexpr int kBins = 2048;
+constexpr int kBatch = 4;
 constexpr int kMoveThreads = 256;
 
 // Integers in the order of the weights; a NaN counts as -infinity, -0 as 0.
@@ -62,6 +63,9 @@ __global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const Evic
             const int id = table[p];
             return id >= 0 && id < a.n_pages ? id : -1;
         };
+        auto weights4 = [&](int id, int t0) {   // of tokens t0 .. t0 + 3
+            return *reinterpret_cast<const float4 *>(a.weights + ((int64_t)id * a.kv_heads + head) * kPage + t0 % kPage);
+        };
         // tokens that are there, and those of them that are spared
         auto spared = [&](int t) { return t < a.sinks || t >= held - a.recent; };
         int mine = 0, safe = 0;
@@ -88,12 +92,30 @@ __global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const Evic
                 const int width = pass < 2 ? 11 : 10, next = pass == 0 ? 10 : 0;
                 for (int i = tid; i < kBins; i += kChooseThreads) bins[i] = 0;
                 __syncthreads();
-                for (int t = tid; t < held; t += kChooseThreads) {
-                    const int id = page_of(t / kPage);
-                    if (id < 0 || spared(t)) continue;
-                    const uint32_t o = order_of(a.weights[((int64_t)id * a.kv_heads + head) * kPage + t % kPage]);
-                    if (pass > 0 && (o ^ least) >> (shift + width)) continue;   // other upper bits
-                    atomicAdd(&bins[o >> shift & (kBins - 1) & ((1 << width) - 1)], 1);
+                // four tokens to a thread, kBatch times: first all loads, then the counts
+                for (int base = 4 * tid; base < held; base += 4 * kChooseThreads * kBatch) {
+                    int id[kBatch];
+                    float4 w[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int t0 = base + 4 * kChooseThreads * i;
+                        id[i] = t0 < held ? page_of(t0 / kPage) : -1;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        w[i] = weights4(max(id[i], 0), base + 4 * kChooseThreads * i);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int t0 = base + 4 * kChooseThreads * i;
+                        const float v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (id[i] < 0 || t0 + e >= held || spared(t0 + e)) continue;
+                            const uint32_t o = order_of(v[e]);
+                            if (pass > 0 && (o ^ least) >> (shift + width)) continue;   // other upper bits
+                            atomicAdd(&bins[o >> shift & ((1 << width) - 1)], 1);
+                        }
+                    }
                 }
                 __syncthreads();
                 // from the top: thread i has bins 2047 - 2 i and 2046 - 2 i
@@ -120,13 +142,15 @@ __global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const Evic
         // ---- places, in the order of the tokens: four tokens to a thread
         int32_t *index = a.index + (seq * a.kv_heads + head) * a.keep;
         int sure_before = 0, ties_before = 0;
-        for (int base = 0; base < pages * kPage; base += 4 * kChooseThreads) {
+        auto entry = [&](int t0) { return t0 < held ? page_of(t0 / kPage) : -1; };
+        int id = entry(4 * tid), id1 = entry(4 * (tid + kChooseThreads));   // of this turn and the next
+        float4 w4 = weights4(max(id, 0), 4 * tid);
+        for (int base = 0; base < held; base += 4 * kChooseThreads) {
             const int t0 = base + 4 * tid;
-            const int id = t0 < held ? page_of(t0 / kPage) : -1;
+            const int id2 = entry(t0 + 8 * kChooseThreads);
+            const float4 next = weights4(max(id1, 0), t0 + 4 * kChooseThreads);
             uint32_t sure = 0, tie = 0;   // bits of the four tokens
             if (id >= 0) {
-                const float4 w4 = *reinterpret_cast<const float4 *>(
-                    a.weights + ((int64_t)id * a.kv_heads + head) * kPage + t0 % kPage);
                 const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -156,6 +180,9 @@ __global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const Evic
             }
             sure_before += (int)(all >> 16);
             ties_before += (int)(all & 0xffffu);
+            id = id1;
+            id1 = id2;
+            w4 = next;
             __syncthreads();
         }
         for (int i = kept + tid; i < a.keep; i += kChooseThreads) index[i] = -1;
