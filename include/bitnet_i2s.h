@@ -613,11 +613,17 @@ int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, int64_t q_str
  *               is what the offsets of bitnet_rotary_kv4_append are for.)
  *   index       DEVICE [n_seqs][n_kv_heads][keep] int32: the position that each token had; -1
  *               behind the last.
+ *   workspace   device scratch of at least bitnet_kv4_evict_workspace bytes (-1: sizes out
+ *               of range) for these sizes, 16-byte aligned (may be NULL where that is 0); used
+ *               until the call's kernels have ended, so calls that may run at once need one each.
  * n_seqs == 0 is a no-op.
  */
+int64_t bitnet_kv4_evict_workspace(int64_t n_seqs, int64_t n_kv_heads, int64_t max_pages);
+
 int bitnet_kv4_evict(const bitnet_kv4_batch *batch, float *weights, const int32_t *new_table,
                      int64_t new_max_pages, int64_t keep, int64_t sinks, int64_t recent,
-                     int32_t *new_len, int32_t *index, void *stream);
+                     int32_t *new_len, int32_t *index, void *workspace, int64_t workspace_bytes,
+                     void *stream);
 
 /* Thread-local description of the last non-OK status on this thread
  * (empty string if none).  The pointer stays valid until the next call on

@@ -162,7 +162,8 @@ def _open(path: str) -> ctypes.CDLL:
     L.bitnet_kv4_weigh_workspace.restype = i64
     L.bitnet_kv4_weigh.argtypes = [kv4, p, i64, i32, i64, i64, f32, i64, i64, i64, p, f32, p, p, i64, p]
     L.bitnet_kv4_weigh.restype = ctypes.c_int
-    L.bitnet_kv4_evict.argtypes = [kv4, p, p, i64, i64, i64, i64, p, p, p]
+    L.bitnet_kv4_evict.argtypes = [kv4, p, p, i64, i64, i64, i64, p, p, p, i64, p]
+    L.bitnet_kv4_evict_workspace.argtypes, L.bitnet_kv4_evict_workspace.restype = [i64] * 3, i64
     L.bitnet_kv4_evict.restype = ctypes.c_int
     w4 = ctypes.POINTER(W4Desc)
     for fn, args in (("bitnet_pack_w4", [p, i32, w4, p]), ("bitnet_pack_w4_codes", [p, p, w4, p]),
@@ -844,7 +845,8 @@ def kv4_weigh_workspace(n_seqs, n, n_heads, n_kv_heads, head_dim, max_kv, window
     return need
 
 
-def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0, out=None):
+def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0, out=None,
+              workspace=None):
     """Copies what is kept of each sequence to the pages of ``new_table`` [B][new_max_pages], kv
     head by kv head: its first ``sinks`` tokens, its last ``recent`` ones, and of the others
     those of the largest weight, ``keep`` in all (or all there are), in order, weights and all.  The new pages must be
@@ -852,7 +854,8 @@ def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0,
 
     Returns (new_len [B], index [B][n_kv_heads][keep]: the places that the tokens had, -1
     behind the last), int32, in ``out`` if given.  The step after goes on with new_table and new_len; its
-    positions are kv_len - new_len further on (rotary_kv4_append's offset)."""
+    positions are kv_len - new_len further on (rotary_kv4_append's offset).  workspace: as in
+    attn_kv4 (kv4_evict_workspace bytes, none for short tables)."""
     import torch
     i32, dev = torch.int32, cache.device
     if weights is None or new_table is None or new_table.dim() != 2:
@@ -865,10 +868,27 @@ def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0,
         index = torch.empty((B, heads, max(keep, 0)), dtype=i32, device=dev)
     else:
         new_len, index = out
-    _launch(load().bitnet_kv4_evict, dev, batch, at_w,
+    L, ws = load(), None
+    need = L.bitnet_kv4_evict_workspace(B, heads, batch.max_pages)
+    if need > 0:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
+            raise ValueError(f"workspace must be {need} bytes of uint8 on {dev}")
+        ws = _ptr(workspace)
+    _launch(L.bitnet_kv4_evict, dev, batch, at_w,
             _at(new_table, "new_table", i32, (B, new_table.shape[1]), dev), new_table.shape[1], keep, sinks, recent,
-            _at(new_len, "new_len", i32, (B,), dev), _at(index, "index", i32, (B, heads, keep), dev))
+            _at(new_len, "new_len", i32, (B,), dev), _at(index, "index", i32, (B, heads, keep), dev),
+            ws, max(need, 0))
     return new_len, index
+
+
+def kv4_evict_workspace(n_seqs, n_kv_heads, max_pages):
+    """Bytes of workspace that kv4_evict takes for n_seqs tables of max_pages entries."""
+    need = load().bitnet_kv4_evict_workspace(n_seqs, n_kv_heads, max_pages)
+    if need < 0:
+        raise BitnetError(E_SHAPE, load().bitnet_last_error().decode(errors="replace"))
+    return need
 
 
 class W4Matrix:

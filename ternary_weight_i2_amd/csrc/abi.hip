@@ -719,10 +719,22 @@ BITNET_API int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, in
     return ok();
 }
 
+BITNET_API int64_t bitnet_kv4_evict_workspace(int64_t n_seqs, int64_t n_kv_heads,
+                                              int64_t max_pages) {
+    const char *fn = "bitnet_kv4_evict_workspace";
+    if (n_seqs < 0 || n_seqs > BITNET_KV4_MAX_SEQS || n_kv_heads < 1 ||
+        n_kv_heads > BITNET_KV4_MAX_HEADS || max_pages < 1 || max_pages > BITNET_KV4_MAX_PAGES) {
+        fail(BITNET_E_SHAPE, "%s: sizes out of range", fn);
+        return -1;
+    }
+    g_last_error.clear();
+    return n_seqs ? bitnet::evict_plan(n_seqs, n_kv_heads, max_pages).bytes : 0;
+}
+
 BITNET_API int bitnet_kv4_evict(const bitnet_kv4_batch *batch, float *weights,
                                 const int32_t *new_table, int64_t new_max_pages, int64_t keep,
                                 int64_t sinks, int64_t recent, int32_t *new_len, int32_t *index,
-                                void *stream) {
+                                void *workspace, int64_t workspace_bytes, void *stream) {
     const char *fn = "bitnet_kv4_evict";
     if (int s = check_kv4(fn, batch, BITNET_F32, 1, false)) return s;
     if (new_max_pages < 1 || new_max_pages > BITNET_KV4_MAX_PAGES)
@@ -737,15 +749,26 @@ BITNET_API int bitnet_kv4_evict(const bitnet_kv4_batch *batch, float *weights,
     if (batch->n_seqs == 0) return ok();
     if (!weights || !new_table || !new_len || !index)
         return fail(BITNET_E_NULL, "%s: weights, new_table, new_len and index are required", fn);
-    if (!aligned(weights, 16))
-        return fail(BITNET_E_ALIGN, "%s: weights must be 16-byte aligned", fn);
+    if (!aligned(weights, 16) || !aligned(workspace, 16))
+        return fail(BITNET_E_ALIGN, "%s: weights and workspace must be 16-byte aligned", fn);
     if (!aligned(new_table, 4) || !aligned(new_len, 4) || !aligned(index, 4))
         return fail(BITNET_E_ALIGN, "%s: new_table, new_len and index must be 4-byte aligned", fn);
+    const bitnet::EvictPlan p =
+        bitnet::evict_plan(batch->n_seqs, batch->n_kv_heads, batch->max_pages);
+    if (p.bytes > 0 && !workspace)
+        return fail(BITNET_E_NULL, "%s: a workspace of %lld bytes is required", fn,
+                    (long long)p.bytes);
+    if (workspace_bytes < p.bytes)
+        return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
+                    (long long)workspace_bytes, (long long)p.bytes);
+    char *const ws = static_cast<char *>(workspace);
     const bitnet::EvictArgs a{static_cast<uint8_t *>(batch->cache), weights, batch->table,
-                              batch->kv_len, new_table, new_len, index, batch->n_pages,
+                              batch->kv_len, new_table, new_len, index,
+                              reinterpret_cast<int *>(ws), reinterpret_cast<int2 *>(ws + p.search_at),
+                              reinterpret_cast<int2 *>(ws + p.slices_at), batch->n_pages,
                               batch->max_pages, new_max_pages, batch->n_seqs,
                               (int)batch->n_kv_heads, (int)keep, (int)sinks, (int)recent};
-    hipError_t e = bitnet::launch_kv4_evict(a, (int)batch->head_dim,
+    hipError_t e = bitnet::launch_kv4_evict(a, p, (int)batch->head_dim,
                                             static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);
     return ok();

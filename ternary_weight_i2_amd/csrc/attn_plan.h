@@ -129,4 +129,24 @@ inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
     return p;
 }
 
+// kv4_evict.hip: the workgroups that choose the tokens of a (sequence, kv head), and what they
+// tell each other: bins of three passes, the search's state after each, counts of each slice.
+constexpr int kBins = 2048;
+constexpr int kEvictSlicesFrom = 320;   // pages: 16384 tokens 35 us by one and 38.5 by four, 32768 52 and 39
+struct EvictPlan {
+    int slices;
+    int64_t search_at, slices_at, bytes;
+};
+inline EvictPlan evict_plan(int64_t n_seqs, int64_t kv_heads, int64_t max_pages) {
+    const int64_t units = n_seqs * kv_heads;
+    EvictPlan p{1, 0, 0, 0};
+    if (max_pages >= kEvictSlicesFrom)
+        p.slices = (int)std::max<int64_t>(std::min({max_pages / 64, 2 * kUnits / units, (int64_t)32}), 1);
+    if (p.slices == 1) return p;
+    p.search_at = 3 * units * p.slices * kBins * 4;
+    p.slices_at = p.search_at + 3 * units * 8;
+    p.bytes = p.slices_at + units * p.slices * 8;
+    return p;
+}
+
 }  // namespace bitnet

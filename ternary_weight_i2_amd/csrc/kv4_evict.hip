@@ -1,10 +1,10 @@
 // kv4_evict.hip -- the tokens of a sequence with the largest weight, its first and its last
 // ones, moved in their order to other pages of the 4-bit cache, kv head by kv head.
 //
-// Choosing: a workgroup to a (sequence, kv head).  Weights become integers of the same
-// order; three passes over them, 11, 11 and 10 bits each, find the smallest one that is
-// kept and how many of its equals are; a last pass over the tokens in order gives each kept
-// one its place.  Moving: a workgroup to a page of the result, which gathers its 64 tokens
+// Choosing: a workgroup to a (sequence, kv head), or several where these are few and histories
+// long.  Weights become integers of the same order; three passes over them, 11, 11 and 10
+// bits each, find the smallest one that is kept and how many of its equals are; a last pass
+// over the tokens in order gives each kept one its place.  Moving: a workgroup to a page of the result, which gathers its 64 tokens
 // (records as kv4.h lays them out) and writes them once.
 #include <algorithm>
 
@@ -16,7 +16,6 @@ namespace {
 
 constexpr int kChooseThreads = 1024;
 constexpr int kChooseWaves = kChooseThreads / 64;
-constexpr int kBins = 2048;
 constexpr int kBatch = 4;
 constexpr int kMoveThreads = 256;
 
@@ -48,144 +47,258 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
     return v;
 }
 
-__global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const EvictArgs a, int64_t units) {
-    __shared__ int bins[kBins], slot[kChooseWaves];
-    __shared__ uint32_t scan[2][kChooseWaves];
-    __shared__ int found[2];   // the bin that the last kept one is in, and how many of it are kept
+// A (sequence, kv head) and how many of its tokens are kept; every thread of a workgroup has it.
+struct Unit {
+    int64_t seq, row;   // row: of the index
+    int head, held;
+    int there, kept, quota;   // tokens whose page is there; of them kept; of those by their weight
+    __device__ bool choose() const { return kept < there && quota > 0; }
+    __device__ bool spared(const EvictArgs &a, int t) const { return t < a.sinks || t >= held - a.recent; }
+    __device__ int page_of(const EvictArgs &a, int t) const {   // or -1
+        const int id = a.table[seq * a.max_pages + t / kPage];
+        return id >= 0 && id < a.n_pages ? id : -1;
+    }
+    __device__ float4 weights4(const EvictArgs &a, int id, int t0) const {   // of tokens t0 .. t0 + 3
+        return *reinterpret_cast<const float4 *>(a.weights + ((int64_t)id * a.kv_heads + head) * kPage + t0 % kPage);
+    }
+};
+__device__ __forceinline__ Unit unit_of(const EvictArgs &a, int64_t unit, int *slot) {
+    Unit u;
+    u.seq = unit / a.kv_heads;
+    u.row = unit;
+    u.head = (int)(unit - u.seq * a.kv_heads);
+    u.held = min(max(a.kv_len[u.seq], 0), (int)(a.max_pages * kPage));
+    int mine = 0, safe = 0;
+    for (int t0 = threadIdx.x * kPage; t0 < u.held; t0 += kChooseThreads * kPage)
+        if (u.page_of(a, t0) >= 0) {
+            const int t1 = min(u.held, t0 + kPage);
+            mine += t1 - t0;
+            // [0, sinks) and [held - recent, held) may meet
+            const int low = min(max(a.sinks - t0, 0), t1 - t0);
+            const int high = min(max(t1 - max(u.held - a.recent, t0), 0), t1 - t0);
+            safe += min(low + high, t1 - t0);
+        }
+    u.there = block_sum(mine, slot);
+    u.kept = min(u.there, a.keep);
+    u.quota = u.kept - block_sum(safe, slot);   // not negative: sinks + recent <= keep
+    return u;
+}
+
+// The search for the smallest order that is kept: its upper bits so far, and how many of the
+// tokens that share them are kept.
+struct Search {
+    uint32_t least;
+    int ties;
+};
+constexpr int kPasses = 3;
+__device__ __forceinline__ int shift_of(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
+__device__ __forceinline__ int width_of(int pass) { return pass < 2 ? 11 : 10; }
+
+// Counts four tokens t0 on by the next bits of their order.
+__device__ __forceinline__ void count_four(const EvictArgs &a, const Unit &u, int pass, const Search &f, int id, int t0,
+                                           int to, const float4 &w, int *bins) {
+    const int shift = shift_of(pass), width = width_of(pass);
+    const float v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (id < 0 || t0 + e >= to || u.spared(a, t0 + e)) continue;
+        const uint32_t o = order_of(v[e]);
+        if (pass > 0 && (o ^ f.least) >> (shift + width)) continue;   // other upper bits
+        atomicAdd(&bins[o >> shift & ((1 << width) - 1)], 1);
+    }
+}
+// Counts the tokens of [from, to) (from a multiple of four).
+__device__ __forceinline__ void count_bins(const EvictArgs &a, const Unit &u, int pass, const Search &f, int from,
+                                           int to, int *bins) {
+    for (int i = threadIdx.x; i < kBins; i += kChooseThreads) bins[i] = 0;
+    __syncthreads();
+    // four tokens to a thread, kBatch times: first all loads, then the counts
+    for (int base = from + 4 * (int)threadIdx.x; base < to; base += 4 * kChooseThreads * kBatch) {
+        int id[kBatch];
+        float4 w[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int t0 = base + 4 * kChooseThreads * i;
+            id[i] = t0 < to ? u.page_of(a, t0) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) w[i] = u.weights4(a, max(id[i], 0), base + 4 * kChooseThreads * i);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) count_four(a, u, pass, f, id[i], base + 4 * kChooseThreads * i, to, w[i], bins);
+    }
+    __syncthreads();
+}
+// One step of the search; c1, c0: what bins 2047 - 2 i and 2046 - 2 i of thread i count.
+__device__ __forceinline__ void pick(Search &f, int pass, int c1, int c0, uint32_t *scan, int *found) {
+    const int wave = threadIdx.x >> 6, b1 = kBins - 1 - 2 * (int)threadIdx.x;
+    uint32_t up = wave_scan((uint32_t)(c1 + c0));
+    if ((threadIdx.x & 63) == 63) scan[wave] = up;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) up += scan[w];
+    const int before = (int)up - c1 - c0;   // in the bins above this thread's
+    if (before < f.ties && before + c1 >= f.ties) {
+        found[0] = b1;
+        found[1] = f.ties - before;
+    } else if (before + c1 < f.ties && before + c1 + c0 >= f.ties) {
+        found[0] = b1 - 1;
+        found[1] = f.ties - before - c1;
+    }
+    __syncthreads();
+    f.least |= (uint32_t)found[0] << shift_of(pass);
+    f.ties = found[1];
+    __syncthreads();
+}
+
+// Which of four tokens t0 on are kept whatever comes before them, and which if they are among
+// the first ties: bits.
+__device__ __forceinline__ void kinds_of(const EvictArgs &a, const Unit &u, const Search &f, int id, int t0, int to,
+                                         const float4 &w4, uint32_t &sure, uint32_t &tie) {
+    sure = tie = 0;
+    if (id < 0) return;
+    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (t0 + e >= to) continue;
+        const uint32_t o = order_of(w[e]);
+        if (u.kept == u.there || u.spared(a, t0 + e) || (u.choose() && o > f.least)) sure |= 1u << e;
+        else if (u.choose() && o == f.least) tie |= 1u << e;
+    }
+}
+// Gives the kept tokens of [from, to) their places, in order, behind those before them.
+__device__ __forceinline__ void place_tokens(const EvictArgs &a, const Unit &u, const Search &f, int from, int to,
+                                             int sure_before, int ties_before, uint32_t *scan) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int32_t *index = a.index + u.row * a.keep;
+    auto entry = [&](int t0) { return t0 < to ? u.page_of(a, t0) : -1; };
+    // this turn's page and the next one's
+    int id = entry(from + 4 * tid), id1 = entry(from + 4 * (tid + kChooseThreads));
+    float4 w4 = u.weights4(a, max(id, 0), from + 4 * tid);
+    for (int base = from; base < to; base += 4 * kChooseThreads) {
+        const int t0 = base + 4 * tid, id2 = entry(t0 + 8 * kChooseThreads);
+        const float4 next = u.weights4(a, max(id1, 0), t0 + 4 * kChooseThreads);
+        uint32_t sure, tie;
+        kinds_of(a, u, f, id, t0, to, w4, sure, tie);
+        const uint32_t counts = (uint32_t)__popc(sure) << 16 | (uint32_t)__popc(tie);
+        const uint32_t up = wave_scan(counts);
+        if (lane == 63) scan[wave] = up;
+        __syncthreads();
+        uint32_t off = up - counts, all = 0;   // 4096 of each at most
+        for (int w = 0; w < kChooseWaves; ++w) {
+            if (w < wave) off += scan[w];
+            all += scan[w];
+        }
+        int s = sure_before + (int)(off >> 16), t = ties_before + (int)(off & 0xffffu);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool is_tie = tie >> e & 1, in = (sure >> e & 1) || (is_tie && t < f.ties);
+            const int at = s + min(t, f.ties);
+            if (in && at < u.kept) index[at] = t0 + e;   // (always, unless the weights change meanwhile)
+            s += sure >> e & 1;
+            t += is_tie;
+        }
+        sure_before += (int)(all >> 16);
+        ties_before += (int)(all & 0xffffu);
+        id = id1;
+        id1 = id2;
+        w4 = next;
+        __syncthreads();
+    }
+}
+
+// The whole choice by one workgroup.
+__global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const EvictArgs a, int64_t units) {
+    __shared__ int bins[kBins], slot[kChooseWaves], found[2];
+    __shared__ uint32_t scan[kChooseWaves];
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t seq = unit / a.kv_heads;
-        const int head = (int)(unit - seq * a.kv_heads);
-        const int held = min(max(a.kv_len[seq], 0), (int)(a.max_pages * kPage));
-        const int pages = (held + kPage - 1) / kPage;
-        const int32_t *table = a.table + seq * a.max_pages;
-        auto page_of = [&](int p) {
-            const int id = table[p];
-            return id >= 0 && id < a.n_pages ? id : -1;
-        };
-        auto weights4 = [&](int id, int t0) {   // of tokens t0 .. t0 + 3
-            return *reinterpret_cast<const float4 *>(a.weights + ((int64_t)id * a.kv_heads + head) * kPage + t0 % kPage);
-        };
-        // tokens that are there, and those of them that are spared
-        auto spared = [&](int t) { return t < a.sinks || t >= held - a.recent; };
-        int mine = 0, safe = 0;
-        for (int p = tid; p < pages; p += kChooseThreads)
-            if (page_of(p) >= 0) {
-                const int t0 = p * kPage, t1 = min(held, t0 + kPage);
-                mine += t1 - t0;
-                // [0, sinks) and [held - recent, held) may meet
-                const int low = min(max(a.sinks - t0, 0), t1 - t0);
-                const int high = min(max(t1 - max(held - a.recent, t0), 0), t1 - t0);
-                safe += min(low + high, t1 - t0);
-            }
-        const int there = block_sum(mine, slot);
-        const int safe_all = block_sum(safe, slot);
-        const int kept = min(there, a.keep), quota = kept - safe_all;   // quota >= 0: sinks + recent <= keep
-        if (head == 0 && tid == 0) a.new_len[seq] = kept;
-        // ---- the smallest order that is kept, bit by bit from the top
-        uint32_t least = 0;   // its upper bits so far
-        int ties = quota;     // how many of those that share them are kept
-        const bool choose = kept < there && quota > 0;
-        if (choose) {
-            int shift = 21;
-            for (int pass = 0; pass < 3; ++pass) {
-                const int width = pass < 2 ? 11 : 10, next = pass == 0 ? 10 : 0;
-                for (int i = tid; i < kBins; i += kChooseThreads) bins[i] = 0;
-                __syncthreads();
-                // four tokens to a thread, kBatch times: first all loads, then the counts
-                for (int base = 4 * tid; base < held; base += 4 * kChooseThreads * kBatch) {
-                    int id[kBatch];
-                    float4 w[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int t0 = base + 4 * kChooseThreads * i;
-                        id[i] = t0 < held ? page_of(t0 / kPage) : -1;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
-                        w[i] = weights4(max(id[i], 0), base + 4 * kChooseThreads * i);
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int t0 = base + 4 * kChooseThreads * i;
-                        const float v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (id[i] < 0 || t0 + e >= held || spared(t0 + e)) continue;
-                            const uint32_t o = order_of(v[e]);
-                            if (pass > 0 && (o ^ least) >> (shift + width)) continue;   // other upper bits
-                            atomicAdd(&bins[o >> shift & ((1 << width) - 1)], 1);
-                        }
-                    }
+        const Unit u = unit_of(a, unit, slot);
+        if (u.head == 0 && threadIdx.x == 0) a.new_len[u.seq] = u.kept;
+        Search f{0, u.quota};
+        // four tokens to a thread are looked at again and again without being loaded again
+        const bool few = u.held <= 4 * kChooseThreads;
+        const int id = few && 4 * (int)threadIdx.x < u.held ? u.page_of(a, 4 * threadIdx.x) : -1;
+        const float4 w4 = u.weights4(a, max(id, 0), 4 * threadIdx.x);
+        if (u.choose())
+            for (int pass = 0; pass < kPasses; ++pass) {
+                if (few) {
+                    for (int i = threadIdx.x; i < kBins; i += kChooseThreads) bins[i] = 0;
+                    __syncthreads();
+                    count_four(a, u, pass, f, id, 4 * threadIdx.x, u.held, w4, bins);
+                    __syncthreads();
+                } else {
+                    count_bins(a, u, pass, f, 0, u.held, bins);
                 }
-                __syncthreads();
-                // from the top: thread i has bins 2047 - 2 i and 2046 - 2 i
-                const int b1 = kBins - 1 - 2 * tid, c1 = bins[b1], c0 = bins[b1 - 1];
-                uint32_t up = wave_scan((uint32_t)(c1 + c0));
-                if (lane == 63) scan[0][wave] = up;
-                __syncthreads();
-                for (int w = 0; w < wave; ++w) up += scan[0][w];
-                const int before = (int)up - c1 - c0;   // in the bins above this thread's
-                if (before < ties && before + c1 >= ties) {
-                    found[0] = b1;
-                    found[1] = ties - before;
-                } else if (before + c1 < ties && before + c1 + c0 >= ties) {
-                    found[0] = b1 - 1;
-                    found[1] = ties - before - c1;
-                }
-                __syncthreads();
-                least |= (uint32_t)found[0] << shift;
-                ties = found[1];
-                __syncthreads();
-                shift = next;
+                const int b1 = kBins - 1 - 2 * (int)threadIdx.x;
+                pick(f, pass, bins[b1], bins[b1 - 1], scan, found);
             }
+        place_tokens(a, u, f, 0, u.held, 0, 0, scan);
+        for (int i = u.kept + threadIdx.x; i < a.keep; i += kChooseThreads) a.index[u.row * a.keep + i] = -1;
+    }
+}
+
+// The choice of a long history by `slices` workgroups, a launch for each step: STEP 0 to 2
+// count a slice's bins, 3 its sure tokens and ties, 4 gives them their places.  A step
+// finishes what the last one's counts of all slices say; what was found before is in a.search.
+template <int STEP>
+__global__ __launch_bounds__(kChooseThreads) void evict_step_kernel(const EvictArgs a, int slices) {
+    __shared__ int bins[kBins], slot[kChooseWaves], found[2];
+    __shared__ uint32_t scan[kChooseWaves];
+    const int64_t unit = blockIdx.x / slices, units = gridDim.x / slices;
+    const int slice = (int)(blockIdx.x - unit * slices), tid = threadIdx.x;
+    const Unit u = unit_of(a, unit, slot);
+    const int share = ((u.held + slices - 1) / slices + 3) & ~3;   // at most 2^30 / 2
+    const int from = min(slice * share, u.held), to = min(from + share, u.held);
+    int *const counts = a.counts + unit * slices * kBins;   // [pass][unit][slice][bin]
+    const int64_t pass_size = units * slices * kBins;
+    Search f{0, u.quota};
+    if (u.choose() && STEP > 0) {
+        // what each step finds has a place of its own: other slices still read the last one's
+        if (STEP > 1) {
+            const int2 before = a.search[(STEP - 2) * units + unit];
+            f = Search{(uint32_t)before.x, before.y};
         }
-        // ---- places, in the order of the tokens: four tokens to a thread
-        int32_t *index = a.index + (seq * a.kv_heads + head) * a.keep;
+        if (STEP <= kPasses) {
+            const int *of_pass = counts + (STEP - 1) * pass_size + kBins - 2 - 2 * tid;
+            int c1 = 0, c0 = 0;
+#pragma unroll 8
+            for (int s = 0; s < slices; ++s) {
+                const int2 c = *reinterpret_cast<const int2 *>(of_pass + s * kBins);
+                c0 += c.x;
+                c1 += c.y;
+            }
+            pick(f, STEP - 1, c1, c0, scan, found);
+            if (slice == 0 && tid == 0) a.search[(STEP - 1) * units + unit] = make_int2((int)f.least, f.ties);
+        }
+    }
+    if constexpr (STEP < kPasses) {
+        if (u.choose()) {
+            count_bins(a, u, STEP, f, from, to, bins);
+            for (int i = tid; i < kBins; i += kChooseThreads)
+                counts[STEP * pass_size + slice * kBins + i] = bins[i];
+        }
+    } else if constexpr (STEP == kPasses) {
+        int n_sure = 0, n_tie = 0;
+        for (int t0 = from + 4 * tid; t0 < to; t0 += 4 * kChooseThreads) {
+            const int id = u.page_of(a, t0);
+            uint32_t sure, tie;
+            kinds_of(a, u, f, id, t0, to, u.weights4(a, max(id, 0), t0), sure, tie);
+            n_sure += __popc(sure);
+            n_tie += __popc(tie);
+        }
+        n_sure = block_sum(n_sure, slot);
+        n_tie = block_sum(n_tie, slot);
+        if (tid == 0) a.slices[unit * slices + slice] = make_int2(n_sure, n_tie);
+    } else {
         int sure_before = 0, ties_before = 0;
-        auto entry = [&](int t0) { return t0 < held ? page_of(t0 / kPage) : -1; };
-        int id = entry(4 * tid), id1 = entry(4 * (tid + kChooseThreads));   // of this turn and the next
-        float4 w4 = weights4(max(id, 0), 4 * tid);
-        for (int base = 0; base < held; base += 4 * kChooseThreads) {
-            const int t0 = base + 4 * tid;
-            const int id2 = entry(t0 + 8 * kChooseThreads);
-            const float4 next = weights4(max(id1, 0), t0 + 4 * kChooseThreads);
-            uint32_t sure = 0, tie = 0;   // bits of the four tokens
-            if (id >= 0) {
-                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (t0 + e >= held) continue;
-                    const uint32_t o = order_of(w[e]);
-                    if (kept == there || spared(t0 + e) || (choose && o > least)) sure |= 1u << e;
-                    else if (choose && o == least) tie |= 1u << e;
-                }
-            }
-            const uint32_t counts = (uint32_t)__popc(sure) << 16 | (uint32_t)__popc(tie);
-            const uint32_t up = wave_scan(counts);
-            if (lane == 63) scan[1][wave] = up;
-            __syncthreads();
-            uint32_t off = up - counts, all = 0;   // 4096 of each at most
-            for (int w = 0; w < kChooseWaves; ++w) {
-                if (w < wave) off += scan[1][w];
-                all += scan[1][w];
-            }
-            int s = sure_before + (int)(off >> 16), t = ties_before + (int)(off & 0xffffu);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool is_tie = tie >> e & 1, in = (sure >> e & 1) || (is_tie && t < ties);
-                const int to = s + min(t, ties);
-                if (in && to < kept) index[to] = t0 + e;   // (always, unless the weights change meanwhile)
-                s += sure >> e & 1;
-                t += is_tie;
-            }
-            sure_before += (int)(all >> 16);
-            ties_before += (int)(all & 0xffffu);
-            id = id1;
-            id1 = id2;
-            w4 = next;
-            __syncthreads();
+#pragma unroll 8
+        for (int s = 0; s < slice; ++s) {
+            const int2 c = a.slices[unit * slices + s];
+            sure_before += c.x;
+            ties_before += c.y;
         }
-        for (int i = kept + tid; i < a.keep; i += kChooseThreads) index[i] = -1;
+        place_tokens(a, u, f, from, to, sure_before, ties_before, scan);
+        for (int i = u.kept + slice * kChooseThreads + tid; i < a.keep; i += slices * kChooseThreads)
+            a.index[u.row * a.keep + i] = -1;
+        if (u.head == 0 && slice == 0 && tid == 0) a.new_len[u.seq] = u.kept;
     }
 }
 
@@ -255,11 +368,20 @@ __global__ __launch_bounds__(kMoveThreads) void evict_move_kernel(const EvictArg
 
 }  // namespace
 
-hipError_t launch_kv4_evict(const EvictArgs &a, int dim, hipStream_t st) {
+hipError_t launch_kv4_evict(const EvictArgs &a, const EvictPlan &p, int dim, hipStream_t st) {
     constexpr int64_t kMost = 1 << 21;   // workgroups; more units take turns
     const int64_t heads = a.n_seqs * a.kv_heads;
-    hipLaunchKernelGGL(evict_choose_kernel, dim3((unsigned)std::min(heads, kMost)), dim3(kChooseThreads), 0, st, a,
-                       heads);
+    if (p.slices == 1) {
+        hipLaunchKernelGGL(evict_choose_kernel, dim3((unsigned)std::min(heads, kMost)), dim3(kChooseThreads), 0, st, a,
+                           heads);
+    } else {
+        const dim3 g((unsigned)(heads * p.slices)), t(kChooseThreads);
+        hipLaunchKernelGGL((evict_step_kernel<0>), g, t, 0, st, a, p.slices);
+        hipLaunchKernelGGL((evict_step_kernel<1>), g, t, 0, st, a, p.slices);
+        hipLaunchKernelGGL((evict_step_kernel<2>), g, t, 0, st, a, p.slices);
+        hipLaunchKernelGGL((evict_step_kernel<3>), g, t, 0, st, a, p.slices);
+        hipLaunchKernelGGL((evict_step_kernel<4>), g, t, 0, st, a, p.slices);
+    }
     const int pages = (a.keep + kPage - 1) / kPage;
     const int64_t units = heads * pages;
     const dim3 g((unsigned)std::min(units, kMost)), t(kMoveThreads);

@@ -158,10 +158,12 @@ struct EvictArgs {
     float *weights;
     const int32_t *table, *kv_len, *new_table;
     int32_t *new_len, *index;
+    int *counts;           // several workgroups to a choice: EvictPlan
+    int2 *search, *slices;
     int64_t n_pages, max_pages, new_pages, n_seqs;
     int kv_heads, keep, sinks, recent;
 };
-hipError_t launch_kv4_evict(const EvictArgs &a, int dim, hipStream_t st);
+hipError_t launch_kv4_evict(const EvictArgs &a, const EvictPlan &plan, int dim, hipStream_t st);
 struct Attn4Args {
     Kv4Args c;
     const void *q;

@@ -199,7 +199,7 @@ def test_weigh_captured_and_on_two_streams(bn):
 
 # ---------------------------------------------------------------- evict
 
-def check_evict(bn, s, keep, sinks=0, recent=0, weights=None, drop=(), spare=2, cap=None, seed=0):
+def check_evict(bn, s, keep, sinks=0, recent=0, weights=None, drop=(), spare=2, cap=None, seed=0, wide=0):
     """s's sequences onto new pages in front of which and behind which nothing may change."""
     rng = np.random.default_rng(seed)
     B, old_pages = len(s.kv_len), s.n_pages
@@ -212,6 +212,9 @@ def check_evict(bn, s, keep, sinks=0, recent=0, weights=None, drop=(), spare=2, 
     table = np.where(s.table == s.n_pages, len(cache), s.table).astype(np.int32)   # absent ones stay absent
     for b, p in drop:
         new_table[b, p] = (-1, len(cache))[p % 2]
+    if wide:    # a table of more entries than any sequence needs
+        table = np.pad(table, ((0, 0), (0, wide - table.shape[1])), constant_values=-1)
+        assert bn.kv4_evict_workspace(B, s.heads, wide) > 0
     c, wd = dev(cache), dev(w)
     new_len, index = bn.kv4_evict(c, wd, dev(table), dev(s.kv_len), dev(new_table), keep, sinks=sinks, recent=recent)
     want_len, want_index = so.evict(cache, w, table, s.kv_len, new_table, keep, sinks, recent)
@@ -240,6 +243,39 @@ def test_evict_long_ones(bn, heads):
     """More tokens than the four of every thread, twice over."""
     check_evict(bn, full([9000, 4096, 4097], heads, 64, seed=1), 1500, 4, 200)
     check_evict(bn, full([9000], heads, 64, seed=2), 8999, 0, 0)
+
+
+@pytest.mark.parametrize("wide", [600, 4096])
+def test_evict_by_several_workgroups(bn, wide):
+    """Tables for long histories, whatever their sequences' lengths."""
+    s = full([9000, 70, 0, 4100, 1], 2, 64, seed=10, gap=[(0, 5), (3, 64)])
+    for keep, sinks, recent in ((1500, 4, 200), (1, 0, 0), (8999, 0, 9), (64, 64, 0), (3, 1, 1)):
+        check_evict(bn, s, keep, sinks, recent, wide=wide)
+    rng = np.random.default_rng(11)
+    w = rng.integers(0, 3, (s.n_pages, 2, 64)).astype(np.float32)      # ties across slices
+    check_evict(bn, s, 3000, 10, 20, weights=w, wide=wide)
+    w[:] = 1
+    check_evict(bn, s, 3000, 0, 20, weights=w, wide=wide)
+    w = rng.choice([np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-45, -1e-45, 3e38, -3e38], w.shape).astype(np.float32)
+    check_evict(bn, s, 3000, 0, 20, weights=w, wide=wide)
+
+
+def test_evict_scratch(bn):
+    """Scratch of any content, and none that is too short."""
+    s = full([5000], 1, 64, seed=12)
+    cache = np.concatenate([s.cache, np.zeros((4, *s.cache.shape[1:]), np.uint8)])
+    w = np.random.default_rng(12).standard_normal((len(cache), 1, 64)).astype(np.float32)
+    table = np.pad(s.table, ((0, 0), (0, 600 - s.table.shape[1])), constant_values=-1)
+    new_table = s.n_pages + np.arange(4, dtype=np.int32)[None]
+    need = bn.kv4_evict_workspace(1, 1, 600)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    c, wd = dev(cache), dev(w)
+    got = bn.kv4_evict(c, wd, dev(table), dev(s.kv_len), dev(new_table), 200, workspace=ws)
+    want = so.evict(cache, w, table, s.kv_len, new_table, 200)
+    assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
+    assert np.array_equal(c.cpu().numpy(), cache) and (ws[need:] == 0xFF).all()
+    with pytest.raises(ValueError):
+        bn.kv4_evict(c, wd, dev(table), dev(s.kv_len), dev(new_table), 200, workspace=ws[:need - 1])
 
 
 def test_evict_by_weights_of_every_kind(bn):

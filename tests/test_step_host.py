@@ -229,8 +229,8 @@ def test_weigh_validation(L):
     assert L.bitnet_kv4_weigh_workspace(0, 3, 4, 2, 64, 64, 0, 0) == 0
 
 
-def _evict(L, b=None, w=FAKE, nt=FAKE, cap=3, keep=64, sinks=4, recent=8, nl=FAKE, idx=FAKE):
-    return L.bitnet_kv4_evict(b or _batch(q_start=None), w, nt, cap, keep, sinks, recent, nl, idx, None)
+def _evict(L, b=None, w=FAKE, nt=FAKE, cap=3, keep=64, sinks=4, recent=8, nl=FAKE, idx=FAKE, ws=None, wb=0):
+    return L.bitnet_kv4_evict(b or _batch(q_start=None), w, nt, cap, keep, sinks, recent, nl, idx, ws, wb, None)
 
 
 def test_evict_validation(L):
@@ -245,8 +245,15 @@ def test_evict_validation(L):
     for p in ("w", "nt", "nl", "idx"):
         assert f(L, **{p: None}) == E_NULL
         assert f(L, **{p: MIS if p == "w" else FAKE + 2}) == E_ALIGN
-    assert L.bitnet_kv4_evict(None, FAKE, FAKE, 3, 64, 0, 0, FAKE, FAKE, None) == E_NULL
+    assert L.bitnet_kv4_evict(None, FAKE, FAKE, 3, 64, 0, 0, FAKE, FAKE, None, 0, None) == E_NULL
     assert f(L, _batch(n_seqs=0, q_start=None), w=None) == OK
+    long = _batch(max_pages=4096)
+    need = L.bitnet_kv4_evict_workspace(2, 2, 4096)
+    assert need > 0 and f(L, long) == E_NULL and f(L, long, ws=FAKE, wb=need - 1) == E_SHAPE
+    assert f(L, ws=MIS) == E_ALIGN
+    assert L.bitnet_kv4_evict_workspace(2, 2, 3) == 0 == L.bitnet_kv4_evict_workspace(0, 2, 4096)
+    for bad in ((-1, 2, 3), (2, 0, 3), (2, 2, 0), (2, 1025, 3), (2, 2, (1 << 24) + 1)):
+        assert L.bitnet_kv4_evict_workspace(*bad) == -1
 
 
 def test_weigh_and_evict_binding_refuses():
