@@ -620,7 +620,17 @@ def kv4_append(cache, table, kv_len, q_start, k, v):
             v.data_ptr(), _rows(v, "v", heads, dim, dev), _float_code(k.dtype, "k"), k.shape[0])
 
 
-class Rotary:
+class _Fixed:
+    """An object whose attributes stay as they were made: its descriptor is made once."""
+    __slots__ = ()
+
+    def __setattr__(self, name, value):
+        if hasattr(self, name):
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make another")
+        object.__setattr__(self, name, value)
+
+
+class Rotary(_Fixed):
     """Rotary positions: turns per position of each pair of channels (``turns`` [rot / 2]
     int64 on the device, 64-bit fractions of a turn), the pairs (i, i + rot / 2) or
     (2 i, 2 i + 1) (``interleaved``) of the first rot channels, and what cosine and sine
@@ -891,7 +901,7 @@ def kv4_evict_workspace(n_seqs, n_kv_heads, max_pages):
     return need
 
 
-class W4Matrix:
+class W4Matrix(_Fixed):
     """A matrix of 4-bit weights [M][K] as pack_w4 lays it out: ``codes`` uint8
     [ceil(M/16)][K/128][64][16], ``steps`` fp16 [ceil(M/16)][K/128][16][128/group], and the number of its
     ``rows`` M (all of the tiles' if None)."""

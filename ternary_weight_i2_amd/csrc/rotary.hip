@@ -243,10 +243,11 @@ void launch_append_d(const RotaryArgs &r, const Kv4Args &c, const AppendRows &a,
                      hipStream_t st) {
     // A workgroup's sequence, angles and rows are a chain of loads, so the lanes of few
     // tokens are spread over several; a prompt's blocks keep theirs together, which shares
-    // the angles.
+    // the angles, unless there are very many (16 heads of 256, pairs of single channels: 45.8 us
+    // whole, 37.6 in two; 8 + 16 heads of 128, 64 to 384 threads in 1 to 6: 38 to 44 us, 39 so).
     const int lanes = c.kv_heads * 2 * (D / 8) + a.heads * items_of(CUT, D, r.rot);
     const int64_t blocks = N / 4 + 2 * c.n_seqs;
-    const int spread = blocks <= 256 ? (lanes + kRotThreads - 1) / kRotThreads : 1;
+    const int turns = (lanes + kRotThreads - 1) / kRotThreads, spread = blocks <= 256 ? turns : turns > 4 ? 2 : 1;
     const dim3 g((unsigned)blocks, (unsigned)spread), t(kRotThreads);
     if (bf16) hipLaunchKernelGGL((rotary_append_kernel<D, CUT, true>), g, t, 0, st, r, c, a, N);
     else hipLaunchKernelGGL((rotary_append_kernel<D, CUT, false>), g, t, 0, st, r, c, a, N);

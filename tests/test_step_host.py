@@ -80,6 +80,8 @@ def test_rotary_binding_refuses():
     with pytest.raises(TypeError):
         bn.Rotary(torch.zeros(64, dtype=torch.int64)[::2])
     p, at = bn.Rotary(t), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(AttributeError):
+        p.magnitude = 2.0
     x = torch.zeros((3, 2, 64))
     for bad in (dict(x=x[0]), dict(x=x.to(torch.float16)), dict(at=at.long()), dict(at=at[:2]), dict(x=x[:, :, :63]),
                 dict(x=x.transpose(0, 1)), dict(out=x[:2]), dict(out=x.bfloat16()), dict()):
@@ -162,6 +164,8 @@ def test_w4_binding_refuses():
     m = bn.W4Matrix.empty(20, 256, 64, device="cpu")
     assert m.codes.shape == (2, 2, 64, 16) and m.steps.shape == (2, 2, 16, 2) and (m.rows, m.k, m.group) == (20, 256, 64)
     assert bn.W4Matrix(m.codes, m.steps).rows == 32
+    with pytest.raises(AttributeError):
+        m.rows = 19
     for rows in (16, 33, 0, -1):
         with pytest.raises(ValueError):
             bn.W4Matrix(m.codes, m.steps, rows)
