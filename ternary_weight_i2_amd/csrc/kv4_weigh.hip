@@ -29,7 +29,7 @@ constexpr int kWeighWaves = kWeighThreads / 64;
 
 // Waves to a SIMD: four where the registers spill little for it (64 bf16 tokens, heads of 128:
 // 72 -> 62 us in all; fp32 rows 24.6 us with three and 28.9 with four for the first launch).
-constexpr int least_waves(int dim, bool bf16) { return dim == 256 ? 2 : dim == 128 && !bf16 ? 3 : 4; }
+constexpr int least_waves(int dim, bool bf16) { return dim == 256 ? 2 : dim == 128 ? 3 : 4; }
 
 // A row's query: 8 channels of every 32 in this lane (quad), times 2^k; the sums of its
 // groups at the same scale; and what makes a product of them a power of two's exponent.
@@ -277,10 +277,11 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_sta
             const Seen seen = seen_of(a, t, G);
             while (t0 >= 0) {
                 share_pairs(k, pairs_all[wave], lane);
+                const int t1 = w.next();   // a page is always loaded, at the end the last one again
+                Keys<D> ahead;
+                load_keys(ahead, cache + w.id * page_bytes, lane);
                 float s[4][4];
                 scores(k, pairs_all[wave], q, one, quad, s);
-                const int t1 = w.next();   // a page is always loaded, at the end the last one again
-                load_keys(k, cache + w.id * page_bytes, lane);
                 if (!seen.all(t0)) {
                     asm volatile("");   // a branch: most pages are seen by all rows
                     hide(s, t0, quad, pos, low, a.sinks);
@@ -298,6 +299,7 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_sta
 #pragma unroll
                     for (int e = 0; e < 4; ++e) l += __builtin_amdgcn_exp2f(fmaf(s[i][e], q.scale, -m));
                 t0 = t1;
+                k = ahead;
             }
         }
         // a row's four lanes, then the waves
@@ -383,8 +385,8 @@ __device__ __forceinline__ int place_of(int lane) {
     return 16 * ((lane & 15) >> 2) + 4 * (lane >> 4) + (lane & 3);
 }
 
-// Few rows: a workgroup has a share of a sequence's pages, its waves taking turns, and a
-// tile's queries stay in registers.  The pages that the first tile does not see get their
+// Few rows: `chunks` workgroups have a sequence's pages, their waves taking turns, and a tile's
+// queries stay in registers.  The pages that the first tile does not see get their
 // old weights; what another tile adds, it adds to what its own lanes have written.
 template <int D, bool BF16>
 __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few_kernel(const WeighArgs a, int chunks, int64_t units) {
@@ -400,17 +402,16 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
         const int begin = a.c.q_start[seq], end = a.c.q_start[seq + 1];
         const int held = min(max(a.c.kv_len[seq], 0), (int)(a.c.max_pages * kPage));
         if (begin < 0 || end <= begin || end > a.N) continue;   // the whole workgroup
-        const int pages = (held + kPage - 1) / kPage, share = share_of(pages, chunks);
-        const int p0 = min(part * share, pages), p1 = min(p0 + share, pages);
-        if (p0 == p1) continue;
+        const int pages = (held + kPage - 1) / kPage;
         const int pos0 = held - (end - begin);
         const uint32_t rows = (uint32_t)(end - begin) * G;
         const int32_t *table = a.c.table + (int64_t)seq * a.c.max_pages;
         const uint8_t *cache = a.c.cache + (int64_t)kv_head * L::kBytes;
         const int64_t page_bytes = (int64_t)a.c.kv_heads * L::kBytes;
         auto weight_at = [&](int id) { return ((int64_t)id * a.c.kv_heads + kv_head) * kPage + place; };
-        // A wave has the pages p0 + wave + 4 k, whichever tile and list they are of, so what it
-        // adds to has been written by itself.
+        // A wave has every stride-th page, whichever tile sees it, so what it adds to has been
+        // written by itself, and a window's pages are spread over the workgroups.
+        const int stride = kWeighWaves * chunks;
         for (uint32_t r = 0; r * 16 < rows; ++r) {
             const uint32_t row0 = r * 16, last = min(row0 + 15, rows - 1), mine = row0 + n, row = min(mine, last), tok = row / G;
             const int pos_a = pos0 + (int)(row0 / G), pos_b = pos0 + (int)(last / G);
@@ -424,11 +425,11 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
             Row rs{0.0f, 0.0f};
             Query<D, BF16> q;
             bool have = false;
-            for (int from = p0 + wave; from < p1; from += 64 * kWeighWaves) {
-                const int i = from + kWeighWaves * lane;
-                const int ids = i < p1 ? table[i] : -1;
+            for (int from = part * kWeighWaves + wave; from < pages; from += 64 * stride) {
+                const int i = from + stride * lane;
+                const int ids = i < pages ? table[i] : -1;
                 const uint64_t there = __ballot(ids >= 0 && ids < a.c.n_pages);
-                uint64_t seen = __ballot(i < p1 && sees(i)) & there;
+                uint64_t seen = __ballot(i < pages && sees(i)) & there;
                 uint64_t rest = r == 0 ? there & ~seen : 0;
                 if (seen) {
                     auto page = [&](uint64_t &bits, int &id) {   // the next one of them, or the last again
@@ -436,7 +437,7 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
                         const int bit = __builtin_ctzll(bits);
                         bits &= bits - 1;
                         id = __builtin_amdgcn_readlane(ids, bit);
-                        return (from + kWeighWaves * bit) * kPage;
+                        return (from + stride * bit) * kPage;
                     };
                     int id = 0, t0 = page(seen, id);
                     Keys<D> k;
@@ -458,10 +459,11 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
                             else if (t0 + place < pos0 && a.decay != 0.0f) was = a.old[at], factor = a.decay;
                         }
                         share_pairs(k, pairs_all[wave], lane);
+                        const int t1 = page(seen, id);
+                        Keys<D> ahead;
+                        load_keys(ahead, cache + id * page_bytes, lane);
                         float x[4][4], w[4][4] = {};
                         scores(k, pairs_all[wave], q, one, quad, x);
-                        const int t1 = page(seen, id);
-                        load_keys(k, cache + id * page_bytes, lane);
                         if (!all.all(t0)) {
                             asm volatile("");
                             hide(x, t0, quad, pos, low, a.sinks);
@@ -470,6 +472,7 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
                         const float sum = sum_rows(w, n);
                         if (write) a.out[at] = fmaf(factor, was, sum);
                         t0 = t1;
+                        k = ahead;
                     }
                 }
                 while (rest) {   // pages that no row of the first tile sees, four at a time
@@ -478,7 +481,7 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few
                     bool write[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int bit = rest ? __builtin_ctzll(rest) : 0, t0 = (from + kWeighWaves * bit) * kPage;
+                        const int bit = rest ? __builtin_ctzll(rest) : 0, t0 = (from + stride * bit) * kPage;
                         at[e] = weight_at(__builtin_amdgcn_readlane(ids, bit));
                         // (weights that stay are not written)
                         write[e] = rest && t0 + place < held && !(a.out == a.old && a.decay == 1.0f && t0 + kPage <= pos0);
