@@ -165,20 +165,32 @@ __device__ __forceinline__ float step_of(const uint2 &w, int g) {
     return (float)as_h2(g < 2 ? w.x : w.y)[g & 1];
 }
 
+// The blocks of a turn: many, to be few turns, where a block's operands take little LDS.  (One
+// token times 2560 x 2560: 7.5 us with eight blocks in turns of four waves, 5.3 with 32; times
+// 128000 x 2560, fp32, a wave to a tile: 43 us with eight, 41 with four.)
+constexpr int blocks_of_turn(int slots, int wk, int terms) {
+    return slots == 4 ? (wk == 1 ? 4 : 8 * wk)
+           : slots == 8 ? (wk == 1 ? 8 : 16)
+           : wk == 4    ? 8
+           : wk == 2    ? 8 / terms
+                        : 4 / terms;
+}
+
 // A workgroup has 16 * TT tokens and eight waves over a share of the blocks (blockIdx.z).  WK of
 // the waves share a tile's blocks, so that few rows have many waves; or a wave has RT tiles,
 // which halves what it reads of the operands in LDS (w4_plan.h chooses).
 // The tokens' operands are made CB blocks at a time in one half of the LDS while the matrix
 // instructions read the other half: the values for it are on their way meanwhile, and so is
 // each block of weights a turn ahead of its use.  Token t of the 16 bytes (j, quad) = p lies
-// in slot (t + 4 p) mod 16 TT, so that the lanes that write eight channels each of a few tokens
-// spread over all banks.
-template <bool BF16, int TT, int GS, int RT, int WK>
+// in slot (t + 4 p) mod SLOTS, so that the lanes that write eight channels each of a few tokens
+// spread over all banks; up to four tokens take four slots, up to eight eight.
+template <bool BF16, int TT, int GS, int RT, int WK, int SLOTS>
 __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w, const void *x, int64_t N,
                                                                   float *y, float *part) {
-    constexpr int NT = BF16 ? 1 : 2, CB = WK == 4 ? 8 : WK == 2 ? 8 / NT : 4 / NT, TOK = 16 * TT, OWN = CB / WK;
-    constexpr int kPieces = CB * TOK * 16 / kW4Threads;   // of 8 channels, at most for a thread
-    __shared__ h8 xs[2][CB * 16 * NT][TOK];
+    constexpr int NT = BF16 ? 1 : 2, TOK = 16 * TT;
+    constexpr int CB = blocks_of_turn(SLOTS, WK, NT), OWN = CB / WK;
+    constexpr int kPieces = (CB * SLOTS * 16 + kW4Threads - 1) / kW4Threads;   // of 8 channels, for a thread
+    __shared__ h8 xs[2][CB * 16 * NT][SLOTS];
     __shared__ __align__(16) float sc[2][CB][TOK];
     const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -204,7 +216,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w
     auto load_tokens = [&](int b0) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int u = u0 + 32 * i, c = u / TOK, t = min(u % TOK, toks - 1);
+            const int u = u0 + 32 * i, c = u / SLOTS, t = min(u % SLOTS, toks - 1);
             const int64_t at = (tok0 + t) * w.K + (int64_t)min(b0 + c, end - 1) * 128 + 8 * p;
 #pragma unroll
             for (int k = 0; k < NT; ++k) v[i][k] = reinterpret_cast<const uint4 *>(x)[at / (8 / NT) + k];
@@ -213,14 +225,14 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w
     auto put_tokens = [&](int half) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int u = u0 + 32 * i, c = u / TOK, t = u % TOK;
-            if (TT == 1 && t >= toks) continue;   // the same for the 16 lanes
+            const int u = u0 + 32 * i, c = u / SLOTS, t = u % SLOTS;
+            if (c >= CB || (TT == 1 && t >= toks)) continue;   // the same for the 16 lanes
             h8 h[NT];
             float f[8];
             load8<BF16>(v[i], 0, f);
             const float down = halves_of<NT>(f, h);
 #pragma unroll
-            for (int k = 0; k < NT; ++k) xs[half][(c * 4 + (p >> 2)) * NT * 4 + k * 4 + (p & 3)][(t + 4 * p) % TOK] = h[k];
+            for (int k = 0; k < NT; ++k) xs[half][(c * 4 + (p >> 2)) * NT * 4 + k * 4 + (p & 3)][(t + 4 * p) % SLOTS] = h[k];
             if (p == 0) sc[half][c][t] = down;
         }
     };
@@ -268,7 +280,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w
                     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                         for (int k = 0; k < NT; ++k) {
-                            const h8 a = xs[half][(c * 4 + j) * NT * 4 + k * 4 + quad][(tok[tt] + 16 * j) % TOK];
+                            const h8 a = xs[half][(c * 4 + j) * NT * 4 + k * 4 + quad][(tok[tt] + 16 * j) % SLOTS];
 #pragma unroll
                             for (int r = 0; r < RT; ++r) acc[r][tt] = mfma(a, wq[r], acc[r][tt]);
                         }
@@ -344,19 +356,27 @@ void launch_pack_form(int groups, dim3 g, hipStream_t st, const void *w, const u
 #undef W4_PACK
 }
 
-template <bool BF16, int TT, int RT, int WK>
+template <bool BF16, int TT, int RT, int WK, int SLOTS = 16 * TT>
 void launch_linear_t(const W4Args &w, const void *x, int64_t N, float *y, float *part, const W4Plan &p,
                      hipStream_t st) {
     const dim3 g((unsigned)p.rows, (unsigned)p.tokens, (unsigned)p.shares), t(kW4Threads);
 #define W4_LINEAR(GS) \
-    hipLaunchKernelGGL((w4_linear_kernel<BF16, TT, GS, RT, WK>), g, t, 0, st, w, x, N, y, part)
+    hipLaunchKernelGGL((w4_linear_kernel<BF16, TT, GS, RT, WK, SLOTS>), g, t, 0, st, w, x, N, y, part)
     if (w.groups == 1) W4_LINEAR(1); else if (w.groups == 2) W4_LINEAR(2); else W4_LINEAR(4);
 #undef W4_LINEAR
 }
 template <bool BF16>
 void launch_linear(const W4Args &w, const void *x, int64_t N, float *y, float *part, const W4Plan &p,
                    hipStream_t st) {
-    if (p.tt == 1 && p.wk == 4) launch_linear_t<BF16, 1, 1, 4>(w, x, N, y, part, p, st);
+    if (N <= 4) {
+        if (p.wk == 4) launch_linear_t<BF16, 1, 1, 4, 4>(w, x, N, y, part, p, st);
+        else if (p.wk == 2) launch_linear_t<BF16, 1, 1, 2, 4>(w, x, N, y, part, p, st);
+        else launch_linear_t<BF16, 1, 1, 1, 4>(w, x, N, y, part, p, st);
+    } else if (N <= 8) {
+        if (p.wk == 4) launch_linear_t<BF16, 1, 1, 4, 8>(w, x, N, y, part, p, st);
+        else if (p.wk == 2) launch_linear_t<BF16, 1, 1, 2, 8>(w, x, N, y, part, p, st);
+        else launch_linear_t<BF16, 1, 1, 1, 8>(w, x, N, y, part, p, st);
+    } else if (p.tt == 1 && p.wk == 4) launch_linear_t<BF16, 1, 1, 4>(w, x, N, y, part, p, st);
     else if (p.tt == 1 && p.wk == 2) launch_linear_t<BF16, 1, 1, 2>(w, x, N, y, part, p, st);
     else if (p.tt == 1) launch_linear_t<BF16, 1, 1, 1>(w, x, N, y, part, p, st);
     else if (p.tt == 2 && p.rt == 2) launch_linear_t<BF16, 2, 2, 1>(w, x, N, y, part, p, st);

@@ -93,7 +93,7 @@ def test_products_of_integers_are_exact(bn, dtype, M, K):
     steps = rng.choice([1.0, 2.0, -1.0, 0.0], (M, K // group)).astype(np.float16)
     mat = bn.pack_w4_codes(dev(codes), dev(steps))
     top = 15 if dtype is BF16 else 2 ** 16 + 1
-    for N in (1, 2, 3, 7, 16, 17, 31, 33, 64, 65, 130):
+    for N in (1, 2, 3, 4, 5, 7, 8, 9, 16, 17, 31, 33, 64, 65, 130):
         x = np.zeros((N, K), np.float32)
         for t in range(N):
             at = rng.permutation(K)[:min(K, 8)]
