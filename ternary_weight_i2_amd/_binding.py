@@ -10,6 +10,7 @@ runs in the library's HIP kernels; nothing here computes a result.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -620,14 +621,15 @@ def kv4_append(cache, table, kv_len, q_start, k, v):
             v.data_ptr(), _rows(v, "v", heads, dim, dev), _float_code(k.dtype, "k"), k.shape[0])
 
 
+_put = object.__setattr__
+
+
 class _Fixed:
     """An object whose attributes stay as they were made: its descriptor is made once."""
     __slots__ = ()
 
     def __setattr__(self, name, value):
-        if hasattr(self, name):
-            raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make another")
-        object.__setattr__(self, name, value)
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make another")
 
 
 class Rotary(_Fixed):
@@ -641,8 +643,11 @@ class Rotary(_Fixed):
         import torch
         if turns.dim() != 1 or turns.dtype != torch.int64 or not turns.is_contiguous():
             raise TypeError("turns must be a contiguous 1-D int64 tensor")
-        self.turns, self.interleaved, self.magnitude = turns, bool(interleaved), float(magnitude)
-        self._plan = RotaryPlan(turns.data_ptr(), 2 * turns.shape[0], self.interleaved, self.magnitude)
+        interleaved, magnitude = bool(interleaved), float(magnitude)
+        _put(self, "turns", turns)
+        _put(self, "interleaved", interleaved)
+        _put(self, "magnitude", magnitude)
+        _put(self, "_plan", RotaryPlan(turns.data_ptr(), 2 * turns.shape[0], interleaved, magnitude))
 
 
 def rotary_plan(rot, base=10000.0, factor=1.0, length=0, low=1.0, high=32.0, freqs=None,
@@ -909,19 +914,24 @@ class W4Matrix(_Fixed):
 
     def __init__(self, codes, steps, rows=None):
         import torch
-        if codes.dim() != 4 or codes.dtype != torch.uint8 or codes.shape[2:] != (64, 16):
+        shape, groups = codes.shape, steps.shape
+        if codes.dtype != torch.uint8 or len(shape) != 4 or shape[2] != 64 or shape[3] != 16:
             raise TypeError("codes must be uint8 [tiles][K/128][64][16]")
-        if steps.dim() != 4 or steps.dtype != torch.float16 or steps.shape[3] not in (1, 2, 4) or \
-                steps.shape[:3] != (codes.shape[0], codes.shape[1], 16):
+        if steps.dtype != torch.float16 or len(groups) != 4 or groups[3] not in (1, 2, 4) or \
+                groups[:3] != (shape[0], shape[1], 16):
             raise TypeError("steps must be float16 [tiles][K/128][16][128/group]")
         if steps.device != codes.device or not codes.is_contiguous() or not steps.is_contiguous():
             raise ValueError("codes and steps must be contiguous, on one device")
-        tiles, blocks = codes.shape[:2]
-        self.rows = 16 * tiles if rows is None else rows
-        if not 16 * (tiles - 1) < self.rows <= 16 * tiles and (tiles or self.rows):
-            raise ValueError(f"{self.rows} rows are not {tiles} tiles of 16")
-        self.codes, self.steps, self.k, self.group = codes, steps, 128 * blocks, 128 // steps.shape[3]
-        self._desc = W4Desc(codes.data_ptr(), steps.data_ptr(), self.rows, self.k, self.group)
+        tiles, k, group = shape[0], 128 * shape[1], 128 // groups[3]
+        rows = 16 * tiles if rows is None else rows
+        if not 16 * (tiles - 1) < rows <= 16 * tiles and (tiles or rows):
+            raise ValueError(f"{rows} rows are not {tiles} tiles of 16")
+        _put(self, "codes", codes)
+        _put(self, "steps", steps)
+        _put(self, "rows", rows)
+        _put(self, "k", k)
+        _put(self, "group", group)
+        _put(self, "_desc", W4Desc(codes.data_ptr(), steps.data_ptr(), rows, k, group))
 
     @classmethod
     def empty(cls, rows, k, group=64, device="cuda"):
@@ -998,8 +1008,8 @@ def linear_w4(x, mat, out=None, workspace=None):
         to = out.data_ptr()
     else:
         to = _at(out, "out", torch.float32, (N, mat.rows), dev)
-    L = load()
-    need, ws = L.bitnet_linear_w4_workspace(N, mat.rows, mat.k), None
+    L, ws = load(), None
+    need = _w4_need(N, mat.rows, mat.k)
     if need > 0:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -1008,6 +1018,11 @@ def linear_w4(x, mat, out=None, workspace=None):
         ws = _ptr(workspace)
     _launch(L.bitnet_linear_w4, dev, at, _float_code(x.dtype, "x"), N, mat._desc, to, ws, max(need, 0))
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _w4_need(n, rows, k):   # of the sizes alone
+    return load().bitnet_linear_w4_workspace(n, rows, k)
 
 
 def linear_w4_workspace(n, rows, k):
