@@ -15,6 +15,13 @@
 // q . k_t = sum_g step_tg (q_g . (code_tg - 8)) + mid_tg sum(q_g), the products of codes on
 // the fp16 matrix instruction (q scaled by a power of two a row, in two fp16 terms of 22
 // bits for fp32 rows, exactly for bf16 ones), all else in fp32.
+//
+// What bounds it: 64 tokens over up to 4096, 64/8 heads of 128, bf16, take 26 + 33 us for 88 MB of
+// keys each time (3.4 and 2.7 TB/s): workgroups of 820 to 4096 tokens that start together, each
+// with a chain of five dependent loads, about 350 vector operations a page (11 us of them in
+// all).  131 fp32 rows of 20/5 heads that see 66 pages: 22 + 28 us, vector operations and, in
+// the second launch, 660 workgroups where 512 fit.  A prompt of 2048, 20/5 heads, bf16: 45 + 47 +
+// 4 us, vector operations.
 #include <algorithm>
 
 #include "codes4.h"
@@ -27,9 +34,9 @@ namespace {
 constexpr int kWeighThreads = 256;
 constexpr int kWeighWaves = kWeighThreads / 64;
 
-// Waves to a SIMD: four where the registers spill little for it (64 bf16 tokens, heads of 128:
-// 72 -> 62 us in all; fp32 rows 24.6 us with three and 28.9 with four for the first launch).
-constexpr int least_waves(int dim, bool bf16) { return dim == 256 ? 2 : dim == 128 ? 3 : 4; }
+// Waves to a SIMD: what the registers of a head hold beside the page asked for ahead (64 bf16
+// tokens, heads of 128: 61 us in all with three, 64.5 with four, which spill).
+constexpr int least_waves(int dim) { return dim == 256 ? 2 : dim == 128 ? 3 : 4; }
 
 // A row's query: 8 channels of every 32 in this lane (quad), times 2^k; the sums of its
 // groups at the same scale; and what makes a product of them a power of two's exponent.
@@ -241,7 +248,7 @@ __device__ __forceinline__ int share_of(int pages, int shares) {
 }
 
 template <int D, bool BF16>
-__global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_stats_kernel(const WeighArgs a, int64_t units) {
+__global__ __launch_bounds__(kWeighThreads, least_waves(D)) void weigh_stats_kernel(const WeighArgs a, int64_t units) {
     using L = Kv4Page<D>;
     __shared__ float m_all[kWeighWaves][16], l_all[kWeighWaves][16];
     __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
@@ -389,7 +396,7 @@ __device__ __forceinline__ int place_of(int lane) {
 // queries stay in registers.  The pages that the first tile does not see get their
 // old weights; what another tile adds, it adds to what its own lanes have written.
 template <int D, bool BF16>
-__global__ __launch_bounds__(kWeighThreads, least_waves(D, BF16)) void weigh_few_kernel(const WeighArgs a, int chunks, int64_t units) {
+__global__ __launch_bounds__(kWeighThreads, least_waves(D)) void weigh_few_kernel(const WeighArgs a, int chunks, int64_t units) {
     using L = Kv4Page<D>;
     __shared__ __align__(16) uint32_t pairs_all[kWeighWaves][D];
     const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4, place = place_of(lane);

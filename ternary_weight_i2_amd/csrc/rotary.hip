@@ -10,6 +10,12 @@
 // of sine and cosine in binary64 (off by less than 2^-52), so c and s are the nearest
 // fp32 numbers to all but one in 2^27 and what is quantised of a key afterwards does
 // not depend on how they were found.
+//
+// What bounds them: HBM for many rows (8191 of 32 heads of 80, bf16, 84 MB: 13.6 us where the
+// last-level cache has a part of it; prompts of 6800 tokens, 16 + 8 heads of 128, with the
+// append, 91 MB: 27 us, 3.4 TB/s), the launch and a chain of loads for few (64 rows of 32 heads
+// 3.8 us; one token with the append 4.2).  Angles are found once for all heads of a
+// workgroup's tokens and lie in LDS: 60 binary64 operations each, a few percent of a prompt.
 #include <algorithm>
 
 #include "kv4.h"
