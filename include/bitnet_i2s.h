@@ -604,13 +604,14 @@ int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, int64_t q_str
  *   batch       cache, table and kv_len; q_start is not looked at.
  *   weights     [n_pages][n_kv_heads][BITNET_KV4_PAGE], read at the old pages, written at
  *               the new ones.
- *   new_table   DEVICE [n_seqs][new_max_pages] int32.  No page of it may be one that the call
- *               reads (of any sequence), or that it has twice: what they then hold is
- *               unspecified.  Tokens of a page that is absent in it are dropped.
+ *   new_table   DEVICE [n_seqs][new_max_pages] int32, not table itself.  No page of it may be
+ *               one that the call reads (of any sequence), or that it has twice: what they then
+ *               hold is unspecified.  Tokens of a page that is absent in it are dropped.
  *   keep        1 .. 64 * new_max_pages; sinks and recent not negative, together at most keep.
- *   new_len     DEVICE [n_seqs] int32: the number of tokens kept.  (The rows' positions, which
- *               keys carry, do not change: the next row's is kv_len[b], not new_len[b], which
- *               is what the offsets of bitnet_rotary_kv4_append are for.)
+ *   new_len     DEVICE [n_seqs] int32, other memory than kv_len: the number of tokens kept.
+ *               (The rows' positions, which keys carry, do not change: the next row's is
+ *               kv_len[b], not new_len[b], which is what the offsets of
+ *               bitnet_rotary_kv4_append are for.)
  *   index       DEVICE [n_seqs][n_kv_heads][keep] int32: the position that each token had; -1
  *               behind the last.
  *   workspace   device scratch of at least bitnet_kv4_evict_workspace bytes (-1: sizes out

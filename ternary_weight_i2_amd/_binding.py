@@ -868,7 +868,7 @@ def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0,
     none that a sequence of the call has; the old ones are left as they are, to be handed out again.
 
     Returns (new_len [B], index [B][n_kv_heads][keep]: the places that the tokens had, -1
-    behind the last), int32, in ``out`` if given.  The step after goes on with new_table and new_len; its
+    behind the last), int32, in ``out`` if given (other memory than kv_len).  The step after goes on with new_table and new_len; its
     positions are kv_len - new_len further on (rotary_kv4_append's offset).  workspace: as in
     attn_kv4 (kv4_evict_workspace bytes, none for short tables)."""
     import torch

@@ -761,6 +761,11 @@ BITNET_API int bitnet_kv4_evict(const bitnet_kv4_batch *batch, float *weights,
     if (workspace_bytes < p.bytes)
         return fail(BITNET_E_SHAPE, "%s: the workspace has %lld bytes, %lld are required", fn,
                     (long long)workspace_bytes, (long long)p.bytes);
+    // heads that have not begun still read the old lengths
+    if (new_len < batch->kv_len + batch->n_seqs && batch->kv_len < new_len + batch->n_seqs)
+        return fail(BITNET_E_VALUE, "%s: new_len overlaps kv_len", fn);
+    if (new_table == batch->table)
+        return fail(BITNET_E_VALUE, "%s: new_table is table", fn);
     char *const ws = static_cast<char *>(workspace);
     const bitnet::EvictArgs a{static_cast<uint8_t *>(batch->cache), weights, batch->table,
                               batch->kv_len, new_table, new_len, index,

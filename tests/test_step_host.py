@@ -260,6 +260,14 @@ def test_evict_validation(L):
         assert L.bitnet_kv4_evict_workspace(*bad) == -1
 
 
+def test_evict_in_place_is_refused(L):
+    """Heads that have not begun still read kv_len, and every page of the table."""
+    other = FAKE + 4096
+    for nl in (FAKE, FAKE + 4, FAKE - 4):   # two sequences
+        assert _evict(L, nt=other, nl=nl) == E_VALUE
+    assert _evict(L, nl=other) == E_VALUE
+
+
 def test_weigh_and_evict_binding_refuses():
     import ternary_weight_i2_amd as bn
     c, table = torch.zeros((2, 1, 72 * 64), dtype=torch.uint8), torch.zeros((1, 1), dtype=torch.int32)
