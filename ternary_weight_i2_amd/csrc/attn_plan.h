@@ -134,7 +134,7 @@ inline WeighPlan weigh_plan(int64_t n_seqs, int64_t N, int64_t heads, int64_t kv
 // kv4_evict.hip: the workgroups that choose the tokens of a (sequence, kv head), and what they
 // tell each other: bins of three passes, the search's state after each, counts of each slice.
 constexpr int kBins = 2048;
-constexpr int kEvictSlicesFrom = 320;   // pages: 16384 tokens 35 us by one and 38.5 by four, 32768 52 and 39
+constexpr int kEvictSlicesFrom = 320;   // pages: 32768 tokens 52 us by one, 34 by eight; 16384 35 by one
 struct EvictPlan {
     int slices;
     int64_t search_at, slices_at, bytes;
@@ -142,7 +142,7 @@ struct EvictPlan {
 inline EvictPlan evict_plan(int64_t n_seqs, int64_t kv_heads, int64_t max_pages) {
     const int64_t units = n_seqs * kv_heads;
     EvictPlan p{1, 0, 0, 0};
-    // 131072 tokens of one head: 56 us by 16 workgroups, 57 by 32, 63 by 8; of eight: 82, 84, 88.
+    // 131072 tokens of one head: 47 us by 16 workgroups, 49 by 32, 54 by 8; of eight: 71, 73, 78.
     if (max_pages >= kEvictSlicesFrom)
         p.slices = (int)std::max<int64_t>(std::min({max_pages / 64, 2 * kUnits / units, (int64_t)16}), 1);
     if (p.slices == 1) return p;

@@ -8,8 +8,8 @@
 // (records as kv4.h lays them out) and writes them once.
 //
 // What bounds it: latency in the choice, of loads, LDS counts and barriers (16 sequences of
-// 2176 tokens, 8 heads: 12.5 us; one of 131072, 5 heads: 240 us by one workgroup each, 47 by 16 in
-// five launches of 7 to 12), HBM in the move of many tokens (13000 of 8 heads of 128, 34 MB with
+// 2176 tokens, 8 heads: 12.5 us; one of 131072, 5 heads: 240 us by one workgroup each, 38 by 16 in
+// four launches of 7 to 13), HBM in the move of many tokens (13000 of 8 heads of 128, 34 MB with
 // the weights: 10 us).
 #include <algorithm>
 
@@ -42,6 +42,24 @@ __device__ __forceinline__ int block_sum(int v, int *slot) {
     return t;
 }
 
+// Two of them at once, or four.
+template <bool FOUR>
+__device__ __forceinline__ int4 block_sum4(int4 v, int4 *slot) {
+    v.x = wave_sum_i32(v.x);
+    v.y = wave_sum_i32(v.y);
+    if constexpr (FOUR) {
+        v.z = wave_sum_i32(v.z);
+        v.w = wave_sum_i32(v.w);
+    }
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+    __syncthreads();
+    int4 t = make_int4(0, 0, 0, 0);
+    for (int w = 0; w < kChooseWaves; ++w)
+        t = make_int4(t.x + slot[w].x, t.y + slot[w].y, t.z + slot[w].z, t.w + slot[w].w);
+    __syncthreads();
+    return t;
+}
+
 // Inclusive sum over the lanes of a wave.
 __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
     const int lane = threadIdx.x & 63;
@@ -67,26 +85,44 @@ struct Unit {
         return *reinterpret_cast<const float4 *>(a.weights + ((int64_t)id * a.kv_heads + head) * kPage + t0 % kPage);
     }
 };
-__device__ __forceinline__ Unit unit_of(const EvictArgs &a, int64_t unit, int *slot) {
+__device__ __forceinline__ Unit unit_at(const EvictArgs &a, int64_t unit) {   // without its counts
     Unit u;
     u.seq = unit / a.kv_heads;
     u.row = unit;
     u.head = (int)(unit - u.seq * a.kv_heads);
     u.held = min(max(a.kv_len[u.seq], 0), (int)(a.max_pages * kPage));
-    int mine = 0, safe = 0;
+    return u;
+}
+__device__ __forceinline__ void set_counts(const EvictArgs &a, Unit &u, int there, int quota) {
+    u.there = there;
+    u.kept = min(there, a.keep);
+    u.quota = quota;
+}
+// The counts of a unit.  With BEFORE also of the tokens before `from` those whose page is
+// there, and of these the ones kept in any case.
+template <bool BEFORE>
+__device__ __forceinline__ int2 count_unit(const EvictArgs &a, Unit &u, int from, int4 *slot) {
+    int4 mine = make_int4(0, 0, 0, 0);
     for (int t0 = threadIdx.x * kPage; t0 < u.held; t0 += kChooseThreads * kPage)
         if (u.page_of(a, t0) >= 0) {
+            // of [t0, t1): [0, sinks) and [held - recent, held) may meet
+            auto safe = [&](int t1) {
+                const int low = min(max(a.sinks - t0, 0), t1 - t0);
+                const int high = min(max(t1 - max(u.held - a.recent, t0), 0), t1 - t0);
+                return min(low + high, t1 - t0);
+            };
             const int t1 = min(u.held, t0 + kPage);
-            mine += t1 - t0;
-            // [0, sinks) and [held - recent, held) may meet
-            const int low = min(max(a.sinks - t0, 0), t1 - t0);
-            const int high = min(max(t1 - max(u.held - a.recent, t0), 0), t1 - t0);
-            safe += min(low + high, t1 - t0);
+            mine.x += t1 - t0;
+            mine.y += safe(t1);
+            if constexpr (BEFORE) {
+                const int cut = min(max(from, t0), t1);
+                mine.z += cut - t0;
+                mine.w += safe(cut);
+            }
         }
-    u.there = block_sum(mine, slot);
-    u.kept = min(u.there, a.keep);
-    u.quota = u.kept - block_sum(safe, slot);   // not negative: sinks + recent <= keep
-    return u;
+    const int4 all = block_sum4<BEFORE>(mine, slot);
+    set_counts(a, u, all.x, min(all.x, a.keep) - all.y);   // not negative: sinks + recent <= keep
+    return make_int2(all.z, all.w);
 }
 
 // The search for the smallest order that is kept: its upper bits so far, and how many of the
@@ -112,24 +148,30 @@ __device__ __forceinline__ void count_four(const EvictArgs &a, const Unit &u, in
         atomicAdd(&bins[o >> shift & ((1 << width) - 1)], 1);
     }
 }
-// Counts the tokens of [from, to) (from a multiple of four).
+// Four tokens to a thread, kBatch times, are loaded before any is looked at.
+struct Batch {
+    int id[kBatch];
+    float4 w[kBatch];
+};
+__device__ __forceinline__ void load_batch(Batch &b, const EvictArgs &a, const Unit &u, int base, int to) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        const int t0 = base + 4 * kChooseThreads * i;
+        b.id[i] = t0 < to ? u.page_of(a, t0) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) b.w[i] = u.weights4(a, max(b.id[i], 0), base + 4 * kChooseThreads * i);
+}
+// Counts the tokens of [from, to) (from a multiple of four); `b`: the first of each thread.
 __device__ __forceinline__ void count_bins(const EvictArgs &a, const Unit &u, int pass, const Search &f, int from,
-                                           int to, int *bins) {
+                                           int to, int *bins, Batch b) {
     for (int i = threadIdx.x; i < kBins; i += kChooseThreads) bins[i] = 0;
     __syncthreads();
-    // four tokens to a thread, kBatch times: first all loads, then the counts
-    for (int base = from + 4 * (int)threadIdx.x; base < to; base += 4 * kChooseThreads * kBatch) {
-        int id[kBatch];
-        float4 w[kBatch];
+    for (int base = from + 4 * (int)threadIdx.x; base < to;) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int t0 = base + 4 * kChooseThreads * i;
-            id[i] = t0 < to ? u.page_of(a, t0) : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) w[i] = u.weights4(a, max(id[i], 0), base + 4 * kChooseThreads * i);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) count_four(a, u, pass, f, id[i], base + 4 * kChooseThreads * i, to, w[i], bins);
+        for (int i = 0; i < kBatch; ++i) count_four(a, u, pass, f, b.id[i], base + 4 * kChooseThreads * i, to, b.w[i], bins);
+        base += 4 * kChooseThreads * kBatch;
+        if (base < to) load_batch(b, a, u, base, to);
     }
     __syncthreads();
 }
@@ -169,15 +211,25 @@ __device__ __forceinline__ void kinds_of(const EvictArgs &a, const Unit &u, cons
         else if (u.choose() && o == f.least) tie |= 1u << e;
     }
 }
+// A thread's page and weights of a turn of placing, and its next page.
+struct Turn {
+    int id, id1;
+    float4 w4;
+};
+__device__ __forceinline__ Turn first_turn(const EvictArgs &a, const Unit &u, int from, int to) {
+    auto entry = [&](int t0) { return t0 < to ? u.page_of(a, t0) : -1; };
+    Turn t{entry(from + 4 * (int)threadIdx.x), entry(from + 4 * ((int)threadIdx.x + kChooseThreads)), {}};
+    t.w4 = u.weights4(a, max(t.id, 0), from + 4 * threadIdx.x);
+    return t;
+}
 // Gives the kept tokens of [from, to) their places, in order, behind those before them.
 __device__ __forceinline__ void place_tokens(const EvictArgs &a, const Unit &u, const Search &f, int from, int to,
-                                             int sure_before, int ties_before, uint32_t *scan) {
+                                             int sure_before, int ties_before, uint32_t *scan, const Turn &first) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int32_t *index = a.index + u.row * a.keep;
     auto entry = [&](int t0) { return t0 < to ? u.page_of(a, t0) : -1; };
-    // this turn's page and the next one's
-    int id = entry(from + 4 * tid), id1 = entry(from + 4 * (tid + kChooseThreads));
-    float4 w4 = u.weights4(a, max(id, 0), from + 4 * tid);
+    int id = first.id, id1 = first.id1;
+    float4 w4 = first.w4;
     for (int base = from; base < to; base += 4 * kChooseThreads) {
         const int t0 = base + 4 * tid, id2 = entry(t0 + 8 * kChooseThreads);
         const float4 next = u.weights4(a, max(id1, 0), t0 + 4 * kChooseThreads);
@@ -212,16 +264,18 @@ __device__ __forceinline__ void place_tokens(const EvictArgs &a, const Unit &u, 
 
 // The whole choice by one workgroup.
 __global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const EvictArgs a, int64_t units) {
-    __shared__ int bins[kBins], slot[kChooseWaves], found[2];
+    __shared__ int bins[kBins], found[2];
+    __shared__ int4 slot[kChooseWaves];
     __shared__ uint32_t scan[kChooseWaves];
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const Unit u = unit_of(a, unit, slot);
-        if (u.head == 0 && threadIdx.x == 0) a.new_len[u.seq] = u.kept;
-        Search f{0, u.quota};
+        Unit u = unit_at(a, unit);
         // four tokens to a thread are looked at again and again without being loaded again
         const bool few = u.held <= 4 * kChooseThreads;
         const int id = few && 4 * (int)threadIdx.x < u.held ? u.page_of(a, 4 * threadIdx.x) : -1;
         const float4 w4 = u.weights4(a, max(id, 0), 4 * threadIdx.x);
+        count_unit<false>(a, u, 0, slot);
+        if (u.head == 0 && threadIdx.x == 0) a.new_len[u.seq] = u.kept;
+        Search f{0, u.quota};
         if (u.choose())
             for (int pass = 0; pass < kPasses; ++pass) {
                 if (few) {
@@ -230,77 +284,85 @@ __global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const Evic
                     count_four(a, u, pass, f, id, 4 * threadIdx.x, u.held, w4, bins);
                     __syncthreads();
                 } else {
-                    count_bins(a, u, pass, f, 0, u.held, bins);
+                    Batch b;
+                    load_batch(b, a, u, 4 * threadIdx.x, u.held);
+                    count_bins(a, u, pass, f, 0, u.held, bins, b);
                 }
                 const int b1 = kBins - 1 - 2 * (int)threadIdx.x;
                 pick(f, pass, bins[b1], bins[b1 - 1], scan, found);
             }
-        place_tokens(a, u, f, 0, u.held, 0, 0, scan);
+        place_tokens(a, u, f, 0, u.held, 0, 0, scan, few ? Turn{id, -1, w4} : first_turn(a, u, 0, u.held));
         for (int i = u.kept + threadIdx.x; i < a.keep; i += kChooseThreads) a.index[u.row * a.keep + i] = -1;
     }
 }
 
-// The choice of a long history by `slices` workgroups, a launch for each step: STEP 0 to 2
-// count a slice's bins, 3 its sure tokens and ties, 4 gives them their places.  A step
-// finishes what the last one's counts of all slices say; what was found before is in a.search.
+// The choice of a long history by `slices` workgroups, a launch for each step: 0 to 2 count
+// a slice's bins, 3 gives its tokens their places.  A step first finishes the pass before it
+// from the counts of all slices, which also say how many of the slices before its own are kept:
+// its weights are on their way meanwhile.  a.search [3][unit]: what the passes 0 and 1 found, each
+// in a place of its own since other slices still read the last one's, and the unit's counts;
+// a.slices [unit][slice]: tokens before the slice that are known to be kept.
 template <int STEP>
 __global__ __launch_bounds__(kChooseThreads) void evict_step_kernel(const EvictArgs a, int slices) {
-    __shared__ int bins[kBins], slot[kChooseWaves], found[2];
+    __shared__ int bins[kBins], found[2], tied;
+    __shared__ int4 slot[kChooseWaves];
     __shared__ uint32_t scan[kChooseWaves];
     const int64_t unit = blockIdx.x / slices, units = gridDim.x / slices;
     const int slice = (int)(blockIdx.x - unit * slices), tid = threadIdx.x;
-    const Unit u = unit_of(a, unit, slot);
+    Unit u = unit_at(a, unit);
     const int share = ((u.held + slices - 1) / slices + 3) & ~3;   // at most 2^30 / 2
     const int from = min(slice * share, u.held), to = min(from + share, u.held);
+    Batch b;
+    Turn first;
+    if constexpr (STEP < kPasses) load_batch(b, a, u, from + 4 * tid, to);
+    else first = first_turn(a, u, from, to);
     int *const counts = a.counts + unit * slices * kBins;   // [pass][unit][slice][bin]
     const int64_t pass_size = units * slices * kBins;
+    int2 &known = a.slices[unit * slices + slice];
+    int sure_before, ties_before = 0;
+    if constexpr (STEP == 0) {
+        const int2 before = count_unit<true>(a, u, from, slot);
+        sure_before = u.kept == u.there ? before.x : before.y;
+        if (slice == 0 && tid == 0) a.search[2 * units + unit] = make_int2(u.there, u.quota);
+    } else {
+        const int2 c = a.search[2 * units + unit];
+        set_counts(a, u, c.x, c.y);
+        sure_before = known.x;
+    }
     Search f{0, u.quota};
-    if (u.choose() && STEP > 0) {
-        // what each step finds has a place of its own: other slices still read the last one's
+    if (STEP > 0 && u.choose()) {
         if (STEP > 1) {
-            const int2 before = a.search[(STEP - 2) * units + unit];
-            f = Search{(uint32_t)before.x, before.y};
+            const int2 last = a.search[(STEP - 2) * units + unit];
+            f = Search{(uint32_t)last.x, last.y};
         }
-        if (STEP <= kPasses) {
-            const int *of_pass = counts + (STEP - 1) * pass_size + kBins - 2 - 2 * tid;
-            int c1 = 0, c0 = 0;
+        const int *of_pass = counts + (STEP - 1) * pass_size + kBins - 2 - 2 * tid;
+        int c1 = 0, c0 = 0, p1 = 0, p0 = 0;   // p: in the slices before
 #pragma unroll 8
-            for (int s = 0; s < slices; ++s) {
-                const int2 c = *reinterpret_cast<const int2 *>(of_pass + s * kBins);
-                c0 += c.x;
-                c1 += c.y;
-            }
-            pick(f, STEP - 1, c1, c0, scan, found);
-            if (slice == 0 && tid == 0) a.search[(STEP - 1) * units + unit] = make_int2((int)f.least, f.ties);
+        for (int s = 0; s < slices; ++s) {
+            const int2 c = *reinterpret_cast<const int2 *>(of_pass + s * kBins);
+            c0 += c.x;
+            c1 += c.y;
+            p0 += s < slice ? c.x : 0;
+            p1 += s < slice ? c.y : 0;
         }
+        pick(f, STEP - 1, c1, c0, scan, found);
+        const int bin = (int)(f.least >> shift_of(STEP - 1)) & ((1 << width_of(STEP - 1)) - 1);
+        const int b1 = kBins - 1 - 2 * tid;
+        if (bin == b1) tied = p1;
+        if (bin == b1 - 1) tied = p0;
+        sure_before += block_sum((b1 > bin ? p1 : 0) + (b1 - 1 > bin ? p0 : 0), reinterpret_cast<int *>(slot));
+        ties_before = tied;
+        if (STEP < kPasses && slice == 0 && tid == 0) a.search[(STEP - 1) * units + unit] = make_int2((int)f.least, f.ties);
     }
     if constexpr (STEP < kPasses) {
+        if (tid == 0) known.x = sure_before;
         if (u.choose()) {
-            count_bins(a, u, STEP, f, from, to, bins);
+            count_bins(a, u, STEP, f, from, to, bins, b);
             for (int i = tid; i < kBins; i += kChooseThreads)
                 counts[STEP * pass_size + slice * kBins + i] = bins[i];
         }
-    } else if constexpr (STEP == kPasses) {
-        int n_sure = 0, n_tie = 0;
-        for (int t0 = from + 4 * tid; t0 < to; t0 += 4 * kChooseThreads) {
-            const int id = u.page_of(a, t0);
-            uint32_t sure, tie;
-            kinds_of(a, u, f, id, t0, to, u.weights4(a, max(id, 0), t0), sure, tie);
-            n_sure += __popc(sure);
-            n_tie += __popc(tie);
-        }
-        n_sure = block_sum(n_sure, slot);
-        n_tie = block_sum(n_tie, slot);
-        if (tid == 0) a.slices[unit * slices + slice] = make_int2(n_sure, n_tie);
     } else {
-        int sure_before = 0, ties_before = 0;
-#pragma unroll 8
-        for (int s = 0; s < slice; ++s) {
-            const int2 c = a.slices[unit * slices + s];
-            sure_before += c.x;
-            ties_before += c.y;
-        }
-        place_tokens(a, u, f, from, to, sure_before, ties_before, scan);
+        place_tokens(a, u, f, from, to, sure_before, ties_before, scan, first);
         for (int i = u.kept + slice * kChooseThreads + tid; i < a.keep; i += slices * kChooseThreads)
             a.index[u.row * a.keep + i] = -1;
         if (u.head == 0 && slice == 0 && tid == 0) a.new_len[u.seq] = u.kept;
@@ -385,7 +447,6 @@ hipError_t launch_kv4_evict(const EvictArgs &a, const EvictPlan &p, int dim, hip
         hipLaunchKernelGGL((evict_step_kernel<1>), g, t, 0, st, a, p.slices);
         hipLaunchKernelGGL((evict_step_kernel<2>), g, t, 0, st, a, p.slices);
         hipLaunchKernelGGL((evict_step_kernel<3>), g, t, 0, st, a, p.slices);
-        hipLaunchKernelGGL((evict_step_kernel<4>), g, t, 0, st, a, p.slices);
     }
     const int pages = (a.keep + kPage - 1) / kPage;
     const int64_t units = heads * pages;
