@@ -16,13 +16,14 @@
 // the fp16 matrix instruction (q scaled by a power of two a row, in two fp16 terms of 22
 // bits for fp32 rows, exactly for bf16 ones), all else in fp32.
 //
-// What bounds it: 64 tokens over up to 4096, 64/8 heads of 128, bf16, take 26 + 33 us for 88 MB of
-// keys each time (3.4 and 2.7 TB/s): workgroups of 820 to 4096 tokens that start together, each
-// with a chain of five dependent loads, about 350 vector operations a page (11 us of them in
-// all).  131 fp32 rows of 20/5 heads that see 66 pages: 22 + 28 us, vector operations and, in
+// What bounds it: 64 tokens over up to 4096, 64/8 heads of 128, bf16, take 26 + 30 us for 88 MB of
+// keys each time: workgroups of 820 to 4096 tokens that start together, each with a chain of
+// five dependent loads, and about 280 vector operations a page (two pages asked for ahead made it
+// 62 us in place of 60).  131 fp32 rows of 20/5 heads that see 66 pages: 22 + 28 us, vector operations and, in
 // the second launch, 660 workgroups where 512 fit.  A prompt of 2048, 20/5 heads, bf16: 45 + 47 +
 // 4 us, vector operations.
 #include <algorithm>
+#include <type_traits>
 
 #include "codes4.h"
 #include "kv4.h"
@@ -35,7 +36,7 @@ constexpr int kWeighThreads = 256;
 constexpr int kWeighWaves = kWeighThreads / 64;
 
 // Waves to a SIMD: what the registers of a head hold beside the page asked for ahead (64 bf16
-// tokens, heads of 128: 61 us in all with three, 64.5 with four, which spill).
+// tokens, heads of 128: 61 us in all with three, 64.5 with four, which spilled).
 constexpr int least_waves(int dim) { return dim == 256 ? 2 : dim == 128 ? 3 : 4; }
 
 // A row's query: 8 channels of every 32 in this lane (quad), times 2^k; the sums of its
@@ -152,32 +153,53 @@ __device__ __forceinline__ void share_pairs(const Keys<D> &k, uint32_t *pairs, i
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
-// x / q.scale of token 16 i + 4 quad + e and this lane's row, in s[i][e].
+// A tile of eight rows at most has each of them in two of its 16 columns (REP 2), and each of
+// their lanes works on its own half of a page's tokens behind the products: lane n has row
+// n % (16 / REP) and the tokens 16 i + 4 quad + e of 4 / REP i, from first_of<REP>(n) on.  64
+// bf16 tokens, 64/8 heads of 128: 60.2 us in all without, 55.6 so.  With fp32 rows the registers
+// do not do (one token over 131072, 20/5 heads: 43 and 48 us, spills), nor with heads of 256; four
+// rows four times took 48.9 there, and 16.1 for 15.5 us with heads of 64.
 template <int D, bool BF16>
+constexpr bool kTwice = BF16 && D <= 128;
+template <int D, bool BF16>
+__device__ __forceinline__ int rep_of(uint32_t left) { return kTwice<D, BF16> && left <= 8 ? 2 : 1; }
+template <int REP>
+__device__ __forceinline__ int first_of(int n) { return n / (16 / REP) * (4 / REP); }
+template <int REP>
+using Rep = std::integral_constant<int, REP>;
+
+// x / q.scale of token 16 i + 4 quad + e and this lane's row, in s[i - first_of][e].
+template <int REP, int D, bool BF16>
 __device__ __forceinline__ void scores(const Keys<D> &k, const uint32_t *pairs, const Query<D, BF16> &q,
-                                       uint32_t one, int quad, float (&s)[4][4]) {
+                                       uint32_t one, int n, int quad, float (&s)[4 / REP][4]) {
     using Q = Query<D, BF16>;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4 / REP; ++i) {
         f4 acc[Q::NG];
 #pragma unroll
-        for (int g = 0; g < Q::NG; ++g) {
-            acc[g] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int g = 0; g < Q::NG; ++g)
 #pragma unroll
-            for (int j = 2 * g; j < 2 * g + 2; ++j) {
-                h2 c[4];
-                codes8<false>(k.code[i][j], one, c);
-                const h8 kc = join(c[0], c[1], c[2], c[3]);
+            for (int part = 0; part < REP; ++part) {
+                f4 of_part = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int t = 0; t < Q::NT; ++t) acc[g] = mfma(kc, q.f[t][j], acc[g]);
+                for (int j = 2 * g; j < 2 * g + 2; ++j) {
+                    h2 c[4];
+                    codes8<false>(k.code[part * (4 / REP) + i][j], one, c);
+                    const h8 kc = join(c[0], c[1], c[2], c[3]);
+#pragma unroll
+                    for (int t = 0; t < Q::NT; ++t) of_part = mfma(kc, q.f[t][j], of_part);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[g][e] = part == 0 || n / (16 / REP) == part ? of_part[e] : acc[g][e];
             }
-        }
+        const int token = 16 * (first_of<REP>(n) + i) + 4 * quad;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float x = 0.0f;
 #pragma unroll
             for (int g = 0; g < Q::NG; ++g) {
-                const h2 p = as_h2(pairs[(16 * i + 4 * quad + e) * Q::NG + g]);   // (step, middle)
+                const h2 p = as_h2(pairs[(token + e) * Q::NG + g]);   // (step, middle)
                 x = fmaf((float)p[0], acc[g][e], fmaf((float)p[1], q.sum[g], x));
             }
             s[i][e] = x;
@@ -186,12 +208,13 @@ __device__ __forceinline__ void scores(const Keys<D> &k, const uint32_t *pairs, 
 }
 
 // Hides what a row at `pos`, whose window begins at `low`, does not see of page t0.
-__device__ __forceinline__ void hide(float (&s)[4][4], int t0, int quad, int pos, int low, int sinks) {
+template <int REP>
+__device__ __forceinline__ void hide(float (&s)[4 / REP][4], int t0, int n, int quad, int pos, int low, int sinks) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4 / REP; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int j = t0 + 16 * i + 4 * quad + e;
+            const int j = t0 + 16 * (first_of<REP>(n) + i) + 4 * quad + e;
             const bool hidden = (j > pos) | ((j < low) & (j >= sinks));
             s[i][e] = hidden ? -INFINITY : s[i][e];
         }
@@ -262,7 +285,8 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D)) void weigh_stats_ker
         const int kv_head = (int)(unit - u * a.c.kv_heads), split = (int)(u % a.splits);
         const Tile t = find_tile<16>(a.c, a.N, a.window, a.sinks, (uint32_t)(u / a.splits), G);
         if (t.rows == 0) continue;   // the whole workgroup
-        const uint32_t row = min(t.row0 + n, t.rows - 1), tok = row / G;
+        const int rep = rep_of<D, BF16>(t.rows - t.row0);
+        const uint32_t row = min(t.row0 + (n & (16 / rep - 1)), t.rows - 1), tok = row / G;
         const int head = kv_head * (int)G + (int)(row - tok * G);
         const int64_t line = (int64_t)(t.token0 + (int)tok) * a.heads + head;
         const int share = share_of(t.pages, a.splits), begin = min(split * share, t.pages), end = min(begin + share, t.pages);
@@ -282,32 +306,37 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D)) void weigh_stats_ker
                 keep_query(a.kept + ((u / a.splits) * a.c.kv_heads + kv_head) * (kept_pieces<D, BF16> * 64), q, lane);
             const int pos = t.pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
             const Seen seen = seen_of(a, t, G);
-            while (t0 >= 0) {
-                share_pairs(k, pairs_all[wave], lane);
-                const int t1 = w.next();   // a page is always loaded, at the end the last one again
-                Keys<D> ahead;
-                load_keys(ahead, cache + w.id * page_bytes, lane);
-                float s[4][4];
-                scores(k, pairs_all[wave], q, one, quad, s);
-                if (!seen.all(t0)) {
-                    asm volatile("");   // a branch: most pages are seen by all rows
-                    hide(s, t0, quad, pos, low, a.sinks);
+            auto walk = [&](auto reps) {
+                constexpr int REP = decltype(reps)::value;
+                while (t0 >= 0) {
+                    share_pairs(k, pairs_all[wave], lane);
+                    const int t1 = w.next();   // a page is always loaded, at the end the last one again
+                    Keys<D> ahead;
+                    load_keys(ahead, cache + w.id * page_bytes, lane);
+                    float s[4 / REP][4];
+                    scores<REP>(k, pairs_all[wave], q, one, n, quad, s);
+                    if (!seen.all(t0)) {
+                        asm volatile("");   // a branch: most pages are seen by all rows
+                        hide<REP>(s, t0, n, quad, pos, low, a.sinks);
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4 / REP; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][e]);
+                    const float m_new = fmaxf(m, top * q.scale);
+                    l *= __builtin_amdgcn_exp2f(m - m_new);
+                    m = m_new;
+#pragma unroll
+                    for (int i = 0; i < 4 / REP; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) l += __builtin_amdgcn_exp2f(fmaf(s[i][e], q.scale, -m));
+                    t0 = t1;
+                    k = ahead;
                 }
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[i][e]);
-                const float m_new = fmaxf(m, top * q.scale);
-                l *= __builtin_amdgcn_exp2f(m - m_new);
-                m = m_new;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) l += __builtin_amdgcn_exp2f(fmaf(s[i][e], q.scale, -m));
-                t0 = t1;
-                k = ahead;
-            }
+            };
+            if (kTwice<D, BF16> && rep == 2) walk(Rep<kTwice<D, BF16> ? 2 : 1>{});
+            else walk(Rep<1>{});
         }
         // a row's four lanes, then the waves
         const float top = quad_max(m);
@@ -318,13 +347,15 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D)) void weigh_stats_ker
             l_all[wave][n] = l;
         }
         __syncthreads();
-        if (threadIdx.x < 16 && t.row0 + n < t.rows) {
+        if ((int)threadIdx.x < 16 / rep && t.row0 + n < t.rows) {
             float best = m_all[0][n], sum = 0.0f;
+            for (int c = n; c < 16; c += 16 / rep)   // the row's columns
 #pragma unroll
-            for (int w = 1; w < kWeighWaves; ++w) best = fmaxf(best, m_all[w][n]);
+                for (int w = 0; w < kWeighWaves; ++w) best = fmaxf(best, m_all[w][c]);
+            for (int c = n; c < 16; c += 16 / rep)
 #pragma unroll
-            for (int w = 0; w < kWeighWaves; ++w)
-                sum = fmaf(l_all[w][n], __builtin_amdgcn_exp2f(m_all[w][n] - best), sum);
+                for (int w = 0; w < kWeighWaves; ++w)
+                    sum = fmaf(l_all[w][c], __builtin_amdgcn_exp2f(m_all[w][c] - best), sum);
             a.part[split * a.N * a.heads + line] = make_float2(best, sum);
         }
     }
@@ -356,34 +387,36 @@ __device__ __forceinline__ Row row_of(const WeighArgs &a, int64_t line, bool rea
     const bool good = real && l > 0.0f && l < INFINITY;
     return Row{good ? best : 0.0f, good ? 1.0f / l : 0.0f};
 }
-__device__ __forceinline__ void add_weights(float (&x)[4][4], float scale, const Row &r, float (&w)[4][4]) {
+template <int N>
+__device__ __forceinline__ void add_weights(float (&x)[N][4], float scale, const Row &r, float (&w)[N][4]) {
     if (__any(r.inv == 0.0f))   // their scores may be no numbers
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[i][e] = r.inv > 0.0f ? x[i][e] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             w[i][e] = fmaf(__builtin_amdgcn_exp2f(fmaf(x[i][e], scale, -r.max)), r.inv, w[i][e]);
 }
 // Over the 16 rows; lane n of a quad keeps token 16 (n / 4) + 4 quad + n % 4: lanes hand each
-// other the half of the values that the other keeps.
-template <int CTRL, int HALF>
-__device__ __forceinline__ void fold(float (&v)[16], bool upper) {
+// other the half of the values that the other keeps, but for what they have not (REP).
+template <int CTRL, int HALF, int N>
+__device__ __forceinline__ void fold(float (&v)[N], bool upper) {
 #pragma unroll
     for (int k = 0; k < HALF; ++k) {
         const float keep = upper ? v[k + HALF] : v[k], give = upper ? v[k] : v[k + HALF];
         v[k] = keep + dpp_f32<CTRL>(give);
     }
 }
-__device__ __forceinline__ float sum_rows(const float (&w)[4][4], int n) {
-    float v[16];
+template <int N>
+__device__ __forceinline__ float sum_rows(const float (&w)[N][4], int n) {
+    float v[4 * N];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = w[k >> 2][k & 3];
-    fold<kDppMirror, 8>(v, n & 8);
-    fold<kDppHalfMirror, 4>(v, n & 4);
+    for (int k = 0; k < 4 * N; ++k) v[k] = w[k >> 2][k & 3];
+    if constexpr (N == 4) fold<kDppMirror, 8>(v, n & 8);
+    if constexpr (N >= 2) fold<kDppHalfMirror, 4>(v, n & 4);
     fold<kDppXor2, 2>(v, n & 2);
     fold<kDppXor1, 1>(v, n & 1);
     return v[0];
@@ -420,7 +453,9 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D)) void weigh_few_kerne
         // written by itself, and a window's pages are spread over the workgroups.
         const int stride = kWeighWaves * chunks;
         for (uint32_t r = 0; r * 16 < rows; ++r) {
-            const uint32_t row0 = r * 16, last = min(row0 + 15, rows - 1), mine = row0 + n, row = min(mine, last), tok = row / G;
+            const uint32_t row0 = r * 16, last = min(row0 + 15, rows - 1);
+            const int rep = rep_of<D, BF16>(rows - row0);
+            const uint32_t mine = row0 + (n & (16 / rep - 1)), row = min(mine, last), tok = row / G;
             const int pos_a = pos0 + (int)(row0 / G), pos_b = pos0 + (int)(last / G);
             // the pages that its rows see: [0, sink_end) and [win, see_end)
             const int see_end = pos_b < 0 ? 0 : min(pos_b / kPage + 1, pages);
@@ -457,30 +492,35 @@ __global__ __launch_bounds__(kWeighThreads, least_waves(D)) void weigh_few_kerne
                         make_query(q, raw, a.scale_log2);
                     }
                     const Seen all{pos_a, a.window > 0 ? pos_b - a.window + 1 : 0, a.sinks};
-                    while (t0 >= 0) {
-                        const int64_t at = weight_at(id);
-                        const bool write = t0 + place < held;
-                        float was = 0.0f, factor = 1.0f;
-                        if (write) {
-                            if (r > 0) was = a.out[at];
-                            else if (t0 + place < pos0 && a.decay != 0.0f) was = a.old[at], factor = a.decay;
+                    auto walk = [&](auto reps) {
+                        constexpr int REP = decltype(reps)::value;
+                        while (t0 >= 0) {
+                            const int64_t at = weight_at(id);
+                            const bool write = t0 + place < held;
+                            float was = 0.0f, factor = 1.0f;
+                            if (write) {
+                                if (r > 0) was = a.out[at];
+                                else if (t0 + place < pos0 && a.decay != 0.0f) was = a.old[at], factor = a.decay;
+                            }
+                            share_pairs(k, pairs_all[wave], lane);
+                            const int t1 = page(seen, id);
+                            Keys<D> ahead;
+                            load_keys(ahead, cache + id * page_bytes, lane);
+                            float x[4 / REP][4], w[4 / REP][4] = {};
+                            scores<REP>(k, pairs_all[wave], q, one, n, quad, x);
+                            if (!all.all(t0)) {
+                                asm volatile("");
+                                hide<REP>(x, t0, n, quad, pos, low, a.sinks);
+                            }
+                            add_weights(x, q.scale, rs, w);
+                            const float sum = sum_rows(w, n);
+                            if (write) a.out[at] = fmaf(factor, was, sum);
+                            t0 = t1;
+                            k = ahead;
                         }
-                        share_pairs(k, pairs_all[wave], lane);
-                        const int t1 = page(seen, id);
-                        Keys<D> ahead;
-                        load_keys(ahead, cache + id * page_bytes, lane);
-                        float x[4][4], w[4][4] = {};
-                        scores(k, pairs_all[wave], q, one, quad, x);
-                        if (!all.all(t0)) {
-                            asm volatile("");
-                            hide(x, t0, quad, pos, low, a.sinks);
-                        }
-                        add_weights(x, q.scale, rs, w);
-                        const float sum = sum_rows(w, n);
-                        if (write) a.out[at] = fmaf(factor, was, sum);
-                        t0 = t1;
-                        k = ahead;
-                    }
+                    };
+                    if (kTwice<D, BF16> && rep == 2) walk(Rep<kTwice<D, BF16> ? 2 : 1>{});
+                    else walk(Rep<1>{});
                 }
                 while (rest) {   // pages that no row of the first tile sees, four at a time
                     int64_t at[4];
@@ -564,11 +604,11 @@ __global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const Weig
                     ask(min(r + kWeighWaves, r1 - 1));
                     const int pos = pos0 + (int)tok, low = a.window > 0 ? pos - a.window + 1 : 0;
                     float x[4][4];
-                    scores(k, pairs_all[wave], q, o, quad, x);
+                    scores<1>(k, pairs_all[wave], q, o, n, quad, x);
                     const Seen all{pos0 + (int)(r * 16 / G), a.window > 0 ? pos0 + (int)(last / G) - a.window + 1 : 0, a.sinks};
                     if (!all.all(t0)) {
                         asm volatile("");
-                        hide(x, t0, quad, pos, low, a.sinks);
+                        hide<1>(x, t0, n, quad, pos, low, a.sinks);
                     }
                     add_weights(x, q.scale, rs, w);
                 }

@@ -91,6 +91,24 @@ def test_weigh_rows_in_parts(bn, d, dtype):
     check_weigh(bn, s, 8, dtype, window=100, sinks=3)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group,new", [(1, [8, 9, 7]), (3, [3, 2, 8]), (7, [1, 2, 3]), (8, [1, 3, 2]), (9, [1, 1, 1])])
+def test_weigh_last_tiles_of_few_rows(bn, d, dtype, group, new):
+    """Tiles of up to eight rows, alone and behind full ones; whole histories and windows."""
+    s = Seqs([330, 64, 129], new, 2, d, seed=32, fill=0xFF).fill()
+    check_weigh(bn, s, 2 * group, dtype, decay=0.5)
+    check_weigh(bn, s, 2 * group, dtype, window=65, sinks=2)
+
+
+def test_weigh_few_rows_that_are_no_numbers(bn):
+    s = Seqs([200, 70], [1, 2], 1, 128, seed=33, fill=0xFF).fill()
+    q = s.rng.standard_normal((3, 8, 128)).astype(np.float32)
+    q[0, 2, 5], q[0, 7, 0], q[1], q[2, 0, 3] = np.nan, np.inf, -np.inf, np.nan
+    g, written = check_weigh(bn, s, 8, BF16, q=q)
+    assert np.isfinite(g[written]).all()
+
+
 def test_weigh_leaves_what_is_not_its_own(bn):
     """Absent pages, rows in front of the first sequence and behind the last, sequences without
     rows, rows before the first position, unwritten memory."""
