@@ -351,7 +351,7 @@ def _plain_place(s):
 
 def _pack_w4(w, group):
     """w[m][k] -> codes [16 rows][128 channels][quad, row][four times 8 channels of 4 bits] and
-    steps [16 rows][128 channels][row][group]; rows up to a multiple of 16 are zeros."""
+    steps [16 rows][128 channels][group][row]; rows up to a multiple of 16 are zeros."""
     m, k = w.shape
     tiles = -(-m // 16)
     w = torch.nn.functional.pad(w.float().clamp(-W4MAX, W4MAX), (0, 0, 0, 16 * tiles - m))
@@ -362,14 +362,14 @@ def _pack_w4(w, group):
     code = ((w * inv).round().clamp(-8, 7) + 8).to(torch.uint8)
     code = code.view(tiles, 16, k // 128, 4, 4, 4, 2).permute(0, 2, 4, 1, 3, 5, 6)
     code = (code[..., 0] | code[..., 1] << 4).reshape(tiles, k // 128, 64, 16)
-    return code, step.view(tiles, 16, k // 128, -1).transpose(1, 2).contiguous()
+    return code, step.view(tiles, 16, k // 128, -1).permute(0, 2, 3, 1).contiguous()
 
 
 def _plain_w4(s):
     c = s["case"]
     code = s["codes"].view(-1, c["k"] // 128, 4, 16, 4, 4).permute(0, 3, 1, 4, 2, 5)
     w = _nibbles(code).float().sub_(8).view(-1, c["k"] // c["group"], c["group"])
-    w.mul_(s["steps"].transpose(1, 2).float().reshape(w.shape[0], -1, 1))
+    w.mul_(s["steps"].permute(0, 3, 1, 2).float().reshape(w.shape[0], -1, 1))
     return torch.matmul(s["x"].float(), w.view(-1, c["k"])[:c["rows"]].t())
 
 
@@ -574,7 +574,7 @@ def exact(case, seed):
             byte = c % 128 // 32 * 4 + c % 8 // 2
             code = words[:, c // 128, c % 32 // 8, :, byte].permute(1, 2, 0)  # [tile][row][k]
             code = (code >> (4 * (c % 2)).to(torch.uint8) & 15).double() - 8
-            step = s["steps"][t:t + 256][:, c // 128, :, c % 128 // g].permute(1, 2, 0).double()
+            step = s["steps"][t:t + 256][:, c // 128, c % 128 // g].transpose(1, 2).double()
             outs.append(x @ (code * step).flatten(0, 1).t().contiguous())
         return torch.cat(outs, 1)[:, :m]
     if case["op"] == "turn":
