@@ -54,6 +54,7 @@ extern "C" {
 #define BITNET_KV4_MAX_SEQS (1 << 20)  /* sequences of a call                  */
 #define BITNET_KV4_MAX_PAGES (1 << 24) /* pages of a sequence (2^30 tokens)    */
 #define BITNET_W4_MAX_ROWS (1 << 24) /* rows of a matrix of 4-bit weights      */
+#define BITNET_W4_BY_GROUP 0x1000   /* bitnet_w4_matrix.group: order of the steps */
 #define BITNET_ROTARY_MAX_DIM 1024  /* channels of a head that positions turn   */
 
 typedef enum {
@@ -500,14 +501,15 @@ int bitnet_rotary_kv4_append(const bitnet_kv4_batch *batch, const bitnet_rotary_
  * as dwords of 8 channels, the first in the low bits:
  *   codes  [ceil(M/16)][K/128][4 quads][16 rows][4] dwords: dword (quad, row, j) has the
  *          block's channels 32 j + 8 quad + 0..7
- *   steps  [ceil(M/16)][K/128][16 rows][128/group] fp16
+ *   steps  [ceil(M/16)][K/128][16 rows][128/group] fp16, or with BITNET_W4_BY_GROUP
+ *          [ceil(M/16)][K/128][128/group][16 rows]
  */
 typedef struct {
     void *codes;            /* DEVICE, 16-byte aligned, ceil(M/16) * 8 * K bytes */
     void *steps;            /* DEVICE, 16-byte aligned, ceil(M/16) * 32 * K / group bytes */
     int64_t M;              /* 0 .. BITNET_W4_MAX_ROWS */
     int64_t K;              /* as K of the other matmuls */
-    int64_t group;          /* 32, 64 or 128 */
+    int64_t group;          /* 32, 64 or 128, plus BITNET_W4_BY_GROUP for steps in that order */
 } bitnet_w4_matrix;
 
 /*

@@ -36,6 +36,7 @@ class I2SMatrix(ctypes.Structure):
 
 
 KV4_PAGE = 64              # tokens of a page of the 4-bit cache
+W4_BY_GROUP = 0x1000       # W4Desc.group: the steps lie group by group
 
 
 class KV4Batch(ctypes.Structure):
@@ -906,10 +907,14 @@ def kv4_evict_workspace(n_seqs, n_kv_heads, max_pages):
     return need
 
 
+# groups of a block's 128 channels, by the last two sizes of the steps in either order
+_W4_PER_BLOCK = {s: p for p in (1, 2, 4) for s in ((16, p), (p, 16))}
+
+
 class W4Matrix(_Fixed):
     """A matrix of 4-bit weights [M][K] as pack_w4 lays it out: ``codes`` uint8
-    [ceil(M/16)][K/128][64][16], ``steps`` fp16 [ceil(M/16)][K/128][16][128/group], and the number of its
-    ``rows`` M (all of the tiles' if None)."""
+    [ceil(M/16)][K/128][64][16], ``steps`` fp16 [ceil(M/16)][K/128][16][128/group] or, group by
+    group, [ceil(M/16)][K/128][128/group][16], and the number of its ``rows`` M (all of the tiles' if None)."""
     __slots__ = ("codes", "steps", "rows", "k", "group", "_desc")
 
     def __init__(self, codes, steps, rows=None):
@@ -917,12 +922,12 @@ class W4Matrix(_Fixed):
         shape, groups = codes.shape, steps.shape
         if codes.dtype != torch.uint8 or len(shape) != 4 or shape[2] != 64 or shape[3] != 16:
             raise TypeError("codes must be uint8 [tiles][K/128][64][16]")
-        if steps.dtype != torch.float16 or len(groups) != 4 or groups[3] not in (1, 2, 4) or \
-                groups[:3] != (shape[0], shape[1], 16):
-            raise TypeError("steps must be float16 [tiles][K/128][16][128/group]")
+        per = _W4_PER_BLOCK.get(tuple(groups[2:]))
+        if steps.dtype != torch.float16 or per is None or groups[:2] != shape[:2]:
+            raise TypeError("steps must be float16 [tiles][K/128][16][128/group] or [tiles][K/128][128/group][16]")
         if steps.device != codes.device or not codes.is_contiguous() or not steps.is_contiguous():
             raise ValueError("codes and steps must be contiguous, on one device")
-        tiles, k, group = shape[0], 128 * shape[1], 128 // groups[3]
+        tiles, k, group = shape[0], 128 * shape[1], 128 // per
         rows = 16 * tiles if rows is None else rows
         if not 16 * (tiles - 1) < rows <= 16 * tiles and (tiles or rows):
             raise ValueError(f"{rows} rows are not {tiles} tiles of 16")
@@ -931,7 +936,8 @@ class W4Matrix(_Fixed):
         _put(self, "rows", rows)
         _put(self, "k", k)
         _put(self, "group", group)
-        _put(self, "_desc", W4Desc(codes.data_ptr(), steps.data_ptr(), rows, k, group))
+        _put(self, "_desc", W4Desc(codes.data_ptr(), steps.data_ptr(), rows, k,
+                                   group | (W4_BY_GROUP if groups[3] == 16 else 0)))
 
     @classmethod
     def empty(cls, rows, k, group=64, device="cuda"):

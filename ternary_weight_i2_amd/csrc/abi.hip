@@ -865,7 +865,8 @@ static int check_w4(const char *fn, const bitnet_w4_matrix *m) {
         return fail(BITNET_E_SHAPE, "%s: M=%lld outside [0, %d]", fn, (long long)m->M,
                     BITNET_W4_MAX_ROWS);
     if (int s = check_k(fn, m->K)) return s;
-    if (m->group != 32 && m->group != 64 && m->group != 128)
+    const int64_t group = m->group & ~(int64_t)BITNET_W4_BY_GROUP;
+    if (group != 32 && group != 64 && group != 128)
         return fail(BITNET_E_SHAPE, "%s: group=%lld must be 32, 64 or 128", fn, (long long)m->group);
     if (m->M == 0) return BITNET_OK;
     if (!m->codes || !m->steps) return fail(BITNET_E_NULL, "%s: codes and steps are required", fn);
@@ -874,15 +875,13 @@ static int check_w4(const char *fn, const bitnet_w4_matrix *m) {
     return BITNET_OK;
 }
 static bitnet::W4Args w4_args(const bitnet_w4_matrix *m) {
-    return bitnet::W4Args{static_cast<const uint8_t *>(m->codes),
-                          static_cast<const uint16_t *>(m->steps), (int)m->M, (int)m->K,
-                          (int)(128 / m->group)};
+    const int64_t group = m->group & ~(int64_t)BITNET_W4_BY_GROUP;
+    return bitnet::W4Args{static_cast<uint8_t *>(m->codes), static_cast<uint16_t *>(m->steps),
+                          (int)m->M, (int)m->K, (int)(128 / group), m->group != group};
 }
 static int pack_w4(const char *fn, const void *w, int form, const void *given,
                    const bitnet_w4_matrix *m, void *stream) {
-    hipError_t e = bitnet::launch_w4_pack(w, form, static_cast<const uint16_t *>(given), m->M, m->K,
-                                          (int)(128 / m->group), static_cast<uint8_t *>(m->codes),
-                                          static_cast<uint16_t *>(m->steps),
+    hipError_t e = bitnet::launch_w4_pack(w, form, static_cast<const uint16_t *>(given), w4_args(m),
                                           static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(fn, e);
     return ok();

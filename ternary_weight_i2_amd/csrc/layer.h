@@ -125,14 +125,14 @@ hipError_t launch_rotary_append(const RotaryArgs &r, const Kv4Args &c, const voi
                                 const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                 const int32_t *offset, int bf16, int64_t N, int dim,
                                 hipStream_t st);
-// A matrix of 4-bit weights (w4.hip has its layout); groups: steps of a row's 128 channels.
+// A matrix of 4-bit weights (w4.hip has its layout); groups: steps of a row's 128 channels,
+// by_group: these lie group by group, not row by row.
 struct W4Args {
-    const uint8_t *codes;
-    const uint16_t *steps;
-    int M, K, groups;
+    uint8_t *codes;
+    uint16_t *steps;
+    int M, K, groups, by_group;
 };
-hipError_t launch_w4_pack(const void *w, int form, const uint16_t *given, int64_t M, int64_t K,
-                          int groups, uint8_t *codes, uint16_t *steps, hipStream_t st);
+hipError_t launch_w4_pack(const void *w, int form, const uint16_t *given, const W4Args &to, hipStream_t st);
 hipError_t launch_w4_rows(const W4Args &w, const int32_t *ids, int64_t n, void *out, int bf16,
                           hipStream_t st);
 hipError_t launch_w4_linear(const W4Args &w, const void *x, int bf16, int64_t N, float *y,

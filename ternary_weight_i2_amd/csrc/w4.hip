@@ -7,7 +7,8 @@
 // Layout: tiles of 16 rows, blocks of 128 channels.  codes[tile][block][quad][row][j] is a
 // dword with channels 32 j + 8 quad + 0..7 of the block, the first in its low bits: 16
 // bytes of a lane (quad, row), 1 KB side by side for a wave, and each dword one operand
-// of the 16x16x32 matrix instruction.  steps[tile][block][row][128 / GROUP].
+// of the 16x16x32 matrix instruction.  steps[tile][block][row][128 / GROUP], or by group
+// steps[tile][block][128 / GROUP][row].
 //
 // The product runs on that instruction for any number of tokens: a code becomes code - 8 in
 // fp16 exactly, a token's 128 channels are scaled by a power of two so that the largest is
@@ -39,11 +40,10 @@ constexpr float kW4Max = 7.0f * 65504.0f; // 7 steps of the largest fp16
 // A wave takes a tile's block: lane (row, quad), 8 channels of each 32.  FORM 0: fp32, 1:
 // bf16 weights; 2: int8 codes -8..7 with steps given as [M][K / GROUP].
 template <int FORM, int GS>
-__global__ __launch_bounds__(256) void w4_pack_kernel(const void *w, const uint16_t *given, int64_t M,
-                                                      int64_t K, uint8_t *codes, uint16_t *steps) {
+__global__ __launch_bounds__(256) void w4_pack_kernel(const void *w, const uint16_t *given, const W4Args to) {
 #pragma clang fp contract(off)
     const int lane = threadIdx.x & 63, row = lane & 15, quad = lane >> 4;
-    const int64_t nblk = K / 128, m = (int64_t)blockIdx.x * 16 + row;
+    const int64_t M = to.M, K = to.K, nblk = K / 128, m = (int64_t)blockIdx.x * 16 + row;
     for (int64_t blk = blockIdx.y * 4 + (threadIdx.x >> 6); blk < nblk; blk += 4 * gridDim.y) {
         const int64_t at = m * K + blk * 128 + 8 * quad, out = ((int64_t)blockIdx.x * nblk + blk) * 64 + lane;
         uint32_t word[4] = {0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
@@ -102,11 +102,11 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const void *w, const uint1
                 }
             }
         }
-        reinterpret_cast<uint4 *>(codes)[out] = make_uint4(word[0], word[1], word[2], word[3]);
+        reinterpret_cast<uint4 *>(to.codes)[out] = make_uint4(word[0], word[1], word[2], word[3]);
         if (quad == 0)
 #pragma unroll
             for (int g = 0; g < GS; ++g)
-                steps[(((int64_t)blockIdx.x * nblk + blk) * 16 + row) * GS + g] = st[g];
+                to.steps[((int64_t)blockIdx.x * nblk + blk) * 16 * GS + (to.by_group ? g * 16 + row : row * GS + g)] = st[g];
     }
 }
 
@@ -124,8 +124,9 @@ __global__ __launch_bounds__(256) void w4_rows_kernel(const W4Args w, const int3
         if (there) {
             const int64_t at = (m >> 4) * nblk + blk;
             c = reinterpret_cast<const uint32_t *>(w.codes)[(at * 64 + quad * 16 + (m & 15)) * 4 + j];
+            const int row = (int)(m & 15), g = w.groups == 4 ? j : w.groups == 2 ? j >> 1 : 0;
             s = (float)__builtin_bit_cast(
-                _Float16, w.steps[(at * 16 + (m & 15)) * w.groups + (w.groups == 4 ? j : w.groups == 2 ? j >> 1 : 0)]);
+                _Float16, w.steps[at * 16 * w.groups + (w.by_group ? g * 16 + row : row * w.groups + g)]);
         }
         float x[8];
 #pragma unroll
@@ -159,17 +160,43 @@ __device__ __forceinline__ float halves_of(const float (&x)[8], h8 (&t)[NT]) {
     return ldexpf(1.0f, -k);
 }
 
+// The steps of a tile's block as a lane loads them: its row's, side by side; or by group one of
+// the tile's, which the lanes hand each other.
 template <int GS>
-struct StepWord;
-template <> struct StepWord<1> { using type = uint16_t; };
-template <> struct StepWord<2> { using type = uint32_t; };
-template <> struct StepWord<4> { using type = uint2; };
-__device__ __forceinline__ float step_of(uint16_t w, int) {
-    return (float)__builtin_bit_cast(_Float16, w);
+struct ByGroup {
+    uint16_t mine;   // of 16 GS: row n of group `quad` (two groups: quad % 2)
+};
+template <int GS, bool BY_GROUP>
+struct StepWord { using type = ByGroup<GS>; };
+template <> struct StepWord<1, false> { using type = uint16_t; };
+template <> struct StepWord<2, false> { using type = uint32_t; };
+template <> struct StepWord<4, false> { using type = uint2; };
+template <typename Word>
+__device__ __forceinline__ void load_steps(Word &w, const uint16_t *steps, int64_t block, int lane) {
+    w = reinterpret_cast<const Word *>(steps)[block * 16 + (lane & 15)];
 }
-__device__ __forceinline__ float step_of(uint32_t w, int g) { return (float)as_h2(w)[g]; }
-__device__ __forceinline__ float step_of(const uint2 &w, int g) {
-    return (float)as_h2(g < 2 ? w.x : w.y)[g & 1];
+template <int GS>
+__device__ __forceinline__ void load_steps(ByGroup<GS> &w, const uint16_t *steps, int64_t block, int lane) {
+    w.mine = steps[block * (16 * GS) + (lane & (16 * GS - 1))];
+}
+__device__ __forceinline__ float half_of(uint16_t w) { return (float)__builtin_bit_cast(_Float16, w); }
+__device__ __forceinline__ void steps_of(uint16_t w, float (&s)[1]) { s[0] = half_of(w); }
+__device__ __forceinline__ void steps_of(uint32_t w, float (&s)[2]) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) s[g] = (float)as_h2(w)[g];
+}
+__device__ __forceinline__ void steps_of(const uint2 &w, float (&s)[4]) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) s[g] = (float)as_h2(g < 2 ? w.x : w.y)[g & 1];
+}
+__device__ __forceinline__ void steps_of(const ByGroup<2> &w, float (&s)[2]) {
+    partners16(half_of(w.mine), s[0], s[1]);
+}
+__device__ __forceinline__ void steps_of(const ByGroup<4> &w, float (&s)[4]) {
+    float even, odd;
+    partners16(half_of(w.mine), even, odd);   // groups 0 0 2 2 and 1 1 3 3
+    partners32(even, s[0], s[2]);
+    partners32(odd, s[1], s[3]);
 }
 
 // The blocks of a turn: many, to be few turns, where a block's operands take little LDS.  (One
@@ -191,7 +218,7 @@ constexpr int blocks_of_turn(int slots, int wk, int terms) {
 // each block of weights a turn ahead of its use.  Token t of the 16 bytes (j, quad) = p lies
 // in slot (t + 4 p) mod SLOTS, so that the lanes that write eight channels each of a few tokens
 // spread over all banks; up to four tokens take four slots, up to eight eight.
-template <bool BF16, int TT, int GS, int RT, int WK, int SLOTS>
+template <bool BF16, int TT, int GS, bool BY_GROUP, int RT, int WK, int SLOTS>
 __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w, const void *x, int64_t N,
                                                                   float *y, float *part) {
     constexpr int NT = BF16 ? 1 : 2, TOK = 16 * TT;
@@ -207,7 +234,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w
     const int begin = (int)((int64_t)nblk * blockIdx.z / gridDim.z), end = (int)((int64_t)nblk * (blockIdx.z + 1) / gridDim.z);
     const int turn = wave % WK;   // of the waves of a tile: its blocks are turn, turn + WK, ...
     const int tile0 = ((int)blockIdx.x * (kW4Waves / WK) + wave / WK) * RT;
-    using Word = typename StepWord<GS>::type;
+    using Word = typename StepWord<GS, BY_GROUP>::type;
     uint4 raw[OWN][RT];
     Word st[OWN][RT];
     auto load_weights = [&](int i, int b0) {
@@ -215,7 +242,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w
         for (int r = 0; r < RT; ++r) {
             const int64_t at = (int64_t)min(tile0 + r, tiles - 1) * nblk + min(b0 + i * WK + turn, end - 1);
             raw[i][r] = reinterpret_cast<const uint4 *>(w.codes)[at * 64 + lane];
-            st[i][r] = reinterpret_cast<const Word *>(w.steps)[at * 16 + n];
+            load_steps(st[i][r], w.steps, at, lane);
         }
     };
     uint4 v[kPieces][NT];   // eight channels as they are
@@ -266,6 +293,9 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w
             const int c = i * WK + turn;
             if (b0 + c >= end) continue;
             f4 block[RT][TT];
+            float step[RT][GS];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) steps_of(st[i][r], step[r]);
 #pragma unroll
             for (int g = 0; g < GS; ++g) {
                 f4 acc[RT][TT];
@@ -293,14 +323,12 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_linear_kernel(const W4Args w
                         }
                 }
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const float step = step_of(st[i][r], g);
+                for (int r = 0; r < RT; ++r)
 #pragma unroll
                     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            block[r][tt][e] = g == 0 ? acc[r][tt][e] * step : fmaf(acc[r][tt][e], step, block[r][tt][e]);
-                }
+                            block[r][tt][e] = g == 0 ? acc[r][tt][e] * step[r][g] : fmaf(acc[r][tt][e], step[r][g], block[r][tt][e]);
             }
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt) {
@@ -355,11 +383,9 @@ __global__ __launch_bounds__(256) void w4_join_kernel(const float *part, int64_t
 }
 
 template <int FORM>
-void launch_pack_form(int groups, dim3 g, hipStream_t st, const void *w, const uint16_t *given, int64_t M,
-                      int64_t K, uint8_t *codes, uint16_t *steps) {
-#define W4_PACK(GS) \
-    hipLaunchKernelGGL((w4_pack_kernel<FORM, GS>), g, dim3(256), 0, st, w, given, M, K, codes, steps)
-    if (groups == 1) W4_PACK(1); else if (groups == 2) W4_PACK(2); else W4_PACK(4);
+void launch_pack_form(dim3 g, hipStream_t st, const void *w, const uint16_t *given, const W4Args &to) {
+#define W4_PACK(GS) hipLaunchKernelGGL((w4_pack_kernel<FORM, GS>), g, dim3(256), 0, st, w, given, to)
+    if (to.groups == 1) W4_PACK(1); else if (to.groups == 2) W4_PACK(2); else W4_PACK(4);
 #undef W4_PACK
 }
 
@@ -367,9 +393,12 @@ template <bool BF16, int TT, int RT, int WK, int SLOTS = 16 * TT>
 void launch_linear_t(const W4Args &w, const void *x, int64_t N, float *y, float *part, const W4Plan &p,
                      hipStream_t st) {
     const dim3 g((unsigned)p.rows, (unsigned)p.tokens, (unsigned)p.shares), t(kW4Threads);
-#define W4_LINEAR(GS) \
-    hipLaunchKernelGGL((w4_linear_kernel<BF16, TT, GS, RT, WK, SLOTS>), g, t, 0, st, w, x, N, y, part)
-    if (w.groups == 1) W4_LINEAR(1); else if (w.groups == 2) W4_LINEAR(2); else W4_LINEAR(4);
+#define W4_LINEAR(GS, BY_GROUP) \
+    hipLaunchKernelGGL((w4_linear_kernel<BF16, TT, GS, BY_GROUP, RT, WK, SLOTS>), g, t, 0, st, w, x, N, y, part)
+    if (w.groups == 1) W4_LINEAR(1, false);   // both orders are the same
+    else if (w.by_group) { if (w.groups == 2) W4_LINEAR(2, true); else W4_LINEAR(4, true); }
+    else if (w.groups == 2) W4_LINEAR(2, false);
+    else W4_LINEAR(4, false);
 #undef W4_LINEAR
 }
 template <bool BF16>
@@ -394,13 +423,12 @@ void launch_linear(const W4Args &w, const void *x, int64_t N, float *y, float *p
 
 }  // namespace
 
-hipError_t launch_w4_pack(const void *w, int form, const uint16_t *given, int64_t M, int64_t K, int groups,
-                          uint8_t *codes, uint16_t *steps, hipStream_t st) {
-    const int64_t tiles = (M + 15) / 16;
-    const dim3 g((unsigned)tiles, (unsigned)std::min<int64_t>((K / 128 + 3) / 4, 64));
-    if (form == 0) launch_pack_form<0>(groups, g, st, w, given, M, K, codes, steps);
-    else if (form == 1) launch_pack_form<1>(groups, g, st, w, given, M, K, codes, steps);
-    else launch_pack_form<2>(groups, g, st, w, given, M, K, codes, steps);
+hipError_t launch_w4_pack(const void *w, int form, const uint16_t *given, const W4Args &to, hipStream_t st) {
+    const int tiles = (to.M + 15) / 16;
+    const dim3 g((unsigned)tiles, (unsigned)std::min((to.K / 128 + 3) / 4, 64));
+    if (form == 0) launch_pack_form<0>(g, st, w, given, to);
+    else if (form == 1) launch_pack_form<1>(g, st, w, given, to);
+    else launch_pack_form<2>(g, st, w, given, to);
     return hipGetLastError();
 }
 

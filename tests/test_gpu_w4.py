@@ -235,3 +235,52 @@ def test_nothing_to_multiply(bn):
     none = bn.pack_w4(torch.empty((0, 128), device="cuda"))
     assert none.rows == 0 and bn.linear_w4(torch.ones((3, 128), device="cuda"), none).shape == (3, 0)
     assert (bn.w4_rows(none, torch.zeros(2, dtype=torch.int32, device="cuda")) == 0).all()
+
+
+def by_group(bn, mat):
+    return bn.W4Matrix(mat.codes, mat.steps.transpose(2, 3).contiguous(), mat.rows)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_steps_that_lie_group_by_group(bn, dtype, group):
+    """Packed and read in either order of the steps, a matrix is the same, bit for bit, and so are
+    its products, in every form of launch."""
+    rng = np.random.default_rng([9, group])
+    w = rng.standard_normal((37, 640)).astype(np.float32)
+    mat = bn.pack_w4(dev(w, dtype), group)
+    other = by_group(bn, mat)
+    into = bn.W4Matrix(torch.empty_like(other.codes), torch.empty_like(other.steps), 37)
+    assert bn.pack_w4(dev(w, dtype), group, out=into) is into
+    assert torch.equal(into.codes, other.codes) and torch.equal(into.steps, other.steps)
+    codes, steps = so.w4_quantise(host(dev(w, dtype)), group)
+    into.codes.zero_()
+    into.steps.zero_()
+    bn.pack_w4_codes(dev(codes), dev(steps), out=into)
+    assert torch.equal(into.codes, other.codes) and torch.equal(into.steps, other.steps)
+    ids = dev(np.array([36, 0, -1, 37, 16, 15], np.int32))
+    assert torch.equal(bn.w4_rows(other), bn.w4_rows(mat)) and torch.equal(bn.w4_rows(other, ids), bn.w4_rows(mat, ids))
+    for M, K in SHAPES + [(20000, 256), (12000, 4480), (4200, 2560)]:
+        codes = rng.integers(-8, 8, (M, K)).astype(np.int8)
+        steps = rng.choice([1.0, 2.0, -1.0, 0.5], (M, K // group)).astype(np.float16)
+        mat = bn.pack_w4_codes(dev(codes), dev(steps))
+        other, v = by_group(bn, mat), so.w4_values(codes, steps)
+        for N in (1, 3, 4, 5, 8, 16, 20, 33, 64):
+            x = np.zeros((N, K), np.float32)
+            for t in range(N):     # every sum is a multiple of 1/2 below 2^22
+                x[t, rng.permutation(K)[:8]] = rng.integers(-15, 16, 8)
+            y = bn.linear_w4(dev(x, dtype), other)
+            assert torch.equal(y, bn.linear_w4(dev(x, dtype), mat)), (M, K, N)
+            if N in (1, 5, 20, 64):
+                assert np.array_equal(host(y), (x.astype(np.float64) @ v.T).astype(np.float32)), (M, K, N)
+
+
+@pytest.mark.parametrize("group", [32, 64])
+def test_products_of_floats_with_steps_group_by_group(bn, group):
+    rng = np.random.default_rng([10, group])
+    for N, M, K in ((1, 2560, 2560), (5, 531, 1024), (64, 530, 4096)):
+        w = (0.02 * rng.standard_normal((M, K))).astype(np.float32)
+        mat = by_group(bn, bn.pack_w4(dev(w), group))
+        x = (rng.standard_normal((N, K)) * (1 + 30 * (rng.random(K) < 0.01))).astype(np.float32)
+        want, tol = so.w4_linear(x, so.w4_values(*so.w4_quantise(w, group)), group, False)
+        assert (np.abs(host(bn.linear_w4(dev(x), mat)) - want) <= tol).all()

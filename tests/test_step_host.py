@@ -198,6 +198,33 @@ def test_w4_binding_refuses():
         bn.w4_rows(m, torch.zeros(3, dtype=torch.int64))
 
 
+@pytest.mark.parametrize("name", W4)
+def test_w4_steps_in_either_order_validation(L, name):
+    """A group may carry the order of the steps; nothing else beside its size is taken."""
+    f, none = W4[name], dict(M=0, codes=None, steps=None)
+    for g in (32, 64, 128):
+        kw = {"rows": dict(n=0, out=None), "linear": dict(N=0, x=None, y=None)}.get(name, {})
+        assert f(L, _mat(group=g | 0x1000, **(none if not kw else {})), **kw) == OK
+    for g in (0x1000, 0x1000 | 48, 0x1000 | 256, 0x2000 | 64, 0x1800 | 64, (1 << 32) | 64):
+        assert f(L, _mat(group=g)) == E_SHAPE
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_matrix_takes_steps_in_either_order(group):
+    import ternary_weight_i2_amd as bn
+    m = bn.W4Matrix.empty(20, 256, group, device="cpu")
+    by_group = bn.W4Matrix(m.codes, m.steps.transpose(2, 3).contiguous(), 20)
+    for a in (m, by_group):
+        assert (a.rows, a.k, a.group) == (20, 256, group)
+    assert m._desc.group == group and by_group._desc.group in (group, group | 0x1000)
+    assert group == 128 or by_group._desc.group == group | 0x1000
+    for shape in ((2, 2, 3, 16), (2, 2, 16, 3), (2, 2, 8, 16), (2, 2, 16, 16), (2, 2, 4, 4), (2, 3, 4, 16), (1, 2, 4, 16)):
+        with pytest.raises(TypeError):
+            bn.W4Matrix(m.codes, torch.empty(shape, dtype=torch.float16), 20)
+    with pytest.raises(ValueError):     # not laid out so
+        bn.W4Matrix(m.codes, torch.empty((2, 2, 16, 4), dtype=torch.float16).transpose(2, 3), 20)
+
+
 # ---------------------------------------------------------------- weights of cached tokens, eviction
 
 def _weigh(L, b=None, q=FAKE, qs=256, dt=0, N=3, heads=4, scale=0.125, window=0, sinks=0, max_kv=64, w=FAKE,
