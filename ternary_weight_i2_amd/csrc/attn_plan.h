@@ -151,5 +151,16 @@ inline EvictPlan evict_plan(int64_t n_seqs, int64_t kv_heads, int64_t max_pages)
     p.bytes = p.slices_at + units * p.slices * 8;
     return p;
 }
+// The tokens [from, to) of a slice of a history of `held`.  `from` is a multiple of four also
+// behind the end (where to <= from): threads load four weights at once from there on, whether
+// they are the slice's or not, and four from a multiple of four on are in one page.
+struct EvictSlice {
+    int from, to;
+};
+constexpr EvictSlice evict_slice(int held, int slices, int slice) {
+    const int share = ((held + slices - 1) / slices + 3) & ~3;   // held is at most 2^30
+    const int end = (held + 3) & ~3, from = slice * share < end ? slice * share : end;
+    return EvictSlice{from, from + share < held ? from + share : held};
+}
 
 }  // namespace bitnet

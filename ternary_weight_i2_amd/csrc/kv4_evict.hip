@@ -310,8 +310,8 @@ __global__ __launch_bounds__(kChooseThreads) void evict_step_kernel(const EvictA
     const int64_t unit = blockIdx.x / slices, units = gridDim.x / slices;
     const int slice = (int)(blockIdx.x - unit * slices), tid = threadIdx.x;
     Unit u = unit_at(a, unit);
-    const int share = ((u.held + slices - 1) / slices + 3) & ~3;   // at most 2^30 / 2
-    const int from = min(slice * share, u.held), to = min(from + share, u.held);
+    const EvictSlice part = evict_slice(u.held, slices, slice);
+    const int from = part.from, to = part.to;
     Batch b;
     Turn first;
     if constexpr (STEP < kPasses) load_batch(b, a, u, from + 4 * tid, to);

@@ -278,6 +278,13 @@ def test_evict_by_several_workgroups(bn, wide):
     check_evict(bn, s, 3000, 0, 20, weights=w, wide=wide)
 
 
+def test_evict_of_histories_shorter_than_their_slices(bn):
+    """Most workgroups have no token: what they load lies inside a page all the same."""
+    for held in (33, 61, 62, 63, 64, 127):
+        for heads in (1, 3):
+            check_evict(bn, full([held], heads, 64, seed=held), 20, 2, 5, spare=0, wide=600)
+
+
 def test_evict_scratch(bn):
     """Scratch of any content, and none that is too short."""
     s = full([5000], 1, 64, seed=12)

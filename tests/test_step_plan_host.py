@@ -26,6 +26,11 @@ extern "C" void evict(const int64_t *a, int64_t *r) {
     const int64_t v[] = {p.slices, p.search_at, p.slices_at, p.bytes};
     for (int i = 0; i < 4; ++i) r[i] = v[i];
 }
+extern "C" void slice(const int64_t *a, int64_t *r) {
+    const bitnet::EvictSlice s = bitnet::evict_slice((int)a[0], (int)a[1], (int)a[2]);
+    r[0] = s.from;
+    r[1] = s.to;
+}
 """
 
 
@@ -39,7 +44,7 @@ def plan(tmp_path_factory):
 
     def call(name, *args):
         names = {"w4": "tt rt wk rows tokens shares", "weigh": "tiles splits chunks many parts kept_at sums_at bytes",
-                 "evict": "slices search_at slices_at bytes"}[name].split()
+                 "evict": "slices search_at slices_at bytes", "slice": "from to"}[name].split()
         out = (ctypes.c_int64 * len(names))()
         getattr(lib, name)((ctypes.c_int64 * len(args))(*args), out)
         return dict(zip(names, out))
@@ -130,3 +135,24 @@ def test_long_histories_are_chosen_from_by_several(plan):
             assert p["slices_at"] == p["search_at"] + 3 * seqs * kv * 8
             assert p["bytes"] == p["slices_at"] + seqs * kv * p["slices"] * 8
     assert plan("evict", 1, 5, 2048)["slices"] > 8
+
+
+def test_slices_of_a_history_load_inside_a_page(plan):
+    """Every token is in one slice, and the four weights that each of a slice's threads loads at
+    once lie in one page and on 16 bytes, also where the slice has no token."""
+    rng = random.Random(5)
+    helds = list(range(0, 400)) + [spread(rng, 400, 2 ** 30) for _ in range(300)] + [2 ** 30 - i for i in range(4)]
+    for held in helds:
+        for slices in (range(2, 17) if held < 400 else (rng.randint(2, 16), 16)):
+            at = 0
+            for k in range(slices):
+                s = plan("slice", held, slices, k)
+                assert s["from"] % 4 == 0, (held, slices, k)
+                for t in (s["from"], s["from"] + 4 * 1023, s["from"] + 4 * 1024 * 7 + 60):
+                    assert t % 64 + 4 <= 64 and t < 2 ** 31
+                if s["from"] < s["to"]:
+                    assert s["from"] == at and s["to"] <= held
+                    at = s["to"]
+                else:
+                    assert s["from"] >= held
+            assert at == held
