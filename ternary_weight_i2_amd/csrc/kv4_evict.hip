@@ -249,7 +249,9 @@ __device__ __forceinline__ void place_tokens(const EvictArgs &a, const Unit &u, 
         for (int e = 0; e < 4; ++e) {
             const bool is_tie = tie >> e & 1, in = (sure >> e & 1) || (is_tie && t < f.ties);
             const int at = s + min(t, f.ties);
-            if (in && at < u.kept) index[at] = t0 + e;   // (always, unless the weights change meanwhile)
+            // (always a place of the index, unless another stream writes the weights during the call:
+            // then a search may end without a result and `at` be anything, below 0 too)
+            if (in && (uint32_t)at < (uint32_t)u.kept) index[at] = t0 + e;
             s += sure >> e & 1;
             t += is_tie;
         }
