@@ -127,6 +127,7 @@ __global__ __launch_bounds__(256) void w4_rows_kernel(const W4Args w, const int3
             const int row = (int)(m & 15), g = w.groups == 4 ? j : w.groups == 2 ? j >> 1 : 0;
             s = (float)__builtin_bit_cast(
                 _Float16, w.steps[at * 16 * w.groups + (w.by_group ? g * 16 + row : row * w.groups + g)]);
+            if (s != s) s = __uint_as_float(0x7fc00000u);   // bf16_bits would carry other NaNs into the sign
         }
         float x[8];
 #pragma unroll

@@ -284,3 +284,12 @@ def test_products_of_floats_with_steps_group_by_group(bn, group):
         x = (rng.standard_normal((N, K)) * (1 + 30 * (rng.random(K) < 0.01))).astype(np.float32)
         want, tol = so.w4_linear(x, so.w4_values(*so.w4_quantise(w, group)), group, False)
         assert (np.abs(host(bn.linear_w4(dev(x), mat)) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_of_steps_that_are_no_numbers(bn, dtype):
+    """A NaN of any bits stays one when it is rounded to bf16."""
+    codes = np.arange(-8, 8, dtype=np.int8).repeat(8)[None].repeat(6, 0)
+    bits = np.array([[0x7FFF], [0xFFFF], [0x7E00], [0x7C01], [0xFDFF], [0x3C00]], np.uint16)
+    got = host(bn.w4_rows(bn.pack_w4_codes(dev(codes), dev(bits.view(np.float16))), dtype=dtype))
+    assert np.isnan(got[:5]).all() and np.array_equal(got[5], codes[5].astype(np.float32))
