@@ -14,6 +14,13 @@ constexpr int kMaxSplits = 256;
 constexpr int kPromptFrom = 2048, kPromptRows = 128;   // see attn4_plan
 constexpr int64_t kAttn4Workgroups = 1 << 24;   // of 256 threads: a launch has fewer than 2^32
 
+// The first of a sequence's own tiles of ROWS rows, G rows to a token: `begin` its first token in the
+// call, SLACK the tiles that a sequence may have beyond its rows' share.
+template <int ROWS, int SLACK>
+constexpr uint32_t first_tile(int begin, uint32_t G, int seq) {
+    return (uint32_t)begin * G / ROWS + (uint32_t)(SLACK * seq);
+}
+
 // Which kernel a call's sizes take (prompt: its tiles to a workgroup, or 0), how many
 // workgroups share the pages of one row tile, how many may be on a compute unit at
 // once (0: any), the tiles of a kv head and the workgroups of all.

@@ -43,8 +43,8 @@ struct Kv4Page {
     static constexpr int kBytes = 72 * D;
 };
 
-// Tiles of ROWS rows, a sequence's own from start[b] * G / ROWS + SLACK * b on: the
-// sequence of tile x, the largest b for which that is at most x; its rows [begin,
+// Tiles of ROWS rows, a sequence's own from first_tile on: the sequence of tile x, the
+// largest b for which that is at most x; its rows [begin,
 // end) as q_start has them, and `held`, the tokens that the cache can hold of it,
 // kv_len held to [0, 64 max_pages].  64 probes at a time, the same x in every lane;
 // the last 64 bring the lengths with them, which saves a round trip.  The result is
@@ -55,7 +55,7 @@ struct SeqAt {
 template <int ROWS, int SLACK>
 __device__ __forceinline__ SeqAt sequence_of(const Kv4Args &c, uint32_t G, uint32_t x) {
     const int lane = threadIdx.x & 63;
-    auto at_most = [&](int b, int begin) { return (uint32_t)begin * G / ROWS + SLACK * b <= x; };
+    auto at_most = [&](int b, int begin) { return first_tile<ROWS, SLACK>(begin, G, b) <= x; };
     int lo = 0, n = (int)c.n_seqs;   // the answer is in [lo, lo + n)
     while (n > 64) {
         const int step = (n + 63) >> 6, b = lo + lane * step;
@@ -101,7 +101,7 @@ __device__ __forceinline__ Tile find_tile(const Kv4Args &c, int64_t N, int windo
     t.token0 = s.begin;
     const bool good = s.begin >= 0 && s.end > s.begin && s.end <= (int)N;
     t.rows = good ? (uint32_t)(s.end - s.begin) * G : 0;
-    const int tile = (int)(x - ((uint32_t)s.begin * G / ROWS + s.seq));
+    const int tile = (int)(x - first_tile<ROWS, 1>(s.begin, G, s.seq));
     if (tile < 0) t.rows = 0;
     t.row0 = (uint32_t)tile * ROWS;
     t.held = s.held;
@@ -176,7 +176,7 @@ struct Block4 {
 __device__ __forceinline__ Block4 find_block(const Kv4Args &c, int64_t N) {
     Block4 k{-1, 0, 0, 0, 0, 0};
     const SeqAt s = sequence_of<4, 2>(c, 1, blockIdx.x);
-    const int tile = (int)(blockIdx.x - ((uint32_t)s.begin / 4 + 2 * s.seq));
+    const int tile = (int)(blockIdx.x - first_tile<4, 2>(s.begin, 1, s.seq));
     if (tile < 0 || s.begin < 0 || s.end <= s.begin || s.end > N) return k;
     const int pos0 = s.held - (s.end - s.begin), base = (pos0 & ~3) + 4 * tile;
     k.row = s.begin + base - pos0;

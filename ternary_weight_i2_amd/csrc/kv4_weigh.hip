@@ -565,7 +565,7 @@ __global__ __launch_bounds__(kWeighThreads, 2) void weigh_many_kernel(const Weig
         if (begin < 0 || end <= begin || end > a.N) continue;   // the whole workgroup
         const int pos0 = held - (end - begin);
         const uint32_t rows = (uint32_t)(end - begin) * G;
-        const uint32_t tile0 = (uint32_t)begin * G / 16 + seq;   // the sequence's first (find_tile)
+        const uint32_t tile0 = first_tile<16, 1>(begin, G, seq);   // as the first launch has them (find_tile)
         for (int t0 = chunk * kPage; t0 < held; t0 += chunks * kPage) {
             const int id = a.c.table[seq * a.c.max_pages + t0 / kPage];
             if (id < 0 || id >= a.c.n_pages) continue;   // the whole workgroup

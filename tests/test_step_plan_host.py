@@ -31,6 +31,10 @@ extern "C" void slice(const int64_t *a, int64_t *r) {
     r[0] = s.from;
     r[1] = s.to;
 }
+extern "C" void tile(const int64_t *a, int64_t *r) {
+    r[0] = bitnet::first_tile<16, 1>((int)a[0], (uint32_t)a[1], (int)a[2]);
+    r[1] = bitnet::first_tile<4, 2>((int)a[0], 1, (int)a[2]);
+}
 """
 
 
@@ -44,7 +48,7 @@ def plan(tmp_path_factory):
 
     def call(name, *args):
         names = {"w4": "tt rt wk rows tokens shares", "weigh": "tiles splits chunks many parts kept_at sums_at bytes",
-                 "evict": "slices search_at slices_at bytes", "slice": "from to"}[name].split()
+                 "evict": "slices search_at slices_at bytes", "slice": "from to", "tile": "rows16 block4"}[name].split()
         out = (ctypes.c_int64 * len(names))()
         getattr(lib, name)((ctypes.c_int64 * len(args))(*args), out)
         return dict(zip(names, out))
@@ -156,3 +160,40 @@ def test_slices_of_a_history_load_inside_a_page(plan):
                 else:
                     assert s["from"] >= held
             assert at == held
+
+
+def test_forms_of_a_product_go_by_the_tokens(plan):
+    """The kernels of up to 16 tokens are those that the planner means, and so are the others."""
+    rng = random.Random(6)
+    for i in range(4000):
+        N, M = rng.choice([1, 4, 16, 17, 32, 33, spread(rng, 1, 2 ** 21)]), spread(rng, 1, 2 ** 24)
+        p = plan("w4", N, M, 128 * spread(rng, 1, 256))
+        assert p["tt"] == (1 if N <= 16 else 2 if N <= 32 else 4)
+        assert p["rt"] == 1 if N <= 16 else p["wk"] == 1
+
+
+def test_a_history_has_sixteen_workgroups_at_most(plan):
+    rng = random.Random(7)
+    for i in range(2000):
+        p = plan("evict", spread(rng, 1, 2 ** 20), rng.choice([1, 5, 8, 1024]), spread(rng, 1, 2 ** 24))
+        assert 1 <= p["slices"] <= 16
+
+
+def test_first_tiles_leave_each_sequence_its_own(plan):
+    """Where the launches look for a sequence's tiles of 16 rows, or blocks of four positions, is
+    another's place for none of them, and none lies behind those that the planner counts."""
+    rng = random.Random(8)
+    for i in range(300):
+        G, new = rng.choice([1, 3, 4, 8]), [rng.choice([0, 1, 2, 30, 100]) for _ in range(rng.randint(1, 20))]
+        start, tiles, blocks = 0, [], []
+        for b, n in enumerate(new):
+            at = plan("tile", start, G, b)
+            tiles += [at["rows16"] + r for r in range(-(-n * G // 16))]
+            # from any place in a page on, n positions touch up to (n + 3) // 4 + 1 blocks of four
+            blocks += [at["block4"] + r for r in range((n + 3 + 3) // 4 if n else 0)]
+            start += n
+        for taken in (tiles, blocks):
+            assert len(set(taken)) == len(taken)
+        if start:
+            assert max(tiles) < plan("weigh", len(new), start, G, 1, 64, 4096, 0, 0, 1)["tiles"]
+            assert max(blocks) < start // 4 + 2 * len(new)
