@@ -585,6 +585,8 @@ int bitnet_linear_w4(const void *x, int dtype, int64_t N, const bitnet_w4_matrix
  * (fp32; bf16 exactly), all else in fp32 (a p below 2^-126 of the row's largest may count as
  * 0); rows whose |q| or scaled scores reach 2^100 are
  * unspecified.  Repeated calls with the same sizes give identical bits.
+ * One form of launch is taken for the whole call, by the rows of a sequence on average: long
+ * chunks are quicker in a call of their own than in one with many single tokens.
  */
 int64_t bitnet_kv4_weigh_workspace(int64_t n_seqs, int64_t N, int64_t n_heads, int64_t n_kv_heads,
                                    int64_t head_dim, int64_t max_kv, int64_t window,
@@ -619,7 +621,8 @@ int bitnet_kv4_weigh(const bitnet_kv4_batch *batch, const void *q, int64_t q_str
  *   workspace   device scratch of at least bitnet_kv4_evict_workspace bytes (-1: sizes out
  *               of range) for these sizes, 16-byte aligned (may be NULL where that is 0); used
  *               until the call's kernels have ended, so calls that may run at once need one each.
- * n_seqs == 0 is a no-op.
+ * A table of 320 pages or more is taken for one of long histories: of few sequences and heads it
+ * has more launches, and a workspace.  n_seqs == 0 is a no-op.
  */
 int64_t bitnet_kv4_evict_workspace(int64_t n_seqs, int64_t n_kv_heads, int64_t max_pages);
 

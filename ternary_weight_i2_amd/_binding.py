@@ -825,7 +825,8 @@ def kv4_weigh(weights, q, cache, table, kv_len, q_start, decay=1.0, scale=None, 
     share a kv head) to ``decay`` times its weight so far; tokens of the rows themselves begin
     at 0.  ``weights`` fp32 [n_pages][n_kv_heads][64] is updated, or with ``out`` left as it is (None will do with
     a decay of 0).  Sequences without rows keep theirs.  workspace: as in attn_kv4
-    (kv4_weigh_workspace bytes).  Returns out."""
+    (kv4_weigh_workspace bytes).  Long chunks are quicker in a call of their own than among many
+    single tokens.  Returns out."""
     import torch
     batch, kv_heads, dim = _kv4_batch(cache, table, kv_len, q_start)
     if q.dim() != 3:
@@ -871,7 +872,8 @@ def kv4_evict(cache, weights, table, kv_len, new_table, keep, sinks=0, recent=0,
     Returns (new_len [B], index [B][n_kv_heads][keep]: the places that the tokens had, -1
     behind the last), int32, in ``out`` if given (other memory than kv_len).  The step after goes on with new_table and new_len; its
     positions are kv_len - new_len further on (rotary_kv4_append's offset).  workspace: as in
-    attn_kv4 (kv4_evict_workspace bytes, none for short tables)."""
+    attn_kv4 (kv4_evict_workspace bytes, none for tables of fewer than 320 pages, which
+    take fewer launches too)."""
     import torch
     i32, dev = torch.int32, cache.device
     if weights is None or new_table is None or new_table.dim() != 2:

@@ -8,8 +8,8 @@
 // (records as kv4.h lays them out) and writes them once.
 //
 // What bounds it: latency in the choice, of loads, LDS counts and barriers (16 sequences of
-// 2176 tokens, 8 heads: 12.5 us; one of 131072, 5 heads: 240 us by one workgroup each, 38 by 16 in
-// four launches of 7 to 13), HBM in the move of many tokens (13000 of 8 heads of 128, 34 MB with
+// 2176 tokens, 8 heads: 12 to 14 us; one of 131072, 5 heads: 240 us by one workgroup each, 38 by 16 in
+// four launches of 7 to 12), HBM in the move of many tokens (13000 of 8 heads of 128, 34 MB with
 // the weights: 10 us).
 #include <algorithm>
 
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(kChooseThreads) void evict_choose_kernel(const Evic
 // from the counts of all slices, which also say how many of the slices before its own are kept:
 // its weights are on their way meanwhile.  a.search [3][unit]: what the passes 0 and 1 found, each
 // in a place of its own since other slices still read the last one's, and the unit's counts;
-// a.slices [unit][slice]: tokens before the slice that are known to be kept.
+// a.slices [unit][slice]: tokens before the slice that are known to be kept (x; y is not used).
 template <int STEP>
 __global__ __launch_bounds__(kChooseThreads) void evict_step_kernel(const EvictArgs a, int slices) {
     __shared__ int bins[kBins], found[2], tied;

@@ -6,11 +6,22 @@
 // summed over the rows of a sequence and the heads that share a kv head, whose queries are
 // rows of one problem as in attn_kv4.hip.
 //
-// Two launches.  The first gives each row's maximum m and sum, a workgroup to 16 rows and
+// Two launches or three.  The first gives each row's maximum m and sum, a workgroup to 16 rows and
 // a share of the pages that they see, its waves taking turns at the pages.  The second sums
-// by token: few rows with a wave to every fourth page of a share, many rows with a workgroup
-// to a page, so no token is added to by two of them and the order of the sums is fixed.
-// Between the launches lie 8 bytes a row and share; the keys are read by both.
+// by token.  Few rows: `chunks` workgroups have a sequence's pages, a wave every (4 chunks)-th
+// of the whole history, and go through the sequence's tiles of 16 rows one after another.  Many
+// rows, 64 to a sequence or more: a workgroup to a page, its waves taking turns at the tiles
+// that see it; where pages are few, several workgroups to a page, each with a part of these
+// tiles, and a third launch adds the parts.  So no number is added to by two waves at once and
+// the order of the sums is fixed.  The keys are read by both launches.
+// Between them lie 8 bytes a row and share of the pages; of many rows also the queries as
+// operands (a tile of 16 rows and kv head: 5 KB with bf16 heads of 128, 9 KB with fp32), most of
+// a prompt's workspace; and 256 bytes a page, kv head and part.
+//
+// The form is the whole call's, by the rows of a sequence on average: one long chunk among many
+// single tokens has few workgroups, which take its tiles one after another (255 tokens over 600
+// to 2000 and one chunk of 512 over 4096, 32/8 heads of 128, bf16: 2460 us; the tokens by
+// themselves 89, the chunk 109).  Two calls are the way there.
 //
 // q . k_t = sum_g step_tg (q_g . (code_tg - 8)) + mid_tg sum(q_g), the products of codes on
 // the fp16 matrix instruction (q scaled by a power of two a row, in two fp16 terms of 22

@@ -16,6 +16,11 @@
 // block's largest) or two (fp32: 22 bits, no finer than 2^-40 of the largest).  A group's sum and
 // the sum over groups are fp32.
 //
+// With the steps by group a lane loads one step of the tile's 16 GS and the groups go round by lane
+// swaps: two steps take one and four take three, and no more registers than the other order
+// (in graphs, by row and by group: one token times 128000 x 2560 36.4 and 36.8 us, 5 fp32 tokens
+// times 50001 x 1024, groups of 32, 11.1 and 11.5, 64 times 8192 x 8192 25.0 and 24.8).
+//
 // What bounds it.  Few tokens over a large matrix: HBM (one times 128000 x 2560, bf16, 175 MB in
 // 35 to 38 us, what a copy reaches; fp32 41; 16 tokens 41 and 49).  A small matrix: the chain of
 // launch, tokens, weights and sums (2560 x 2560 5.3 us, 6.1 with fp32).  From 17 tokens on the
